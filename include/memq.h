@@ -11,8 +11,10 @@
  * Around them: the fused decode steps memq_rmsnorm_q8_1_gemv_* (stage 1 inside the GEMV
  * launch), the decode step for host-resident rows memq_decode_step_host, the grouped GEMVs memq_gemv_*_group, the silu(gate) * up -> q8_1 producer
  * memq_silu_mul_q8_1, the load-time repack of E4M3 weights into a Q8_0 slab,
- * memq_repack_e4m3[_blk128]_q8_0, and the t <= 8 MLA decode attention kernels memq_mla_absorb_q,
- * memq_mla_attn_gathered and memq_mla_decompress_v.
+ * memq_repack_e4m3[_blk128]_q8_0, the t <= 8 MLA decode attention kernels memq_mla_absorb_q,
+ * memq_mla_attn_gathered and memq_mla_decompress_v, the producer with the residual stream's addition
+ * in front, memq_add_rmsnorm_q8_1, and latent attention over an 8-bit paged cache:
+ * memq_mla_cache_append, memq_mla_cache_read and memq_mla_attn_paged.
  *
  * The operations are the ones defined on the memra-engine 0.125.0 source pages:
  * q8_fuse_gate.rs (module doc: the `rms_norm` -> `quantize_q8_1` chain and the fused
@@ -83,6 +85,19 @@ typedef enum memq_status {
  */
 int memq_rmsnorm_q8_1(const float *x, const float *w, float *z, int8_t *qs, float *d,
                       int64_t ncols, int64_t rows, float eps, void *stream);
+
+/*
+ * memq_add_rmsnorm_q8_1 -- the residual stream's addition and memq_rmsnorm_q8_1 in one launch:
+ *     h[r][i] = x[r][i] + res[r][i]                    (f32, one rounding)
+ * and z, qs, d as memq_rmsnorm_q8_1 gives them for h, bit for bit.
+ *   x, res  device, f32 [rows][ncols], 16-byte aligned
+ *   h       device, f32 [rows][ncols], 16-byte aligned; may be x or res itself (the residual stream
+ *           updated in place), and may not overlap them otherwise
+ *   w, z, qs, d, ncols, rows, eps: as memq_rmsnorm_q8_1, with the same checks
+ */
+int memq_add_rmsnorm_q8_1(const float *x, const float *res, const float *w, float *h, float *z,
+                          int8_t *qs, float *d, int64_t ncols, int64_t rows, float eps,
+                          void *stream);
 
 /*
  * memq_gemv_e4m3 -- y = s * W_e4m3 . X_q8_1 (per-tensor scale).
@@ -301,6 +316,89 @@ int memq_mla_attn_gathered(const float *q_lat, const float *q_pe, const float *c
                            const int32_t *idx, float *out, int nh, int kv_rank, int d_rope, int t,
                            int n_slots, float scale, int split, void *stream);
 
+/* Element types of the entry points that take one as an argument. */
+typedef enum memq_dtype { MEMQ_F32 = 0, MEMQ_BF16 = 1 } memq_dtype;
+
+/*
+ * The paged latent cache.  A pool of n_pages pages of page_size rows; row s of the pool (its slot,
+ * page * page_size + offset) caches one token:
+ *   cache   device, uint8 E4M3 codes [n_pages][page_size][kv_rank + d_rope], 16-byte aligned: the
+ *           latent vector, then the decoupled position part of the key
+ *   scales  device, f32 [n_pages][page_size]: one scale per row, >= 0; element = scale * e4m3(code)
+ * kv_rank is 128, 256 or 512; d_rope is 0, 32, 64 or 128; the pool has at most 2^31 - 1 rows (byte
+ * offsets are 64-bit).
+ *
+ * memq_mla_cache_append: for r < n, with x = (latent[r], k_pe[r]) and s = slots[r]:
+ *     scales[s] = max |x| / 448;   cache[s][i] = e4m3(x[i] / scales[s])   (nearest, ties to even;
+ *     0 when the scale is 0)
+ * with IEEE f32 divisions.  A row with an infinity or a NaN is stored as zero codes under a NaN
+ * scale, so that queries that see it are NaN and all others are not touched by it; codes 0x7F and
+ * 0xFF (NaN) are never written.
+ *   dtype         a memq_dtype: the type of latent and k_pe
+ *   latent        device, [n][kv_rank], aligned to four elements (16 bytes f32, 8 bytes bf16)
+ *   k_pe          device, [n][d_rope], aligned alike; may be NULL when d_rope == 0
+ *   slots         device int32 [n]: a negative slot skips its row (a padded batch); a slot >= pool
+ *                 skips it too and sets bit 5 of the device fault word.  Slots should differ: when
+ *                 two rows name one slot, that slot's contents are a mixture of them.
+ *   pool          rows of the pool, n_pages * page_size
+ * memq_mla_cache_read: out[r][i] = scales[s] * e4m3(cache[s][i]) with s = slots[r], rounded once to
+ * the output's type; a negative slot gives a row of zeros, a slot >= pool too, with bit 5 set.  Slots
+ * may repeat.  Its f32 form rebuilds the cache that memq_mla_attn_gathered reads.
+ *   out           device, dtype [n][kv_rank + d_rope], aligned to four elements
+ * n >= 0 (0 = no-op).  Errors: MEMQ_ERR_SHAPE, MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
+ */
+int memq_mla_cache_append(int dtype, const void *latent, const void *k_pe, const int32_t *slots,
+                          uint8_t *cache, float *scales, int64_t n, int kv_rank, int d_rope,
+                          int64_t pool, void *stream);
+int memq_mla_cache_read(int dtype, const uint8_t *cache, const float *scales, const int32_t *slots,
+                        void *out, int64_t n, int kv_rank, int d_rope, int64_t pool, void *stream);
+
+/*
+ * memq_mla_attn_paged -- causal attention of each sequence's new tokens over its rows of the paged
+ * latent cache, with queries and outputs in the latent space (memq_mla_absorb_q before it,
+ * memq_mla_decompress_v after it).  Sequence b has the query tokens cu_q[b] .. cu_q[b + 1] - 1, its
+ * last t_b = cu_q[b + 1] - cu_q[b] tokens, and kv_len[b] cached rows, theirs included: cached row j
+ * lies in page block_table[b][j / page_size] at offset j % page_size, and token i of the t_b sees
+ * the rows j <= kv_len[b] - t_b + i.  With c_j the row's values:
+ *     s_j = scale * (q_lat . c_j[:kv_rank] + q_pe . c_j[kv_rank:])
+ *     out = sum_j softmax(s)_j * c_j[:kv_rank]
+ * A token that sees no row (kv_len[b] = 0, or fewer rows than new tokens) gets zeros.  Rows of q and
+ * out that belong to no sequence (before cu_q[0], from cu_q[n_seq] on) are neither read nor written.
+ *   q_dtype      a memq_dtype: the type of q_lat [n_tok][nh][kv_rank] and q_pe [n_tok][nh][d_rope]
+ *                (device, aligned to four elements; q_pe may be NULL when d_rope == 0)
+ *   cache, scales  the pool (scales 16-byte aligned); codes of visible rows are not NaN (what
+ *                memq_mla_cache_append writes); rows past a sequence's end may hold anything
+ *   block_table  device int32 [n_seq][max_pages]; entries past a sequence's last page are not read
+ *   kv_len       device int32 [n_seq];  cu_q  device int32 [n_seq + 1], ascending
+ *   out_dtype    a memq_dtype: the type of out [n_tok][nh][kv_rank] (device, aligned to four
+ *                elements); f32 holds the accumulators before the rounding to bf16
+ *   workspace    device, 16-byte aligned, at least memq_mla_attn_paged_workspace(kv_rank) bytes; it
+ *                is scratch of this call alone: calls that may run at the same time (two streams, two
+ *                graphs) need one each.  Nothing in it has to be initialised or kept.
+ *   page_size    a power of two, 16 to 1024;  1 <= nh <= 1024;  n_tok <= 2^24;  n_seq <= 4096;
+ *                scale finite.  n_tok == 0 or n_seq == 0 is a no-op that accepts NULL pointers.
+ * The lengths are read on the device only, so a captured call serves other lengths of the same
+ * arrays.  A kv_len outside [0, max_pages * page_size] is clamped, a page index outside the pool
+ * reads page 0, and cu_q outside [0, n_tok] is clamped: bit 5 of the device fault word is set for the
+ * first two, and the outputs of the sequence are invalid.
+ * Numerics: codes are used exactly; a query element with 8 significant bits (a bf16 value exactly
+ * down to 2^-10 of the row's largest element, an absolute 2^-18 of it below); a softmax weight within
+ * 2^-7 of its value (2^-10 rms) and 2^-20 of the row's largest weight, 2^-8 past it at most; products
+ * exact, sums, maxima and normalisation in f32.  Results do not depend on timing; they depend on how
+ * the tiles are split, so the same row may differ in the last bits between batches.
+ * Errors: MEMQ_ERR_SHAPE (also a workspace too small), MEMQ_ERR_NULL, MEMQ_ERR_ALIGN,
+ * MEMQ_ERR_LAUNCH.
+ */
+int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q_pe, const uint8_t *cache,
+                        const float *scales, const int32_t *block_table, const int32_t *kv_len,
+                        const int32_t *cu_q, int out_dtype, void *out, void *workspace,
+                        int64_t workspace_bytes, int64_t n_tok, int n_seq, int nh, int kv_rank,
+                        int d_rope, int64_t n_pages, int page_size, int max_pages, float scale,
+                        void *stream);
+/* Workspace bytes of memq_mla_attn_paged on the current device; -1 for an unsupported kv_rank or
+ * when the device cannot be queried. */
+int64_t memq_mla_attn_paged_workspace(int kv_rank);
+
 /* Human-readable name of a memq_status value (static storage; never NULL). */
 const char *memq_status_string(int status);
 
@@ -313,7 +411,9 @@ const char *memq_status_string(int status);
  * and returns; the call's outputs are invalid.  Bit 2: an
  * memq_mla_attn_gathered CTA's bounded wait for its gathered rows expired; bit 3: the same in
  * memq_mla_absorb_q / memq_mla_decompress_v.  That CTA stopped streaming, waited (bounded) for
- * its copies in flight and returned; the call's outputs are invalid.
+ * its copies in flight and returned; the call's outputs are invalid.  Bit 4: a bounded wait of
+ * memq_mla_attn_paged expired; the call's outputs are invalid.  Bit 5: a slot, page index or cached
+ * length given to the paged cache's calls was out of range (see there).
  * Returns MEMQ_ERR_NULL for a NULL fault_out, MEMQ_ERR_DEVICE if the copy fails.
  */
 int memq_device_fault(void *stream, uint32_t *fault_out);

@@ -24,10 +24,12 @@ from ._binding import (  # noqa: F401
     MAX_M,
     MAX_NCOLS,
     Container,
+    Dtype,
     MemqError,
     Status,
     lib,
     lib_path,
+    memq_add_rmsnorm_q8_1,
     memq_decode_step_host,
     memq_device_fault,
     memq_gemv_e4m3,
@@ -38,6 +40,10 @@ from ._binding import (  # noqa: F401
     memq_gemv_q8_0_group,
     memq_mla_absorb_q,
     memq_mla_attn_gathered,
+    memq_mla_attn_paged,
+    memq_mla_attn_paged_workspace,
+    memq_mla_cache_append,
+    memq_mla_cache_read,
     memq_mla_decompress_v,
     memq_rmsnorm_q8_1,
     memq_rmsnorm_q8_1_gemv_e4m3,

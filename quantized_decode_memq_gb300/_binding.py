@@ -34,6 +34,11 @@ class Container(enum.IntEnum):
     Q8_0 = 2
 
 
+class Dtype(enum.IntEnum):
+    F32 = 0
+    BF16 = 1
+
+
 class MemqError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -81,6 +86,13 @@ def lib() -> ctypes.CDLL:
                                                  ctypes.c_float, I32, P]
             L.memq_decode_step_host.argtypes = [I32, P, P, P, ctypes.c_float, P, P, P, P, P, P,
                                                 P, I64, I64, I32, P]
+            L.memq_add_rmsnorm_q8_1.argtypes = [P, P, P, P, P, P, P, I64, I64, ctypes.c_float, P]
+            L.memq_mla_cache_append.argtypes = [I32, P, P, P, P, P, I64, I32, I32, I64, P]
+            L.memq_mla_cache_read.argtypes = [I32, P, P, P, P, I64, I32, I32, I64, P]
+            L.memq_mla_attn_paged.argtypes = [I32, P, P, P, P, P, P, P, I32, P, P, I64, I64, I32,
+                                              I32, I32, I32, I64, I32, I32, ctypes.c_float, P]
+            L.memq_mla_attn_paged_workspace.argtypes = [I32]
+            L.memq_mla_attn_paged_workspace.restype = I64
             L.memq_device_fault.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
             L.memq_status_string.argtypes = [I32]
             L.memq_status_string.restype = ctypes.c_char_p
@@ -173,6 +185,40 @@ def memq_rmsnorm_q8_1(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, *, z=
                                  ctypes.c_float(eps), _stream(stream))
     _check("memq_rmsnorm_q8_1", rc)
     return z, qs, d
+
+
+def memq_add_rmsnorm_q8_1(x: torch.Tensor, res: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, *,
+                          h=None, z=None, qs=None, d=None, want_z: bool = True, stream=None):
+    """h = x + res, then RMSNorm -> q8_1 of h, in one launch.  x, res: f32 [rows, ncols] (or
+    [ncols]), w: f32 [ncols].
+
+    Returns (h f32 [rows, ncols], z f32 [rows, ncols] or None, qs int8 [rows, ncols],
+    d f32 [rows, ncols/32]).  h may be x or res itself (the residual updated in place).
+    """
+    x2 = x if x.dim() == 2 else x.reshape(1, -1)
+    r2 = res if res.dim() == 2 else res.reshape(1, -1)
+    _cuda("x", x2, torch.float32)
+    rows, ncols = x2.shape
+    _cuda("res", r2, torch.float32, (rows, ncols))
+    _cuda("w", w, torch.float32, (ncols,))
+    if h is None:
+        h = torch.empty((rows, ncols), dtype=torch.float32, device=x.device)
+    if qs is None:
+        qs = torch.empty((rows, ncols), dtype=torch.int8, device=x.device)
+    if d is None:
+        d = torch.empty((rows, ncols // 32), dtype=torch.float32, device=x.device)
+    if z is None and want_z:
+        z = torch.empty((rows, ncols), dtype=torch.float32, device=x.device)
+    h2 = h if h.dim() == 2 else h.reshape(1, -1)
+    _cuda("h", h2, torch.float32, (rows, ncols))
+    _cuda("qs", qs, torch.int8, (rows, ncols))
+    _cuda("d", d, torch.float32, (rows, ncols // 32))
+    if z is not None:
+        _cuda("z", z, torch.float32, (rows, ncols))
+    rc = lib().memq_add_rmsnorm_q8_1(_ptr(x2), _ptr(r2), _ptr(w), _ptr(h2), _ptr(z), _ptr(qs),
+                                     _ptr(d), ncols, rows, eps, _stream(stream))
+    _check("memq_add_rmsnorm_q8_1", rc)
+    return h, z, qs, d
 
 
 def _act(qs, d, in_f):
@@ -540,4 +586,131 @@ def memq_mla_attn_gathered(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, idx: 
                                       nh, kv_rank, d_rope, t, n_slots, float(scale), split,
                                       _stream(stream))
     _check("memq_mla_attn_gathered", rc)
+    return out
+
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _float(name: str, t: torch.Tensor, dtype=None, shape=None):
+    """A contiguous f32 or bf16 CUDA tensor; its memq_dtype."""
+    kind = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if isinstance(t, torch.Tensor) and kind is None:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    _cuda(name, t, t.dtype if dtype is None and kind is not None else dtype, shape)
+    return kind
+
+
+def _pool(fn: str, cache, scales, kv_rank=None):
+    """The paged cache's (width, pages, page_size)."""
+    _cuda("cache", cache, torch.uint8)
+    if cache.dim() != 3:
+        raise ValueError(f"{fn}: cache must be [n_pages, page_size, kv_rank + d_rope]")
+    pages, page_size, width = cache.shape
+    _cuda("scales", scales, torch.float32, (pages, page_size))
+    return width, pages, page_size
+
+
+def memq_mla_cache_append(latent: torch.Tensor, k_pe, slots: torch.Tensor, cache: torch.Tensor,
+                          scales: torch.Tensor, *, stream=None):
+    """Quantise rows into the paged latent cache: row r goes to pool row slots[r].
+
+    latent f32 or bf16 [n, kv_rank]; k_pe the same type [n, d_rope], or None (d_rope 0); slots
+    int32 [n], negative = skip; cache uint8 (E4M3 codes) [n_pages, page_size, kv_rank + d_rope] and
+    scales f32 [n_pages, page_size] are written in place."""
+    fn = "memq_mla_cache_append"
+    kind = _float("latent", latent)
+    if latent.dim() != 2:
+        raise ValueError(f"{fn}: latent must be [n, kv_rank]")
+    n, kv_rank = latent.shape
+    width, pages, page_size = _pool(fn, cache, scales)
+    d_rope = width - kv_rank
+    if k_pe is not None:
+        _float("k_pe", k_pe, latent.dtype, (n, d_rope))
+    elif d_rope != 0:
+        raise ValueError(f"{fn}: k_pe is required when the cache rows are wider than kv_rank")
+    _cuda("slots", slots, torch.int32, (n,))
+    rc = lib().memq_mla_cache_append(kind, _ptr(latent), _ptr(k_pe), _ptr(slots), _ptr(cache),
+                                     _ptr(scales), n, kv_rank, d_rope, pages * page_size,
+                                     _stream(stream))
+    _check(fn, rc)
+
+
+# (kv_rank, d_rope) of a row width; the read needs only their sum, which names one pair's sum
+_WIDTHS = {r + p: (r, p) for r in (128, 256, 512) for p in (0, 32, 64, 128)}
+
+
+def memq_mla_cache_read(cache: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, *,
+                        out=None, dtype=torch.bfloat16, stream=None):
+    """The values of the pool rows named by slots (int32 [n], repeats allowed, negative = zeros):
+    f32 or bf16 [n, kv_rank + d_rope], in `out` or a new tensor of `dtype`."""
+    fn = "memq_mla_cache_read"
+    width, pages, page_size = _pool(fn, cache, scales)
+    if width not in _WIDTHS:
+        raise ValueError(f"{fn}: rows of {width} elements are no kv_rank + d_rope")
+    _cuda("slots", slots, torch.int32)
+    if slots.dim() != 1:
+        raise ValueError(f"{fn}: slots must be [n]")
+    n = slots.shape[0]
+    if out is None:
+        out = torch.empty((n, width), dtype=dtype, device=cache.device)
+    kind = _float("out", out, None, (n, width))
+    rc = lib().memq_mla_cache_read(kind, _ptr(cache), _ptr(scales), _ptr(slots), _ptr(out), n,
+                                   *_WIDTHS[width], pages * page_size, _stream(stream))
+    _check(fn, rc)
+    return out
+
+
+def memq_mla_attn_paged_workspace(kv_rank: int) -> int:
+    """Workspace bytes of memq_mla_attn_paged on the current device."""
+    n = lib().memq_mla_attn_paged_workspace(kv_rank)
+    if n < 0:
+        raise ValueError(f"memq_mla_attn_paged: kv_rank must be 128, 256 or 512, got {kv_rank}")
+    return n
+
+
+def memq_mla_attn_paged(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, scales: torch.Tensor,
+                        block_table: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor,
+                        scale: float, *, out=None, workspace=None, stream=None):
+    """Causal attention of each sequence's new tokens over its rows of the paged latent cache.
+
+    q_lat f32 or bf16 [n_tok, nh, kv_rank]; q_pe the same type [n_tok, nh, d_rope], or None (d_rope
+    0); cache, scales as memq_mla_cache_append writes them; block_table int32 [n_seq, max_pages];
+    kv_len int32 [n_seq]; cu_q int32 [n_seq + 1] -> out [n_tok, nh, kv_rank], bf16 unless an f32
+    `out` is given.  workspace: uint8 scratch of at least memq_mla_attn_paged_workspace(kv_rank)
+    bytes, one per call that may run at the same time; a new one is taken when it is None."""
+    fn = "memq_mla_attn_paged"
+    q_kind = _float("q_lat", q_lat)
+    if q_lat.dim() != 3:
+        raise ValueError(f"{fn}: q_lat must be [n_tok, nh, kv_rank]")
+    n_tok, nh, kv_rank = q_lat.shape
+    width, pages, page_size = _pool(fn, cache, scales)
+    d_rope = width - kv_rank
+    if q_pe is not None:
+        _float("q_pe", q_pe, q_lat.dtype, (n_tok, nh, d_rope))
+    elif d_rope != 0:
+        raise ValueError(f"{fn}: q_pe is required when the cache rows are wider than kv_rank")
+    _cuda("block_table", block_table, torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError(f"{fn}: block_table must be [n_seq, max_pages]")
+    n_seq, max_pages = block_table.shape
+    _cuda("kv_len", kv_len, torch.int32, (n_seq,))
+    _cuda("cu_q", cu_q, torch.int32, (n_seq + 1,))
+    if out is None:
+        out = torch.empty((n_tok, nh, kv_rank), dtype=torch.bfloat16, device=q_lat.device)
+    o_kind = _float("out", out, None, (n_tok, nh, kv_rank))
+    st = _stream(stream)
+    if workspace is None:
+        need = memq_mla_attn_paged_workspace(kv_rank)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
+        else:  # memory of the stream that uses it
+            with torch.cuda.stream(torch.cuda.ExternalStream(st)):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
+    _cuda("workspace", workspace, torch.uint8)
+    rc = lib().memq_mla_attn_paged(q_kind, _ptr(q_lat), _ptr(q_pe), _ptr(cache), _ptr(scales),
+                                   _ptr(block_table), _ptr(kv_len), _ptr(cu_q), o_kind, _ptr(out),
+                                   _ptr(workspace), workspace.numel(), n_tok, n_seq, nh, kv_rank,
+                                   d_rope, pages, page_size, max_pages, scale, st)
+    _check(fn, rc)
     return out
