@@ -20,11 +20,14 @@
 //   q = 2^e (hi + lo), both E4M3, e per row: 8 significant bits, which hold a bf16 value exactly
 //       down to 2^-10 of the row's largest; below that an absolute 2^-18 of the largest;
 //   p = hi (E4M3) + lo (E5M2), with p in (0, 2^8]: a relative 2^-7 at most (about 2^-10 rms), and
-//       an absolute 2^-17, 2^-21 of the running maximum: E5M2 carries the long tail of small
-//       weights that a second E4M3 term would flush.
-// The key's scale is folded into its weight (p_j = 2^4 exp2(s_j + log2 scales_j - R)), so R, the
+//       an absolute 2^-17, 2^-19 of the running maximum: E5M2 carries the long tail of small
+//       weights that a second E4M3 term would flush.  Both codes are bit fields of f16 numbers:
+//       E4M3 of v is bits 14..7 of f16(v / 256), E5M2 of v the high byte of f16(v), so the split
+//       needs one conversion per pair of weights and integer operations.
+// The key's scale is folded into its weight (p_j = 2^8 exp2(s_j + log2 scales_j - R - 6)), so R, the
 // running reference, bounds what the 8-bit terms must hold; the sum of weights is kept apart in f32.
-// R moves, and the accumulators are rescaled, only when a tile's maximum exceeds it by 2^4.
+// R moves, and the accumulators are rescaled, only when a tile's maximum exceeds it by 2^6: a tile
+// then needs one vote instead of 64 maxima over its keys.
 //
 // One CTA per SM.  The 128-key tiles of all (sequence, token group, head block) items form one list
 // that is cut into equal runs, one per CTA; every CTA derives its run from the lengths on the device
@@ -67,8 +70,7 @@ constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxGrid = 256;
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
-constexpr float kSlack = 4.0f;    // log2 of how far weights may exceed the reference
-constexpr float kBase = 4.0f;     // log2 of a weight at the reference
+constexpr float kSlack = 6.0f;    // log2 of how far a score may exceed the reference
 constexpr int kScoreCol = 256;    // TMEM: accumulators in columns 0..255, scores after them
 
 struct Owner {
@@ -96,6 +98,12 @@ struct PagedArgs {
     float scale_log2;
 };
 
+struct Item {
+    int seq, start, t, kv;  // sequence, its first token row, new tokens, cached rows
+    int tok, block;         // first token of the group, head block
+    int vis, tiles;         // keys that its last token sees, tiles
+};
+
 struct Control {
     uint32_t tops[3][kRows];  // column maxima of three successive tiles (order_bits)
     float row_scale[kRows];
@@ -103,8 +111,9 @@ struct Control {
     uint64_t rope_full, rope_free, scale_full[2], scale_free[2], score_full[2];
     uint64_t weights_ready, out_done, q_ready, drain;
     uint32_t tmem;
-    int first_seq, first_tok, first_block, first_off;
-    long long total, warp_sum[kThreads / 32];
+    int first_off;
+    Item first;
+    long long warp_sum[kThreads / 32];
 };
 static_assert(sizeof(Control) <= 2048, "the control block has 2 KB of shared memory");
 
@@ -114,12 +123,6 @@ __host__ __device__ constexpr int smem_ring_off(int rank, int rope) {
     return rank * 128 + 128 * rope + 2 * kKeys * kRows + kKeys * rope;
 }
 __host__ __device__ constexpr int smem_tail() { return 2 * kKeys * 4 + 2048; }
-
-struct Item {
-    int seq, start, t, kv;  // sequence, its first token row, new tokens, cached rows
-    int tok, block;         // first token of the group, head block
-    int vis, tiles;         // keys that its last token sees, tiles
-};
 
 __device__ __forceinline__ void item_sizes(const PagedArgs &a, Item &it) {
     const int last = min(it.tok + a.group, it.t) - 1;
@@ -152,6 +155,14 @@ __device__ __forceinline__ void next_item(const PagedArgs &a, Item &it) {
     item_sizes(a, it);
 }
 
+// The item's rows of q and out: consecutive (token, head) rows.
+__device__ __forceinline__ int64_t item_row0(const PagedArgs &a, const Item &it) {
+    return (static_cast<int64_t>(it.start) + it.tok) * a.nh + it.block * a.heads_per;
+}
+__device__ __forceinline__ int item_rows(const PagedArgs &a, const Item &it) {
+    return a.head_blocks > 1 ? min(a.heads_per, a.nh - it.block * a.heads_per) : min(a.group, it.t - it.tok) * a.nh;
+}
+
 // Waits for a barrier phase; after one wait expired, none is made any more (the kernel then runs to
 // its end on whatever is there, and the fault word says so).
 struct Waiter {
@@ -164,30 +175,63 @@ struct Waiter {
     }
 };
 
-// Four consecutive query elements.
-__device__ __forceinline__ float4 load_q4(const void *p, int64_t i, bool bf16) {
-    if (bf16) {
-        const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i));
-        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+// The same for a single thread.
+struct ThreadWaiter {
+    bool dead = false;
+    __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
+        if (dead || mbar_try_wait(bar, parity)) return;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, parity)) {
+            if (clock64() - t0 > kWaitCycles) {
+                dead = true;
+                atomicOr(&g_paged_fault, kFaultWait);
+                return;
+            }
+        }
     }
-    return __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
+};
+
+// Four consecutive query elements, as they lie in memory and as f32.
+template <bool BF16>
+struct Q4 {
+    uint4 raw;
+    __device__ __forceinline__ void load(const void *p, int64_t i) { raw = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i)); }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w));
+    }
+    __device__ __forceinline__ void clear() { raw = make_uint4(0, 0, 0, 0); }
+};
+template <>
+struct Q4<true> {
+    uint2 raw;
+    __device__ __forceinline__ void load(const void *p, int64_t i) { raw = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i)); }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
+                           __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u));
+    }
+    __device__ __forceinline__ void clear() { raw = make_uint2(0, 0); }
+};
+
+// E4M3 codes of 256 times four f16 numbers in (-1, 1], which have at most three fraction bits.
+__device__ __forceinline__ uint32_t e4m3_bits(uint32_t a, uint32_t b) {
+    return __byte_perm((a << 1 & 0x7f007f00u) | (a & 0x80008000u), (b << 1 & 0x7f007f00u) | (b & 0x80008000u), 0x7531);
 }
 
-__device__ __forceinline__ bool finite4(float4 v) {
-    return isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w);
-}
-
-// hi and lo terms of four scaled query elements.
+// hi and lo terms of four query elements; `inv` takes them into (-1, 1).
 __device__ __forceinline__ void split_q4(float4 v, float inv, uint32_t &hi, uint32_t &lo) {
-    const float x[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    const uint32_t h0 = f32x2_to_e4m3x2(x[0], x[1]), h1 = f32x2_to_e4m3x2(x[2], x[3]);
-    const uint32_t b0 = e4m3x2_to_f16x2(h0), b1 = e4m3x2_to_f16x2(h1);
-    const float2 r0 = __half22float2(*reinterpret_cast<const __half2 *>(&b0));
-    const float2 r1 = __half22float2(*reinterpret_cast<const __half2 *>(&b1));
-    hi = h0 | (h1 << 16);
-    lo = f32x2_to_e4m3x2(x[0] - r0.x, x[1] - r0.y) | (f32x2_to_e4m3x2(x[2] - r1.x, x[3] - r1.y) << 16);
+    const uint32_t x0 = f32x2_to_f16x2(v.x * inv, v.y * inv), x1 = f32x2_to_f16x2(v.z * inv, v.w * inv);
+    const uint32_t h0 = (x0 + 0x00400040u) & 0xff80ff80u, h1 = (x1 + 0x00400040u) & 0xff80ff80u;
+    const uint32_t l0 = sub_f16x2(x0, h0) + 0x00400040u, l1 = sub_f16x2(x1, h1) + 0x00400040u;
+    hi = e4m3_bits(h0, h1);
+    lo = e4m3_bits(l0, l1);
 }
+
+__device__ __forceinline__ void prefetch_l2(const uint8_t *p, int64_t bytes, int lane) {
+    for (int64_t i = lane * 128; i < bytes; i += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Byte offset of element `i` of row `r` in an operand of `row_bytes`-byte swizzled rows.
 __device__ __forceinline__ int swizzled(int r, int i, int row_bytes) {
@@ -195,52 +239,51 @@ __device__ __forceinline__ int swizzled(int r, int i, int row_bytes) {
     return r * row_bytes + (i ^ (x << 4));
 }
 
-// The 64 query rows of an item -> their 8-bit terms and scales in shared memory (eight warps, eight
-// rows each, four at a time).  Rows past `rows` are zeros.
+// The 64 query rows of an item -> their 8-bit terms and scales in shared memory.  Rows past `rows`
+// are zeros.  Eight warps, eight rows each, R of them in flight at a time (80 registers).  On the
+// first item the producer starts its copies when the first loads are out: behind a ring of cache rows
+// in the memory's queues they took 10 us and more.
+template <bool BF16, int R>
 __device__ __forceinline__ void stage_q(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows,
-                                        int warp, int lane) {
+                                        int warp, int lane, bool first) {
     const int pieces = a.rank / 128;
     uint8_t *lat_lo = smem + a.rank * kRows;
     uint8_t *rope_hi = smem + 2 * a.rank * kRows, *rope_lo = rope_hi + kRows * a.rope;
+    for (int r0 = warp * 8; r0 < warp * 8 + 8; r0 += R) {
+        Q4<BF16> v[R][5];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        float4 v[4][5];
-        float amax[4];
-        bool ok[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = warp * 8 + half * 4 + k;
-            amax[k] = 0.f;
-            ok[k] = true;
+        for (int k = 0; k < R; ++k) {
 #pragma unroll
             for (int c = 0; c < 5; ++c) {
-                v[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < rows) {
-                    if (c < pieces) v[k][c] = load_q4(a.q_lat, (row0 + r) * a.rank + c * 128 + lane * 4, a.q_bf16);
-                    if (c == 4 && lane * 4 < a.rope) v[k][c] = load_q4(a.q_pe, (row0 + r) * a.rope + lane * 4, a.q_bf16);
+                v[k][c].clear();
+                if (r0 + k < rows) {
+                    if (c < pieces) v[k][c].load(a.q_lat, (row0 + r0 + k) * a.rank + c * 128 + lane * 4);
+                    if (c == 4 && lane * 4 < a.rope) v[k][c].load(a.q_pe, (row0 + r0 + k) * a.rope + lane * 4);
                 }
             }
         }
+        if (first) named_bar_arrive(4, kSoftmaxWarps * 32 + 32);
+        first = false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = warp * 8 + half * 4 + k;
+        for (int k = 0; k < R; ++k) {
+            const int r = r0 + k;
+            uint32_t top = 0;  // of |x| as bits: infinities and NaN lie above all numbers
 #pragma unroll
             for (int c = 0; c < 5; ++c) {
-                const float4 x = v[k][c];
-                amax[k] = fmaxf(amax[k], fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-                ok[k] = ok[k] && finite4(x);
+                const float4 x = v[k][c].get();
+                top = max(max(top, abs_bits(x.x)), max(abs_bits(x.y), max(abs_bits(x.z), abs_bits(x.w))));
             }
-            const float m = warp_max(amax[k]);
-            const bool fin = __all_sync(kFullMask, ok[k]);
-            // 2^e with m / 2^e in [128, 256); tiny rows keep a normal reciprocal
-            const int e = max(static_cast<int>(__float_as_uint(m) >> 23), 32);
-            const float inv = fin ? __uint_as_float(static_cast<uint32_t>(261 - e) << 23) : 0.f;
+            top = __reduce_max_sync(kFullMask, top);
+            // 2^e with max / 2^e in [1/2, 1); tiny rows keep a normal reciprocal, rows past 2^126 have none
+            const bool fin = top < 0x7e800000u;
+            const int e = min(max(static_cast<int>(top >> 23), 32), 252);
+            const float inv = __uint_as_float(static_cast<uint32_t>(253 - e) << 23);
             if (lane == 0) ctl->row_scale[r] = fin ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
 #pragma unroll
             for (int c = 0; c < 5; ++c) {
                 uint32_t hi, lo;
-                const float4 x = fin ? v[k][c] : make_float4(0.f, 0.f, 0.f, 0.f);
-                split_q4(x, inv, hi, lo);
+                split_q4(v[k][c].get(), inv, hi, lo);
+                if (!fin) hi = lo = 0;
                 if (c < pieces) {
                     const int at = c * kRows * 128 + swizzled(r, lane * 4, 128);
                     *reinterpret_cast<uint32_t *>(smem + at) = hi;
@@ -270,11 +313,26 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
     return v[0];
 }
 
+// Maximum over the 32 lanes of v[c], for every c, in lane c.
+__device__ __forceinline__ float column_maxima(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const bool up = (lane & o) != 0;
+            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+            v[i] = fmaxf(keep, __shfl_xor_sync(kFullMask, send, o));
+        }
+    }
+    return v[0];
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap map_lat, const __grid_constant__ CUtensorMap map_rope,
                       const PagedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFullMask, tid >> 5, 0);
     const int pieces = a.rank / 128;
     uint8_t *weights = smem + a.rank * 128 + 128 * a.rope;
     uint8_t *rope_k = weights + 2 * kKeys * kRows;
@@ -344,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             item_sizes(a, it);
             const long long n = static_cast<long long>(it.tiles) * a.head_blocks;
             if (pass == 1 && sum <= run_lo && run_lo < sum + n) {
-                ctl->first_seq = it.seq;
-                ctl->first_tok = it.tok;
-                ctl->first_block = static_cast<int>((run_lo - sum) / it.tiles);
-                ctl->first_off = static_cast<int>((run_lo - sum) % it.tiles);
+                const int at = static_cast<int>(run_lo - sum);
+                it.block = at / it.tiles;
+                ctl->first = it;
+                ctl->first_off = at - it.block * it.tiles;
             }
             sum += n;
         }
@@ -375,15 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = ctl->tmem;
+    const uint32_t tmem = __shfl_sync(kFullMask, ctl->tmem, 0);
 
     if (run_lo < run_hi) {
-        Item it{};
-        it.seq = ctl->first_seq;
-        it.tok = ctl->first_tok;
-        it.block = ctl->first_block;
-        seq_sizes(a, __ldcg(a.cu_q + it.seq), __ldcg(a.cu_q + it.seq + 1), __ldcg(a.kv_len + it.seq), it);
-        item_sizes(a, it);
+        Item it = ctl->first;
         int off = ctl->first_off;
         Waiter wait;
 
@@ -391,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------------------------------------------------------- TMA producer
             uint32_t tile = 0, slot = 0, lap = 0;
             const int per_tile = kKeys / a.box;
+            named_bar_sync(4, kSoftmaxWarps * 32 + 32);  // the first query rows' loads are out
             for (long long pos = run_lo; pos < run_hi;) {
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                 const int32_t *table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
@@ -445,7 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 pos += n;
                 off = 0;
-                if (pos < run_hi) next_item(a, it);
+                if (pos < run_hi) {
+                    next_item(a, it);
+                    // The softmax warps are about two tiles behind: the next query rows come into L2.
+                    const int64_t row0 = item_row0(a, it);
+                    const int64_t size = a.q_bf16 ? 2 : 4, rows = item_rows(a, it);
+                    prefetch_l2(static_cast<const uint8_t *>(a.q_lat) + row0 * a.rank * size, rows * a.rank * size, lane);
+                    if (a.rope) prefetch_l2(static_cast<const uint8_t *>(a.q_pe) + row0 * a.rope * size, rows * a.rope * size, lane);
+                }
             }
             if (wait.dead) {
                 // Copies in flight: every slot's last phase that was announced, each wait bounded.
@@ -458,106 +519,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 9) {
             // ---------------------------------------------------------------- tensor-core products
-            constexpr uint32_t idesc_s = f8_idesc(kKeys, kRows, kE4M3, kE4M3, false, false);
-            constexpr uint32_t idesc_hi = f8_idesc(128, kRows, kE4M3, kE4M3, true, true);
-            constexpr uint32_t idesc_lo = f8_idesc(128, kRows, kE4M3, kE5M2, true, true);
-            const uint32_t q_hi = smem_u32(smem), q_lo = q_hi + a.rank * kRows;
-            const uint32_t qr_hi = q_hi + 2 * a.rank * kRows, qr_lo = qr_hi + kRows * a.rope;
-            const uint32_t p_hi = smem_u32(weights), p_lo = p_hi + kKeys * kRows;
-            const uint32_t ring_u = smem_u32(ring), rope_u = smem_u32(rope_k);
-            // Pieces of the next tile's scores that may be awaited before this tile's pieces are free.
-            const int lead = min(pieces, a.slots - pieces);
-            uint32_t tile_s = 0;              // tiles whose scores were issued
-            uint32_t slot_s = 0, lap_s = 0;   // ring position of the scores
-            uint32_t slot_o = 0;              // ring position of the outputs
-            uint32_t item_count = 0;
+            // One thread issues everything.  The tensor cores hold about four products (200 cycles) of
+            // work in hand, so a barrier is tested while the products before it are being issued and
+            // its latency stays hidden.
+            if (elect_one()) {
+                constexpr uint32_t idesc_s = f8_idesc(kKeys, kRows, kE4M3, kE4M3, false, false);
+                constexpr uint32_t idesc_hi = f8_idesc(128, kRows, kE4M3, kE4M3, true, true);
+                constexpr uint32_t idesc_lo = f8_idesc(128, kRows, kE4M3, kE5M2, true, true);
+                const uint32_t q_u = smem_u32(smem), qr_u = q_u + 2 * a.rank * kRows, p_u = smem_u32(weights);
+                // descriptors; a step along an operand adds its bytes / 16
+                const uint64_t d_ring = smem_desc(smem_u32(ring), 128), d_rope = smem_desc(smem_u32(rope_k), a.rope);
+                const uint64_t d_q[2] = {smem_desc(q_u, 128), smem_desc(q_u + a.rank * kRows, 128)};
+                const uint64_t d_qr[2] = {smem_desc(qr_u, a.rope), smem_desc(qr_u + kRows * a.rope, a.rope)};
+                const uint64_t d_p[2] = {smem_desc(p_u, 64), smem_desc(p_u + kKeys * kRows, 64)};
+                // Pieces of the next tile's scores that may be awaited before this tile's pieces are free.
+                const int lead = min(pieces, a.slots - pieces);
+                ThreadWaiter wait;
+                uint32_t tile_s = 0;             // tiles whose scores were issued
+                uint32_t slot_s = 0, lap_s = 0;  // ring position of the scores
+                uint32_t slot_o = 0;             // ring position of the outputs
+                uint32_t item_count = 0;
+                bool ready = false;  // the ring slot that the scores read next was seen full
 
-            // Scores of one tile: pieces [c0, c1), the rope part before piece 0.
-            const auto scores = [&](int c0, int c1) {
-                const uint32_t d = tmem + kScoreCol + (tile_s & 1) * kRows;
-                if (c0 == 0 && a.rope) {
-                    wait(&ctl->rope_full, tile_s & 1);
-                    tc_fence_after();
-                    if (lane == 0) {
+                // Scores of one tile: pieces [c0, c1), the rope part before piece 0.
+                const auto scores = [&](int c0, int c1) {
+                    const uint32_t d = tmem + kScoreCol + (tile_s & 1) * kRows;
+                    if (c0 == 0 && a.rope) {
+                        wait(&ctl->rope_full, tile_s & 1);
+                        tc_fence_after();
+                        ready = mbar_test(&ctl->full[slot_s], lap_s & 1);
                         for (int k = 0; k < a.rope / 32; ++k) {
-                            const uint64_t ka = smem_desc(rope_u + k * 32, a.rope);
-                            mma_f8(d, ka, smem_desc(qr_hi + k * 32, a.rope), idesc_s, k != 0);
-                            mma_f8(d, ka, smem_desc(qr_lo + k * 32, a.rope), idesc_s, true);
+                            mma_f8(d, d_rope + k * 2, d_qr[0] + k * 2, idesc_s, k != 0);
+                            mma_f8(d, d_rope + k * 2, d_qr[1] + k * 2, idesc_s, true);
                         }
                         tc_commit(&ctl->rope_free);
                     }
-                }
-                for (int c = c0; c < c1; ++c) {
-                    wait(&ctl->full[slot_s], lap_s & 1);
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t ka = smem_desc(ring_u + slot_s * kPiece, 128);
-                        const uint64_t qa = smem_desc(q_hi + c * kRows * 128, 128);
-                        const uint64_t qb = smem_desc(q_lo + c * kRows * 128, 128);
+                    for (int c = c0; c < c1; ++c) {
+                        if (!ready) wait(&ctl->full[slot_s], lap_s & 1);
+                        tc_fence_after();
+                        const uint64_t ka = d_ring + slot_s * (kPiece / 16);
+                        const uint64_t qa = d_q[0] + c * (kRows * 8), qb = d_q[1] + c * (kRows * 8);
+                        if (++slot_s == static_cast<uint32_t>(a.slots)) {
+                            slot_s = 0;
+                            ++lap_s;
+                        }
+                        ready = mbar_test(&ctl->full[slot_s], lap_s & 1);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             mma_f8(d, ka + k * 2, qa + k * 2, idesc_s, a.rope || c != 0 || k != 0);
                             mma_f8(d, ka + k * 2, qb + k * 2, idesc_s, true);
                         }
                     }
-                    if (++slot_s == static_cast<uint32_t>(a.slots)) {
-                        slot_s = 0;
-                        ++lap_s;
-                    }
-                }
-                if (c1 == pieces) {
-                    if (lane == 0) tc_commit(&ctl->score_full[tile_s & 1]);
-                    ++tile_s;
-                }
-                __syncwarp();
-            };
+                    if (c1 == pieces) tc_commit(&ctl->score_full[tile_s++ & 1]);
+                };
 
-            const uint32_t total = static_cast<uint32_t>(run_hi - run_lo);
-            int left = 0;       // tiles of the current segment that follow this one
-            bool first = true;  // the tile starts a segment
-            long long pos = run_lo;
-            wait(&ctl->q_ready, 0);
-            tc_fence_after();
-            scores(0, pieces);
-            for (uint32_t i = 0; i < total; ++i) {
-                if (first) {
-                    left = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
-                    off = 0;
-                    pos += left;
-                    next_item(a, it);
-                }
-                --left;
-                const bool more = i + 1 < total, same = left > 0;
-                if (more && same) scores(0, lead);
-                wait(&ctl->weights_ready, i & 1);
+                const uint32_t total = static_cast<uint32_t>(run_hi - run_lo);
+                int left = 0;       // tiles of the current segment that follow this one
+                bool first = true;  // the tile starts a segment
+                long long pos = run_lo;
+                wait(&ctl->q_ready, 0);
                 tc_fence_after();
-                for (int c = 0; c < pieces; ++c) {
-                    if (lane == 0) {
-                        const uint32_t v = ring_u + slot_o * kPiece;
+                scores(0, pieces);
+                for (uint32_t i = 0; i < total; ++i) {
+                    if (first) {
+                        left = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
+                        off = 0;
+                        pos += left;
+                        next_item(a, it);
+                    }
+                    --left;
+                    const bool more = i + 1 < total, same = left > 0;
+                    if (more && same) scores(0, lead);
+                    wait(&ctl->weights_ready, i & 1);
+                    tc_fence_after();
+                    for (int c = 0; c < pieces; ++c) {
+                        const uint64_t va = d_ring + slot_o * (kPiece / 16);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint64_t va = smem_desc(v + k * 4096, 128);
-                            mma_f8(tmem + c * kRows, va, smem_desc(p_hi + k * 2048, 64), idesc_hi, !first || k != 0);
-                            mma_f8(tmem + c * kRows, va, smem_desc(p_lo + k * 2048, 64), idesc_lo, true);
+                            mma_f8(tmem + c * kRows, va + k * 256, d_p[0] + k * 128, idesc_hi, !first || k != 0);
+                            mma_f8(tmem + c * kRows, va + k * 256, d_p[1] + k * 128, idesc_lo, true);
                         }
                         tc_commit(&ctl->freed[slot_o]);
+                        if (++slot_o == static_cast<uint32_t>(a.slots)) slot_o = 0;
                     }
-                    if (++slot_o == static_cast<uint32_t>(a.slots)) slot_o = 0;
-                }
-                if (lane == 0) tc_commit(&ctl->out_done);
-                __syncwarp();
-                if (more) {
-                    if (same) {
-                        if (lead < pieces) scores(lead, pieces);
-                    } else {
-                        wait(&ctl->q_ready, ++item_count & 1);
-                        tc_fence_after();
-                        scores(0, pieces);
+                    tc_commit(&ctl->out_done);
+                    if (more) {
+                        if (same) {
+                            if (lead < pieces) scores(lead, pieces);
+                        } else {
+                            wait(&ctl->q_ready, ++item_count & 1);
+                            tc_fence_after();
+                            scores(0, pieces);
+                        }
                     }
+                    first = !same;
                 }
-                first = !same;
+                tc_commit(&ctl->drain);
             }
-            if (lane == 0) tc_commit(&ctl->drain);
             __syncwarp();
             (void)warp_wait_bounded(&ctl->drain, 0);
         } else {
@@ -569,11 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tid == 0) a.owner_flag[blockIdx.x] = 0;
             for (long long pos = run_lo; pos < run_hi;) {
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
-                // rows: consecutive (token, head) rows of q and out
-                const int64_t row0 = (static_cast<int64_t>(it.start) + it.tok) * a.nh + it.block * a.heads_per;
-                const int rows = a.head_blocks > 1 ? min(a.heads_per, a.nh - it.block * a.heads_per)
-                                                   : min(a.group, it.t - it.tok) * a.nh;
-                stage_q(a, ctl, smem, row0, rows, warp, lane);
+                const int64_t row0 = item_row0(a, it);
+                const int rows = item_rows(a, it);
+                if (a.q_bf16)
+                    stage_q<true, 8>(a, ctl, smem, row0, rows, warp, lane, pos == run_lo);
+                else
+                    stage_q<false, 4>(a, ctl, smem, row0, rows, warp, lane, pos == run_lo);
                 fence_async_smem();
                 named_bar_sync(3, kSoftmaxWarps * 32);
                 if (lane == 0) mbar_arrive(&ctl->q_ready);
@@ -583,11 +642,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                            (a.head_blocks > 1 ? 0 : min(col / a.nh, a.group - 1))));
                 const int lim_min = max(0, min(it.vis, it.kv - it.t + it.tok + 1));
                 float ref = kUnset;  // of column `col`
-                float refs[32], sums[32];
+                uint64_t shift[16], sums[16];  // per pair of columns: -(reference + slack); sums of weights
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    refs[c] = kUnset;
-                    sums[c] = 0.f;
+                for (int c = 0; c < 16; ++c) {
+                    shift[c] = pack2(-kUnset, -kUnset);
+                    sums[c] = 0;
                 }
                 for (int i = off; i < off + n; ++i, ++tile) {
                     const int k = i * kKeys + key;
@@ -597,50 +656,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&ctl->scale_free[tile & 1]);
                     const bool in = k < it.vis;
                     if (!in || sj == 0.f) sj = 1.f;  // a zero row's codes are zeros
-                    const float f = sj * a.scale_log2;
-                    const float add = __log2f(sj), inv = sj == sj ? __fdiv_rn(1.f, sj) : 1.f;
+                    const float f = sj * a.scale_log2, add = __log2f(sj);
+                    const uint64_t ff = pack2(f, f), aa = pack2(add, add);
+                    // 256 is the weights' common factor; a NaN scale must not reach the columns that do
+                    // not see its row
+                    const float iv = sj == sj ? __fdiv_rn(256.f, sj) : 256.f;
+                    const uint64_t inv = pack2(iv, iv);
+                    const bool masked = (i + 1) * kKeys > lim_min;  // some column does not see some key
+                    const uint32_t at_s = tmem + lane_base + kScoreCol + (tile & 1) * kRows + half * 32;
 
+                    // s = log2 of the weight over 2^8: score + log2 scale - reference - slack
+                    float s[32];
+                    const auto load_scores = [&](bool shifted) {
+                        uint32_t r[32];
+                        tmem_ld32(at_s, r);
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) {
+                            const ulonglong2 g = *reinterpret_cast<const ulonglong2 *>(&ctl->row_scale[half * 32 + 2 * c]);
+                            const uint64_t r0 = pack2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+                            const uint64_t r1 = pack2(__uint_as_float(r[2 * c + 2]), __uint_as_float(r[2 * c + 3]));
+                            const float2 v0 = unpack2(fma2(r0, mul2(ff, g.x), shifted ? add2(aa, shift[c]) : aa));
+                            const float2 v1 = unpack2(fma2(r1, mul2(ff, g.y), shifted ? add2(aa, shift[c + 1]) : aa));
+                            s[2 * c] = v0.x;
+                            s[2 * c + 1] = v0.y;
+                            s[2 * c + 2] = v1.x;
+                            s[2 * c + 3] = v1.y;
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (k >= __shfl_sync(kFullMask, lim_col, c)) s[c] = -INFINITY;
+                        }
+                    };
                     wait(&ctl->score_full[tile & 1], (tile >> 1) & 1);
                     tc_fence_after();
-                    float s[32];
-                    tmem_ld32(tmem + lane_base + kScoreCol + (tile & 1) * kRows + half * 32, s);
+                    load_scores(true);
+                    float m = s[0];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 g = *reinterpret_cast<const float4 *>(&ctl->row_scale[half * 32 + c]);
-                        s[c] = fmaf(s[c] * f, g.x, add);
-                        s[c + 1] = fmaf(s[c + 1] * f, g.y, add);
-                        s[c + 2] = fmaf(s[c + 2] * f, g.z, add);
-                        s[c + 3] = fmaf(s[c + 3] * f, g.w, add);
-                    }
-                    if ((i + 1) * kKeys > lim_min) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (k >= __shfl_sync(kFullMask, lim_col, c)) s[c] = -INFINITY;
-                    }
-                    float mine = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float m = warp_max(s[c]);
-                        if (lane == c) mine = m;
-                    }
-                    // Maxima over the half's four warps.  Past this tile's barrier nobody reads the previous
-                    // tile's entry any more, so it is cleared there for the tile after the next.
-                    atomicMax(&ctl->tops[top][col], order_bits(mine));
-                    named_bar_sync(1 + half, 128);
-                    const float m = unorder_bits(ctl->tops[top][col]);
-                    if (wq == 0) ctl->tops[top == 0 ? 2 : top - 1][col] = 0;
-                    top = top == 2 ? 0 : top + 1;
-                    const bool move = __any_sync(kFullMask, m > ref + kSlack);  // the same in the half's 4 warps
-                    if (move) {
-                        const float to = fmaxf(ref, m);
-                        const float shrink = ex2(ref - to);
+                    for (int c = 1; c < 32; ++c) m = fmaxf(m, s[c]);
+                    if (named_bar_any(1 + half, 128, m > 0.f)) {
+                        // A column exceeds its reference by the slack: all columns' references move up
+                        // to their maxima.  Past this barrier nobody reads the maxima of the time
+                        // before any more, so they are cleared there for the time after the next.
+                        load_scores(false);
+                        atomicMax(&ctl->tops[top][col], order_bits(column_maxima(s, lane)));
+                        named_bar_sync(1 + half, 128);
+                        const float to = fmaxf(ref, unorder_bits(ctl->tops[top][col]));
+                        if (wq == 0) ctl->tops[top == 0 ? 2 : top - 1][col] = 0;
+                        top = top == 2 ? 0 : top + 1;
+                        const float shrink = ex2(ref - to), minus = to == kUnset ? -kUnset : -(to + kSlack);
                         ref = to;
-                        float by[32];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            refs[c] = __shfl_sync(kFullMask, ref, c);
-                            by[c] = __shfl_sync(kFullMask, shrink, c);
-                            sums[c] *= by[c];
+                        for (int c = 0; c < 16; ++c) {
+                            shift[c] = pack2(__shfl_sync(kFullMask, minus, 2 * c), __shfl_sync(kFullMask, minus, 2 * c + 1));
+                            sums[c] = mul2(sums[c], pack2(__shfl_sync(kFullMask, shrink, 2 * c),
+                                                          __shfl_sync(kFullMask, shrink, 2 * c + 1)));
                         }
                         if (i > off) {
                             wait(&ctl->out_done, (tile - 1) & 1);
@@ -650,28 +720,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint32_t at = tmem + lane_base + p * kRows + half * 32;
                                 tmem_ld32(at, o);
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) o[c] *= by[c];
+                                for (int c = 0; c < 32; ++c) o[c] *= __shfl_sync(kFullMask, shrink, c);
                                 tmem_st32(at, o);
                             }
                             tc_wait_st();
                         }
+                        load_scores(true);
                     }
                     uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float p0 = ex2(s[c] - refs[c] + kBase), p1 = ex2(s[c + 1] - refs[c + 1] + kBase);
-                        sums[c] = fmaf(p0, inv, sums[c]);
-                        sums[c + 1] = fmaf(p1, inv, sums[c + 1]);
-                        const uint32_t h = f32x2_to_f16x2(p0, p1);
-                        const uint32_t q = f16x2_to_e4m3x2(h);
-                        const uint32_t r = f16x2_to_e5m2x2(sub_f16x2(h, e4m3x2_to_f16x2(q)));
-                        if (c & 2) {
-                            hi[c / 4] |= q << 16;
-                            lo[c / 4] |= r << 16;
-                        } else {
-                            hi[c / 4] = q;
-                            lo[c / 4] = r;
+                    for (int c = 0; c < 32; c += 4) {
+                        uint32_t h[2], l[2];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const float p0 = ex2(s[c + 2 * q]), p1 = ex2(s[c + 2 * q + 1]);
+                            sums[c / 2 + q] = fma2(pack2(p0, p1), inv, sums[c / 2 + q]);
+                            const uint32_t x = f32x2_to_f16x2(p0, p1);
+                            h[q] = x + 0x00400040u;  // to the nearest multiple of three fraction bits
+                            l[q] = mul_f16x2(sub_f16x2(x, h[q] & 0xff80ff80u), 0x5c005c00u) + 0x00800080u;  // times 256
+                            h[q] <<= 1;
                         }
+                        hi[c / 4] = __byte_perm(h[0], h[1], 0x7531);
+                        lo[c / 4] = __byte_perm(l[0], l[1], 0x7531);
                     }
                     if (tile >= 1) wait(&ctl->out_done, (tile - 1) & 1);
 #pragma unroll
@@ -705,15 +775,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 // The weights' shared memory is free: the four warps' sums meet there, in a fixed order.
                 float *scratch = reinterpret_cast<float *>(weights);
-                scratch[wq * kRows + col] = column_sums(sums, lane);
+                float part[32];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float2 u = unpack2(sums[c]);
+                    part[2 * c] = u.x;
+                    part[2 * c + 1] = u.y;
+                }
+                scratch[wq * kRows + col] = column_sums(part, lane);
                 named_bar_sync(1 + half, 128);
                 const float sum = (scratch[col] + scratch[kRows + col]) +
                                   (scratch[2 * kRows + col] + scratch[3 * kRows + col]);
                 const bool whole = off == 0 && n == it.tiles;
                 const int here = 2 * static_cast<int>(blockIdx.x) + (pos == run_lo ? 0 : 1);
                 const float scale_col = whole ? (sum == 0.f ? 0.f : __fdiv_rn(1.f, sum)) : 1.f;
+                float norm[32];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) refs[c] = __shfl_sync(kFullMask, scale_col, c);
+                for (int c = 0; c < 32; ++c) norm[c] = __shfl_sync(kFullMask, scale_col, c);
                 if (!whole) {
                     if (wq == 0) a.stats[here * kRows + col] = make_float2(ref, sum);
                     if (off == 0 && tid == 0) {  // this CTA holds the item's start: it names its parts
@@ -730,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(tmem + lane_base + p * kRows + half * 32, o);
                     const int dim = p * 128 + key;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] = refs[c] == 0.f ? 0.f : o[c] * refs[c];
+                    for (int c = 0; c < 32; ++c) o[c] *= norm[c];
                     if (!whole || !a.out_bf16) {
                         float *dst = whole ? static_cast<float *>(a.out) + row0 * a.rank
                                            : a.part + static_cast<int64_t>(here) * kRows * a.rank;
@@ -769,16 +847,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Adds the partial accumulators of the items that several CTAs shared.  CTA (x, y) serves rows
-// y, y + gridDim.y, ... of the x-th such item; parts are added in CTA order.
-constexpr int kCombineThreads = 256;
+// Adds the partial accumulators of the items that several CTAs shared.  CTA (x, y) serves units y,
+// y + gridDim.y, ... of the x-th such item; a unit is 128 dims of a row.  Warp w adds parts w, w + 8,
+// ... (a lane four dims), and the eight sums are added in warp order.
+constexpr int kCombineWarps = 8;
+constexpr int kCombineThreads = kCombineWarps * 32;
+static_assert(kMaxGrid <= kCombineThreads, "a thread looks at one CTA's part");
 
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArgs a, int grid) {
     __shared__ int found;
-    __shared__ int counts[kCombineThreads / 32];
+    __shared__ int counts[kCombineWarps];
     __shared__ float weight[kMaxGrid];
-    __shared__ float red[2][kCombineThreads / 32];
-    __shared__ float4 other[128];
+    __shared__ float red[2][kCombineWarps];
+    __shared__ float4 sums[kCombineWarps][32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_launch_dependents();
     griddep_wait();
@@ -796,46 +877,48 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArg
     const Owner *op = a.owner + cta;
     const long long row0 = __ldcg(&op->row0);
     const int rows = __ldcg(&op->rows), slot0 = __ldcg(&op->slot), last = __ldcg(&op->last);
-    const int parts = min(last, grid - 1) - cta + 1;
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int parts = min(last, grid - 1) - cta + 1, pieces = a.rank / 128;
+    for (int unit = blockIdx.y; unit < rows * pieces; unit += gridDim.y) {
+        const int r = unit / pieces, d0 = (unit - r * pieces) * 128 + lane * 4;
         float2 st = make_float2(kUnset, 0.f);
         if (tid < parts) st = __ldcg(a.stats + (tid == 0 ? slot0 : 2 * (cta + tid)) * kRows + r);
         const float wm = warp_max(st.x);
         if (lane == 0) red[0][warp] = wm;
         __syncthreads();
         float top = red[0][0];
-        for (int w = 1; w < kCombineThreads / 32; ++w) top = fmaxf(top, red[0][w]);
+        for (int w = 1; w < kCombineWarps; ++w) top = fmaxf(top, red[0][w]);
         const float w = ex2(st.x - top);
         const float l = warp_sum(w * st.y);
         if (lane == 0) red[1][warp] = l;
+        if (tid < parts) weight[tid] = w;
         __syncthreads();
         float total = 0.f;
-        for (int k = 0; k < kCombineThreads / 32; ++k) total += red[1][k];
-        if (tid < parts) weight[tid] = total == 0.f ? 0.f : __fdiv_rn(w, total);
-        __syncthreads();
-        // threads 0..127 take the even parts, 128..255 the odd ones; a thread holds four dims
-        const int side = tid >> 7, d4 = tid & 127;
+        for (int k = 0; k < kCombineWarps; ++k) total += red[1][k];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (d4 * 4 < a.rank) {
-#pragma unroll 4
-            for (int k = side; k < parts; k += 2) {
-                const int64_t s = k == 0 ? slot0 : 2 * (cta + k);
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part + (s * kRows + r) * a.rank) + d4);
-                const float x = weight[k];
-                if (x != 0.f) {  // an empty part's accumulator is not read into the sum
-                    acc.x = fmaf(v.x, x, acc.x);
-                    acc.y = fmaf(v.y, x, acc.y);
-                    acc.z = fmaf(v.z, x, acc.z);
-                    acc.w = fmaf(v.w, x, acc.w);
-                }
-            }
+#pragma unroll 8
+        for (int k = warp; k < parts; k += kCombineWarps) {
+            const int64_t s = k == 0 ? slot0 : 2 * (cta + k);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part + (s * kRows + r) * a.rank + d0));
+            const float x = weight[k];
+            acc.x = fmaf(v.x, x, acc.x);
+            acc.y = fmaf(v.y, x, acc.y);
+            acc.z = fmaf(v.z, x, acc.z);
+            acc.w = fmaf(v.w, x, acc.w);
         }
-        if (side == 1) other[d4] = acc;
+        sums[warp][lane] = acc;
         __syncthreads();
-        if (side == 0 && d4 * 4 < a.rank) {
-            const float4 b = other[d4];
-            const int64_t at = (row0 + r) * a.rank + d4 * 4;
-            const float4 o = make_float4(acc.x + b.x, acc.y + b.y, acc.z + b.z, acc.w + b.w);
+        if (warp == 0) {
+            float4 o = acc;
+            for (int k = 1; k < kCombineWarps; ++k) {
+                const float4 v = sums[k][lane];
+                o.x += v.x;
+                o.y += v.y;
+                o.z += v.z;
+                o.w += v.w;
+            }
+            const float n = total == 0.f ? 0.f : __fdiv_rn(1.f, total);
+            o = make_float4(o.x * n, o.y * n, o.z * n, o.w * n);
+            const int64_t at = (row0 + r) * a.rank + d0;
             if (a.out_bf16) {
                 __nv_bfloat162 v[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
                 *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = *reinterpret_cast<uint2 *>(v);
@@ -843,6 +926,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArg
                 *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = o;
             }
         }
+        // red is rewritten only past this iteration's last barrier by threads that have read it; the
+        // next iteration's first barrier orders sums and weight
         __syncthreads();
     }
 }
@@ -1009,7 +1094,8 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     if (cudaLaunchKernelEx(&cfg, attn_paged_kernel, lat, rope, a) != cudaSuccess) return MEMQ_ERR_LAUNCH;
     const int64_t items = n_tok * a.head_blocks;  // at least the number of items
     const unsigned x = static_cast<unsigned>(std::min<int64_t>(items, grid));
-    cfg.gridDim = dim3(x, std::max(1u, std::min(64u, 608u / x)));
+    // About eight CTAs an SM over all items, and no more than an item's rows have units of 128 dims.
+    cfg.gridDim = dim3(x, std::max(1u, std::min(static_cast<unsigned>(kRows * kv_rank / 128), 8u * grid / x)));
     cfg.blockDim = dim3(kCombineThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, combine_kernel, a, grid) == cudaSuccess ? MEMQ_OK : MEMQ_ERR_LAUNCH;
