@@ -36,8 +36,14 @@
 // order: results do not depend on timing.
 //
 // Warps 0-7 are the softmax warps (thread = key x half of the columns), warp 8 issues the TMA copies
-// of 128 x 128-byte pieces into a ring, warp 9 the tensor-core products.  S^T is double buffered:
-// the scores of tile i + 1 are computed while the softmax of tile i runs.
+// of 128 x 128-byte pieces into a ring, one thread of warp 9 the products.  S^T is double buffered: the
+// scores of tile i + 1 are computed while the softmax of tile i runs.
+//
+// Shared memory's bandwidth bounds a tile: an m128 product of 32-byte rows reads 4 KB of codes and 32
+// bytes per column at 128 bytes a cycle (48 cycles at n = 64, where the arithmetic takes 32; 64 at n =
+// 128, where both do).  So both query terms are one product of 128 columns, S_hi and S_lo, which the
+// softmax warps add; the accumulators of the outputs leave no room in TMEM for the same there.  At
+// rank 512, rope 64: 18 x 64 + 32 x 48 cycles, and 576 for the copies that fill the ring.
 //
 // Codes of a cached row are finite by the cache's contract (a row that was not finite carries a
 // NaN scale); rows past the end of a sequence may hold anything and are zeroed in shared memory
@@ -66,7 +72,8 @@ constexpr int kKeys = 128;      // keys per tile
 constexpr int kPiece = 16384;   // bytes of one 128 x 128 ring slot
 constexpr int kMaxSlots = 12;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 10 * 32;
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxGrid = 256;
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
@@ -117,7 +124,7 @@ struct Control {
 };
 static_assert(sizeof(Control) <= 2048, "the control block has 2 KB of shared memory");
 
-// Shared memory, from a 1024-byte boundary: Q terms (latent hi, lo; rope hi, lo), P terms, the rope
+// Shared memory, from a 1024-byte boundary: Q terms (per 128 latent dims hi, lo; rope hi, lo), P terms, the rope
 // piece, the ring, the scales of two tiles, the control block.
 __host__ __device__ constexpr int smem_ring_off(int rank, int rope) {
     return rank * 128 + 128 * rope + 2 * kKeys * kRows + kKeys * rope;
@@ -191,47 +198,10 @@ struct ThreadWaiter {
     }
 };
 
-// Four consecutive query elements, as they lie in memory and as f32.
-template <bool BF16>
-struct Q4 {
-    uint4 raw;
-    __device__ __forceinline__ void load(const void *p, int64_t i) { raw = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i)); }
-    __device__ __forceinline__ float4 get() const {
-        return make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w));
-    }
-    __device__ __forceinline__ void clear() { raw = make_uint4(0, 0, 0, 0); }
-};
-template <>
-struct Q4<true> {
-    uint2 raw;
-    __device__ __forceinline__ void load(const void *p, int64_t i) { raw = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i)); }
-    __device__ __forceinline__ float4 get() const {
-        return make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                           __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u));
-    }
-    __device__ __forceinline__ void clear() { raw = make_uint2(0, 0); }
-};
-
-// E4M3 codes of 256 times four f16 numbers in (-1, 1], which have at most three fraction bits.
-__device__ __forceinline__ uint32_t e4m3_bits(uint32_t a, uint32_t b) {
-    return __byte_perm((a << 1 & 0x7f007f00u) | (a & 0x80008000u), (b << 1 & 0x7f007f00u) | (b & 0x80008000u), 0x7531);
-}
-
-// hi and lo terms of four query elements; `inv` takes them into (-1, 1).
-__device__ __forceinline__ void split_q4(float4 v, float inv, uint32_t &hi, uint32_t &lo) {
-    const uint32_t x0 = f32x2_to_f16x2(v.x * inv, v.y * inv), x1 = f32x2_to_f16x2(v.z * inv, v.w * inv);
-    const uint32_t h0 = (x0 + 0x00400040u) & 0xff80ff80u, h1 = (x1 + 0x00400040u) & 0xff80ff80u;
-    const uint32_t l0 = sub_f16x2(x0, h0) + 0x00400040u, l1 = sub_f16x2(x1, h1) + 0x00400040u;
-    hi = e4m3_bits(h0, h1);
-    lo = e4m3_bits(l0, l1);
-}
-
 __device__ __forceinline__ void prefetch_l2(const uint8_t *p, int64_t bytes, int lane) {
     for (int64_t i = lane * 128; i < bytes; i += 32 * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
 }
-
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Byte offset of element `i` of row `r` in an operand of `row_bytes`-byte swizzled rows.
 __device__ __forceinline__ int swizzled(int r, int i, int row_bytes) {
@@ -239,64 +209,138 @@ __device__ __forceinline__ int swizzled(int r, int i, int row_bytes) {
     return r * row_bytes + (i ^ (x << 4));
 }
 
-// The 64 query rows of an item -> their 8-bit terms and scales in shared memory.  Rows past `rows`
-// are zeros.  Eight warps, eight rows each, R of them in flight at a time (80 registers).  On the
-// first item the producer starts its copies when the first loads are out: behind a ring of cache rows
-// in the memory's queues they took 10 us and more.
-template <bool BF16, int R>
-__device__ __forceinline__ void stage_q(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows,
-                                        int warp, int lane, bool first) {
-    const int pieces = a.rank / 128;
-    uint8_t *lat_lo = smem + a.rank * kRows;
-    uint8_t *rope_hi = smem + 2 * a.rank * kRows, *rope_lo = rope_hi + kRows * a.rope;
-    for (int r0 = warp * 8; r0 < warp * 8 + 8; r0 += R) {
-        Q4<BF16> v[R][5];
+// E4M3 codes of 256 times the four f16 numbers in (-2, 2) of a and b, which have at most three
+// fraction bits: bits 13..7 behind the sign.
+__device__ __forceinline__ uint32_t e4m3_bits(uint32_t a, uint32_t b) {
+    return __byte_perm(a << 1, b << 1, 0x7531) | (__byte_perm(a, b, 0xfdb9) & 0x80808080u);
+}
+
+// Byte offset of the eight elements from `e` on of row r in the hi terms; the lo terms are rows 64 to
+// 127 of the same operand, `lo` bytes behind.
+__device__ __forceinline__ int q_unit(const PagedArgs &a, int r, int e, int &lo) {
+    if (e < a.rank) {
+        lo = kRows * 128;
+        return (e >> 7) * (2 * kRows * 128) + swizzled(r, e & 127, 128);
+    }
+    lo = kRows * a.rope;
+    return 2 * a.rank * kRows + swizzled(r, e - a.rank, a.rope);
+}
+
+// The eight elements from `e` on of a query row in memory.
+template <bool BF16>
+__device__ __forceinline__ const uint4 *q_source(const PagedArgs &a, int64_t row, int e) {
+    const bool lat = e < a.rank;
+    const int64_t at = lat ? row * a.rank + e : row * a.rope + (e - a.rank);
+    return reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(lat ? a.q_lat : a.q_pe) + at * (BF16 ? 2 : 4));
+}
+
+// The 64 query rows of an item -> their 8-bit terms and scales in shared memory; rows past `rows` are
+// zeros.  Four threads serve a row, in units of eight elements, in two passes, for the row's maximum
+// comes first.  A unit of bf16 queries fills the 8 + 8 bytes of its terms, so the first pass parks it
+// there and the second splits it in place; f32 queries are read a second time, from L2.  Many loads
+// are out at a time and the code stays short: unrolled over registers it was half the kernel, and
+// fetching it took longer than running it.  On the first item the producer starts its copies when
+// the first loads are out; behind a ring of cache rows in the memory's queues they took 10 us and more.
+template <bool BF16, int U>
+__device__ __forceinline__ uint32_t q_maximum(const PagedArgs &a, uint8_t *smem, int64_t row, bool live, int r, int q,
+                                              bool first) {
+    const int units = (a.rank + a.rope) / 32;  // of this thread
+    uint32_t top = 0;
+    for (int j0 = 0; j0 < units; j0 += U) {
+        uint4 v[U][BF16 ? 1 : 2];
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
+        for (int j = 0; j < U; ++j) {
 #pragma unroll
-            for (int c = 0; c < 5; ++c) {
-                v[k][c].clear();
-                if (r0 + k < rows) {
-                    if (c < pieces) v[k][c].load(a.q_lat, (row0 + r0 + k) * a.rank + c * 128 + lane * 4);
-                    if (c == 4 && lane * 4 < a.rope) v[k][c].load(a.q_pe, (row0 + r0 + k) * a.rope + lane * 4);
-                }
+            for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+                v[j][h] = make_uint4(0, 0, 0, 0);
+                if (live && j0 + j < units) v[j][h] = __ldcg(q_source<BF16>(a, row, (q + 4 * (j0 + j)) * 8) + h);
             }
         }
         if (first) named_bar_arrive(4, kSoftmaxWarps * 32 + 32);
         first = false;
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int r = r0 + k;
-            uint32_t top = 0;  // of |x| as bits: infinities and NaN lie above all numbers
+        for (int j = 0; j < U; ++j) {
 #pragma unroll
-            for (int c = 0; c < 5; ++c) {
-                const float4 x = v[k][c].get();
-                top = max(max(top, abs_bits(x.x)), max(abs_bits(x.y), max(abs_bits(x.z), abs_bits(x.w))));
+            for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+                const uint4 w = v[j][h];
+                if (BF16)
+                    top = __vmaxu2(__vmaxu2(top, w.x & 0x7fff7fffu), __vmaxu2(w.y & 0x7fff7fffu,
+                          __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+                else
+                    top = max(max(top, w.x & 0x7fffffffu), max(w.y & 0x7fffffffu,
+                          max(w.z & 0x7fffffffu, w.w & 0x7fffffffu)));
             }
-            top = __reduce_max_sync(kFullMask, top);
-            // 2^e with max / 2^e in [1/2, 1); tiny rows keep a normal reciprocal, rows past 2^126 have none
-            const bool fin = top < 0x7e800000u;
-            const int e = min(max(static_cast<int>(top >> 23), 32), 252);
-            const float inv = __uint_as_float(static_cast<uint32_t>(253 - e) << 23);
-            if (lane == 0) ctl->row_scale[r] = fin ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
-#pragma unroll
-            for (int c = 0; c < 5; ++c) {
-                uint32_t hi, lo;
-                split_q4(v[k][c].get(), inv, hi, lo);
-                if (!fin) hi = lo = 0;
-                if (c < pieces) {
-                    const int at = c * kRows * 128 + swizzled(r, lane * 4, 128);
-                    *reinterpret_cast<uint32_t *>(smem + at) = hi;
-                    *reinterpret_cast<uint32_t *>(lat_lo + at) = lo;
-                }
-                if (c == 4 && lane * 4 < a.rope) {
-                    const int at = swizzled(r, lane * 4, a.rope);
-                    *reinterpret_cast<uint32_t *>(rope_hi + at) = hi;
-                    *reinterpret_cast<uint32_t *>(rope_lo + at) = lo;
-                }
+            if (BF16 && j0 + j < units) {
+                int lo;
+                uint8_t *hi = smem + q_unit(a, r, (q + 4 * (j0 + j)) * 8, lo);
+                *reinterpret_cast<uint2 *>(hi) = make_uint2(v[j][0].x, v[j][0].y);
+                *reinterpret_cast<uint2 *>(hi + lo) = make_uint2(v[j][0].z, v[j][0].w);
             }
         }
     }
+    // as the upper half of an f32's bits: infinities and NaN lie above all numbers
+    return BF16 ? max(top & 0xffffu, top >> 16) : top >> 16;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void q_split(const PagedArgs &a, uint8_t *smem, int64_t row, bool live, int r, int q, bool fin,
+                                        float inv) {
+    const uint64_t by = pack2(inv, inv);
+#pragma unroll 2
+    for (int e = q * 8; e < a.rank + a.rope; e += 32) {
+        int lo_off;
+        uint8_t *at = smem + q_unit(a, r, e, lo_off);
+        uint2 *hi = reinterpret_cast<uint2 *>(at), *lo = reinterpret_cast<uint2 *>(at + lo_off);
+        uint32_t f[4], h[4], l[4];
+        if (BF16) {
+            const uint2 w0 = *hi, w1 = *lo;
+            const uint32_t w[4] = {w0.x, w0.y, w1.x, w1.y};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 x = unpack2(mul2(pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)), by));
+                f[k] = f32x2_to_f16x2(x.x, x.y);
+            }
+        } else {
+            uint4 w[2] = {};
+            if (live) {
+                w[0] = __ldcg(q_source<false>(a, row, e));
+                w[1] = __ldcg(q_source<false>(a, row, e) + 1);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 x = unpack2(mul2(pack2(__uint_as_float(w[k].x), __uint_as_float(w[k].y)), by));
+                const float2 y = unpack2(mul2(pack2(__uint_as_float(w[k].z), __uint_as_float(w[k].w)), by));
+                f[2 * k] = f32x2_to_f16x2(x.x, x.y);
+                f[2 * k + 1] = f32x2_to_f16x2(y.x, y.y);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (!fin) f[k] = 0;
+            h[k] = (f[k] + 0x00400040u) & 0xff80ff80u;  // to the nearest multiple of three fraction bits
+            l[k] = sub_f16x2(f[k], h[k]) + 0x00400040u;
+        }
+        *hi = make_uint2(e4m3_bits(h[0], h[1]), e4m3_bits(h[2], h[3]));
+        *lo = make_uint2(e4m3_bits(l[0], l[1]), e4m3_bits(l[2], l[3]));
+    }
+}
+
+__device__ __forceinline__ void stage_q(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows,
+                                        int tid, bool first) {
+    const int r = tid >> 2, q = tid & 3;
+    uint32_t top = a.q_bf16 ? q_maximum<true, 9>(a, smem, row0 + r, r < rows, r, q, first)
+                            : q_maximum<false, 6>(a, smem, row0 + r, r < rows, r, q, first);
+    top = max(top, __shfl_xor_sync(kFullMask, top, 1));
+    top = max(top, __shfl_xor_sync(kFullMask, top, 2));
+    // 2^e with max / 2^e in [1/2, 1); tiny rows keep a normal reciprocal, rows past 2^126 have none
+    const bool fin = top < 0x7e80u;
+    const int e2 = min(max(static_cast<int>(top >> 7), 32), 252);
+    const float inv = __uint_as_float(static_cast<uint32_t>(253 - e2) << 23);
+    if (q == 0) ctl->row_scale[r] = fin ? __uint_as_float(static_cast<uint32_t>(e2 - 7) << 23) : NAN;
+    if (a.q_bf16)
+        q_split<true>(a, smem, row0 + r, r < rows, r, q, fin, inv);
+    else
+        q_split<false>(a, smem, row0 + r, r < rows, r, q, fin, inv);
 }
 
 // Sum over the 32 lanes of v[c], for every c, in lane c (a fixed tree).
@@ -332,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const PagedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31;
-    const int warp = __shfl_sync(kFullMask, tid >> 5, 0);
+    const int warp = __shfl_sync(kFullMask, tid >> 5, 0);  // uniform
     const int pieces = a.rank / 128;
     uint8_t *weights = smem + a.rank * 128 + 128 * a.rope;
     uint8_t *rope_k = weights + 2 * kKeys * kRows;
@@ -362,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init_fence();
     }
     if (tid < 3 * kRows) ctl->tops[tid / kRows][tid % kRows] = 0;
-    if (warp == 9) tmem_alloc(&ctl->tmem, 512);
+    if (warp == kMmaWarp) tmem_alloc(&ctl->tmem, 512);
     griddep_wait();
 
     // ------------------------------------------------------------------ this CTA's run of tiles
@@ -387,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     long long run_lo = -1, run_hi = 0, per = 0;
     long long before = 0;
+#pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         long long sum = before;  // pass 0: this slice's tiles; pass 1: find the run's first tile
         Item it{};
@@ -440,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int off = ctl->first_off;
         Waiter wait;
 
-        if (warp == 8) {
+        if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- TMA producer
             uint32_t tile = 0, slot = 0, lap = 0;
             const int per_tile = kKeys / a.box;
@@ -517,20 +562,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (tile >= 1 && a.rope) (void)warp_wait_bounded(&ctl->rope_full, (tile - 1) & 1);
                 if (tile >= 1) (void)warp_wait_bounded(&ctl->scale_full[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             }
-        } else if (warp == 9) {
+        } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- tensor-core products
             // One thread issues everything.  The tensor cores hold about four products (200 cycles) of
             // work in hand, so a barrier is tested while the products before it are being issued and
             // its latency stays hidden.
             if (elect_one()) {
-                constexpr uint32_t idesc_s = f8_idesc(kKeys, kRows, kE4M3, kE4M3, false, false);
+                constexpr uint32_t idesc_s = f8_idesc(kKeys, 2 * kRows, kE4M3, kE4M3, false, false);
                 constexpr uint32_t idesc_hi = f8_idesc(128, kRows, kE4M3, kE4M3, true, true);
                 constexpr uint32_t idesc_lo = f8_idesc(128, kRows, kE4M3, kE5M2, true, true);
-                const uint32_t q_u = smem_u32(smem), qr_u = q_u + 2 * a.rank * kRows, p_u = smem_u32(weights);
+                const uint32_t q_u = smem_u32(smem), p_u = smem_u32(weights);
                 // descriptors; a step along an operand adds its bytes / 16
                 const uint64_t d_ring = smem_desc(smem_u32(ring), 128), d_rope = smem_desc(smem_u32(rope_k), a.rope);
-                const uint64_t d_q[2] = {smem_desc(q_u, 128), smem_desc(q_u + a.rank * kRows, 128)};
-                const uint64_t d_qr[2] = {smem_desc(qr_u, a.rope), smem_desc(qr_u + kRows * a.rope, a.rope)};
+                const uint64_t d_q = smem_desc(q_u, 128), d_qr = smem_desc(q_u + 2 * a.rank * kRows, a.rope);
                 const uint64_t d_p[2] = {smem_desc(p_u, 64), smem_desc(p_u + kKeys * kRows, 64)};
                 // Pieces of the next tile's scores that may be awaited before this tile's pieces are free.
                 const int lead = min(pieces, a.slots - pieces);
@@ -543,32 +587,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
                 // Scores of one tile: pieces [c0, c1), the rope part before piece 0.
                 const auto scores = [&](int c0, int c1) {
-                    const uint32_t d = tmem + kScoreCol + (tile_s & 1) * kRows;
+                    const uint32_t d = tmem + kScoreCol + (tile_s & 1) * (2 * kRows);
                     if (c0 == 0 && a.rope) {
                         wait(&ctl->rope_full, tile_s & 1);
                         tc_fence_after();
                         ready = mbar_test(&ctl->full[slot_s], lap_s & 1);
-                        for (int k = 0; k < a.rope / 32; ++k) {
-                            mma_f8(d, d_rope + k * 2, d_qr[0] + k * 2, idesc_s, k != 0);
-                            mma_f8(d, d_rope + k * 2, d_qr[1] + k * 2, idesc_s, true);
-                        }
+#pragma unroll 1
+                        for (int k = 0; k < a.rope / 32; ++k)
+                            mma_f8(d, d_rope + k * 2, d_qr + k * 2, idesc_s, k != 0);
                         tc_commit(&ctl->rope_free);
                     }
+#pragma unroll 1
                     for (int c = c0; c < c1; ++c) {
                         if (!ready) wait(&ctl->full[slot_s], lap_s & 1);
                         tc_fence_after();
-                        const uint64_t ka = d_ring + slot_s * (kPiece / 16);
-                        const uint64_t qa = d_q[0] + c * (kRows * 8), qb = d_q[1] + c * (kRows * 8);
+                        const uint64_t ka = d_ring + slot_s * (kPiece / 16), qa = d_q + c * (2 * kRows * 8);
                         if (++slot_s == static_cast<uint32_t>(a.slots)) {
                             slot_s = 0;
                             ++lap_s;
                         }
                         ready = mbar_test(&ctl->full[slot_s], lap_s & 1);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 4; ++k)
                             mma_f8(d, ka + k * 2, qa + k * 2, idesc_s, a.rope || c != 0 || k != 0);
-                            mma_f8(d, ka + k * 2, qb + k * 2, idesc_s, true);
-                        }
                     }
                     if (c1 == pieces) tc_commit(&ctl->score_full[tile_s++ & 1]);
                 };
@@ -580,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(&ctl->q_ready, 0);
                 tc_fence_after();
                 scores(0, pieces);
+#pragma unroll 1
                 for (uint32_t i = 0; i < total; ++i) {
                     if (first) {
                         left = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
@@ -592,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (more && same) scores(0, lead);
                     wait(&ctl->weights_ready, i & 1);
                     tc_fence_after();
+#pragma unroll 1
                     for (int c = 0; c < pieces; ++c) {
                         const uint64_t va = d_ring + slot_o * (kPiece / 16);
 #pragma unroll
@@ -629,10 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                 const int64_t row0 = item_row0(a, it);
                 const int rows = item_rows(a, it);
-                if (a.q_bf16)
-                    stage_q<true, 8>(a, ctl, smem, row0, rows, warp, lane, pos == run_lo);
-                else
-                    stage_q<false, 4>(a, ctl, smem, row0, rows, warp, lane, pos == run_lo);
+                stage_q(a, ctl, smem, row0, rows, tid, pos == run_lo);
                 fence_async_smem();
                 named_bar_sync(3, kSoftmaxWarps * 32);
                 if (lane == 0) mbar_arrive(&ctl->q_ready);
@@ -663,20 +703,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float iv = sj == sj ? __fdiv_rn(256.f, sj) : 256.f;
                     const uint64_t inv = pack2(iv, iv);
                     const bool masked = (i + 1) * kKeys > lim_min;  // some column does not see some key
-                    const uint32_t at_s = tmem + lane_base + kScoreCol + (tile & 1) * kRows + half * 32;
+                    const uint32_t at_s = tmem + lane_base + kScoreCol + (tile & 1) * (2 * kRows) + half * 32;
 
                     // s = log2 of the weight over 2^8: score + log2 scale - reference - slack
                     float s[32];
-                    const auto load_scores = [&](bool shifted) {
-                        uint32_t r[32];
-                        tmem_ld32(at_s, r);
+                    wait(&ctl->score_full[tile & 1], (tile >> 1) & 1);
+                    tc_fence_after();
+                    // Usually one turn.  When a column exceeds its reference by the slack, a second turn
+                    // takes the plain scores for the columns' maxima, to which all references move up,
+                    // and a third the shifted scores again.
+                    for (int turn = 0;; ++turn) {
+                        uint32_t r[32], r_lo[32];
+                        tmem_ld32_nowait(at_s, r);
+                        tmem_ld32_nowait(at_s + kRows, r_lo);
+                        tc_wait_ld();
+                        tmem_ld32_done(r);
+                        tmem_ld32_done(r_lo);
 #pragma unroll
                         for (int c = 0; c < 16; c += 2) {
                             const ulonglong2 g = *reinterpret_cast<const ulonglong2 *>(&ctl->row_scale[half * 32 + 2 * c]);
-                            const uint64_t r0 = pack2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
-                            const uint64_t r1 = pack2(__uint_as_float(r[2 * c + 2]), __uint_as_float(r[2 * c + 3]));
-                            const float2 v0 = unpack2(fma2(r0, mul2(ff, g.x), shifted ? add2(aa, shift[c]) : aa));
-                            const float2 v1 = unpack2(fma2(r1, mul2(ff, g.y), shifted ? add2(aa, shift[c + 1]) : aa));
+                            const uint64_t r0 = add2(bits2(r[2 * c], r[2 * c + 1]), bits2(r_lo[2 * c], r_lo[2 * c + 1]));
+                            const uint64_t r1 = add2(bits2(r[2 * c + 2], r[2 * c + 3]), bits2(r_lo[2 * c + 2], r_lo[2 * c + 3]));
+                            const float2 v0 = unpack2(fma2(r0, mul2(ff, g.x), add2(aa, shift[c])));
+                            const float2 v1 = unpack2(fma2(r1, mul2(ff, g.y), add2(aa, shift[c + 1])));
                             s[2 * c] = v0.x;
                             s[2 * c + 1] = v0.y;
                             s[2 * c + 2] = v1.x;
@@ -687,18 +736,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int c = 0; c < 32; ++c)
                                 if (k >= __shfl_sync(kFullMask, lim_col, c)) s[c] = -INFINITY;
                         }
-                    };
-                    wait(&ctl->score_full[tile & 1], (tile >> 1) & 1);
-                    tc_fence_after();
-                    load_scores(true);
-                    float m = s[0];
+                        if (turn == 0) {
+                            float m = s[0];
 #pragma unroll
-                    for (int c = 1; c < 32; ++c) m = fmaxf(m, s[c]);
-                    if (named_bar_any(1 + half, 128, m > 0.f)) {
-                        // A column exceeds its reference by the slack: all columns' references move up
-                        // to their maxima.  Past this barrier nobody reads the maxima of the time
-                        // before any more, so they are cleared there for the time after the next.
-                        load_scores(false);
+                            for (int c = 1; c < 32; ++c) m = fmaxf(m, s[c]);
+                            if (!named_bar_any(1 + half, 128, m > 0.f)) break;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) shift[c] = 0;
+                            continue;
+                        }
+                        if (turn == 2) break;
+                        // Past this barrier nobody reads the maxima of the time before any more, so they
+                        // are cleared there for the time after the next.
                         atomicMax(&ctl->tops[top][col], order_bits(column_maxima(s, lane)));
                         named_bar_sync(1 + half, 128);
                         const float to = fmaxf(ref, unorder_bits(ctl->tops[top][col]));
@@ -715,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i > off) {
                             wait(&ctl->out_done, (tile - 1) & 1);
                             tc_fence_after();
+#pragma unroll 1
                             for (int p = 0; p < pieces; ++p) {
                                 float o[32];
                                 const uint32_t at = tmem + lane_base + p * kRows + half * 32;
@@ -725,7 +775,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             tc_wait_st();
                         }
-                        load_scores(true);
                     }
                     uint32_t hi[8], lo[8];
 #pragma unroll
@@ -803,6 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         a.owner_flag[blockIdx.x] = 1;
                     }
                 }
+#pragma unroll 1
                 for (int p = 0; p < pieces; ++p) {
                     float o[32];
                     tmem_ld32(tmem + lane_base + p * kRows + half * 32, o);
@@ -841,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -1073,7 +1123,7 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     a.scale_log2 = scale * 1.4426950408889634f;
     const int fixed = smem_ring_off(kv_rank, d_rope) + smem_tail();
     a.slots = std::min(kMaxSlots, (smem - fixed) / kPiece);
-    if (a.slots < kv_rank / 128 + 1) return MEMQ_ERR_LAUNCH;
+    if (a.slots < kv_rank / 128) return MEMQ_ERR_LAUNCH;
     const uint64_t width = static_cast<uint64_t>(kv_rank + d_rope), pool = static_cast<uint64_t>(n_pages) * page_size;
     CUtensorMap lat, rope;
     if (!encode_rows(&lat, cache, width, pool, 128, a.box) ||
