@@ -76,24 +76,27 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 10 * 32;
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxGrid = 256;
+constexpr int kAhead = 3;        // tiles fetched into L2 ahead of the ring
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
 constexpr float kSlack = 6.0f;    // log2 of how far a score may exceed the reference
 constexpr int kScoreCol = 256;    // TMEM: accumulators in columns 0..255, scores after them
 
-struct Owner {
-    long long row0;  // first output row of the item
-    int rows;
-    int slot;  // its first partial; the others are slots 2 c of the CTAs up to `last`
-    int last;
+// An item that several CTAs share, noted by the CTA that holds its start (`rows` is 0 otherwise).
+struct __align__(16) Owner {
+    long long row0;      // first output row
+    unsigned char rows;  // 1 to 64
+    unsigned char tail;  // its first partial is slot 2 cta + tail; the others are slots 2 c of the
+    short last;          // CTAs c up to this one
     int pad;
 };
+static_assert(sizeof(Owner) == 16, "one load");
 
 struct PagedArgs {
     const void *q_lat, *q_pe;
+    const uint8_t *cache;
     const float *scales;
     const int32_t *table, *kv_len, *cu_q;
     void *out;
-    int *owner_flag;
     Owner *owner;
     float2 *stats;  // [slot][row] (reference, sum of weights)
     float *part;    // [slot][row][rank]
@@ -226,121 +229,176 @@ __device__ __forceinline__ int q_unit(const PagedArgs &a, int r, int e, int &lo)
     return 2 * a.rank * kRows + swizzled(r, e - a.rank, a.rope);
 }
 
-// The eight elements from `e` on of a query row in memory.
-template <bool BF16>
-__device__ __forceinline__ const uint4 *q_source(const PagedArgs &a, int64_t row, int e) {
-    const bool lat = e < a.rank;
-    const int64_t at = lat ? row * a.rank + e : row * a.rope + (e - a.rank);
-    return reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(lat ? a.q_lat : a.q_pe) + at * (BF16 ? 2 : 4));
+// hi and lo terms of eight query elements, as four pairs of f16 in (-1, 1].
+__device__ __forceinline__ void split_unit(uint8_t *hi, uint8_t *lo, const uint32_t (&f)[4]) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        h[k] = (f[k] + 0x00400040u) & 0xff80ff80u;  // to the nearest multiple of three fraction bits
+        l[k] = sub_f16x2(f[k], h[k]) + 0x00400040u;
+    }
+    *reinterpret_cast<uint2 *>(hi) = make_uint2(e4m3_bits(h[0], h[1]), e4m3_bits(h[2], h[3]));
+    *reinterpret_cast<uint2 *>(lo) = make_uint2(e4m3_bits(l[0], l[1]), e4m3_bits(l[2], l[3]));
+}
+__device__ __forceinline__ uint32_t scaled_pair(float a, float b, uint64_t by) {
+    const float2 x = unpack2(mul2(pack2(a, b), by));
+    return f32x2_to_f16x2(x.x, x.y);
+}
+__device__ __forceinline__ void split_bf16(uint8_t *hi, uint8_t *lo, uint2 a, uint2 b, uint64_t by) {
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+    uint32_t f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = scaled_pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u), by);
+    split_unit(hi, lo, f);
+}
+__device__ __forceinline__ void split_f32(uint8_t *hi, uint8_t *lo, uint4 a, uint4 b, uint64_t by) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = scaled_pair(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]), by);
+    split_unit(hi, lo, f);
+}
+
+// Maxima of |x| as bits: infinities and NaN lie above all numbers.
+__device__ __forceinline__ __nv_bfloat162 max_bf16(__nv_bfloat162 m, uint4 v) {
+    const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&v);
+    return __hmax2_nan(__hmax2_nan(m, __hmax2_nan(__habs2(x[0]), __habs2(x[1]))),
+                       __hmax2_nan(__habs2(x[2]), __habs2(x[3])));
+}
+__device__ __forceinline__ uint32_t max_f32(uint32_t m, uint4 v) {
+    return max(max(m, v.x & 0x7fffffffu), max(v.y & 0x7fffffffu, max(v.z & 0x7fffffffu, v.w & 0x7fffffffu)));
 }
 
 // The 64 query rows of an item -> their 8-bit terms and scales in shared memory; rows past `rows` are
 // zeros.  Four threads serve a row, in units of eight elements, in two passes, for the row's maximum
 // comes first.  A unit of bf16 queries fills the 8 + 8 bytes of its terms, so the first pass parks it
-// there and the second splits it in place; f32 queries are read a second time, from L2.  Many loads
-// are out at a time and the code stays short: unrolled over registers it was half the kernel, and
-// fetching it took longer than running it.  On the first item the producer starts its copies when
-// the first loads are out; behind a ring of cache rows in the memory's queues they took 10 us and more.
-template <bool BF16, int U>
-__device__ __forceinline__ uint32_t q_maximum(const PagedArgs &a, uint8_t *smem, int64_t row, bool live, int r, int q,
-                                              bool first) {
-    const int units = (a.rank + a.rope) / 32;  // of this thread
-    uint32_t top = 0;
-    for (int j0 = 0; j0 < units; j0 += U) {
-        uint4 v[U][BF16 ? 1 : 2];
+// there and the second splits it in place; f32 queries are read a second time, from L2.  All of a bf16
+// row's loads are out at once and the code stays short: unrolled over registers it was half the
+// kernel, and fetching it took longer than running it.  On the first item the producer starts its
+// copies when the first loads are out; behind a ring of cache rows in the memory's queues they took
+// 10 us and more.  Returns the bits of the thread's maximum, as bf16.
+__device__ __forceinline__ uint32_t park_bf16(const PagedArgs &a, uint8_t *smem, int64_t row, bool live, int r, int q,
+                                              const int (&at)[4], bool first) {
+    const int pieces = a.rank / 128;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 v[4][4], w[4];
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q_lat) + row * a.rank) + q;
+    const uint4 *pe = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q_pe) + row * a.rope) + q;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
-                v[j][h] = make_uint4(0, 0, 0, 0);
-                if (live && j0 + j < units) v[j][h] = __ldcg(q_source<BF16>(a, row, (q + 4 * (j0 + j)) * 8) + h);
+        for (int j = 0; j < 4; ++j) v[c][j] = live && c < pieces ? __ldcg(src + c * 16 + j * 4) : zero;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = live && j * 32 < a.rope ? __ldcg(pe + j * 4) : zero;
+    if (first) named_bar_arrive(4, kSoftmaxWarps * 32 + 32);
+    __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (c < pieces) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                top = max_bf16(top, v[c][j]);
+                uint8_t *hi = smem + c * (2 * kRows * 128) + at[j];
+                *reinterpret_cast<uint2 *>(hi) = make_uint2(v[c][j].x, v[c][j].y);
+                *reinterpret_cast<uint2 *>(hi + kRows * 128) = make_uint2(v[c][j].z, v[c][j].w);
             }
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j * 32 < a.rope) {
+            top = max_bf16(top, w[j]);
+            int lo;
+            uint8_t *hi = smem + q_unit(a, r, a.rank + j * 32 + q * 8, lo);
+            *reinterpret_cast<uint2 *>(hi) = make_uint2(w[j].x, w[j].y);
+            *reinterpret_cast<uint2 *>(hi + lo) = make_uint2(w[j].z, w[j].w);
+        }
+    }
+    const uint32_t t = *reinterpret_cast<const uint32_t *>(&top);
+    return max(t & 0x7fffu, (t >> 16) & 0x7fffu);
+}
+
+__device__ __forceinline__ uint32_t top_f32(const PagedArgs &a, int64_t row, bool live, int q, bool first) {
+    const int pieces = a.rank / 128;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_lat) + row * a.rank) + 2 * q;
+    const uint4 *pe = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_pe) + row * a.rope) + 2 * q;
+    uint32_t top = 0;
+#pragma unroll 1
+    for (int c = 0; c < pieces; c += 2) {  // two pieces at a time
+        uint4 v[2][8];
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[p][j] = live && c + p < pieces ? __ldcg(src + (c + p) * 32 + (j >> 1) * 8 + (j & 1)) : zero;
         if (first) named_bar_arrive(4, kSoftmaxWarps * 32 + 32);
         first = false;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
-                const uint4 w = v[j][h];
-                if (BF16)
-                    top = __vmaxu2(__vmaxu2(top, w.x & 0x7fff7fffu), __vmaxu2(w.y & 0x7fff7fffu,
-                          __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-                else
-                    top = max(max(top, w.x & 0x7fffffffu), max(w.y & 0x7fffffffu,
-                          max(w.z & 0x7fffffffu, w.w & 0x7fffffffu)));
-            }
-            if (BF16 && j0 + j < units) {
-                int lo;
-                uint8_t *hi = smem + q_unit(a, r, (q + 4 * (j0 + j)) * 8, lo);
-                *reinterpret_cast<uint2 *>(hi) = make_uint2(v[j][0].x, v[j][0].y);
-                *reinterpret_cast<uint2 *>(hi + lo) = make_uint2(v[j][0].z, v[j][0].w);
-            }
-        }
+            for (int j = 0; j < 8; ++j) top = max_f32(top, v[p][j]);
     }
-    // as the upper half of an f32's bits: infinities and NaN lie above all numbers
-    return BF16 ? max(top & 0xffffu, top >> 16) : top >> 16;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void q_split(const PagedArgs &a, uint8_t *smem, int64_t row, bool live, int r, int q, bool fin,
-                                        float inv) {
-    const uint64_t by = pack2(inv, inv);
-#pragma unroll 2
-    for (int e = q * 8; e < a.rank + a.rope; e += 32) {
-        int lo_off;
-        uint8_t *at = smem + q_unit(a, r, e, lo_off);
-        uint2 *hi = reinterpret_cast<uint2 *>(at), *lo = reinterpret_cast<uint2 *>(at + lo_off);
-        uint32_t f[4], h[4], l[4];
-        if (BF16) {
-            const uint2 w0 = *hi, w1 = *lo;
-            const uint32_t w[4] = {w0.x, w0.y, w1.x, w1.y};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 x = unpack2(mul2(pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)), by));
-                f[k] = f32x2_to_f16x2(x.x, x.y);
-            }
-        } else {
-            uint4 w[2] = {};
-            if (live) {
-                w[0] = __ldcg(q_source<false>(a, row, e));
-                w[1] = __ldcg(q_source<false>(a, row, e) + 1);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float2 x = unpack2(mul2(pack2(__uint_as_float(w[k].x), __uint_as_float(w[k].y)), by));
-                const float2 y = unpack2(mul2(pack2(__uint_as_float(w[k].z), __uint_as_float(w[k].w)), by));
-                f[2 * k] = f32x2_to_f16x2(x.x, x.y);
-                f[2 * k + 1] = f32x2_to_f16x2(y.x, y.y);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (!fin) f[k] = 0;
-            h[k] = (f[k] + 0x00400040u) & 0xff80ff80u;  // to the nearest multiple of three fraction bits
-            l[k] = sub_f16x2(f[k], h[k]) + 0x00400040u;
-        }
-        *hi = make_uint2(e4m3_bits(h[0], h[1]), e4m3_bits(h[2], h[3]));
-        *lo = make_uint2(e4m3_bits(l[0], l[1]), e4m3_bits(l[2], l[3]));
-    }
+    if (live)
+        for (int j = 0; j < a.rope / 32; ++j) top = max_f32(max_f32(top, __ldcg(pe + j * 8)), __ldcg(pe + j * 8 + 1));
+    return top >> 16;
 }
 
 __device__ __forceinline__ void stage_q(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows,
                                         int tid, bool first) {
-    const int r = tid >> 2, q = tid & 3;
-    uint32_t top = a.q_bf16 ? q_maximum<true, 9>(a, smem, row0 + r, r < rows, r, q, first)
-                            : q_maximum<false, 6>(a, smem, row0 + r, r < rows, r, q, first);
+    const int r = tid >> 2, q = tid & 3, pieces = a.rank / 128;
+    const int64_t row = row0 + r;
+    const bool live = r < rows;
+    int at[4];  // of the thread's units in a piece
+#pragma unroll
+    for (int j = 0; j < 4; ++j) at[j] = swizzled(r, j * 32 + q * 8, 128);
+    uint32_t top = a.q_bf16 ? park_bf16(a, smem, row, live, r, q, at, first) : top_f32(a, row, live, q, first);
     top = max(top, __shfl_xor_sync(kFullMask, top, 1));
     top = max(top, __shfl_xor_sync(kFullMask, top, 2));
     // 2^e with max / 2^e in [1/2, 1); tiny rows keep a normal reciprocal, rows past 2^126 have none
     const bool fin = top < 0x7e80u;
     const int e2 = min(max(static_cast<int>(top >> 7), 32), 252);
     const float inv = __uint_as_float(static_cast<uint32_t>(253 - e2) << 23);
+    const uint64_t by = pack2(inv, inv);
     if (q == 0) ctl->row_scale[r] = fin ? __uint_as_float(static_cast<uint32_t>(e2 - 7) << 23) : NAN;
-    if (a.q_bf16)
-        q_split<true>(a, smem, row0 + r, r < rows, r, q, fin, inv);
-    else
-        q_split<false>(a, smem, row0 + r, r < rows, r, q, fin, inv);
+    // A row that is not finite has a NaN scale; what its codes hold does not matter to the others.
+    if (a.q_bf16) {
+#pragma unroll 1
+        for (int c = 0; c < pieces; ++c) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint8_t *hi = smem + c * (2 * kRows * 128) + at[j], *lo = hi + kRows * 128;
+                split_bf16(hi, lo, *reinterpret_cast<const uint2 *>(hi), *reinterpret_cast<const uint2 *>(lo), by);
+            }
+        }
+#pragma unroll 1
+        for (int j = 0; j < a.rope / 32; ++j) {
+            int off;
+            uint8_t *hi = smem + q_unit(a, r, a.rank + j * 32 + q * 8, off), *lo = hi + off;
+            split_bf16(hi, lo, *reinterpret_cast<const uint2 *>(hi), *reinterpret_cast<const uint2 *>(lo), by);
+        }
+    } else {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_lat) + row * a.rank) + 2 * q;
+        const uint4 *pe = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_pe) + row * a.rope) + 2 * q;
+#pragma unroll 1
+        for (int c = 0; c < pieces; ++c) {
+            uint4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = live ? __ldcg(src + c * 32 + (j >> 1) * 8 + (j & 1)) : zero;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint8_t *hi = smem + c * (2 * kRows * 128) + at[j];
+                split_f32(hi, hi + kRows * 128, v[2 * j], v[2 * j + 1], by);
+            }
+        }
+#pragma unroll 1
+        for (int j = 0; j < a.rope / 32; ++j) {
+            int off;
+            uint8_t *hi = smem + q_unit(a, r, a.rank + j * 32 + q * 8, off);
+            split_f32(hi, hi + off, live ? __ldcg(pe + j * 8) : zero, live ? __ldcg(pe + j * 8 + 1) : zero, by);
+        }
+    }
 }
 
 // Sum over the 32 lanes of v[c], for every c, in lane c (a fixed tree).
@@ -488,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- TMA producer
             uint32_t tile = 0, slot = 0, lap = 0;
-            const int per_tile = kKeys / a.box;
+            const int per_tile = kKeys / a.box, width = a.rank + a.rope;
             named_bar_sync(4, kSoftmaxWarps * 32 + 32);  // the first query rows' loads are out
             for (long long pos = run_lo; pos < run_hi;) {
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
@@ -503,9 +561,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return (page << a.page_shift) + (key & ((1 << a.page_shift) - 1));
                 };
-                int row = page_row(off * kKeys);
+                const auto fetch_l2 = [&](int row) {  // a box's rows are contiguous
+                    if (row >= 0) bulk_prefetch_l2(a.cache + static_cast<int64_t>(row) * width, a.box * width);
+                };
+                // The ring holds two tiles at most, less than the memory's latency under load: tiles up to
+                // kAhead further on are fetched into L2.  Lane i carries the pool row of its box of each.
+                int rows_ahead[kAhead + 1];
+#pragma unroll
+                for (int k = 0; k <= kAhead; ++k) {
+                    rows_ahead[k] = k < n ? page_row((off + k) * kKeys) : -1;
+                    if (k > 0) fetch_l2(rows_ahead[k]);
+                }
                 for (int i = off; i < off + n; ++i, ++tile) {
-                    const int row_next = i + 1 < off + n ? page_row((i + 1) * kKeys) : -1;
+                    const int row = rows_ahead[0];
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) rows_ahead[k] = rows_ahead[k + 1];
+                    rows_ahead[kAhead] = i + kAhead + 1 < off + n ? page_row((i + kAhead + 1) * kKeys) : -1;
                     const bool mine = row >= 0;
                     const uint32_t boxes = __popc(__ballot_sync(kFullMask, mine));
                     // scales of the tile's keys
@@ -540,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ++lap;
                         }
                     }
-                    row = row_next;
+                    fetch_l2(rows_ahead[kAhead]);
                 }
                 pos += n;
                 off = 0;
@@ -667,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
             const int col = half * 32 + lane;  // the column whose statistics this lane holds
             uint32_t tile = 0, slot = 0, top = 0;
-            if (tid == 0) a.owner_flag[blockIdx.x] = 0;
+            Owner mine_owner = {};
             for (long long pos = run_lo; pos < run_hi;) {
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                 const int64_t row0 = item_row0(a, it);
@@ -844,12 +915,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!whole) {
                     if (wq == 0) a.stats[here * kRows + col] = make_float2(ref, sum);
                     if (off == 0 && tid == 0) {  // this CTA holds the item's start: it names its parts
-                        Owner &w = a.owner[blockIdx.x];
-                        w.row0 = row0;
-                        w.rows = rows;
-                        w.slot = here;
-                        w.last = static_cast<int>((pos + it.tiles - 1) / per);
-                        a.owner_flag[blockIdx.x] = 1;
+                        mine_owner.row0 = row0;
+                        mine_owner.rows = static_cast<unsigned char>(rows);
+                        mine_owner.tail = static_cast<unsigned char>(here & 1);
+                        mine_owner.last = static_cast<short>((pos + it.tiles - 1) / per);
                     }
                 }
 #pragma unroll 1
@@ -885,9 +954,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 off = 0;
                 if (pos < run_hi) next_item(a, it);
             }
+            if (tid == 0) a.owner[blockIdx.x] = mine_owner;
         }
     } else if (tid == 0) {
-        a.owner_flag[blockIdx.x] = 0;
+        a.owner[blockIdx.x] = Owner{};
     }
     tc_fence_before();
     __syncthreads();
@@ -897,15 +967,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Adds the partial accumulators of the items that several CTAs shared.  CTA (x, y) serves units y,
-// y + gridDim.y, ... of the x-th such item; a unit is 128 dims of a row.  Warp w adds parts w, w + 8,
-// ... (a lane four dims), and the eight sums are added in warp order.
+// Adds the partial accumulators of the items that several CTAs shared.  CTAs (x, 0 .. gridDim.y - 1)
+// serve the x-th such item, in units of 128 dims of a row (a lane four dims).  Up to kFewParts parts a
+// warp serves a unit alone: no barrier, 64 units under way on an SM.  Above, a CTA serves it: warp w
+// adds parts w, w + 8, ... and the eight sums are added in warp order.
 constexpr int kCombineWarps = 8;
 constexpr int kCombineThreads = kCombineWarps * 32;
+constexpr int kFewParts = 16;
 static_assert(kMaxGrid <= kCombineThreads, "a thread looks at one CTA's part");
+
+__device__ __forceinline__ void add_part(float4 &acc, const PagedArgs &a, int64_t slot, int r, int d, float x) {
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part + (slot * kRows + r) * a.rank + d));
+    acc.x = fmaf(v.x, x, acc.x);
+    acc.y = fmaf(v.y, x, acc.y);
+    acc.z = fmaf(v.z, x, acc.z);
+    acc.w = fmaf(v.w, x, acc.w);
+}
+
+__device__ __forceinline__ void store_out(const PagedArgs &a, int64_t at, float4 o, float total) {
+    const float n = total == 0.f ? 0.f : __fdiv_rn(1.f, total);
+    o = make_float4(o.x * n, o.y * n, o.z * n, o.w * n);
+    if (a.out_bf16) {
+        __nv_bfloat162 v[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = *reinterpret_cast<uint2 *>(v);
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = o;
+    }
+}
 
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArgs a, int grid) {
     __shared__ int found;
+    __shared__ Owner owner;
     __shared__ int counts[kCombineWarps];
     __shared__ float weight[kMaxGrid];
     __shared__ float red[2][kCombineWarps];
@@ -914,24 +1006,44 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArg
     griddep_launch_dependents();
     griddep_wait();
     if (tid == 0) found = -1;
-    const bool flag = tid < grid && __ldcg(a.owner_flag + tid) != 0;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (tid < grid) raw = __ldcg(reinterpret_cast<const uint4 *>(a.owner + tid));
+    const Owner own = *reinterpret_cast<const Owner *>(&raw);
+    const bool flag = own.rows != 0;
     const unsigned ballot = __ballot_sync(kFullMask, flag);
     if (lane == 0) counts[warp] = __popc(ballot);
     __syncthreads();
     int rank_of = __popc(ballot & ((1u << lane) - 1));
     for (int w = 0; w < warp; ++w) rank_of += counts[w];
-    if (flag && rank_of == static_cast<int>(blockIdx.x)) found = tid;
+    if (flag && rank_of == static_cast<int>(blockIdx.x)) {
+        found = tid;
+        owner = own;
+    }
     __syncthreads();
     if (found < 0) return;
-    const int cta = found;
-    const Owner *op = a.owner + cta;
-    const long long row0 = __ldcg(&op->row0);
-    const int rows = __ldcg(&op->rows), slot0 = __ldcg(&op->slot), last = __ldcg(&op->last);
-    const int parts = min(last, grid - 1) - cta + 1, pieces = a.rank / 128;
-    for (int unit = blockIdx.y; unit < rows * pieces; unit += gridDim.y) {
-        const int r = unit / pieces, d0 = (unit - r * pieces) * 128 + lane * 4;
+    const int cta = found, slot0 = 2 * cta + owner.tail;
+    const long long row0 = owner.row0;
+    const int parts = min(static_cast<int>(owner.last), grid - 1) - cta + 1, pieces = a.rank / 128;
+    const int units = owner.rows * pieces;
+    const auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (cta + k); };
+    if (parts <= kFewParts) {
+        for (int unit = blockIdx.y * kCombineWarps + warp; unit < units; unit += gridDim.y * kCombineWarps) {
+            const int r = unit / pieces, d = (unit - r * pieces) * 128 + lane * 4;
+            float2 st = make_float2(kUnset, 0.f);
+            if (lane < parts) st = __ldcg(a.stats + slot_of(lane) * kRows + r);
+            const float w = ex2(st.x - warp_max(st.x));
+            const float total = warp_sum(w * st.y);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = 0; k < parts; ++k) add_part(acc, a, slot_of(k), r, d, __shfl_sync(kFullMask, w, k));
+            store_out(a, (row0 + r) * a.rank + d, acc, total);
+        }
+        return;
+    }
+    for (int unit = blockIdx.y; unit < units; unit += gridDim.y) {
+        const int r = unit / pieces, d = (unit - r * pieces) * 128 + lane * 4;
         float2 st = make_float2(kUnset, 0.f);
-        if (tid < parts) st = __ldcg(a.stats + (tid == 0 ? slot0 : 2 * (cta + tid)) * kRows + r);
+        if (tid < parts) st = __ldcg(a.stats + slot_of(tid) * kRows + r);
         const float wm = warp_max(st.x);
         if (lane == 0) red[0][warp] = wm;
         __syncthreads();
@@ -946,39 +1058,20 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArg
         for (int k = 0; k < kCombineWarps; ++k) total += red[1][k];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int k = warp; k < parts; k += kCombineWarps) {
-            const int64_t s = k == 0 ? slot0 : 2 * (cta + k);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part + (s * kRows + r) * a.rank + d0));
-            const float x = weight[k];
-            acc.x = fmaf(v.x, x, acc.x);
-            acc.y = fmaf(v.y, x, acc.y);
-            acc.z = fmaf(v.z, x, acc.z);
-            acc.w = fmaf(v.w, x, acc.w);
-        }
+        for (int k = warp; k < parts; k += kCombineWarps) add_part(acc, a, slot_of(k), r, d, weight[k]);
         sums[warp][lane] = acc;
         __syncthreads();
         if (warp == 0) {
-            float4 o = acc;
             for (int k = 1; k < kCombineWarps; ++k) {
                 const float4 v = sums[k][lane];
-                o.x += v.x;
-                o.y += v.y;
-                o.z += v.z;
-                o.w += v.w;
+                acc.x += v.x;
+                acc.y += v.y;
+                acc.z += v.z;
+                acc.w += v.w;
             }
-            const float n = total == 0.f ? 0.f : __fdiv_rn(1.f, total);
-            o = make_float4(o.x * n, o.y * n, o.z * n, o.w * n);
-            const int64_t at = (row0 + r) * a.rank + d0;
-            if (a.out_bf16) {
-                __nv_bfloat162 v[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = *reinterpret_cast<uint2 *>(v);
-            } else {
-                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = o;
-            }
+            store_out(a, (row0 + r) * a.rank + d, acc, total);
         }
-        // red is rewritten only past this iteration's last barrier by threads that have read it; the
-        // next iteration's first barrier orders sums and weight
-        __syncthreads();
+        __syncthreads();  // the shared arrays are free for the next unit
     }
 }
 
@@ -1039,8 +1132,8 @@ bool rank_ok(int rank) { return rank == 128 || rank == 256 || rank == 512; }
 bool rope_ok(int rope) { return rope == 0 || rope == 32 || rope == 64 || rope == 128; }
 bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
-// Workspace: owner flags, owners, statistics, partial accumulators.
-constexpr int64_t kFlagBytes = kMaxGrid * 4, kOwnerBytes = kMaxGrid * sizeof(Owner);
+// Workspace: owners, statistics, partial accumulators.
+constexpr int64_t kOwnerBytes = kMaxGrid * sizeof(Owner);
 int64_t stat_bytes(int grid) { return static_cast<int64_t>(2) * grid * kRows * sizeof(float2); }
 int64_t part_bytes(int grid, int rank) { return static_cast<int64_t>(2) * grid * kRows * rank * sizeof(float); }
 
@@ -1061,7 +1154,7 @@ extern "C" int64_t memq_mla_attn_paged_workspace(int kv_rank) {
     int sms = 0, smem = 0;
     if (!device_info(sms, smem)) return -1;
     const int grid = std::min(sms, kMaxGrid);
-    return kFlagBytes + kOwnerBytes + stat_bytes(grid) + part_bytes(grid, kv_rank);
+    return kOwnerBytes + stat_bytes(grid) + part_bytes(grid, kv_rank);
 }
 
 extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q_pe, const uint8_t *cache,
@@ -1089,21 +1182,21 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     int sms = 0, smem = 0;
     if (!device_info(sms, smem)) return MEMQ_ERR_LAUNCH;
     const int grid = std::min(sms, kMaxGrid);
-    if (workspace_bytes < kFlagBytes + kOwnerBytes + stat_bytes(grid) + part_bytes(grid, kv_rank)) return MEMQ_ERR_SHAPE;
+    if (workspace_bytes < kOwnerBytes + stat_bytes(grid) + part_bytes(grid, kv_rank)) return MEMQ_ERR_SHAPE;
 
     PagedArgs a{};
     a.q_lat = q_lat;
     a.q_pe = q_pe;
+    a.cache = cache;
     a.scales = scales;
     a.table = block_table;
     a.kv_len = kv_len;
     a.cu_q = cu_q;
     a.out = out;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    a.owner_flag = reinterpret_cast<int *>(ws);
-    a.owner = reinterpret_cast<Owner *>(ws + kFlagBytes);
-    a.stats = reinterpret_cast<float2 *>(ws + kFlagBytes + kOwnerBytes);
-    a.part = reinterpret_cast<float *>(ws + kFlagBytes + kOwnerBytes + stat_bytes(grid));
+    a.owner = reinterpret_cast<Owner *>(ws);
+    a.stats = reinterpret_cast<float2 *>(ws + kOwnerBytes);
+    a.part = reinterpret_cast<float *>(ws + kOwnerBytes + stat_bytes(grid));
     a.n_tok = static_cast<int>(n_tok);
     a.n_seq = n_seq;
     a.nh = nh;
