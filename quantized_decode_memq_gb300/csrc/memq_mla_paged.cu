@@ -33,7 +33,8 @@
 // that is cut into equal runs, one per CTA; every CTA derives its run from the lengths on the device
 // (nothing of the plan is on the host, so a captured graph serves other lengths).  An item that
 // spans CTAs leaves f32 partial accumulators in the workspace, and combine_kernel adds them in CTA
-// order: results do not depend on timing.
+// order: results do not depend on timing.  Starting an item (its queries, the first tile's references,
+// the accumulators' way out) costs as much as several tiles, so it counts as `start` tiles in the list.
 //
 // Warps 0-7 are the softmax warps (thread = key x half of the columns), warp 8 issues the TMA copies
 // of 128 x 128-byte pieces into a ring, one thread of warp 9 the products.  S^T is double buffered: the
@@ -76,7 +77,6 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 10 * 32;
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxGrid = 256;
-constexpr int kAhead = 3;        // tiles fetched into L2 ahead of the ring
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
 constexpr float kSlack = 6.0f;    // log2 of how far a score may exceed the reference
 constexpr int kScoreCol = 256;    // TMEM: accumulators in columns 0..255, scores after them
@@ -93,7 +93,6 @@ static_assert(sizeof(Owner) == 16, "one load");
 
 struct PagedArgs {
     const void *q_lat, *q_pe;
-    const uint8_t *cache;
     const float *scales;
     const int32_t *table, *kv_len, *cu_q;
     void *out;
@@ -102,6 +101,7 @@ struct PagedArgs {
     float *part;    // [slot][row][rank]
     int n_tok, n_seq, nh, rank, rope, n_pages, page_shift, box, max_pages;
     int group;  // tokens per item
+    int start;  // what starting an item costs, in tiles
     int heads_per, head_blocks;
     int slots;
     int q_bf16, out_bf16;
@@ -123,6 +123,7 @@ struct Control {
     uint32_t tmem;
     int first_off;
     Item first;
+    long long first_pos;
     long long warp_sum[kThreads / 32];
 };
 static_assert(sizeof(Control) <= 2048, "the control block has 2 KB of shared memory");
@@ -503,12 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k < 0 || ((k + 1) % a.group != 0 && k + 1 != it.t)) continue;
             it.tok = k / a.group * a.group;
             item_sizes(a, it);
-            const long long n = static_cast<long long>(it.tiles) * a.head_blocks;
+            const int units = it.tiles + a.start;
+            const long long n = static_cast<long long>(units) * a.head_blocks;
             if (pass == 1 && sum <= run_lo && run_lo < sum + n) {
-                const int at = static_cast<int>(run_lo - sum);
-                it.block = at / it.tiles;
+                const long long at = run_lo - sum;
+                it.block = static_cast<int>(at / units);
+                const int off = max(0, static_cast<int>(at - static_cast<long long>(it.block) * units) - a.start);
                 ctl->first = it;
-                ctl->first_off = at - it.block * it.tiles;
+                ctl->first_off = off;
+                ctl->first_pos = sum + static_cast<long long>(it.block) * units + a.start + off;
             }
             sum += n;
         }
@@ -537,8 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFullMask, ctl->tmem, 0);
+    const long long run_first = run_lo < run_hi ? ctl->first_pos : run_hi;  // of the run's first tile
 
-    if (run_lo < run_hi) {
+    if (run_first < run_hi) {
         Item it = ctl->first;
         int off = ctl->first_off;
         Waiter wait;
@@ -546,9 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- TMA producer
             uint32_t tile = 0, slot = 0, lap = 0;
-            const int per_tile = kKeys / a.box, width = a.rank + a.rope;
+            const int per_tile = kKeys / a.box;
             named_bar_sync(4, kSoftmaxWarps * 32 + 32);  // the first query rows' loads are out
-            for (long long pos = run_lo; pos < run_hi;) {
+            for (long long pos = run_first; pos < run_hi;) {
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                 const int32_t *table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
                 const auto page_row = [&](int key0) {  // row of this lane's box in the pool
@@ -561,22 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return (page << a.page_shift) + (key & ((1 << a.page_shift) - 1));
                 };
-                const auto fetch_l2 = [&](int row) {  // a box's rows are contiguous
-                    if (row >= 0) bulk_prefetch_l2(a.cache + static_cast<int64_t>(row) * width, a.box * width);
-                };
-                // The ring holds two tiles at most, less than the memory's latency under load: tiles up to
-                // kAhead further on are fetched into L2.  Lane i carries the pool row of its box of each.
-                int rows_ahead[kAhead + 1];
-#pragma unroll
-                for (int k = 0; k <= kAhead; ++k) {
-                    rows_ahead[k] = k < n ? page_row((off + k) * kKeys) : -1;
-                    if (k > 0) fetch_l2(rows_ahead[k]);
-                }
+                int row = page_row(off * kKeys);
                 for (int i = off; i < off + n; ++i, ++tile) {
-                    const int row = rows_ahead[0];
-#pragma unroll
-                    for (int k = 0; k < kAhead; ++k) rows_ahead[k] = rows_ahead[k + 1];
-                    rows_ahead[kAhead] = i + kAhead + 1 < off + n ? page_row((i + kAhead + 1) * kKeys) : -1;
+                    const int row_next = i + 1 < off + n ? page_row((i + 1) * kKeys) : -1;
                     const bool mine = row >= 0;
                     const uint32_t boxes = __popc(__ballot_sync(kFullMask, mine));
                     // scales of the tile's keys
@@ -611,9 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ++lap;
                         }
                     }
-                    fetch_l2(rows_ahead[kAhead]);
+                    row = row_next;
                 }
-                pos += n;
+                pos += n + a.start;
                 off = 0;
                 if (pos < run_hi) {
                     next_item(a, it);
@@ -685,23 +677,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c1 == pieces) tc_commit(&ctl->score_full[tile_s++ & 1]);
                 };
 
-                const uint32_t total = static_cast<uint32_t>(run_hi - run_lo);
                 int left = 0;       // tiles of the current segment that follow this one
                 bool first = true;  // the tile starts a segment
-                long long pos = run_lo;
+                long long pos = run_first;
                 wait(&ctl->q_ready, 0);
                 tc_fence_after();
                 scores(0, pieces);
+                bool more = true;
 #pragma unroll 1
-                for (uint32_t i = 0; i < total; ++i) {
+                for (uint32_t i = 0; more; ++i) {
                     if (first) {
                         left = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                         off = 0;
-                        pos += left;
-                        next_item(a, it);
+                        pos += left + a.start;
+                        if (pos < run_hi) next_item(a, it);
                     }
                     --left;
-                    const bool more = i + 1 < total, same = left > 0;
+                    const bool same = left > 0;
+                    more = same || pos < run_hi;
                     if (more && same) scores(0, lead);
                     wait(&ctl->weights_ready, i & 1);
                     tc_fence_after();
@@ -739,11 +732,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col = half * 32 + lane;  // the column whose statistics this lane holds
             uint32_t tile = 0, slot = 0, top = 0;
             Owner mine_owner = {};
-            for (long long pos = run_lo; pos < run_hi;) {
+            for (long long pos = run_first; pos < run_hi;) {
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                 const int64_t row0 = item_row0(a, it);
                 const int rows = item_rows(a, it);
-                stage_q(a, ctl, smem, row0, rows, tid, pos == run_lo);
+                stage_q(a, ctl, smem, row0, rows, tid, pos == run_first);
                 fence_async_smem();
                 named_bar_sync(3, kSoftmaxWarps * 32);
                 if (lane == 0) mbar_arrive(&ctl->q_ready);
@@ -907,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float sum = (scratch[col] + scratch[kRows + col]) +
                                   (scratch[2 * kRows + col] + scratch[3 * kRows + col]);
                 const bool whole = off == 0 && n == it.tiles;
-                const int here = 2 * static_cast<int>(blockIdx.x) + (pos == run_lo ? 0 : 1);
+                const int here = 2 * static_cast<int>(blockIdx.x) + (pos == run_first ? 0 : 1);
                 const float scale_col = whole ? (sum == 0.f ? 0.f : __fdiv_rn(1.f, sum)) : 1.f;
                 float norm[32];
 #pragma unroll
@@ -950,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 named_bar_sync(3, kSoftmaxWarps * 32);  // the scratch and the row scales are free again
-                pos += n;
+                pos += n + a.start;
                 off = 0;
                 if (pos < run_hi) next_item(a, it);
             }
@@ -1187,7 +1180,6 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     PagedArgs a{};
     a.q_lat = q_lat;
     a.q_pe = q_pe;
-    a.cache = cache;
     a.scales = scales;
     a.table = block_table;
     a.kv_len = kv_len;
@@ -1211,6 +1203,8 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     a.head_blocks = (nh + kRows - 1) / kRows;
     a.heads_per = (nh + a.head_blocks - 1) / a.head_blocks;
     a.group = a.head_blocks > 1 ? 1 : kRows / nh;
+    // About 20,000 cycles, against about 1,050 for each 128 dims of a tile.
+    a.start = 1 + 2560 / kv_rank;
     a.q_bf16 = q_dtype == MEMQ_BF16;
     a.out_bf16 = out_dtype == MEMQ_BF16;
     a.scale_log2 = scale * 1.4426950408889634f;
