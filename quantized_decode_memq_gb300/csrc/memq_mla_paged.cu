@@ -19,14 +19,14 @@
 // the operations at twice the 16-bit rate):
 //   q = 2^e (hi + lo), both E4M3, e per row: 8 significant bits, which hold a bf16 value exactly
 //       down to 2^-10 of the row's largest; below that an absolute 2^-18 of the largest;
-//   p = hi (E4M3) + lo (E5M2), with p in (0, 2^8]: a relative 2^-7 at most (about 2^-10 rms), and
-//       an absolute 2^-17, 2^-19 of the running maximum: E5M2 carries the long tail of small
+//   p = hi (E4M3) + lo (E5M2), with p in (0, 2^8.8]: a relative 2^-7 at most (about 2^-10 rms), and
+//       an absolute 2^-17, 2^-18 of the reference: E5M2 carries the long tail of small
 //       weights that a second E4M3 term would flush.  Both codes are bit fields of f16 numbers:
 //       E4M3 of v is bits 14..7 of f16(v / 256), E5M2 of v the high byte of f16(v), so the split
 //       needs one conversion per pair of weights and integer operations.
-// The key's scale is folded into its weight (p_j = 2^8 exp2(s_j + log2 scales_j - R - 6)), so R, the
+// The key's scale is folded into its weight (p_j = 2^8 exp2(s_j + log2 scales_j - R - 7)), so R, the
 // running reference, bounds what the 8-bit terms must hold; the sum of weights is kept apart in f32.
-// R moves, and the accumulators are rescaled, only when a tile's maximum exceeds it by 2^6: a tile
+// R moves, and the accumulators are rescaled, only when a score exceeds it by 7.8: a tile
 // then needs one vote instead of 64 maxima over its keys.
 //
 // One CTA per SM.  The 128-key tiles of all (sequence, token group, head block) items form one list
@@ -34,7 +34,8 @@
 // (nothing of the plan is on the host, so a captured graph serves other lengths).  An item that
 // spans CTAs leaves f32 partial accumulators in the workspace, and combine_kernel adds them in CTA
 // order: results do not depend on timing.  Starting an item (its queries, the first tile's references,
-// the accumulators' way out) costs as much as several tiles, so it counts as `start` tiles in the list.
+// the accumulators' way out) costs as much as several tiles and counts as
+// kStart tiles in the list.
 //
 // Warps 0-7 are the softmax warps (thread = key x half of the columns), warp 8 issues the TMA copies
 // of 128 x 128-byte pieces into a ring, one thread of warp 9 the products.  S^T is double buffered: the
@@ -77,8 +78,11 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 10 * 32;
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxGrid = 256;
+// Tiles that starting an item counts as.
+constexpr int kStart = 5;
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
-constexpr float kSlack = 6.0f;    // log2 of how far a score may exceed the reference
+constexpr float kSlack = 7.0f;    // log2 of how far a score may exceed the reference, before
+constexpr float kOver = 0.8f;     // this much more: weights end at 2^8.8, E4M3's largest is 448
 constexpr int kScoreCol = 256;    // TMEM: accumulators in columns 0..255, scores after them
 
 // An item that several CTAs share, noted by the CTA that holds its start (`rows` is 0 otherwise).
@@ -101,7 +105,6 @@ struct PagedArgs {
     float *part;    // [slot][row][rank]
     int n_tok, n_seq, nh, rank, rope, n_pages, page_shift, box, max_pages;
     int group;  // tokens per item
-    int start;  // what starting an item costs, in tiles
     int heads_per, head_blocks;
     int slots;
     int q_bf16, out_bf16;
@@ -122,7 +125,8 @@ struct Control {
     uint64_t weights_ready, out_done, q_ready, drain;
     uint32_t tmem;
     int first_off;
-    Item first;
+    Item first;  // of the run
+    Item next;   // after the softmax warps' current one
     long long first_pos;
     long long warp_sum[kThreads / 32];
 };
@@ -504,15 +508,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k < 0 || ((k + 1) % a.group != 0 && k + 1 != it.t)) continue;
             it.tok = k / a.group * a.group;
             item_sizes(a, it);
-            const int units = it.tiles + a.start;
+            const int units = it.tiles + kStart;
             const long long n = static_cast<long long>(units) * a.head_blocks;
             if (pass == 1 && sum <= run_lo && run_lo < sum + n) {
                 const long long at = run_lo - sum;
                 it.block = static_cast<int>(at / units);
-                const int off = max(0, static_cast<int>(at - static_cast<long long>(it.block) * units) - a.start);
+                const int off = max(0, static_cast<int>(at - static_cast<long long>(it.block) * units) - kStart);
                 ctl->first = it;
                 ctl->first_off = off;
-                ctl->first_pos = sum + static_cast<long long>(it.block) * units + a.start + off;
+                ctl->first_pos = sum + static_cast<long long>(it.block) * units + kStart + off;
             }
             sum += n;
         }
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     row = row_next;
                 }
-                pos += n + a.start;
+                pos += n + kStart;
                 off = 0;
                 if (pos < run_hi) {
                     next_item(a, it);
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (first) {
                         left = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                         off = 0;
-                        pos += left + a.start;
+                        pos += left + kStart;
                         if (pos < run_hi) next_item(a, it);
                     }
                     --left;
@@ -732,14 +736,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col = half * 32 + lane;  // the column whose statistics this lane holds
             uint32_t tile = 0, slot = 0, top = 0;
             Owner mine_owner = {};
+            // An item's queries are staged ahead of the previous item's way out, so that the tensor cores
+            // have its first scores ready by then.
+            const auto stage = [&](const Item &next, bool first) {
+                stage_q(a, ctl, smem, item_row0(a, next), item_rows(a, next), tid, first);
+                fence_async_smem();
+                named_bar_sync(3, kSoftmaxWarps * 32);
+                if (lane == 0) mbar_arrive(&ctl->q_ready);
+            };
+            stage(it, true);
             for (long long pos = run_first; pos < run_hi;) {
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                 const int64_t row0 = item_row0(a, it);
                 const int rows = item_rows(a, it);
-                stage_q(a, ctl, smem, row0, rows, tid, pos == run_first);
-                fence_async_smem();
-                named_bar_sync(3, kSoftmaxWarps * 32);
-                if (lane == 0) mbar_arrive(&ctl->q_ready);
+                const bool last = pos + n + kStart >= run_hi;
+                if (tid == 0 && !last) {
+                    Item next = it;
+                    next_item(a, next);
+                    ctl->next = next;
+                }
 
                 // keys that the column's token sees
                 const int lim_col = max(0, min(it.vis, it.kv - it.t + it.tok + 1 +
@@ -749,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint64_t shift[16], sums[16];  // per pair of columns: -(reference + slack); sums of weights
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                    shift[c] = pack2(-kUnset, -kUnset);
+                    shift[c] = 0;
                     sums[c] = 0;
                 }
                 for (int i = off; i < off + n; ++i, ++tile) {
@@ -773,10 +788,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float s[32];
                     wait(&ctl->score_full[tile & 1], (tile >> 1) & 1);
                     tc_fence_after();
-                    // Usually one turn.  When a column exceeds its reference by the slack, a second turn
-                    // takes the plain scores for the columns' maxima, to which all references move up,
-                    // and a third the shifted scores again.
-                    for (int turn = 0;; ++turn) {
+                    // Usually one turn, number 0.  When a column exceeds its reference by the slack, and on
+                    // the first tile, turn 1 takes the plain scores for the columns' maxima, to which all
+                    // references move up, and turn 2 the shifted scores again.
+                    for (int turn = i == off ? 1 : 0;; ++turn) {
                         uint32_t r[32], r_lo[32];
                         tmem_ld32_nowait(at_s, r);
                         tmem_ld32_nowait(at_s + kRows, r_lo);
@@ -804,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float m = s[0];
 #pragma unroll
                             for (int c = 1; c < 32; ++c) m = fmaxf(m, s[c]);
-                            if (!named_bar_any(1 + half, 128, m > 0.f)) break;
+                            if (!named_bar_any(1 + half, 128, m > kOver)) break;
 #pragma unroll
                             for (int c = 0; c < 16; ++c) shift[c] = 0;
                             continue;
@@ -884,6 +899,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 
                 // ------------------------------------------------------------ the segment's end
+                Item next = it;
+                if (!last) {
+                    named_bar_sync(3, kSoftmaxWarps * 32);  // nobody reads the row scales any more
+                    next = ctl->next;
+                    stage(next, false);
+                }
                 wait(&ctl->out_done, (tile - 1) & 1);
                 tc_fence_after();
                 // The weights' shared memory is free: the four warps' sums meet there, in a fixed order.
@@ -942,10 +963,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_before();
-                named_bar_sync(3, kSoftmaxWarps * 32);  // the scratch and the row scales are free again
-                pos += n + a.start;
+                named_bar_sync(3, kSoftmaxWarps * 32);  // the scratch is free again, everyone has `next`
+                pos += n + kStart;
                 off = 0;
-                if (pos < run_hi) next_item(a, it);
+                it = next;
             }
             if (tid == 0) a.owner[blockIdx.x] = mine_owner;
         }
@@ -966,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // adds parts w, w + 8, ... and the eight sums are added in warp order.
 constexpr int kCombineWarps = 8;
 constexpr int kCombineThreads = kCombineWarps * 32;
-constexpr int kFewParts = 16;
+constexpr int kFewParts = 32;
 static_assert(kMaxGrid <= kCombineThreads, "a thread looks at one CTA's part");
 
 __device__ __forceinline__ void add_part(float4 &acc, const PagedArgs &a, int64_t slot, int r, int d, float x) {
@@ -1027,8 +1048,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArg
             const float w = ex2(st.x - warp_max(st.x));
             const float total = warp_sum(w * st.y);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = 0; k < parts; ++k) add_part(acc, a, slot_of(k), r, d, __shfl_sync(kFullMask, w, k));
+#pragma unroll 2
+            for (int k0 = 0; k0 < parts; k0 += 4) {  // past the last part: the last again, with weight 0
+#pragma unroll
+                for (int k = k0; k < k0 + 4; ++k) {
+                    const float x = __shfl_sync(kFullMask, w, k);
+                    add_part(acc, a, slot_of(min(k, parts - 1)), r, d, k < parts ? x : 0.f);
+                }
+            }
             store_out(a, (row0 + r) * a.rank + d, acc, total);
         }
         return;
@@ -1203,8 +1230,6 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     a.head_blocks = (nh + kRows - 1) / kRows;
     a.heads_per = (nh + a.head_blocks - 1) / a.head_blocks;
     a.group = a.head_blocks > 1 ? 1 : kRows / nh;
-    // About 20,000 cycles, against about 1,050 for each 128 dims of a tile.
-    a.start = 1 + 2560 / kv_rank;
     a.q_bf16 = q_dtype == MEMQ_BF16;
     a.out_bf16 = out_dtype == MEMQ_BF16;
     a.scale_log2 = scale * 1.4426950408889634f;
