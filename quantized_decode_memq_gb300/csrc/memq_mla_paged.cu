@@ -178,6 +178,11 @@ __device__ __forceinline__ int item_rows(const PagedArgs &a, const Item &it) {
     return a.head_blocks > 1 ? min(a.heads_per, a.nh - it.block * a.heads_per) : min(a.group, it.t - it.tok) * a.nh;
 }
 
+// x / y of non-negative numbers; a 64-bit division costs some 500 cycles.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
+}
+
 // Waits for a barrier phase; after one wait expired, none is made any more (the kernel then runs to
 // its end on whatever is there, and the fault word says so).
 struct Waiter {
@@ -223,45 +228,37 @@ __device__ __forceinline__ uint32_t e4m3_bits(uint32_t a, uint32_t b) {
     return __byte_perm(a << 1, b << 1, 0x7531) | (__byte_perm(a, b, 0xfdb9) & 0x80808080u);
 }
 
-// Byte offset of the eight elements from `e` on of row r in the hi terms; the lo terms are rows 64 to
-// 127 of the same operand, `lo` bytes behind.
-__device__ __forceinline__ int q_unit(const PagedArgs &a, int r, int e, int &lo) {
-    if (e < a.rank) {
-        lo = kRows * 128;
-        return (e >> 7) * (2 * kRows * 128) + swizzled(r, e & 127, 128);
-    }
-    lo = kRows * a.rope;
-    return 2 * a.rank * kRows + swizzled(r, e - a.rank, a.rope);
-}
+// Byte offset of element `e` of row r in the hi terms, and how far behind its lo term lies: the lo terms
+// are rows 64 to 127 of the same operand.
+__device__ __forceinline__ int q_lat_at(int r, int e) { return (e >> 7) * (2 * kRows * 128) + swizzled(r, e & 127, 128); }
+__device__ __forceinline__ int q_pe_at(const PagedArgs &a, int r, int e) { return 2 * a.rank * kRows + swizzled(r, e, a.rope); }
+constexpr int kLatLo = kRows * 128;
 
-// hi and lo terms of eight query elements, as four pairs of f16 in (-1, 1].
-__device__ __forceinline__ void split_unit(uint8_t *hi, uint8_t *lo, const uint32_t (&f)[4]) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        h[k] = (f[k] + 0x00400040u) & 0xff80ff80u;  // to the nearest multiple of three fraction bits
-        l[k] = sub_f16x2(f[k], h[k]) + 0x00400040u;
-    }
-    *reinterpret_cast<uint2 *>(hi) = make_uint2(e4m3_bits(h[0], h[1]), e4m3_bits(h[2], h[3]));
-    *reinterpret_cast<uint2 *>(lo) = make_uint2(e4m3_bits(l[0], l[1]), e4m3_bits(l[2], l[3]));
+// hi and lo terms of four query elements, given as two pairs of f16 in (-1, 1].
+__device__ __forceinline__ void split4(uint32_t f0, uint32_t f1, uint32_t &hi, uint32_t &lo) {
+    const uint32_t h0 = (f0 + 0x00400040u) & 0xff80ff80u, h1 = (f1 + 0x00400040u) & 0xff80ff80u;
+    hi = e4m3_bits(h0, h1);  // to the nearest multiple of three fraction bits
+    lo = e4m3_bits(sub_f16x2(f0, h0) + 0x00400040u, sub_f16x2(f1, h1) + 0x00400040u);
 }
-__device__ __forceinline__ uint32_t scaled_pair(float a, float b, uint64_t by) {
-    const float2 x = unpack2(mul2(pack2(a, b), by));
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t a, uint32_t b, uint64_t by) {
+    const float2 x = unpack2(mul2(bits2(a, b), by));
     return f32x2_to_f16x2(x.x, x.y);
 }
-__device__ __forceinline__ void split_bf16(uint8_t *hi, uint8_t *lo, uint2 a, uint2 b, uint64_t by) {
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
-    uint32_t f[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = scaled_pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u), by);
-    split_unit(hi, lo, f);
+__device__ __forceinline__ uint32_t scaled_bf16(uint32_t w, uint64_t by) { return scaled_pair(w << 16, w & 0xffff0000u, by); }
+
+// Eight bf16, parked in the places of their terms -> the terms.
+__device__ __forceinline__ void split_parked(uint8_t *hi, uint8_t *lo, uint64_t by) {
+    uint2 *h = reinterpret_cast<uint2 *>(hi), *l = reinterpret_cast<uint2 *>(lo);
+    const uint2 w0 = *h, w1 = *l;
+    uint2 th, tl;
+    split4(scaled_bf16(w0.x, by), scaled_bf16(w0.y, by), th.x, tl.x);
+    split4(scaled_bf16(w1.x, by), scaled_bf16(w1.y, by), th.y, tl.y);
+    *h = th;
+    *l = tl;
 }
-__device__ __forceinline__ void split_f32(uint8_t *hi, uint8_t *lo, uint4 a, uint4 b, uint64_t by) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t f[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = scaled_pair(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]), by);
-    split_unit(hi, lo, f);
+__device__ __forceinline__ void split_f32(uint8_t *hi, uint8_t *lo, uint4 v, uint64_t by) {
+    split4(scaled_pair(v.x, v.y, by), scaled_pair(v.z, v.w, by), *reinterpret_cast<uint32_t *>(hi),
+           *reinterpret_cast<uint32_t *>(lo));
 }
 
 // Maxima of |x| as bits: infinities and NaN lie above all numbers.
@@ -274,136 +271,174 @@ __device__ __forceinline__ uint32_t max_f32(uint32_t m, uint4 v) {
     return max(max(m, v.x & 0x7fffffffu), max(v.y & 0x7fffffffu, max(v.z & 0x7fffffffu, v.w & 0x7fffffffu)));
 }
 
-// The 64 query rows of an item -> their 8-bit terms and scales in shared memory; rows past `rows` are
-// zeros.  Four threads serve a row, in units of eight elements, in two passes, for the row's maximum
-// comes first.  A unit of bf16 queries fills the 8 + 8 bytes of its terms, so the first pass parks it
-// there and the second splits it in place; f32 queries are read a second time, from L2.  All of a bf16
-// row's loads are out at once and the code stays short: unrolled over registers it was half the
-// kernel, and fetching it took longer than running it.  On the first item the producer starts its
-// copies when the first loads are out; behind a ring of cache rows in the memory's queues they took
-// 10 us and more.  Returns the bits of the thread's maximum, as bf16.
-__device__ __forceinline__ uint32_t park_bf16(const PagedArgs &a, uint8_t *smem, int64_t row, bool live, int r, int q,
-                                              const int (&at)[4], bool first) {
-    const int pieces = a.rank / 128;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 v[4][4], w[4];
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q_lat) + row * a.rank) + q;
-    const uint4 *pe = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q_pe) + row * a.rope) + q;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[c][j] = live && c < pieces ? __ldcg(src + c * 16 + j * 4) : zero;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = live && j * 32 < a.rope ? __ldcg(pe + j * 4) : zero;
-    if (first) named_bar_arrive(4, kSoftmaxWarps * 32 + 32);
-    __nv_bfloat162 top = __float2bfloat162_rn(0.f);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (c < pieces) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                top = max_bf16(top, v[c][j]);
-                uint8_t *hi = smem + c * (2 * kRows * 128) + at[j];
-                *reinterpret_cast<uint2 *>(hi) = make_uint2(v[c][j].x, v[c][j].y);
-                *reinterpret_cast<uint2 *>(hi + kRows * 128) = make_uint2(v[c][j].z, v[c][j].w);
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j * 32 < a.rope) {
-            top = max_bf16(top, w[j]);
-            int lo;
-            uint8_t *hi = smem + q_unit(a, r, a.rank + j * 32 + q * 8, lo);
-            *reinterpret_cast<uint2 *>(hi) = make_uint2(w[j].x, w[j].y);
-            *reinterpret_cast<uint2 *>(hi + lo) = make_uint2(w[j].z, w[j].w);
-        }
-    }
-    const uint32_t t = *reinterpret_cast<const uint32_t *>(&top);
-    return max(t & 0x7fffu, (t >> 16) & 0x7fffu);
+// What a row's largest |x| (its upper 16 bits) makes of it: 2^e with max / 2^e in [1/2, 1) is divided out.
+// Tiny rows keep a normal reciprocal; a row that is not finite, or past 2^126, gets a NaN scale, and
+// what its codes hold then does not matter to the others.
+__device__ __forceinline__ uint64_t row_factor(uint32_t top, float &scale) {
+    const int e = min(max(static_cast<int>(top >> 7), 32), 252);
+    scale = top < 0x7e80u ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
+    const float inv = __uint_as_float(static_cast<uint32_t>(253 - e) << 23);
+    return pack2(inv, inv);
+}
+__device__ __forceinline__ uint32_t max_of8(uint32_t v) {  // over the 8 lanes of a row
+    v = max(v, __shfl_xor_sync(kFullMask, v, 1));
+    v = max(v, __shfl_xor_sync(kFullMask, v, 2));
+    return max(v, __shfl_xor_sync(kFullMask, v, 4));
 }
 
-__device__ __forceinline__ uint32_t top_f32(const PagedArgs &a, int64_t row, bool live, int q, bool first) {
+// The 64 query rows of an item -> their 8-bit terms and scales in shared memory; rows past `rows` are
+// zeros.  Eight lanes read 128 consecutive bytes of a row; a lane serves rows r and r + 4.  Two passes,
+// for the row's maximum comes first.  Eight bf16 fill the 8 + 8 bytes of their terms, so the first pass
+// parks them there and the second splits them in place; f32 queries are read a second time, from L2.
+// Many loads are out at once and the code stays short: unrolled over registers it was half the kernel,
+// and fetching it took longer than running it.  On the first item the producer starts its copies when
+// the first loads are out; behind a ring of cache rows in the memory's queues they took 10 us and more.
+__device__ __forceinline__ void stage_bf16(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows, int r,
+                                           int q, bool first) {
     const int pieces = a.rank / 128;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_lat) + row * a.rank) + 2 * q;
-    const uint4 *pe = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_pe) + row * a.rope) + 2 * q;
-    uint32_t top = 0;
+    uint4 v[2][4][2], w[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const bool live = r + 4 * k < rows;
+        const int64_t row = row0 + r + 4 * k;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q_lat) + row * a.rank) + q;
+        const uint4 *pe = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q_pe) + row * a.rope) + q;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) v[k][c][j] = live && c < pieces ? __ldcg(src + c * 16 + j * 8) : zero;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[k][j] = live && (q + 8 * j) * 8 < a.rope ? __ldcg(pe + j * 8) : zero;
+    }
+    if (first) named_bar_arrive(4, kSoftmaxWarps * 32 + 32);
+    uint64_t by[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int rk = r + 4 * k;
+        __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint8_t *at = smem + swizzled(rk, (q + 8 * j) * 8, 128);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c < pieces) {
+                    top = max_bf16(top, v[k][c][j]);
+                    uint8_t *hi = at + c * (2 * kRows * 128);
+                    *reinterpret_cast<uint2 *>(hi) = make_uint2(v[k][c][j].x, v[k][c][j].y);
+                    *reinterpret_cast<uint2 *>(hi + kLatLo) = make_uint2(v[k][c][j].z, v[k][c][j].w);
+                }
+            }
+            if ((q + 8 * j) * 8 < a.rope) {
+                top = max_bf16(top, w[k][j]);
+                uint8_t *hi = smem + q_pe_at(a, rk, (q + 8 * j) * 8);
+                *reinterpret_cast<uint2 *>(hi) = make_uint2(w[k][j].x, w[k][j].y);
+                *reinterpret_cast<uint2 *>(hi + kRows * a.rope) = make_uint2(w[k][j].z, w[k][j].w);
+            }
+        }
+        const uint32_t t = *reinterpret_cast<const uint32_t *>(&top);
+        float scale;
+        by[k] = row_factor(max_of8(max(t & 0x7fffu, (t >> 16) & 0x7fffu)), scale);
+        if (q == 0) ctl->row_scale[rk] = scale;
+    }
+    int at[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) at[k][j] = swizzled(r + 4 * k, (q + 8 * j) * 8, 128);
 #pragma unroll 1
-    for (int c = 0; c < pieces; c += 2) {  // two pieces at a time
+    for (int c = 0; c < pieces; ++c) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint8_t *hi = smem + c * (2 * kRows * 128) + at[k][j];
+                split_parked(hi, hi + kLatLo, by[k]);
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        for (int u = q; u * 8 < a.rope; u += 8) {
+            uint8_t *hi = smem + q_pe_at(a, r + 4 * k, u * 8);
+            split_parked(hi, hi + kRows * a.rope, by[k]);
+        }
+}
+
+__device__ __forceinline__ void stage_f32(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows, int r,
+                                          int q, bool first) {
+    const int pieces = a.rank / 128;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 *src[2], *pe[2];
+    bool live[2];
+    uint32_t top[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        live[k] = r + 4 * k < rows;
+        const int64_t row = row0 + r + 4 * k;
+        src[k] = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_lat) + row * a.rank) + q;
+        pe[k] = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_pe) + row * a.rope) + q;
+    }
+#pragma unroll 1
+    for (int c = 0; c < pieces; c += 2) {
         uint4 v[2][8];
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[p][j] = live && c + p < pieces ? __ldcg(src + (c + p) * 32 + (j >> 1) * 8 + (j & 1)) : zero;
+            for (int j = 0; j < 8; ++j) v[k][j] = live[k] && c + (j >> 2) < pieces ? __ldcg(src[k] + c * 32 + j * 8) : zero;
         if (first) named_bar_arrive(4, kSoftmaxWarps * 32 + 32);
         first = false;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = max_f32(top, v[p][j]);
+            for (int j = 0; j < 8; ++j) top[k] = max_f32(top[k], v[k][j]);
     }
-    if (live)
-        for (int j = 0; j < a.rope / 32; ++j) top = max_f32(max_f32(top, __ldcg(pe + j * 8)), __ldcg(pe + j * 8 + 1));
-    return top >> 16;
+    for (int u = q; u * 4 < a.rope; u += 8) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (live[k]) top[k] = max_f32(top[k], __ldcg(pe[k] + (u - q)));
+    }
+    uint64_t by[2];
+    uint4 v[2][4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float scale;
+        by[k] = row_factor(max_of8(top[k]) >> 16, scale);
+        if (q == 0) ctl->row_scale[r + 4 * k] = scale;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[k][j] = live[k] ? __ldcg(src[k] + j * 8) : zero;
+    }
+#pragma unroll 1
+    for (int c = 0; c < pieces; ++c) {
+        uint4 next[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                next[k][j] = live[k] && c + 1 < pieces ? __ldcg(src[k] + (c + 1) * 32 + j * 8) : zero;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint8_t *hi = smem + q_lat_at(r + 4 * k, c * 128 + (q + 8 * j) * 4);
+                split_f32(hi, hi + kLatLo, v[k][j], by[k]);
+                v[k][j] = next[k][j];
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        for (int u = q; u * 4 < a.rope; u += 8) {
+            uint8_t *hi = smem + q_pe_at(a, r + 4 * k, u * 4);
+            split_f32(hi, hi + kRows * a.rope, live[k] ? __ldcg(pe[k] + (u - q)) : zero, by[k]);
+        }
 }
 
 __device__ __forceinline__ void stage_q(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows,
                                         int tid, bool first) {
-    const int r = tid >> 2, q = tid & 3, pieces = a.rank / 128;
-    const int64_t row = row0 + r;
-    const bool live = r < rows;
-    int at[4];  // of the thread's units in a piece
-#pragma unroll
-    for (int j = 0; j < 4; ++j) at[j] = swizzled(r, j * 32 + q * 8, 128);
-    uint32_t top = a.q_bf16 ? park_bf16(a, smem, row, live, r, q, at, first) : top_f32(a, row, live, q, first);
-    top = max(top, __shfl_xor_sync(kFullMask, top, 1));
-    top = max(top, __shfl_xor_sync(kFullMask, top, 2));
-    // 2^e with max / 2^e in [1/2, 1); tiny rows keep a normal reciprocal, rows past 2^126 have none
-    const bool fin = top < 0x7e80u;
-    const int e2 = min(max(static_cast<int>(top >> 7), 32), 252);
-    const float inv = __uint_as_float(static_cast<uint32_t>(253 - e2) << 23);
-    const uint64_t by = pack2(inv, inv);
-    if (q == 0) ctl->row_scale[r] = fin ? __uint_as_float(static_cast<uint32_t>(e2 - 7) << 23) : NAN;
-    // A row that is not finite has a NaN scale; what its codes hold does not matter to the others.
-    if (a.q_bf16) {
-#pragma unroll 1
-        for (int c = 0; c < pieces; ++c) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint8_t *hi = smem + c * (2 * kRows * 128) + at[j], *lo = hi + kRows * 128;
-                split_bf16(hi, lo, *reinterpret_cast<const uint2 *>(hi), *reinterpret_cast<const uint2 *>(lo), by);
-            }
-        }
-#pragma unroll 1
-        for (int j = 0; j < a.rope / 32; ++j) {
-            int off;
-            uint8_t *hi = smem + q_unit(a, r, a.rank + j * 32 + q * 8, off), *lo = hi + off;
-            split_bf16(hi, lo, *reinterpret_cast<const uint2 *>(hi), *reinterpret_cast<const uint2 *>(lo), by);
-        }
-    } else {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_lat) + row * a.rank) + 2 * q;
-        const uint4 *pe = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_pe) + row * a.rope) + 2 * q;
-#pragma unroll 1
-        for (int c = 0; c < pieces; ++c) {
-            uint4 v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = live ? __ldcg(src + c * 32 + (j >> 1) * 8 + (j & 1)) : zero;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint8_t *hi = smem + c * (2 * kRows * 128) + at[j];
-                split_f32(hi, hi + kRows * 128, v[2 * j], v[2 * j + 1], by);
-            }
-        }
-#pragma unroll 1
-        for (int j = 0; j < a.rope / 32; ++j) {
-            int off;
-            uint8_t *hi = smem + q_unit(a, r, a.rank + j * 32 + q * 8, off);
-            split_f32(hi, hi + off, live ? __ldcg(pe + j * 8) : zero, live ? __ldcg(pe + j * 8 + 1) : zero, by);
-        }
-    }
+    const int r = (tid >> 5) * 8 + ((tid >> 3) & 3), q = tid & 7;
+    if (a.q_bf16)
+        stage_bf16(a, ctl, smem, row0, rows, r, q, first);
+    else
+        stage_f32(a, ctl, smem, row0, rows, r, q, first);
 }
 
 // Sum over the 32 lanes of v[c], for every c, in lane c (a fixed tree).
@@ -511,12 +546,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int units = it.tiles + kStart;
             const long long n = static_cast<long long>(units) * a.head_blocks;
             if (pass == 1 && sum <= run_lo && run_lo < sum + n) {
-                const long long at = run_lo - sum;
-                it.block = static_cast<int>(at / units);
-                const int off = max(0, static_cast<int>(at - static_cast<long long>(it.block) * units) - kStart);
+                const int at = static_cast<int>(run_lo - sum);  // less than 2^25 units x 16 blocks
+                it.block = at / units;
+                const int off = max(0, at - it.block * units - kStart);
                 ctl->first = it;
                 ctl->first_off = off;
-                ctl->first_pos = sum + static_cast<long long>(it.block) * units + kStart + off;
+                ctl->first_pos = sum + it.block * units + kStart + off;
             }
             sum += n;
         }
@@ -535,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w < warp) before += ctl->warp_sum[w];
                 total += ctl->warp_sum[w];
             }
-            per = (total + gridDim.x - 1) / gridDim.x;
+            per = quotient(total + gridDim.x - 1, gridDim.x);
             run_lo = blockIdx.x * per;
             run_hi = min(total, run_lo + per);
         }
@@ -736,22 +771,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col = half * 32 + lane;  // the column whose statistics this lane holds
             uint32_t tile = 0, slot = 0, top = 0;
             Owner mine_owner = {};
-            // An item's queries are staged ahead of the previous item's way out, so that the tensor cores
-            // have its first scores ready by then.
-            const auto stage = [&](const Item &next, bool first) {
-                stage_q(a, ctl, smem, item_row0(a, next), item_rows(a, next), tid, first);
-                fence_async_smem();
-                named_bar_sync(3, kSoftmaxWarps * 32);
-                if (lane == 0) mbar_arrive(&ctl->q_ready);
-            };
-            stage(it, true);
-            for (long long pos = run_first; pos < run_hi;) {
-                const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
-                const int64_t row0 = item_row0(a, it);
-                const int rows = item_rows(a, it);
-                const bool last = pos + n + kStart >= run_hi;
-                if (tid == 0 && !last) {
-                    Item next = it;
+            // The segment whose accumulators are in TMEM: item `it`, tiles off .. off + n - 1.
+            Item next = it;
+            long long pos = run_first;
+            int n = 0;
+            bool have = false, more = true;  // a segment is complete; another one follows
+            float ref = kUnset;              // of column `col`
+            uint64_t sums[16];               // per pair of columns: sums of weights
+            for (;;) {
+                // The next item's queries are staged ahead of the accumulators' way out, so that the
+                // tensor cores have its first scores ready by then.
+                if (more) {
+                    if (have) {
+                        named_bar_sync(3, kSoftmaxWarps * 32);  // nobody reads the row scales any more
+                        next = ctl->next;
+                    }
+                    stage_q(a, ctl, smem, item_row0(a, next), item_rows(a, next), tid, !have);
+                    fence_async_smem();
+                    named_bar_sync(3, kSoftmaxWarps * 32);
+                    if (lane == 0) mbar_arrive(&ctl->q_ready);
+                }
+                if (have) {
+                    const int64_t row0 = item_row0(a, it);
+                    const int rows = item_rows(a, it);
+                    wait(&ctl->out_done, (tile - 1) & 1);
+                    tc_fence_after();
+                    // The weights' shared memory is free: the four warps' sums meet there, in a fixed order.
+                    float *scratch = reinterpret_cast<float *>(weights);
+                    float part[32];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 u = unpack2(sums[c]);
+                        part[2 * c] = u.x;
+                        part[2 * c + 1] = u.y;
+                    }
+                    scratch[wq * kRows + col] = column_sums(part, lane);
+                    named_bar_sync(1 + half, 128);
+                    const float sum = (scratch[col] + scratch[kRows + col]) +
+                                      (scratch[2 * kRows + col] + scratch[3 * kRows + col]);
+                    const bool whole = off == 0 && n == it.tiles;
+                    const int here = 2 * static_cast<int>(blockIdx.x) + (pos == run_first ? 0 : 1);
+                    const float scale_col = whole ? (sum == 0.f ? 0.f : __fdiv_rn(1.f, sum)) : 1.f;
+                    float norm[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) norm[c] = __shfl_sync(kFullMask, scale_col, c);
+                    if (!whole) {
+                        if (wq == 0) a.stats[here * kRows + col] = make_float2(ref, sum);
+                        if (off == 0 && tid == 0) {  // this CTA holds the item's start: it names its parts
+                            mine_owner.row0 = row0;
+                            mine_owner.rows = static_cast<unsigned char>(rows);
+                            mine_owner.tail = static_cast<unsigned char>(here & 1);
+                            mine_owner.last = static_cast<short>(quotient(pos + it.tiles - 1, per));
+                        }
+                    }
+#pragma unroll 1
+                    for (int p = 0; p < pieces; ++p) {
+                        float o[32];
+                        tmem_ld32(tmem + lane_base + p * kRows + half * 32, o);
+                        const int dim = p * 128 + key;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] *= norm[c];
+                        if (!whole || !a.out_bf16) {
+                            float *dst = whole ? static_cast<float *>(a.out) + row0 * a.rank
+                                               : a.part + static_cast<int64_t>(here) * kRows * a.rank;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (half * 32 + c < rows) dst[(half * 32 + c) * a.rank + dim] = o[c];
+                        } else {
+                            // lanes 2 k and 2 k + 1 hold neighbouring dims: each stores one pair of one column
+                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + row0 * a.rank + (dim & ~1);
+                            const int odd = lane & 1;
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) {
+                                const float got = __shfl_xor_sync(kFullMask, odd ? o[c] : o[c + 1], 1);
+                                const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, o[c + 1])
+                                                             : __floats2bfloat162_rn(o[c], got);
+                                const int r = half * 32 + c + odd;
+                                if (r < rows) *reinterpret_cast<__nv_bfloat162 *>(dst + r * a.rank) = v;
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    named_bar_sync(3, kSoftmaxWarps * 32);  // the scratch is free again
+                    pos += n + kStart;
+                    off = 0;
+                }
+                if (!more) break;
+                it = next;
+                n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
+                have = true;
+                more = pos + n + kStart < run_hi;
+                if (tid == 0 && more) {
                     next_item(a, next);
                     ctl->next = next;
                 }
@@ -760,8 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int lim_col = max(0, min(it.vis, it.kv - it.t + it.tok + 1 +
                                                            (a.head_blocks > 1 ? 0 : min(col / a.nh, a.group - 1))));
                 const int lim_min = max(0, min(it.vis, it.kv - it.t + it.tok + 1));
-                float ref = kUnset;  // of column `col`
-                uint64_t shift[16], sums[16];  // per pair of columns: -(reference + slack); sums of weights
+                ref = kUnset;
+                uint64_t shift[16];  // per pair of columns: -(reference + slack)
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     shift[c] = 0;
@@ -897,76 +1007,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->weights_ready);
                 }
-
-                // ------------------------------------------------------------ the segment's end
-                Item next = it;
-                if (!last) {
-                    named_bar_sync(3, kSoftmaxWarps * 32);  // nobody reads the row scales any more
-                    next = ctl->next;
-                    stage(next, false);
-                }
-                wait(&ctl->out_done, (tile - 1) & 1);
-                tc_fence_after();
-                // The weights' shared memory is free: the four warps' sums meet there, in a fixed order.
-                float *scratch = reinterpret_cast<float *>(weights);
-                float part[32];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const float2 u = unpack2(sums[c]);
-                    part[2 * c] = u.x;
-                    part[2 * c + 1] = u.y;
-                }
-                scratch[wq * kRows + col] = column_sums(part, lane);
-                named_bar_sync(1 + half, 128);
-                const float sum = (scratch[col] + scratch[kRows + col]) +
-                                  (scratch[2 * kRows + col] + scratch[3 * kRows + col]);
-                const bool whole = off == 0 && n == it.tiles;
-                const int here = 2 * static_cast<int>(blockIdx.x) + (pos == run_first ? 0 : 1);
-                const float scale_col = whole ? (sum == 0.f ? 0.f : __fdiv_rn(1.f, sum)) : 1.f;
-                float norm[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) norm[c] = __shfl_sync(kFullMask, scale_col, c);
-                if (!whole) {
-                    if (wq == 0) a.stats[here * kRows + col] = make_float2(ref, sum);
-                    if (off == 0 && tid == 0) {  // this CTA holds the item's start: it names its parts
-                        mine_owner.row0 = row0;
-                        mine_owner.rows = static_cast<unsigned char>(rows);
-                        mine_owner.tail = static_cast<unsigned char>(here & 1);
-                        mine_owner.last = static_cast<short>((pos + it.tiles - 1) / per);
-                    }
-                }
-#pragma unroll 1
-                for (int p = 0; p < pieces; ++p) {
-                    float o[32];
-                    tmem_ld32(tmem + lane_base + p * kRows + half * 32, o);
-                    const int dim = p * 128 + key;
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] *= norm[c];
-                    if (!whole || !a.out_bf16) {
-                        float *dst = whole ? static_cast<float *>(a.out) + row0 * a.rank
-                                           : a.part + static_cast<int64_t>(here) * kRows * a.rank;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (half * 32 + c < rows) dst[(half * 32 + c) * a.rank + dim] = o[c];
-                    } else {
-                        // lanes 2 k and 2 k + 1 hold neighbouring dims: each stores one pair of one column
-                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + row0 * a.rank + (dim & ~1);
-                        const int odd = lane & 1;
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float got = __shfl_xor_sync(kFullMask, odd ? o[c] : o[c + 1], 1);
-                            const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, o[c + 1])
-                                                         : __floats2bfloat162_rn(o[c], got);
-                            const int r = half * 32 + c + odd;
-                            if (r < rows) *reinterpret_cast<__nv_bfloat162 *>(dst + r * a.rank) = v;
-                        }
-                    }
-                }
-                tc_fence_before();
-                named_bar_sync(3, kSoftmaxWarps * 32);  // the scratch is free again, everyone has `next`
-                pos += n + kStart;
-                off = 0;
-                it = next;
             }
             if (tid == 0) a.owner[blockIdx.x] = mine_owner;
         }
@@ -990,8 +1030,10 @@ constexpr int kCombineThreads = kCombineWarps * 32;
 constexpr int kFewParts = 32;
 static_assert(kMaxGrid <= kCombineThreads, "a thread looks at one CTA's part");
 
-__device__ __forceinline__ void add_part(float4 &acc, const PagedArgs &a, int64_t slot, int r, int d, float x) {
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part + (slot * kRows + r) * a.rank + d));
+__device__ __forceinline__ float4 load_part(const PagedArgs &a, int64_t slot, int r, int d) {
+    return __ldcg(reinterpret_cast<const float4 *>(a.part + (slot * kRows + r) * a.rank + d));
+}
+__device__ __forceinline__ void fma4(float4 &acc, float4 v, float x) {
     acc.x = fmaf(v.x, x, acc.x);
     acc.y = fmaf(v.y, x, acc.y);
     acc.z = fmaf(v.z, x, acc.z);
@@ -1053,7 +1095,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArg
 #pragma unroll
                 for (int k = k0; k < k0 + 4; ++k) {
                     const float x = __shfl_sync(kFullMask, w, k);
-                    add_part(acc, a, slot_of(min(k, parts - 1)), r, d, k < parts ? x : 0.f);
+                    fma4(acc, load_part(a, slot_of(min(k, parts - 1)), r, d), k < parts ? x : 0.f);
                 }
             }
             store_out(a, (row0 + r) * a.rank + d, acc, total);
@@ -1064,6 +1106,10 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArg
         const int r = unit / pieces, d = (unit - r * pieces) * 128 + lane * 4;
         float2 st = make_float2(kUnset, 0.f);
         if (tid < parts) st = __ldcg(a.stats + slot_of(tid) * kRows + r);
+        // the first parts come in while the weights are formed
+        float4 early[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) early[k] = load_part(a, slot_of(min(warp + k * kCombineWarps, parts - 1)), r, d);
         const float wm = warp_max(st.x);
         if (lane == 0) red[0][warp] = wm;
         __syncthreads();
@@ -1077,8 +1123,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const PagedArg
         float total = 0.f;
         for (int k = 0; k < kCombineWarps; ++k) total += red[1][k];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int part = warp + k * kCombineWarps;
+            fma4(acc, early[k], part < parts ? weight[part] : 0.f);
+        }
 #pragma unroll 8
-        for (int k = warp; k < parts; k += kCombineWarps) add_part(acc, a, slot_of(k), r, d, weight[k]);
+        for (int k = warp + 8 * kCombineWarps; k < parts; k += kCombineWarps)
+            fma4(acc, load_part(a, slot_of(k), r, d), weight[k]);
         sums[warp][lane] = acc;
         __syncthreads();
         if (warp == 0) {
