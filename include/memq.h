@@ -365,7 +365,7 @@ int memq_mla_cache_read(int dtype, const uint8_t *cache, const float *scales, co
  * A token that sees no row (kv_len[b] = 0, or fewer rows than new tokens) gets zeros.  Rows of q and
  * out that belong to no sequence (before cu_q[0], from cu_q[n_seq] on) are neither read nor written.
  *   q_dtype      a memq_dtype: the type of q_lat [n_tok][nh][kv_rank] and q_pe [n_tok][nh][d_rope]
- *                (device, aligned to four elements; q_pe may be NULL when d_rope == 0)
+ *                (device, 16-byte aligned; q_pe may be NULL when d_rope == 0)
  *   cache, scales  the pool (scales 16-byte aligned); codes of visible rows are not NaN (what
  *                memq_mla_cache_append writes); rows past a sequence's end may hold anything
  *   block_table  device int32 [n_seq][max_pages]; entries past a sequence's last page are not read
@@ -379,13 +379,15 @@ int memq_mla_cache_read(int dtype, const uint8_t *cache, const float *scales, co
  *                scale finite.  n_tok == 0 or n_seq == 0 is a no-op that accepts NULL pointers.
  * The lengths are read on the device only, so a captured call serves other lengths of the same
  * arrays.  A kv_len outside [0, max_pages * page_size] is clamped, a page index outside the pool
- * reads page 0, and cu_q outside [0, n_tok] is clamped: bit 5 of the device fault word is set for the
- * first two, and the outputs of the sequence are invalid.
- * Numerics: codes are used exactly; a query element with 8 significant bits (a bf16 value exactly
- * down to 2^-10 of the row's largest element, an absolute 2^-18 of it below); a softmax weight within
- * 2^-7 of its value (2^-10 rms) and 2^-20 of the row's largest weight, 2^-8 past it at most; products
- * exact, sums, maxima and normalisation in f32.  Results do not depend on timing; they depend on how
- * the tiles are split, so the same row may differ in the last bits between batches.
+ * reads page 0, and cu_q outside [0, n_tok] is clamped: bit 5 of the device fault word is set, as for
+ * a cu_q that descends, and the outputs of those sequences are invalid (nothing outside the arrays is
+ * read or written).
+ * Numerics: codes are used exactly; a query element within 1.13 x 2^-8 of its value (a bf16 value
+ * exactly) down to 2^-10 of the row's largest element, within 2^-17 of that below; a softmax weight
+ * (times its row's scale) within 1.07 x 2^-7 of its value (2^-10 rms) and 2^-14 of the largest of its
+ * query; products exact, sums, maxima and normalisation in f32.  A query row that is not finite, or has an element past 2^126, gives NaN.
+ * Results do not depend on timing; they depend on how the tiles are split, so the same row may differ
+ * in the last bits between batches.
  * Errors: MEMQ_ERR_SHAPE (also a workspace too small), MEMQ_ERR_NULL, MEMQ_ERR_ALIGN,
  * MEMQ_ERR_LAUNCH.
  */

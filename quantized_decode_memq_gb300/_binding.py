@@ -211,6 +211,7 @@ def memq_add_rmsnorm_q8_1(x: torch.Tensor, res: torch.Tensor, w: torch.Tensor, e
         z = torch.empty((rows, ncols), dtype=torch.float32, device=x.device)
     h2 = h if h.dim() == 2 else h.reshape(1, -1)
     _cuda("h", h2, torch.float32, (rows, ncols))
+    _here("memq_add_rmsnorm_q8_1", x2, r2, w, h2, qs, d, z)
     _cuda("qs", qs, torch.int8, (rows, ncols))
     _cuda("d", d, torch.float32, (rows, ncols // 32))
     if z is not None:
@@ -601,7 +602,15 @@ def _float(name: str, t: torch.Tensor, dtype=None, shape=None):
     return kind
 
 
-def _pool(fn: str, cache, scales, kv_rank=None):
+def _here(fn: str, *tensors):
+    """The call runs on the current device: so must its tensors lie there."""
+    dev = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _pool(fn: str, cache, scales):
     """The paged cache's (width, pages, page_size)."""
     _cuda("cache", cache, torch.uint8)
     if cache.dim() != 3:
@@ -630,6 +639,7 @@ def memq_mla_cache_append(latent: torch.Tensor, k_pe, slots: torch.Tensor, cache
     elif d_rope != 0:
         raise ValueError(f"{fn}: k_pe is required when the cache rows are wider than kv_rank")
     _cuda("slots", slots, torch.int32, (n,))
+    _here(fn, latent, k_pe, slots, cache, scales)
     rc = lib().memq_mla_cache_append(kind, _ptr(latent), _ptr(k_pe), _ptr(slots), _ptr(cache),
                                      _ptr(scales), n, kv_rank, d_rope, pages * page_size,
                                      _stream(stream))
@@ -655,6 +665,7 @@ def memq_mla_cache_read(cache: torch.Tensor, scales: torch.Tensor, slots: torch.
     if out is None:
         out = torch.empty((n, width), dtype=dtype, device=cache.device)
     kind = _float("out", out, None, (n, width))
+    _here(fn, cache, scales, slots, out)
     rc = lib().memq_mla_cache_read(kind, _ptr(cache), _ptr(scales), _ptr(slots), _ptr(out), n,
                                    *_WIDTHS[width], pages * page_size, _stream(stream))
     _check(fn, rc)
@@ -699,6 +710,7 @@ def memq_mla_attn_paged(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, scales: 
     if out is None:
         out = torch.empty((n_tok, nh, kv_rank), dtype=torch.bfloat16, device=q_lat.device)
     o_kind = _float("out", out, None, (n_tok, nh, kv_rank))
+    _here(fn, q_lat, q_pe, cache, scales, block_table, kv_len, cu_q, out, workspace)
     st = _stream(stream)
     if workspace is None:
         need = memq_mla_attn_paged_workspace(kv_rank)

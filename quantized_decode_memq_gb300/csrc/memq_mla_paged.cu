@@ -17,11 +17,11 @@
 // kind::f8f6f4 multiplies 8-bit operands exactly and adds in f32, so the operands that are not
 // codes are sums of two 8-bit terms, each with its own product into the same accumulator (twice
 // the operations at twice the 16-bit rate):
-//   q = 2^e (hi + lo), both E4M3, e per row: 8 significant bits, which hold a bf16 value exactly
-//       down to 2^-10 of the row's largest; below that an absolute 2^-18 of the largest;
-//   p = hi (E4M3) + lo (E5M2), with p in (0, 2^8.8]: a relative 2^-7 at most (about 2^-10 rms), and
-//       an absolute 2^-17, 2^-18 of the reference: E5M2 carries the long tail of small
-//       weights that a second E4M3 term would flush.  Both codes are bit fields of f16 numbers:
+//   q = 2^e (hi + lo), both E4M3, e per row: a relative 2^-8 (a bf16 value exactly) down to 2^-10 of
+//       the row's largest; below that an absolute 2^-17 of the largest;
+//   p = hi (E4M3) + lo (E5M2), with p in (0, 2^8.8] and 2 at the reference: a relative 2^-7 at most
+//       (about 2^-10 rms) down to 2^-6, an absolute 2^-13 and a relative 2^-3 below that, down to
+//       2^-16: E5M2 carries the long tail of small weights that a second E4M3 term would flush.  Both codes are bit fields of f16 numbers:
 //       E4M3 of v is bits 14..7 of f16(v / 256), E5M2 of v the high byte of f16(v), so the split
 //       needs one conversion per pair of weights and integer operations.
 // The key's scale is folded into its weight (p_j = 2^8 exp2(s_j + log2 scales_j - R - 7)), so R, the
@@ -160,8 +160,9 @@ __device__ __forceinline__ void next_item(const PagedArgs &a, Item &it) {
     if (it.tok >= it.t) {
         it.tok = 0;
         do {
-            if (++it.seq >= a.n_seq) {  // past the last sequence: an empty item, never reached
-                it.t = 0;
+            if (++it.seq >= a.n_seq) {  // only if cu_q descends: an item without rows and keys
+                it.seq = a.n_seq;
+                it.t = it.kv = 0;
                 break;
             }
             seq_sizes(a, __ldcg(a.cu_q + it.seq), __ldcg(a.cu_q + it.seq + 1), __ldcg(a.kv_len + it.seq), it);
@@ -175,6 +176,7 @@ __device__ __forceinline__ int64_t item_row0(const PagedArgs &a, const Item &it)
     return (static_cast<int64_t>(it.start) + it.tok) * a.nh + it.block * a.heads_per;
 }
 __device__ __forceinline__ int item_rows(const PagedArgs &a, const Item &it) {
+    if (it.tok >= it.t) return 0;
     return a.head_blocks > 1 ? min(a.heads_per, a.nh - it.block * a.heads_per) : min(a.group, it.t - it.tok) * a.nh;
 }
 
@@ -509,11 +511,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ------------------------------------------------------------------ this CTA's run of tiles
     int32_t *cu = reinterpret_cast<int32_t *>(ring), *kvl = cu + a.n_seq + 1;
-    for (int i = tid; i <= a.n_seq; i += kThreads) cu[i] = __ldcg(a.cu_q + i);
-    for (int i = tid; i < a.n_seq; i += kThreads) {
-        const int kv = __ldcg(a.kv_len + i);
-        kvl[i] = kv;
-        if (kv < 0 || kv > (static_cast<long long>(a.max_pages) << a.page_shift)) atomicOr(&g_paged_fault, kFaultInput);
+    for (int i = tid; i <= a.n_seq; i += kThreads) {
+        const bool seq = i < a.n_seq;
+        const int c0 = __ldcg(a.cu_q + i), c1 = seq ? __ldcg(a.cu_q + i + 1) : a.n_tok;
+        const int kv = seq ? __ldcg(a.kv_len + i) : 0;
+        cu[i] = c0;
+        if (seq) kvl[i] = kv;
+        if (c0 < 0 || c0 > c1 || kv < 0 || kv > (static_cast<long long>(a.max_pages) << a.page_shift))
+            atomicOr(&g_paged_fault, kFaultInput);
     }
     __syncthreads();
     // Thread i counts the tiles of the groups whose last token lies in its slice of the tokens.
@@ -1246,8 +1251,8 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     if (n_pages < 1 || max_pages < 1) return MEMQ_ERR_SHAPE;
     if (!q_lat || (d_rope > 0 && !q_pe) || !cache || !scales || !block_table || !kv_len || !cu_q || !out || !workspace)
         return MEMQ_ERR_NULL;
-    const uintptr_t q_al = q_dtype == MEMQ_F32 ? 16 : 8, o_al = out_dtype == MEMQ_F32 ? 16 : 8;
-    if (misaligned(q_lat, q_al) || (d_rope > 0 && misaligned(q_pe, q_al)) || misaligned(cache, 16) ||
+    const uintptr_t o_al = out_dtype == MEMQ_F32 ? 16 : 8;
+    if (misaligned(q_lat, 16) || (d_rope > 0 && misaligned(q_pe, 16)) || misaligned(cache, 16) ||
         misaligned(scales, 16) || misaligned(block_table, 4) || misaligned(kv_len, 4) || misaligned(cu_q, 4) ||
         misaligned(out, o_al) || misaligned(workspace, 16))
         return MEMQ_ERR_ALIGN;
