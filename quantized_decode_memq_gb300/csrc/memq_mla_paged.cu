@@ -289,7 +289,7 @@ __device__ __forceinline__ uint32_t max_of8(uint32_t v) {  // over the 8 lanes o
 }
 
 // The 64 query rows of an item -> their 8-bit terms and scales in shared memory; rows past `rows` are
-// zeros.  Eight lanes read 128 consecutive bytes of a row; a lane serves rows r and r + 4.  Two passes,
+// zeros.  Eight lanes read 128 consecutive bytes of a row; a lane serves rows r and r + 1.  Two passes,
 // for the row's maximum comes first.  Eight bf16 fill the 8 + 8 bytes of their terms, so the first pass
 // parks them there and the second splits them in place; f32 queries are read a second time, from L2.
 // Many loads are out at once and the code stays short: unrolled over registers it was half the kernel,
@@ -302,8 +302,8 @@ __device__ __forceinline__ void stage_bf16(const PagedArgs &a, Control *ctl, uin
     uint4 v[2][4][2], w[2][2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const bool live = r + 4 * k < rows;
-        const int64_t row = row0 + r + 4 * k;
+        const bool live = r + k < rows;
+        const int64_t row = row0 + r + k;
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q_lat) + row * a.rank) + q;
         const uint4 *pe = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q_pe) + row * a.rope) + q;
 #pragma unroll
@@ -317,7 +317,7 @@ __device__ __forceinline__ void stage_bf16(const PagedArgs &a, Control *ctl, uin
     uint64_t by[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int rk = r + 4 * k;
+        const int rk = r + k;
         __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -347,7 +347,7 @@ __device__ __forceinline__ void stage_bf16(const PagedArgs &a, Control *ctl, uin
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) at[k][j] = swizzled(r + 4 * k, (q + 8 * j) * 8, 128);
+        for (int j = 0; j < 2; ++j) at[k][j] = swizzled(r + k, (q + 8 * j) * 8, 128);
 #pragma unroll 1
     for (int c = 0; c < pieces; ++c) {
 #pragma unroll
@@ -361,7 +361,7 @@ __device__ __forceinline__ void stage_bf16(const PagedArgs &a, Control *ctl, uin
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         for (int u = q; u * 8 < a.rope; u += 8) {
-            uint8_t *hi = smem + q_pe_at(a, r + 4 * k, u * 8);
+            uint8_t *hi = smem + q_pe_at(a, r + k, u * 8);
             split_parked(hi, hi + kRows * a.rope, by[k]);
         }
 }
@@ -375,8 +375,8 @@ __device__ __forceinline__ void stage_f32(const PagedArgs &a, Control *ctl, uint
     uint32_t top[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        live[k] = r + 4 * k < rows;
-        const int64_t row = row0 + r + 4 * k;
+        live[k] = r + k < rows;
+        const int64_t row = row0 + r + k;
         src[k] = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_lat) + row * a.rank) + q;
         pe[k] = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q_pe) + row * a.rope) + q;
     }
@@ -405,7 +405,7 @@ __device__ __forceinline__ void stage_f32(const PagedArgs &a, Control *ctl, uint
     for (int k = 0; k < 2; ++k) {
         float scale;
         by[k] = row_factor(max_of8(top[k]) >> 16, scale);
-        if (q == 0) ctl->row_scale[r + 4 * k] = scale;
+        if (q == 0) ctl->row_scale[r + k] = scale;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[k][j] = live[k] ? __ldcg(src[k] + j * 8) : zero;
     }
@@ -421,7 +421,7 @@ __device__ __forceinline__ void stage_f32(const PagedArgs &a, Control *ctl, uint
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint8_t *hi = smem + q_lat_at(r + 4 * k, c * 128 + (q + 8 * j) * 4);
+                uint8_t *hi = smem + q_lat_at(r + k, c * 128 + (q + 8 * j) * 4);
                 split_f32(hi, hi + kLatLo, v[k][j], by[k]);
                 v[k][j] = next[k][j];
             }
@@ -429,14 +429,16 @@ __device__ __forceinline__ void stage_f32(const PagedArgs &a, Control *ctl, uint
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         for (int u = q; u * 4 < a.rope; u += 8) {
-            uint8_t *hi = smem + q_pe_at(a, r + 4 * k, u * 4);
+            uint8_t *hi = smem + q_pe_at(a, r + k, u * 4);
             split_f32(hi, hi + kRows * a.rope, live[k] ? __ldcg(pe[k] + (u - q)) : zero, by[k]);
         }
 }
 
 __device__ __forceinline__ void stage_q(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows,
                                         int tid, bool first) {
-    const int r = (tid >> 5) * 8 + ((tid >> 3) & 3), q = tid & 7;
+    // rows r and r + 1; the warp's other rows lie 2 and 4 apart, so that the swizzle keeps them off
+    // each other's banks
+    const int r = (tid >> 5) * 8 + ((tid >> 3) & 1) * 4 + ((tid >> 4) & 1) * 2, q = tid & 7;
     if (a.q_bf16)
         stage_bf16(a, ctl, smem, row0, rows, r, q, first);
     else
@@ -533,32 +535,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     long long run_lo = -1, run_hi = 0, per = 0;
-    long long before = 0;
+    long long before = 0, own = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         long long sum = before;  // pass 0: this slice's tiles; pass 1: find the run's first tile
+        if (pass == 1 && (run_lo < before || run_lo >= before + own)) break;
         Item it{};
-        it.seq = seq0;
-        if (tok_lo < tok_hi && it.seq < a.n_seq) seq_sizes(a, cu[it.seq], cu[it.seq + 1], kvl[it.seq], it);
-        for (int j = tok_lo; j < tok_hi && it.seq < a.n_seq; ++j) {
-            while (j >= it.start + it.t && ++it.seq < a.n_seq)
-                seq_sizes(a, cu[it.seq], cu[it.seq + 1], kvl[it.seq], it);
-            if (it.seq >= a.n_seq) break;
-            const int k = j - it.start;
-            if (k < 0 || ((k + 1) % a.group != 0 && k + 1 != it.t)) continue;
-            it.tok = k / a.group * a.group;
-            item_sizes(a, it);
-            const int units = it.tiles + kStart;
-            const long long n = static_cast<long long>(units) * a.head_blocks;
-            if (pass == 1 && sum <= run_lo && run_lo < sum + n) {
-                const int at = static_cast<int>(run_lo - sum);  // less than 2^25 units x 16 blocks
-                it.block = at / units;
-                const int off = max(0, at - it.block * units - kStart);
-                ctl->first = it;
-                ctl->first_off = off;
-                ctl->first_pos = sum + it.block * units + kStart + off;
+        for (it.seq = seq0; it.seq < a.n_seq && cu[it.seq] < tok_hi; ++it.seq) {
+            seq_sizes(a, cu[it.seq], cu[it.seq + 1], kvl[it.seq], it);
+            const int k0 = max(tok_lo - it.start, 0), k1 = min(tok_hi - it.start, it.t);
+            for (it.tok = a.group == 1 ? k0 : k0 / a.group * a.group; min(it.tok + a.group, it.t) <= k1 && it.tok < it.t;
+                 it.tok += a.group) {
+                item_sizes(a, it);
+                const int units = it.tiles + kStart;
+                const long long n = static_cast<long long>(units) * a.head_blocks;
+                if (pass == 1 && sum <= run_lo && run_lo < sum + n) {
+                    const int at = static_cast<int>(run_lo - sum);  // less than 2^25 units x 16 blocks
+                    it.block = a.head_blocks == 1 ? 0 : at / units;
+                    const int off = max(0, at - it.block * units - kStart);
+                    ctl->first = it;
+                    ctl->first_off = off;
+                    ctl->first_pos = sum + it.block * units + kStart + off;
+                }
+                sum += n;
             }
-            sum += n;
         }
         if (pass == 0) {
             long long incl = sum;
@@ -569,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 31) ctl->warp_sum[warp] = incl;
             __syncthreads();
+            own = sum;
             before = incl - sum;
             long long total = 0;
             for (int w = 0; w < kThreads / 32; ++w) {
@@ -950,12 +951,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float shrink = ex2(ref - to), minus = to == kUnset ? -kUnset : -(to + kSlack);
                         ref = to;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
+                        for (int c = 0; c < 16; ++c)
                             shift[c] = pack2(__shfl_sync(kFullMask, minus, 2 * c), __shfl_sync(kFullMask, minus, 2 * c + 1));
-                            sums[c] = mul2(sums[c], pack2(__shfl_sync(kFullMask, shrink, 2 * c),
-                                                          __shfl_sync(kFullMask, shrink, 2 * c + 1)));
-                        }
                         if (i > off) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                sums[c] = mul2(sums[c], pack2(__shfl_sync(kFullMask, shrink, 2 * c),
+                                                              __shfl_sync(kFullMask, shrink, 2 * c + 1)));
                             wait(&ctl->out_done, (tile - 1) & 1);
                             tc_fence_after();
 #pragma unroll 1
