@@ -16,13 +16,6 @@
 // Launched with programmatic stream serialization: it releases the next launch at entry (so a
 // following GEMV can start streaming its weights) and waits for its own predecessors before
 // reading x.
-//
-// memq_add_rmsnorm_q8_1 is the same kernel with the residual stream's addition in front (ADD):
-// each thread adds its slices as it loads them, keeps the sums in the registers that held x and
-// writes them back as the new residual, so everything behind h is bit for bit what
-// memq_rmsnorm_q8_1 gives on h.  It moves 13.1 bytes an element instead of the 21.1 of an addition
-// followed by the producer (12 + 9.1).  h may be x or the residual itself: a thread writes an
-// element after it has read both.
 #include <cmath>
 #include <cstdint>
 
@@ -39,9 +32,9 @@ __device__ __forceinline__ int8_t quant1(float z, float dd) {
 // V float4 slices per thread.  Up to V = 8 the CTA has at most 256 threads and keeps w in
 // registers from the first load; at V = 16 (rows wider than 8192) it has up to 512 threads and
 // reads w only in the second pass, to stay within 128 registers.
-template <int V, bool ADD>
+template <int V>
 __global__ void __launch_bounds__(V <= 8 ? 256 : 512)
-    rmsnorm_q8_1_kernel(const float *x, const float *res, float *h, const float *__restrict__ w,
+    rmsnorm_q8_1_kernel(const float *__restrict__ x, const float *__restrict__ w,
                         float *__restrict__ z, int8_t *__restrict__ qs, float *__restrict__ d,
                         int ncols, float eps) {
     griddep_launch_dependents();
@@ -61,30 +54,16 @@ __global__ void __launch_bounds__(V <= 8 ? 256 : 512)
     const float4 *w4 = reinterpret_cast<const float4 *>(w);
 
     constexpr bool kKeepW = V <= 8;
-    float4 xv[V], wv[kKeepW ? V : 1], rv[ADD ? V : 1];
+    float4 xv[V], wv[kKeepW ? V : 1];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int f = tid + v * nthr;
         if (f < nf4) {
             xv[v] = __ldcg(xr + f);
-            if (ADD) rv[ADD ? v : 0] = __ldcg(reinterpret_cast<const float4 *>(res + row * ncols) + f);
             if (kKeepW) wv[kKeepW ? v : 0] = __ldg(w4 + f);
         } else {
             xv[v] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (kKeepW) wv[kKeepW ? v : 0] = xv[v];
-        }
-    }
-
-    if (ADD) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int f = tid + v * nthr;
-            if (f < nf4) {
-                const float4 a = rv[ADD ? v : 0];
-                xv[v] = make_float4(__fadd_rn(xv[v].x, a.x), __fadd_rn(xv[v].y, a.y),
-                                    __fadd_rn(xv[v].z, a.z), __fadd_rn(xv[v].w, a.w));
-                reinterpret_cast<float4 *>(h + row * ncols)[f] = xv[v];
-            }
         }
     }
 
@@ -143,10 +122,9 @@ __global__ void __launch_bounds__(V <= 8 ? 256 : 512)
     }
 }
 
-template <int V, bool ADD>
-cudaError_t launch_v(const float *x, const float *res, float *h, const float *w, float *z,
-                     int8_t *qs, float *d, int ncols, int rows, float eps, int threads,
-                     cudaStream_t st) {
+template <int V>
+cudaError_t launch_v(const float *x, const float *w, float *z, int8_t *qs, float *d, int ncols,
+                     int rows, float eps, int threads, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -157,21 +135,24 @@ cudaError_t launch_v(const float *x, const float *res, float *h, const float *w,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rmsnorm_q8_1_kernel<V, ADD>, x, res, h, w, z, qs, d, ncols, eps);
+    return cudaLaunchKernelEx(&cfg, rmsnorm_q8_1_kernel<V>, x, w, z, qs, d, ncols, eps);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-template <bool ADD>
-int producer_entry(const float *x, const float *res, float *h, const float *w, float *z,
-                   int8_t *qs, float *d, int64_t ncols, int64_t rows, float eps, void *stream) {
+}  // namespace
+}  // namespace memq
+
+extern "C" int memq_rmsnorm_q8_1(const float *x, const float *w, float *z, int8_t *qs, float *d,
+                                 int64_t ncols, int64_t rows, float eps, void *stream) {
+    using namespace memq;
     if (ncols < 32 || ncols > MEMQ_MAX_NCOLS || (ncols % 32) != 0) return MEMQ_ERR_SHAPE;
     if (rows < 0 || rows > 0x7fffffffLL) return MEMQ_ERR_SHAPE;
     if (!(eps >= 0.0f) || std::isinf(eps)) return MEMQ_ERR_SHAPE;
     if (rows == 0) return MEMQ_OK;  // empty input: nothing to read or write, pointers unused
-    if (!x || !w || !qs || !d || (ADD && (!res || !h))) return MEMQ_ERR_NULL;
+    if (!x || !w || !qs || !d) return MEMQ_ERR_NULL;
     if (!aligned(x, 16) || !aligned(w, 16) || (z && !aligned(z, 16)) || !aligned(qs, 4) ||
-        !aligned(d, 4) || (ADD && (!aligned(res, 16) || !aligned(h, 16))))
+        !aligned(d, 4))
         return MEMQ_ERR_ALIGN;
 
     // V float4 slices per thread: the smallest power of two that keeps the CTA at <= 256
@@ -184,25 +165,11 @@ int producer_entry(const float *x, const float *res, float *h, const float *w, f
     const int nc = static_cast<int>(ncols), nr = static_cast<int>(rows);
     cudaError_t e;
     switch (v) {
-        case 1: e = launch_v<1, ADD>(x, res, h, w, z, qs, d, nc, nr, eps, threads, st); break;
-        case 2: e = launch_v<2, ADD>(x, res, h, w, z, qs, d, nc, nr, eps, threads, st); break;
-        case 4: e = launch_v<4, ADD>(x, res, h, w, z, qs, d, nc, nr, eps, threads, st); break;
-        case 8: e = launch_v<8, ADD>(x, res, h, w, z, qs, d, nc, nr, eps, threads, st); break;
-        default: e = launch_v<16, ADD>(x, res, h, w, z, qs, d, nc, nr, eps, threads, st); break;
+        case 1: e = launch_v<1>(x, w, z, qs, d, nc, nr, eps, threads, st); break;
+        case 2: e = launch_v<2>(x, w, z, qs, d, nc, nr, eps, threads, st); break;
+        case 4: e = launch_v<4>(x, w, z, qs, d, nc, nr, eps, threads, st); break;
+        case 8: e = launch_v<8>(x, w, z, qs, d, nc, nr, eps, threads, st); break;
+        default: e = launch_v<16>(x, w, z, qs, d, nc, nr, eps, threads, st); break;
     }
     return e == cudaSuccess ? MEMQ_OK : MEMQ_ERR_LAUNCH;
-}
-
-}  // namespace
-}  // namespace memq
-
-extern "C" int memq_rmsnorm_q8_1(const float *x, const float *w, float *z, int8_t *qs, float *d,
-                                 int64_t ncols, int64_t rows, float eps, void *stream) {
-    return memq::producer_entry<false>(x, nullptr, nullptr, w, z, qs, d, ncols, rows, eps, stream);
-}
-
-extern "C" int memq_add_rmsnorm_q8_1(const float *x, const float *res, const float *w, float *h,
-                                     float *z, int8_t *qs, float *d, int64_t ncols, int64_t rows,
-                                     float eps, void *stream) {
-    return memq::producer_entry<true>(x, res, h, w, z, qs, d, ncols, rows, eps, stream);
 }
