@@ -602,8 +602,16 @@ def _float(name: str, t: torch.Tensor, dtype=None, shape=None):
     return kind
 
 
+_devices = 0
+
+
 def _here(fn: str, *tensors):
     """The call runs on the current device: so must its tensors lie there."""
+    global _devices
+    if _devices == 0:
+        _devices = torch.cuda.device_count()
+    if _devices == 1:
+        return
     dev = _cur_device() if _cur_device is not None else torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
@@ -714,7 +722,7 @@ def memq_mla_attn_paged(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, scales: 
     st = _stream(stream)
     if workspace is None:
         need = memq_mla_attn_paged_workspace(kv_rank)
-        if stream is None:
+        if stream is None or st == 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
         else:  # memory of the stream that uses it
             with torch.cuda.stream(torch.cuda.ExternalStream(st)):

@@ -127,3 +127,20 @@ def test_binding_refuses_host_tensors(lib):
         m.memq_mla_cache_read(torch.zeros(1, 16, 512, dtype=torch.uint8), torch.zeros(1, 16), None)
     with pytest.raises(ValueError, match="CUDA"):
         m.memq_mla_attn_paged(torch.zeros(1, 1, 512), None, None, None, None, None, None, 1.0)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """With more than one GPU, a tensor that is not on the current one is refused by name."""
+    import quantized_decode_memq_gb300._binding as b
+
+    class On:
+        def __init__(self, index):
+            self.index, self.device = index, f"cuda:{index}"
+
+        def get_device(self):
+            return self.index
+    monkeypatch.setattr(b, "_devices", 2)
+    monkeypatch.setattr(b, "_cur_device", lambda: 0)
+    b._here("f", On(0), None, On(0))
+    with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+        b._here("f", On(0), None, On(1))
