@@ -680,11 +680,18 @@ def memq_mla_cache_read(cache: torch.Tensor, scales: torch.Tensor, slots: torch.
     return out
 
 
+_workspace_bytes = {}  # by (device, kv_rank): fixed by the device's SM count
+
+
 def memq_mla_attn_paged_workspace(kv_rank: int) -> int:
     """Workspace bytes of memq_mla_attn_paged on the current device."""
-    n = lib().memq_mla_attn_paged_workspace(kv_rank)
-    if n < 0:
-        raise ValueError(f"memq_mla_attn_paged: kv_rank must be 128, 256 or 512, got {kv_rank}")
+    key = (_cur_device() if _cur_device is not None else torch.cuda.current_device(), kv_rank)
+    n = _workspace_bytes.get(key)
+    if n is None:
+        n = lib().memq_mla_attn_paged_workspace(kv_rank)
+        if n < 0:
+            raise ValueError(f"memq_mla_attn_paged: kv_rank must be 128, 256 or 512, got {kv_rank}")
+        _workspace_bytes[key] = n
     return n
 
 
@@ -727,10 +734,12 @@ def memq_mla_attn_paged(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, scales: 
         else:  # memory of the stream that uses it
             with torch.cuda.stream(torch.cuda.ExternalStream(st)):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
-    _cuda("workspace", workspace, torch.uint8)
+    else:
+        _cuda("workspace", workspace, torch.uint8)
+        need = workspace.numel()
     rc = lib().memq_mla_attn_paged(q_kind, _ptr(q_lat), _ptr(q_pe), _ptr(cache), _ptr(scales),
                                    _ptr(block_table), _ptr(kv_len), _ptr(cu_q), o_kind, _ptr(out),
-                                   _ptr(workspace), workspace.numel(), n_tok, n_seq, nh, kv_rank,
+                                   _ptr(workspace), need, n_tok, n_seq, nh, kv_rank,
                                    d_rope, pages, page_size, max_pages, scale, st)
     _check(fn, rc)
     return out
