@@ -16,6 +16,9 @@ in one native call.  Around them:
 and ``memq_repack_e4m3[_blk128]_q8_0`` (gemv_e4m3_bench.rs, "QUESTION": E4M3 weights converted to
 Q8_0 once at load).  The MLA decode attention kernels ``memq_mla_absorb_q``,
 ``memq_mla_attn_gathered`` and ``memq_mla_decompress_v``: mla_decode_arm_gate.rs (module doc).
+``memq_add_rmsnorm_q8_1`` puts the residual stream's addition in front of stage 1;
+``memq_mla_cache_append``, ``memq_mla_cache_read`` and ``memq_mla_attn_paged`` keep the latent cache
+in 8 bits and in pages and attend to it, causally, from any number of new tokens.
 """
 from __future__ import annotations
 
