@@ -83,6 +83,7 @@ constexpr int kStart = 5;
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
 constexpr float kSlack = 7.0f;    // log2 of how far a score may exceed the reference, before
 constexpr float kOver = 0.8f;     // this much more: weights end at 2^8.8, E4M3's largest is 448
+constexpr float kLeastScale = 0x1p-64f;  // smaller scales of a row count as this in the outputs
 constexpr int kScoreCol = 256;    // TMEM: accumulators in columns 0..255, scores after them
 
 // An item that several CTAs share, noted by the CTA that holds its start (`rows` is 0 otherwise).
@@ -890,8 +891,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->scale_free[tile & 1]);
                     const bool in = k < it.vis;
-                    if (!in || sj == 0.f) sj = 1.f;  // a zero row's codes are zeros
-                    const float f = sj * a.scale_log2, add = __log2f(sj);
+                    if (!in) sj = 1.f;  // no column sees it
+                    const float f = sj * a.scale_log2;
+                    // The weight of a row that is zero, or nearly, in every column must count in the sums
+                    // and not lift the reference above the others', nor leave f32's range.
+                    if (sj < kLeastScale) sj = kLeastScale;
+                    const float add = __log2f(sj);
                     const uint64_t ff = pack2(f, f), aa = pack2(add, add);
                     // 256 is the weights' common factor; a NaN scale must not reach the columns that do
                     // not see its row

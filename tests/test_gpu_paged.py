@@ -240,6 +240,32 @@ def test_attention_scales_far_apart(memq):
     b.check(memq)
 
 
+@pytest.mark.parametrize("size", [2.0 ** -6, 2.0 ** -12, 2.0 ** -20, 2.0 ** -40])
+@pytest.mark.parametrize("least", [0.0, 1e-42, 1e-37, 1e-30])
+def test_attention_zero_and_tiny_rows_among_small_ones(memq, size, least):
+    """Rows whose scale is zero or nearly weigh as any other, whatever the others' scale is."""
+    b = Batch([(1, 8), (2, 200)], 5, 128, 32, 16, seed=25, row_scale=0.0, q_scale=0.5 / size)
+    b.scales *= np.float32(size)
+    for slot in (0, 3, 7):
+        for page in (b.table[0, 0], b.table[1, 0], b.table[1, 9]):
+            b.scales[page, slot] = least
+            if least == 0:
+                b.codes[page, slot] = 0
+    got = b.run(memq, torch.float32).double().cpu().numpy()
+    want, bound = b.reference(torch.float32)
+    # a scale below 2^-64 counts as 2^-64: up to 448 * 2^-64 off in the output
+    assert np.all(np.abs(got - want) <= bound + 448 * 2.0 ** -64)
+    assert memq.memq_device_fault() == 0
+
+
+def test_attention_over_zero_rows_only(memq):
+    b = Batch([(1, 8), (3, 300)], 3, 128, 0, 16, seed=26)
+    b.scales[:] = 0
+    b.codes[:] = 0
+    for out_type in (torch.float32, torch.bfloat16):
+        assert torch.all(b.run(memq, out_type) == 0)
+
+
 def test_attention_sink_and_long_tail(memq):
     """One key far above thousands that carry half of the sum: small weights must not be flushed."""
     b = Batch([(1, 12000)], 4, 128, 0, 64, seed=10, row_scale=0.0)
