@@ -376,7 +376,8 @@ int memq_mla_cache_read(int dtype, const uint8_t *cache, const float *scales, co
  *                is scratch of this call alone: calls that may run at the same time (two streams, two
  *                graphs) need one each.  Nothing in it has to be initialised or kept.
  *   page_size    a power of two, 16 to 1024;  1 <= nh <= 1024;  n_tok <= 2^24;  n_seq <= 4096;
- *                scale finite.  n_tok == 0 or n_seq == 0 is a no-op that accepts NULL pointers.
+ *                max_pages * page_size <= 2^30;  scale * log2(e) finite.  n_tok == 0 or n_seq == 0 is a
+ *                no-op that accepts NULL pointers; otherwise n_pages >= 1 and max_pages >= 1.
  * The lengths are read on the device only, so a captured call serves other lengths of the same
  * arrays.  A kv_len outside [0, max_pages * page_size] is clamped, a page index outside the pool
  * reads page 0, and cu_q outside [0, n_tok] is clamped: bit 5 of the device fault word is set, as for

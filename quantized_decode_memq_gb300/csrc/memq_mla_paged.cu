@@ -78,6 +78,8 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 10 * 32;
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxGrid = 256;
+constexpr int kMaxCached = 1 << 30;  // rows a sequence: key indices rounded up to a tile stay in 31 bits
+constexpr float kLog2e = 1.4426950408889634f;
 // Tiles that starting an item counts as.
 constexpr int kStart = 5;
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
@@ -1251,8 +1253,8 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
         return MEMQ_ERR_SHAPE;
     if (n_tok < 0 || n_tok > (1 << 24) || n_seq < 0 || n_seq > kMaxSeqs || nh < 1 || nh > 1024 || !rank_ok(kv_rank) ||
         !rope_ok(d_rope) || page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0 || n_pages < 0 ||
-        n_pages > 0x7fffffffLL / page_size || max_pages < 0 || max_pages > 0x7fffffffLL / page_size ||
-        !std::isfinite(scale))
+        n_pages > 0x7fffffffLL / page_size || max_pages < 0 || max_pages > kMaxCached / page_size ||
+        !std::isfinite(scale * kLog2e))
         return MEMQ_ERR_SHAPE;
     if (n_tok == 0 || n_seq == 0) return MEMQ_OK;  // no query rows
     if (n_pages < 1 || max_pages < 1) return MEMQ_ERR_SHAPE;
@@ -1296,7 +1298,7 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     a.group = a.head_blocks > 1 ? 1 : kRows / nh;
     a.q_bf16 = q_dtype == MEMQ_BF16;
     a.out_bf16 = out_dtype == MEMQ_BF16;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale * kLog2e;
     const int fixed = smem_ring_off(kv_rank, d_rope) + smem_tail();
     a.slots = std::min(kMaxSlots, (smem - fixed) / kPiece);
     if (a.slots < kv_rank / 128) return MEMQ_ERR_LAUNCH;

@@ -104,6 +104,10 @@ def test_validation_rejects_before_any_cuda_call(lib):
                 dict(page=48), dict(page=2048), dict(pages=0), dict(pages=1 << 26), dict(max_pages=0),
                 dict(max_pages=1 << 26), dict(scale=float("nan")), dict(scale=float("inf"))):
         assert attn(**bad) == S.ERR_SHAPE, bad
+    # key indices of a sequence, rounded up to a tile, stay in 31 bits; the scale in the exponent is finite
+    assert attn(max_pages=(1 << 24) + 1) == S.ERR_SHAPE and attn(max_pages=1 << 20, page=1024, q=None) == S.ERR_NULL
+    assert attn(max_pages=(1 << 20) + 1, page=1024) == S.ERR_SHAPE and attn(max_pages=1 << 24, q=None) == S.ERR_NULL
+    assert attn(scale=3e38) == S.ERR_SHAPE and attn(scale=2e38, q=None) == S.ERR_NULL
     for name in ("q", "pe", "cache", "scales", "table", "kv", "cu", "out", "ws"):
         assert attn(**{name: None}) == S.ERR_NULL, name
     for name in ("q", "pe", "cache", "scales", "ws"):
