@@ -729,10 +729,10 @@ def memq_mla_attn_paged(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, scales: 
     st = _stream(stream)
     if workspace is None:
         need = memq_mla_attn_paged_workspace(kv_rank)
-        if stream is None or st == 0:
+        if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
         else:  # memory of the stream that uses it
-            with torch.cuda.stream(torch.cuda.ExternalStream(st)):
+            with torch.cuda.stream(torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
     else:
         _cuda("workspace", workspace, torch.uint8)

@@ -382,6 +382,27 @@ def test_two_streams_at_once(memq):
         assert all(torch.equal(o, alone[i]) for o in outs[i])
 
 
+def test_workspace_is_memory_of_the_stream_that_uses_it(memq, monkeypatch):
+    """Also when the default stream is named inside another stream's context: memory of that other
+    stream would be handed out again while the call still runs."""
+    b = Batch([(1, 40)], 4, 128, 0, 16, seed=27)
+    args = b.device()
+    out = torch.empty(b.q.shape[:2] + (128,), device="cuda")
+    torch.cuda.synchronize()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    seen, empty = [], torch.empty
+
+    def recording(*a, **kw):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+    monkeypatch.setattr(torch, "empty", recording)
+    for use in (torch.cuda.default_stream(), 0, other, other.cuda_stream, None):
+        with torch.cuda.stream(side):
+            memq.memq_mla_attn_paged(*args, b.scale, out=out, stream=use)
+        torch.cuda.synchronize()
+    assert seen == [0, 0, other.cuda_stream, other.cuda_stream, side.cuda_stream]
+
+
 def test_input_faults_are_reported_and_contained(memq):
     """Lengths past the table, page indexes outside the pool, offsets that descend: the fault bit is
     set, nothing outside the arrays is touched, and other sequences are right."""
