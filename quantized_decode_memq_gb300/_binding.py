@@ -209,13 +209,13 @@ def memq_add_rmsnorm_q8_1(x: torch.Tensor, res: torch.Tensor, w: torch.Tensor, e
         d = torch.empty((rows, ncols // 32), dtype=torch.float32, device=x.device)
     if z is None and want_z:
         z = torch.empty((rows, ncols), dtype=torch.float32, device=x.device)
-    h2 = h if h.dim() == 2 else h.reshape(1, -1)
+    h2 = h if not isinstance(h, torch.Tensor) or h.dim() != 1 else h.view(1, -1)  # never a copy
     _cuda("h", h2, torch.float32, (rows, ncols))
-    _here("memq_add_rmsnorm_q8_1", x2, r2, w, h2, qs, d, z)
     _cuda("qs", qs, torch.int8, (rows, ncols))
     _cuda("d", d, torch.float32, (rows, ncols // 32))
     if z is not None:
         _cuda("z", z, torch.float32, (rows, ncols))
+    _here("memq_add_rmsnorm_q8_1", x2, r2, w, h2, qs, d, z)
     rc = lib().memq_add_rmsnorm_q8_1(_ptr(x2), _ptr(r2), _ptr(w), _ptr(h2), _ptr(z), _ptr(qs),
                                      _ptr(d), ncols, rows, eps, _stream(stream))
     _check("memq_add_rmsnorm_q8_1", rc)

@@ -49,6 +49,36 @@ def test_add_rmsnorm_is_the_producer_on_the_sum(memq, rows, ncols):
         assert torch.equal(b if t is a else a, res if t is a else x)
 
 
+@pytest.mark.parametrize("rows,ncols", [(6, 5120), (6, 96), (6, 17408), (400, 2048)])
+def test_add_rmsnorm_special_values(memq, rows, ncols):
+    """Rows that are not finite, overflow in the sum, or are denormal: the producer's bits all the same."""
+    g = torch.Generator("cuda").manual_seed(ncols)
+    x = torch.randn(rows, ncols, device="cuda", generator=g)
+    x[0, 5], x[1, 7] = float("inf"), float("nan")
+    x[2] *= 1e-39
+    x[3] = 3e38
+    x[4] *= 1e18
+    res = torch.where(x.abs() > 1e17, x, 0.25 * x)
+    w = torch.randn(ncols, device="cuda", generator=g)
+    w[:32], w[32:64], w[64:96] = 1e-38, 1e30, 0
+    h, z, qs, d = memq.memq_add_rmsnorm_q8_1(x, res, w)
+    bits = lambda t: t.view(torch.int32)
+    assert torch.equal(bits(h), bits(x + res))
+    z2, qs2, d2 = memq.memq_rmsnorm_q8_1(h, w)
+    assert torch.equal(bits(z), bits(z2)) and torch.equal(qs, qs2) and torch.equal(bits(d), bits(d2))
+
+
+def test_add_rmsnorm_vector_in_place_is_not_a_copy(memq):
+    x, w = torch.randn(64, device="cuda"), torch.ones(64, device="cuda")
+    h = torch.zeros(64, device="cuda")
+    assert memq.memq_add_rmsnorm_q8_1(x, x, w, h=h)[0] is h and torch.equal(h, x + x)
+    for bad in (torch.zeros(128, device="cuda")[::2], torch.zeros(2, 4, 16, device="cuda").transpose(0, 1)):
+        with pytest.raises(ValueError):
+            memq.memq_add_rmsnorm_q8_1(x, x, w, h=bad)
+    with pytest.raises((TypeError, ValueError)):
+        memq.memq_add_rmsnorm_q8_1(x, x, w, h=[0.0] * 64)
+
+
 def test_add_rmsnorm_edges(memq):
     w = torch.ones(64, device="cuda")
     h, z, qs, d = memq.memq_add_rmsnorm_q8_1(torch.empty(0, 64, device="cuda"), torch.empty(0, 64, device="cuda"), w)
