@@ -4,8 +4,8 @@
 //   h = x + res;   z = (h * rr) * w;   d = max |z| / 127 and qs = round(z / d) per 32 elements
 //
 // It reads x, res and writes h, qs, d: 13.1 bytes an element instead of the 17.1 of an addition
-// followed by memq_rmsnorm_q8_1 (12 + 5.1), and is bound by memory on many rows (4096 x 8192: 86.4 us,
-// 5.1 TB/s, 75% of a copy's rate) and by latency on few (1 x 5120: 2.8 us a launch, back to back).
+// followed by memq_rmsnorm_q8_1 (12 + 5.1), and is bound by memory on many rows (4096 x 8192: 85.2 us,
+// 5.2 TB/s, 76% of a copy's rate) and by latency on few (1 x 5120: 2.8 us a launch, back to back).
 //
 // z, qs and d are bit for bit what memq_rmsnorm_q8_1 gives for h.  The only order that matters is that
 // of the sum of squares: a thread of that kernel adds the float4 slices tid, tid + threads, ... of the
@@ -84,8 +84,10 @@ __global__ void __launch_bounds__(R == 1 ? 256 : 1024, R == 1 ? (S <= 2 ? 8 : 4)
             v[i] = f < nf4 ? __ldcg(x4 + f) : zero;
             b[i] = f < nf4 ? __ldcg(r4 + f) : zero;
         }
+        if (R == 1) {
 #pragma unroll
-        for (int i = 0; i < S; ++i) wk[i] = f0 + i * step < nf4 ? __ldg(w4 + f0 + i * step) : zero;
+            for (int i = 0; i < S; ++i) wk[i] = f0 + i * step < nf4 ? __ldg(w4 + f0 + i * step) : zero;
+        }
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             v[i] = make_float4(__fadd_rn(v[i].x, b[i].x), __fadd_rn(v[i].y, b[i].y), __fadd_rn(v[i].z, b[i].z),
@@ -94,7 +96,15 @@ __global__ void __launch_bounds__(R == 1 ? 256 : 1024, R == 1 ? (S <= 2 ? 8 : 4)
             if (f0 + i * step < nf4) h4[f0 + i * step] = v[i];
         }
     }
-    if (R > 1) __syncthreads();
+    // Where threads share, w is loaded here: the first loads then have its registers, and it arrives while
+    // one of four threads sums (us, here / with the first loads / after the sum: 2048 rows of 17408 107 /
+    // 129 / 118, 4096 of 8192 85.2 / 87.3 / 84.4, 1000 of 8192 25.9 / 26.2 / 27.0; without sharing, 1000 of
+    // 4096 14.2 / 13.4 / 15.8).
+    if (R > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < S; ++i) wk[i] = f0 + i * step < nf4 ? __ldg(w4 + f0 + i * step) : zero;
+    }
     if (k == 0) {
         float ss = 0.0f;  // a slice past the row's end adds zeros
 #pragma unroll
@@ -208,7 +218,7 @@ extern "C" int memq_add_rmsnorm_q8_1(const float *x, const float *res, const flo
     while (v < 16 && (nf4 + v - 1) / v > 256) v *= 2;
     const int nwarps = ((nf4 + v - 1) / v + 31) / 32;
     // A cluster of eight shares a row that is wider than 8192 (us, 8 CTAs a row against 2: 8 rows of
-    // 17408 4.4 / 5.3, 64 7.5 / 7.2, 512 37.3 / 45.5), and one wider than 4096 while there are SMs for it
+    // 17408 4.2 / 5.3, 64 7.5 / 7.2, 512 33.1 / 45.5), and one wider than 4096 while there are SMs for it
     // (8 / 1: 1 row of 5120 2.8 / 3.4, 8 of 8192 3.0 / 4.3, but 2048 of 5120 44.2 / 30.1).
     const bool split = v == 16 || (v == 8 && rows * kMaxCluster <= sms);
     const int per_cta = split ? (nwarps + kMaxCluster - 1) / kMaxCluster : nwarps;
