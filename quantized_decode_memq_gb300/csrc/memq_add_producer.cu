@@ -4,8 +4,8 @@
 //   h = x + res;   z = (h * rr) * w;   d = max |z| / 127 and qs = round(z / d) per 32 elements
 //
 // It reads x, res and writes h, qs, d: 13.1 bytes an element instead of the 17.1 of an addition
-// followed by memq_rmsnorm_q8_1 (12 + 5.1), and is bound by memory on many rows (4096 x 8192: 85.2 us,
-// 5.2 TB/s, 76% of a copy's rate) and by latency on few (1 x 5120: 2.8 us a launch, back to back).
+// followed by memq_rmsnorm_q8_1 (12 + 5.1), and is bound by memory on many rows (4096 x 8192: 83.6 us,
+// 5.3 TB/s, 77% of a copy's rate) and by latency on few (1 x 5120: 2.8 us a launch, back to back).
 //
 // z, qs and d are bit for bit what memq_rmsnorm_q8_1 gives for h.  The only order that matters is that
 // of the sum of squares: a thread of that kernel adds the float4 slices tid, tid + threads, ... of the
@@ -52,7 +52,7 @@ __device__ __forceinline__ uint32_t code_of(float z, float dd, float inv) {
 // CTA `part` of a row's `ctas`.  `nwarps` summing warps serve the row, `per_cta` of them this CTA, whose
 // threads are R times as many; thread (k, t) holds the slices of summing thread t from number k on in
 // steps of R.
-template <int S, int R>
+template <int S, int R, bool LATE>
 __global__ void __launch_bounds__(R == 1 ? 256 : 1024, R == 1 ? (S <= 2 ? 8 : 4) : S <= 2 ? 2 : 1)
     add_rmsnorm_q8_1_kernel(const float *x, const float *res, float *h, const float *__restrict__ w, float *z,
                             int8_t *qs, float *d, int ncols, float eps, int nwarps, int per_cta, int ctas) {
@@ -97,13 +97,13 @@ __global__ void __launch_bounds__(R == 1 ? 256 : 1024, R == 1 ? (S <= 2 ? 8 : 4)
         }
     }
     // Where threads share, w is loaded here: the first loads then have its registers, and it arrives while
-    // one of four threads sums (us, here / with the first loads / after the sum: 2048 rows of 17408 107 /
-    // 129 / 118, 4096 of 8192 85.2 / 87.3 / 84.4, 1000 of 8192 25.9 / 26.2 / 27.0; without sharing, 1000 of
-    // 4096 14.2 / 13.4 / 15.8).
+    // one of four threads sums (us, here / with the first loads: 2048 rows of 17408 107 / 129, 4096 of 8192
+    // 85.2 / 87.3; without sharing, 1000 of 4096 14.2 / 13.4).  LATE: after the sum.
     if (R > 1) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < S; ++i) wk[i] = f0 + i * step < nf4 ? __ldg(w4 + f0 + i * step) : zero;
+        for (int i = 0; i < S; ++i)
+            if (!LATE) wk[i] = f0 + i * step < nf4 ? __ldg(w4 + f0 + i * step) : zero;
     }
     if (k == 0) {
         float ss = 0.0f;  // a slice past the row's end adds zeros
@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(R == 1 ? 256 : 1024, R == 1 ? (S <= 2 ? 8 : 4)
 #pragma unroll
     for (int i = 0; i < S; ++i) {
         const int f = f0 + i * step;
+        if (LATE) wk[i] = f < nf4 ? __ldg(w4 + f) : zero;
         const float4 zz = make_float4(__fmul_rn(__fmul_rn(v[i].x, r), wk[i].x), __fmul_rn(__fmul_rn(v[i].y, r), wk[i].y),
                                       __fmul_rn(__fmul_rn(v[i].z, r), wk[i].z), __fmul_rn(__fmul_rn(v[i].w, r), wk[i].w));
         float am = fmaxf(fmaxf(fabsf(zz.x), fabsf(zz.y)), fmaxf(fabsf(zz.z), fabsf(zz.w)));
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(R == 1 ? 256 : 1024, R == 1 ? (S <= 2 ? 8 : 4)
     }
 }
 
-template <int S, int R>
+template <int S, int R, bool LATE = false>
 cudaError_t launch(const float *x, const float *res, const float *w, float *h, float *z, int8_t *qs, float *d, int ncols,
                    int rows, float eps, int nwarps, int per_cta, int ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
@@ -175,7 +176,7 @@ cudaError_t launch(const float *x, const float *res, const float *w, float *h, f
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, add_rmsnorm_q8_1_kernel<S, R>, x, res, h, w, z, qs, d, ncols, eps, nwarps, per_cta,
+    return cudaLaunchKernelEx(&cfg, add_rmsnorm_q8_1_kernel<S, R, LATE>, x, res, h, w, z, qs, d, ncols, eps, nwarps, per_cta,
                               ctas);
 }
 
@@ -231,6 +232,10 @@ extern "C" int memq_add_rmsnorm_q8_1(const float *x, const float *res, const flo
     // more rows have the loads in flight without it (us, shared / not: 160 x 4096 5.2 / 5.8, 3000 x 4096
     // 43.7 / 31.7).
     const bool few = rows <= 2 * sms;
+    // Up to 8192 columns, w is loaded after the sum once many rows follow one another on an SM: other rows
+    // hide its latency, and the first loads go out ahead of it (us, after the sum / before: 1000 x 7168
+    // 23.6 / 23.1, 2000 x 5120 29.1 / 30.3, 8192 x 5120 95.0 / 101.7, 4096 x 8192 83.6 / 84.8).
+    const bool many = rows >= 10 * sms;
     switch (v) {
         case 1: e = launch<1, 1>(x, res, w, h, z, qs, d, nc, nr, eps, nwarps, per_cta, ctas, st); break;
         case 2:
@@ -241,7 +246,10 @@ extern "C" int memq_add_rmsnorm_q8_1(const float *x, const float *res, const flo
             e = few ? launch<1, 4>(x, res, w, h, z, qs, d, nc, nr, eps, nwarps, per_cta, ctas, st)
                     : launch<4, 1>(x, res, w, h, z, qs, d, nc, nr, eps, nwarps, per_cta, ctas, st);
             break;
-        case 8: e = launch<2, 4>(x, res, w, h, z, qs, d, nc, nr, eps, nwarps, per_cta, ctas, st); break;
+        case 8:
+            e = many ? launch<2, 4, true>(x, res, w, h, z, qs, d, nc, nr, eps, nwarps, per_cta, ctas, st)
+                     : launch<2, 4>(x, res, w, h, z, qs, d, nc, nr, eps, nwarps, per_cta, ctas, st);
+            break;
         default: e = launch<4, 4>(x, res, w, h, z, qs, d, nc, nr, eps, nwarps, per_cta, ctas, st); break;
     }
     return e == cudaSuccess ? MEMQ_OK : MEMQ_ERR_LAUNCH;

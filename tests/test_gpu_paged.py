@@ -30,7 +30,7 @@ def memq():
 # ------------------------------------------------------------------------------- the producer
 @pytest.mark.parametrize("rows,ncols", [(1, 32), (1, 5120), (8, 17408), (3, 160), (5, 8224), (1, 32768), (4097, 64),
                                        (2, 1056), (40, 2080), (3, 4096), (19, 8192), (20, 8192), (300, 16416),
-                                       (1, 4128), (25, 32768), (600, 1536)])
+                                       (1, 4128), (25, 32768), (600, 1536), (1600, 5152)])
 def test_add_rmsnorm_is_the_producer_on_the_sum(memq, rows, ncols):
     g = torch.Generator("cuda").manual_seed(rows * ncols)
     x = torch.randn(rows, ncols, device="cuda", generator=g)
