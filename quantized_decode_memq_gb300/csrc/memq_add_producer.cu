@@ -5,7 +5,7 @@
 //
 // It reads x, res and writes h, qs, d: 13.1 bytes an element instead of the 17.1 of an addition
 // followed by memq_rmsnorm_q8_1 (12 + 5.1), and is bound by memory on many rows (4096 x 8192: 83.6 us,
-// 5.3 TB/s, 77% of a copy's rate) and by latency on few (1 x 5120: 2.8 us a launch, back to back).
+// 5.3 TB/s, 77% of a copy's rate) and by latency on few (1 x 5120: 3.2 us a launch, back to back).
 //
 // z, qs and d are bit for bit what memq_rmsnorm_q8_1 gives for h.  The only order that matters is that
 // of the sum of squares: a thread of that kernel adds the float4 slices tid, tid + threads, ... of the
@@ -33,6 +33,13 @@ __device__ __forceinline__ void store_dsmem(double *p, int cta, double v) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(cta));
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(v) : "memory");
 }
+// A CTA's shared memory may be written from outside only once it runs, which co-scheduling alone does
+// not say: every CTA of the cluster arrives at its entry, and waits for the others ahead of its first
+// remote store.  No data passes here, so the arrival orders nothing.
+__device__ __forceinline__ void cluster_started_arrive() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_started_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -59,6 +66,7 @@ __global__ void __launch_bounds__(R == 1 ? 256 : 1024, R == 1 ? (S <= 2 ? 8 : 4)
     extern __shared__ __align__(16) float4 held[];  // [S R][summing threads of this CTA]
     __shared__ double red[32];
     __shared__ float r_shared;
+    if (ctas > 1) cluster_started_arrive();
     griddep_launch_dependents();
     griddep_wait();
 
@@ -105,6 +113,7 @@ __global__ void __launch_bounds__(R == 1 ? 256 : 1024, R == 1 ? (S <= 2 ? 8 : 4)
         for (int i = 0; i < S; ++i)
             if (!LATE) wk[i] = f0 + i * step < nf4 ? __ldg(w4 + f0 + i * step) : zero;
     }
+    if (ctas > 1) cluster_started_wait();  // long over by the time that the row's loads are back
     if (k == 0) {
         float ss = 0.0f;  // a slice past the row's end adds zeros
 #pragma unroll
@@ -219,8 +228,8 @@ extern "C" int memq_add_rmsnorm_q8_1(const float *x, const float *res, const flo
     while (v < 16 && (nf4 + v - 1) / v > 256) v *= 2;
     const int nwarps = ((nf4 + v - 1) / v + 31) / 32;
     // A cluster of eight shares a row that is wider than 8192 (us, 8 CTAs a row against 2: 8 rows of
-    // 17408 4.2 / 5.3, 64 7.5 / 7.2, 512 33.1 / 45.5), and one wider than 4096 while there are SMs for it
-    // (8 / 1: 1 row of 5120 2.8 / 3.4, 8 of 8192 3.0 / 4.3, but 2048 of 5120 44.2 / 30.1).
+    // 17408 4.3 / 5.3, 64 6.9 / 7.2, 512 31.4 / 45.5), and one wider than 4096 while there are SMs for it
+    // (8 / 1: 1 row of 5120 3.2 / 3.4, 8 of 8192 3.4 / 4.3, but 2048 of 5120 44.2 / 30.1).
     const bool split = v == 16 || (v == 8 && rows * kMaxCluster <= sms);
     const int per_cta = split ? (nwarps + kMaxCluster - 1) / kMaxCluster : nwarps;
     const int ctas = (nwarps + per_cta - 1) / per_cta;

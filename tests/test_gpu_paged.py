@@ -544,3 +544,24 @@ def test_a_layer_step(memq):
     first = memq.memq_mla_attn_gathered(q_lat[:1].contiguous(), pe[:1].contiguous(), rows, to_dev(idx[None]), b.scale)
     assert np.all(np.abs(first.double().cpu().numpy() - want[:1]) <= bound[:1])
     assert memq.memq_device_fault() == 0
+
+
+@pytest.mark.parametrize("ncols", [4128, 6176, 8192, 8224, 12288, 14368, 16384, 24576, 32768])
+def test_add_rmsnorm_clusters_started_at_once(memq, ncols):
+    """Rows shared by clusters of five to eight CTAs, launch behind launch on two streams, so that CTAs of
+    a cluster start while others still run: every launch gives the same bits."""
+    rows = 18 if ncols <= 8192 else 333
+    g = torch.Generator("cuda").manual_seed(ncols)
+    x, res = torch.randn(2, rows, ncols, device="cuda", generator=g)
+    w = torch.randn(ncols, device="cuda", generator=g)
+    z, qs, d = memq.memq_rmsnorm_q8_1(x + res, w)
+    sts = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(12):
+        for st in sts:
+            with torch.cuda.stream(st):
+                outs.append(memq.memq_add_rmsnorm_q8_1(x, res, w))
+    torch.cuda.synchronize()
+    for h2, z2, qs2, d2 in outs:
+        assert torch.equal(h2, x + res) and torch.equal(z2, z) and torch.equal(qs2, qs) and torch.equal(d2, d)
