@@ -64,6 +64,7 @@
 
 #include "memq.h"
 #include "memq_dev.cuh"
+#include "memq_phases.cuh"
 #include "memq_tc.cuh"
 
 namespace memq {
@@ -193,8 +194,10 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
     return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
 }
 
-// Waits for a barrier phase; after one wait expired, none is made any more (the kernel then runs to
-// its end on whatever is there, and the fault word says so).
+// Waits for a barrier phase; after one wait expired, none is made any more, and the fault word says so.
+// A warp whose wait expired frees no buffer any more, so that nothing is announced on a barrier whose last
+// phase is not over: the copies stop and what is in flight is awaited, the products stop, and the softmax
+// warps run to their end on whatever is there.
 struct Waiter {
     bool dead = false;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
@@ -603,10 +606,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- TMA producer
-            uint32_t tile = 0, slot = 0, lap = 0;
+            CopyPhases sent;
+            const uint32_t slots = static_cast<uint32_t>(a.slots);
             const int per_tile = kKeys / a.box;
             named_bar_sync(4, kSoftmaxWarps * 32 + 32);  // the first query rows' loads are out
-            for (long long pos = run_first; pos < run_hi;) {
+            for (long long pos = run_first; pos < run_hi && !wait.dead;) {
                 const int n = static_cast<int>(min(static_cast<long long>(it.tiles - off), run_hi - pos));
                 const int32_t *table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
                 const auto page_row = [&](int key0) {  // row of this lane's box in the pool
@@ -620,47 +624,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return (page << a.page_shift) + (key & ((1 << a.page_shift) - 1));
                 };
                 int row = page_row(off * kKeys);
-                for (int i = off; i < off + n; ++i, ++tile) {
+                for (int i = off; i < off + n; ++i) {
                     const int row_next = i + 1 < off + n ? page_row((i + 1) * kKeys) : -1;
                     const bool mine = row >= 0;
                     const uint32_t boxes = __popc(__ballot_sync(kFullMask, mine));
                     // scales of the tile's keys
-                    uint64_t *bar = &ctl->scale_full[tile & 1];
-                    if (tile >= 2) wait(&ctl->scale_free[tile & 1], ((tile >> 1) - 1) & 1);
-                    if (!wait.dead) {
-                        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * a.box * 4);
+                    const uint32_t buf = sent.scales & 1;
+                    if (sent.scales >= 2) wait(&ctl->scale_free[buf], last_parity(sent.scales >> 1));
+                    if (wait.dead) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&ctl->scale_full[buf], boxes * a.box * 4);
+                    __syncwarp();
+                    if (mine) bulk_g2s_plain(tile_scale + buf * kKeys + lane * a.box, a.scales + row, a.box * 4, &ctl->scale_full[buf]);
+                    ++sent.scales;
+                    if (a.rope) {
+                        if (sent.ropes >= 1) wait(&ctl->rope_free, last_parity(sent.ropes));
+                        if (wait.dead) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&ctl->rope_full, boxes * a.box * a.rope);
                         __syncwarp();
                         if (mine)
-                            bulk_g2s_plain(tile_scale + (tile & 1) * kKeys + lane * a.box, a.scales + row, a.box * 4, bar);
-                    }
-                    if (a.rope) {
-                        if (tile >= 1) wait(&ctl->rope_free, (tile - 1) & 1);
-                        if (!wait.dead) {
-                            if (lane == 0) mbar_arrive_expect_tx(&ctl->rope_full, boxes * a.box * a.rope);
-                            __syncwarp();
-                            if (mine)
-                                tma_load_2d_plain(rope_k + lane * a.box * a.rope, &map_rope, a.rank, row, &ctl->rope_full);
-                        }
+                            tma_load_2d_plain(rope_k + lane * a.box * a.rope, &map_rope, a.rank, row, &ctl->rope_full);
+                        ++sent.ropes;
                     }
                     for (int c = 0; c < pieces; ++c) {
-                        if (lap >= 1) wait(&ctl->freed[slot], (lap - 1) & 1);
-                        if (!wait.dead) {
-                            if (lane == 0) mbar_arrive_expect_tx(&ctl->full[slot], boxes * a.box * 128);
-                            __syncwarp();
-                            if (mine)
-                                tma_load_2d_plain(ring + slot * kPiece + lane * a.box * 128, &map_lat, c * 128, row,
-                                                  &ctl->full[slot]);
-                        }
-                        if (++slot == static_cast<uint32_t>(a.slots)) {
-                            slot = 0;
-                            ++lap;
-                        }
+                        const uint32_t slot = sent.slot;
+                        if (sent.lap >= 1) wait(&ctl->freed[slot], last_parity(sent.lap));
+                        if (wait.dead) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&ctl->full[slot], boxes * a.box * 128);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_2d_plain(ring + slot * kPiece + lane * a.box * 128, &map_lat, c * 128, row,
+                                              &ctl->full[slot]);
+                        sent.piece_announced(slots);
                     }
+                    if (wait.dead) break;
                     row = row_next;
                 }
                 pos += n + kStart;
                 off = 0;
-                if (pos < run_hi) {
+                if (pos < run_hi && !wait.dead) {
                     next_item(a, it);
                     // The softmax warps are about two tiles behind: the next query rows come into L2.
                     const int64_t row0 = item_row0(a, it);
@@ -670,13 +671,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (wait.dead) {
-                // Copies in flight: every slot's last phase that was announced, each wait bounded.
-                for (int s = 0; s < a.slots; ++s) {
-                    const uint32_t uses = lap + (static_cast<uint32_t>(s) < slot ? 1 : 0);
-                    if (uses) (void)warp_wait_bounded(&ctl->full[s], (uses - 1) & 1);
-                }
-                if (tile >= 1 && a.rope) (void)warp_wait_bounded(&ctl->rope_full, (tile - 1) & 1);
-                if (tile >= 1) (void)warp_wait_bounded(&ctl->scale_full[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
+                // Copies in flight: the last phase that was announced on every barrier, each wait bounded.
+                for (uint32_t s = 0; s < slots; ++s)
+                    if (sent.pieces_in(s)) (void)warp_wait_bounded(&ctl->full[s], last_parity(sent.pieces_in(s)));
+                if (sent.ropes) (void)warp_wait_bounded(&ctl->rope_full, last_parity(sent.ropes));
+                for (uint32_t b = 0; b < 2; ++b)
+                    if (sent.scales_in(b)) (void)warp_wait_bounded(&ctl->scale_full[b], last_parity(sent.scales_in(b)));
             }
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- tensor-core products
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int k = 0; k < a.rope / 32; ++k)
                             mma_f8(d, d_rope + k * 2, d_qr + k * 2, idesc_s, k != 0);
-                        tc_commit(&ctl->rope_free);
+                        if (!wait.dead) tc_commit(&ctl->rope_free);
                     }
 #pragma unroll 1
                     for (int c = c0; c < c1; ++c) {
@@ -750,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     more = same || pos < run_hi;
                     if (more && same) scores(0, lead);
                     wait(&ctl->weights_ready, i & 1);
+                    if (wait.dead) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < pieces; ++c) {
@@ -896,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait(&ctl->scale_full[tile & 1], (tile >> 1) & 1);
                     float sj = tile_scale[(tile & 1) * kKeys + key];
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->scale_free[tile & 1]);
+                    if (lane == 0 && !wait.dead) mbar_arrive(&ctl->scale_free[tile & 1]);
                     const bool in = k < it.vis;
                     if (!in) sj = 1.f;  // no column sees it
                     const float f = sj * a.scale_log2;
