@@ -380,9 +380,9 @@ int memq_mla_cache_read(int dtype, const uint8_t *cache, const float *scales, co
  *                no-op that accepts NULL pointers; otherwise n_pages >= 1 and max_pages >= 1.
  * The lengths are read on the device only, so a captured call serves other lengths of the same
  * arrays.  A kv_len outside [0, max_pages * page_size] is clamped, a page index outside the pool
- * reads page 0, and cu_q outside [0, n_tok] is clamped: bit 5 of the device fault word is set, as for
- * a cu_q that descends, and the outputs of those sequences are invalid (nothing outside the arrays is
- * read or written).
+ * reads page 0, and cu_q outside [0, n_tok] is clamped: bit 5 of the device fault word is set, and the
+ * outputs of those sequences are invalid (nothing outside the arrays is read or written).  A cu_q that
+ * descends sets bit 5 too, and the call writes no output at all.
  * Numerics: codes are used exactly; a query element within 1.13 x 2^-8 of its value (a bf16 value
  * exactly) down to 2^-10 of the row's largest element, within 2^-17 of that below; a softmax weight
  * (times its row's scale) within 1.07 x 2^-7 of its value (2^-10 rms) and 2^-14 of the largest of its

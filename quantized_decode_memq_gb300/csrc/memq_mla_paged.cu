@@ -169,7 +169,7 @@ __device__ __forceinline__ void next_item(const PagedArgs &a, Item &it) {
     if (it.tok >= it.t) {
         it.tok = 0;
         do {
-            if (++it.seq >= a.n_seq) {  // only if cu_q descends: an item without rows and keys
+            if (++it.seq >= a.n_seq) {  // not with offsets that stand still: an item without rows and keys
                 it.seq = a.n_seq;
                 it.t = it.kv = 0;
                 break;
@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ------------------------------------------------------------------ this CTA's run of tiles
     int32_t *cu = reinterpret_cast<int32_t *>(ring), *kvl = cu + a.n_seq + 1;
+    bool descends = false;
     for (int i = tid; i <= a.n_seq; i += kThreads) {
         const bool seq = i < a.n_seq;
         const int c0 = __ldcg(a.cu_q + i), c1 = seq ? __ldcg(a.cu_q + i + 1) : a.n_tok;
@@ -532,14 +533,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (seq) kvl[i] = kv;
         if (c0 < 0 || c0 > c1 || kv < 0 || kv > (static_cast<long long>(a.max_pages) << a.page_shift))
             atomicOr(&g_paged_fault, kFaultInput);
+        descends = descends || (seq && c0 > c1);
     }
-    __syncthreads();
+    // Offsets that descend would name tokens again and again, n_seq / 2 times at worst: nothing is done then.
+    const int n_seq = __syncthreads_or(descends) ? 0 : a.n_seq;
     // Thread i counts the tiles of the groups whose last token lies in its slice of the tokens.
     const int slice = (a.n_tok + kThreads - 1) / kThreads;
     const int tok_lo = min(a.n_tok, tid * slice), tok_hi = min(a.n_tok, tok_lo + slice);
     int seq0 = 0;
     {
-        int hi = a.n_seq;  // first sequence that ends after tok_lo
+        int hi = n_seq;  // first sequence that ends after tok_lo
         while (seq0 < hi) {
             const int mid = (seq0 + hi) >> 1;
             if (cu[mid + 1] <= tok_lo) seq0 = mid + 1; else hi = mid;
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long sum = before;  // pass 0: this slice's tiles; pass 1: find the run's first tile
         if (pass == 1 && (run_lo < before || run_lo >= before + own)) break;
         Item it{};
-        for (it.seq = seq0; it.seq < a.n_seq && cu[it.seq] < tok_hi; ++it.seq) {
+        for (it.seq = seq0; it.seq < n_seq && cu[it.seq] < tok_hi; ++it.seq) {
             seq_sizes(a, cu[it.seq], cu[it.seq + 1], kvl[it.seq], it);
             const int k0 = max(tok_lo - it.start, 0), k1 = min(tok_hi - it.start, it.t);
             for (it.tok = a.group == 1 ? k0 : k0 / a.group * a.group; min(it.tok + a.group, it.t) <= k1 && it.tok < it.t;

@@ -565,3 +565,15 @@ def test_add_rmsnorm_clusters_started_at_once(memq, ncols):
     torch.cuda.synchronize()
     for h2, z2, qs2, d2 in outs:
         assert torch.equal(h2, x + res) and torch.equal(z2, z) and torch.equal(qs2, qs) and torch.equal(d2, d)
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 0, 5, 0], [3, 2, 5, 5, 5], [0, 5, 5, 5, 4], [5, 5, 5, 5, -1]])
+def test_offsets_that_descend_write_nothing(memq, cu):
+    """They would name the same tokens over and over: the call reports them and leaves the outputs alone."""
+    b = Batch([(2, 100), (3, 60), (0, 40), (0, 9)], 8, 128, 32, 16, seed=28)
+    assert b.q.shape[0] == 5
+    b.cu = np.array(cu, np.int32)
+    assert torch.all(b.run(memq, fill=7.0) == 7)
+    assert memq.memq_device_fault() == 32
+    b.cu = np.array([0, 2, 5, 5, 5], np.int32)
+    b.check(memq)
