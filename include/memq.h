@@ -385,8 +385,12 @@ int memq_mla_cache_read(int dtype, const uint8_t *cache, const float *scales, co
  * descends sets bit 5 too, and the call writes no output at all.
  * Numerics: codes are used exactly; a query element within 1.13 x 2^-8 of its value (a bf16 value
  * exactly) down to 2^-10 of the row's largest element, within 2^-17 of that below; a softmax weight
- * (times its row's scale) within 1.07 x 2^-7 of its value (2^-10 rms) and 2^-14 of the largest of its
- * query; products exact, sums, maxima and normalisation in f32.  A row's scale below 2^-64 counts as
+ * (times its row's scale) within 1.13 x 2^-8 of its value (2^-9.6 rms), or 1.13 x 2^-17 of the largest of
+ * its query where that is more.  The largest is one nearby: a weight of less than 2^-20 of an earlier
+ * row's may count as 0 in the 2176 rows behind that (256 if it stood 2^8 above those before it), and after
+ * them is held against the largest of its own 128 rows, down to 2^-36 of the query's largest.  So a
+ * long tail of small weights behind a large one arrives.  Products are exact, sums, maxima and
+ * normalisation in f32.  A row's scale below 2^-64 counts as
  * 2^-64 in the output (the scores use it as it is), and a weight times its row's scale below 2^-110 of
  * the largest as 0.  A query row that is not finite, or has an element past 2^126, gives NaN.
  * Results do not depend on timing; they depend on how the tiles are split, so the same row may differ

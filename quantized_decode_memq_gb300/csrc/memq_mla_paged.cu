@@ -19,16 +19,18 @@
 // the operations at twice the 16-bit rate):
 //   q = 2^e (hi + lo), both E4M3, e per row: a relative 2^-8 (a bf16 value exactly) down to 2^-10 of
 //       the row's largest; below that an absolute 2^-17 of the largest;
-//   p = hi (E4M3) + lo (E5M2), with p in (0, 2^8.8] and 2 at the reference: a relative 2^-7 at most
-//       (about 2^-10 rms) down to 2^-6, an absolute 2^-13 and a relative 2^-3 below that, down to
-//       2^-16: E5M2 carries the long tail of small weights that a second E4M3 term would flush.  Both
-//       codes are bit fields of f16 numbers: E4M3 of v is bits 14..7 of f16(v / 256), E5M2 of v the
-//       high byte of f16(v), so the split needs one conversion per pair of weights and integer
-//       operations.
+//   p = hi (E4M3) + lo (E5M2), with p in (0, 2^8.8] and 8 at the reference: a relative 1.13 x 2^-8 at most
+//       (about 2^-9.6 rms) down to 2^-6, an absolute 2^-14 below that, steps of 2^-16 from 2^-14 on, and
+//       0 below 2^-17: E5M2 carries small weights that a second E4M3 term would flush.  Both codes are bit
+//       fields of f16 numbers: E4M3 of v is bits 14..7 of f16(v / 256), E5M2 of v the high byte of
+//       f16(v), so the split needs one conversion per pair of weights and integer operations.
 // The key's scale is folded into its weight (p_j = 2^8 exp2(s_j + log2 scales_j - R - 7)), so R, the
 // running reference, bounds what the 8-bit terms must hold; the sum of weights is kept apart in f32.
-// R moves, and the accumulators are rescaled, only when a score exceeds it by 7.8: a tile
-// then needs one vote instead of 64 maxima over its keys.
+// R moves, and the accumulators are rescaled, only when a score exceeds it by 5.8, so that a tile needs one
+// vote instead of 64 maxima over its keys, or when a look at a tile's codes finds a query all of whose
+// weights are below 2^-8: thousands of small weights behind one large one (a sink) carry a part of the
+// sum that must not be lost.  The f32 accumulators take a reference that comes down as well as one that
+// goes up.  The look comes two tiles after a reference went up far, and every 16 tiles.
 //
 // One CTA per SM.  The 128-key tiles of all (sequence, token group, head block) items form one list
 // that is cut into equal runs, one per CTA; every CTA derives its run from the lengths on the device
@@ -47,9 +49,9 @@
 // 128, where both do).  So both query terms are one product of 128 columns, S_hi and S_lo, which the
 // softmax warps add; the accumulators of the outputs leave no room in TMEM for the same there.  At
 // rank 512, rope 64: 18 x 64 + 32 x 48 cycles, and 576 for the copies that fill the ring; a tile takes
-// 3480.  64 heads, rank 512, rope 64, bf16: 2048 new tokens over 8192 rows 1.59 ms, 1.28 PFLOP/s (two
-// thirds of the bf16 peak); 48 single tokens over up to 16384 rows 92 us, 4.9 TB/s once it runs, of which
-// starts and partial accumulators take 30; 8 tokens over 32768 rows 48 us.
+// 3480.  64 heads, rank 512, rope 64, bf16: 2048 new tokens over 8192 rows 1.71 ms, 1.20 PFLOP/s (61% of the
+// bf16 peak; moves of the references take 0.1 ms of it); 48 single tokens over up to 16384 rows 91 us, 4.9 TB/s
+// once it runs, of which starts and partial accumulators take 30; 8 tokens over 32768 rows 49 us.
 //
 // Codes of a cached row are finite by the cache's contract (a row that was not finite carries a
 // NaN scale); rows past the end of a sequence may hold anything and are zeroed in shared memory
@@ -89,8 +91,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 // single tokens 103 / 95 / 92 / 94; rank 256, whose tiles are shorter, is best at 4 to 5).
 constexpr int kStart = 5;
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
-constexpr float kSlack = 7.0f;    // log2 of how far a score may exceed the reference, before
-constexpr float kOver = 0.8f;     // this much more: weights end at 2^8.8, E4M3's largest is 448
+// log2 of how far a score may exceed the reference, before kOver more: weights end at 2^8.8, E4M3's largest is
+// 448.  Less slack keeps more bits of small weights and moves the references more often (2048 tokens over 8192
+// rows, slack 4 / 5 / 6 us: 1737 / 1707 / 1676).
+constexpr float kSlack = 5.0f;
+constexpr float kOver = 0.8f;
+// References come down on a look, to a tile's maxima that lie more than kKeep (log2) below them, but no more
+// than kDepth below the highest that they were: the sums' range, and less than 2^-36 of the largest weight
+// lost there.  Tiles between two looks, 8 / 16: 1721 / 1707 us, 1614 without any.
+constexpr int kLook = 16;
+constexpr float kKeep = 4.0f;
+constexpr float kDepth = 16.0f;
+constexpr float kJump = 0x1p-8f;  // a reference that went up by 8 calls for a look: codes keep 2^-8 above that
 constexpr float kLeastScale = 0x1p-64f;  // smaller scales of a row count as this in the outputs
 constexpr int kScoreCol = 256;    // TMEM: accumulators in columns 0..255, scores after them
 
@@ -127,8 +139,11 @@ struct Item {
 };
 
 struct Control {
-    uint32_t tops[3][kRows];  // column maxima of three successive tiles (order_bits)
+    uint32_t tops[kRows];  // column maxima of a tile (order_bits); 0 between uses
+    float ref[kRows], peak[kRows];  // the columns' references, the highest that they were
+    alignas(16) uint32_t near[kSoftmaxWarps];  // bit 8 (c % 4) + c / 4: column c has a weight of 2^-8 or more
     float row_scale[kRows];
+    alignas(16) float shrink[kRows], minus[kRows];  // what a move of the references means to a column
     uint64_t full[kMaxSlots], freed[kMaxSlots];
     uint64_t rope_full, rope_free, scale_full[2], scale_free[2], score_full[2];
     uint64_t weights_ready, out_done, q_ready, drain;
@@ -240,6 +255,9 @@ __device__ __forceinline__ int swizzled(int r, int i, int row_bytes) {
 __device__ __forceinline__ uint32_t e4m3_bits(uint32_t a, uint32_t b) {
     return __byte_perm(a << 1, b << 1, 0x7531) | (__byte_perm(a, b, 0xfdb9) & 0x80808080u);
 }
+
+// Of four codes of weights, a bit 0 in the place of each that is 2^-8 or more (code 4).
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return (w + 0x7c7c7c7cu) >> 7 & 0x01010101u; }
 
 // Byte offset of element `e` of row r in the hi terms, and how far behind its lo term lies: the lo terms
 // are rows 64 to 127 of the same operand.
@@ -518,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ctl->drain, 1);
         mbar_init_fence();
     }
-    if (tid < 3 * kRows) ctl->tops[tid / kRows][tid % kRows] = 0;
+    if (tid < kRows) ctl->tops[tid] = 0;
     if (warp == kMmaWarp) tmem_alloc(&ctl->tmem, 512);
     griddep_wait();
 
@@ -787,14 +805,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int key = tid & (kKeys - 1), half = tid >> 7, wq = warp & 3;
             const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
             const int col = half * 32 + lane;  // the column whose statistics this lane holds
-            uint32_t tile = 0, slot = 0, top = 0;
-            Owner mine_owner = {};
+            uint32_t tile = 0, slot = 0;
+            if (tid == 0) a.owner[blockIdx.x] = Owner{};
             // The segment whose accumulators are in TMEM: item `it`, tiles off .. off + n - 1.
             Item next = it;
             long long pos = run_first;
             int n = 0;
             bool have = false, more = true;  // a segment is complete; another one follows
-            float ref = kUnset;              // of column `col`
             uint64_t sums[16];               // per pair of columns: sums of weights
             for (;;) {
                 // The next item's queries are staged ahead of the accumulators' way out, so that the
@@ -834,12 +851,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 32; ++c) norm[c] = __shfl_sync(kFullMask, scale_col, c);
                     if (!whole) {
-                        if (wq == 0) a.stats[here * kRows + col] = make_float2(ref, sum);
+                        if (wq == 0) a.stats[here * kRows + col] = make_float2(ctl->ref[col], sum);
                         if (off == 0 && tid == 0) {  // this CTA holds the item's start: it names its parts
-                            mine_owner.row0 = row0;
-                            mine_owner.rows = static_cast<unsigned char>(rows);
-                            mine_owner.tail = static_cast<unsigned char>(here & 1);
-                            mine_owner.last = static_cast<short>(quotient(pos + it.tiles - 1, per));
+                            Owner o = {};
+                            o.row0 = row0;
+                            o.rows = static_cast<unsigned char>(rows);
+                            o.tail = static_cast<unsigned char>(here & 1);
+                            o.last = static_cast<short>(quotient(pos + it.tiles - 1, per));
+                            a.owner[blockIdx.x] = o;
                         }
                     }
 #pragma unroll 1
@@ -885,10 +904,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 
                 // keys that the column's token sees
-                const int lim_col = max(0, min(it.vis, it.kv - it.t + it.tok + 1 +
-                                                           (a.head_blocks > 1 ? 0 : min(col / a.nh, a.group - 1))));
                 const int lim_min = max(0, min(it.vis, it.kv - it.t + it.tok + 1));
-                ref = kUnset;
+                if (wq == 0) ctl->ref[col] = ctl->peak[col] = kUnset;
+                int watch = off + 2;  // tile that begins with a look at the weights of the one before
                 uint64_t shift[16];  // per pair of columns: -(reference + slack)
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
@@ -920,10 +938,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float s[32];
                     wait(&ctl->score_full[tile & 1], (tile >> 1) & 1);
                     tc_fence_after();
-                    // Usually one turn, number 0.  When a column exceeds its reference by the slack, and on
-                    // the first tile, turn 1 takes the plain scores for the columns' maxima, to which all
-                    // references move up, and turn 2 the shifted scores again.
-                    for (int turn = i == off ? 1 : 0;; ++turn) {
+                    // A look at this thread's own codes of the tile before, which every column saw.
+                    bool down = false;
+                    if (i == watch) {
+                        watch = i + kLook;
+                        if (i * kKeys <= lim_min) {
+                            uint32_t near = 0;
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const uint4 w = *reinterpret_cast<const uint4 *>(weights + swizzled(key, (half * 2 + q) * 16, 64));
+                                near |= high_codes(w.x) << (4 * q) | high_codes(w.y) << (4 * q + 1) |
+                                        high_codes(w.z) << (4 * q + 2) | high_codes(w.w) << (4 * q + 3);
+                            }
+                            near = __reduce_or_sync(kFullMask, near);
+                            if (lane == 0) ctl->near[half * 4 + wq] = near;
+                            named_bar_sync(1 + half, 128);
+                            const uint4 w = *reinterpret_cast<const uint4 *>(&ctl->near[half * 4]);
+                            down = (w.x | w.y | w.z | w.w) != kFullMask;
+                            if (down) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) shift[c] = 0;
+                            }
+                        }
+                    }
+                    // Usually one turn, number 0.  When a column exceeds its reference by the slack, or was
+                    // found far below it, and on the first tile, turn 1 takes the plain scores for the
+                    // columns' maxima, to which the references move, and turn 2 the shifted scores again.
+                    for (int turn = i == off || down ? 1 : 0;; ++turn) {
                         uint32_t r[32], r_lo[32];
                         tmem_ld32_nowait(at_s, r);
                         tmem_ld32_nowait(at_s + kRows, r_lo);
@@ -943,6 +984,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             s[2 * c + 3] = v1.y;
                         }
                         if (masked) {
+                            const int lim_col = max(0, min(it.vis, it.kv - it.t + it.tok + 1 +
+                                                                       (a.head_blocks > 1 ? 0 : min(col / a.nh, a.group - 1))));
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
                                 if (k >= __shfl_sync(kFullMask, lim_col, c)) s[c] = -INFINITY;
@@ -957,23 +1000,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                             continue;
                         }
                         if (turn == 2) break;
-                        // Past this barrier nobody reads the maxima of the time before any more, so they
-                        // are cleared there for the time after the next.
-                        atomicMax(&ctl->tops[top][col], order_bits(column_maxima(s, lane)));
+                        atomicMax(&ctl->tops[col], order_bits(column_maxima(s, lane)));
                         named_bar_sync(1 + half, 128);
-                        const float to = fmaxf(ref, unorder_bits(ctl->tops[top][col]));
-                        if (wq == 0) ctl->tops[top == 0 ? 2 : top - 1][col] = 0;
-                        top = top == 2 ? 0 : top + 1;
-                        const float shrink = ex2(ref - to), minus = to == kUnset ? -kUnset : -(to + kSlack);
-                        ref = to;
+                        const float ref = ctl->ref[col], peak = ctl->peak[col], here = unorder_bits(ctl->tops[col]);
+                        const float low = fmaxf(here, peak - kDepth);
+                        const float to = down && low < ref - kKeep ? low : fmaxf(ref, here);
+                        const float shrink = ex2(ref - to);
+                        if (wq == 0) {
+                            ctl->shrink[col] = shrink;
+                            ctl->minus[col] = to == kUnset ? -kUnset : -(to + kSlack);
+                        }
+                        named_bar_sync(1 + half, 128);
+                        if (wq == 0) {
+                            ctl->tops[col] = 0;
+                            ctl->ref[col] = to;
+                            ctl->peak[col] = fmaxf(peak, to);
+                        }
+                        const uint64_t *by = reinterpret_cast<const uint64_t *>(&ctl->shrink[half * 32]);
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
-                            shift[c] = pack2(__shfl_sync(kFullMask, minus, 2 * c), __shfl_sync(kFullMask, minus, 2 * c + 1));
-                        if (i > off) {
+                            shift[c] = *reinterpret_cast<const uint64_t *>(&ctl->minus[half * 32 + 2 * c]);
+                        if (i > off && __any_sync(kFullMask, shrink != 1.f)) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                sums[c] = mul2(sums[c], pack2(__shfl_sync(kFullMask, shrink, 2 * c),
-                                                              __shfl_sync(kFullMask, shrink, 2 * c + 1)));
+                            for (int c = 0; c < 16; ++c) sums[c] = mul2(sums[c], by[c]);
+                            if (__any_sync(kFullMask, shrink < kJump)) watch = i + 2;
                             wait(&ctl->out_done, (tile - 1) & 1);
                             tc_fence_after();
 #pragma unroll 1
@@ -982,7 +1032,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint32_t at = tmem + lane_base + p * kRows + half * 32;
                                 tmem_ld32(at, o);
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) o[c] *= __shfl_sync(kFullMask, shrink, c);
+                                for (int c = 0; c < 16; ++c) {
+                                    const float2 u = unpack2(mul2(pack2(o[2 * c], o[2 * c + 1]), by[c]));
+                                    o[2 * c] = u.x;
+                                    o[2 * c + 1] = u.y;
+                                }
                                 tmem_st32(at, o);
                             }
                             tc_wait_st();
@@ -1031,7 +1085,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&ctl->weights_ready);
                 }
             }
-            if (tid == 0) a.owner[blockIdx.x] = mine_owner;
         }
     } else if (tid == 0) {
         a.owner[blockIdx.x] = Owner{};
