@@ -371,7 +371,7 @@ int memq_mla_cache_read(int dtype, const uint8_t *cache, const float *scales, co
  *   block_table  device int32 [n_seq][max_pages]; entries past a sequence's last page are not read
  *   kv_len       device int32 [n_seq];  cu_q  device int32 [n_seq + 1], ascending
  *   out_dtype    a memq_dtype: the type of out [n_tok][nh][kv_rank] (device, aligned to four
- *                elements); f32 holds the accumulators before the rounding to bf16
+ *                elements)
  *   workspace    device, 16-byte aligned, at least memq_mla_attn_paged_workspace(kv_rank) bytes; it
  *                is scratch of this call alone: calls that may run at the same time (two streams, two
  *                graphs) need one each.  Nothing in it has to be initialised or kept.
@@ -383,16 +383,18 @@ int memq_mla_cache_read(int dtype, const uint8_t *cache, const float *scales, co
  * reads page 0, and cu_q outside [0, n_tok] is clamped: bit 5 of the device fault word is set, and the
  * outputs of those sequences are invalid (nothing outside the arrays is read or written).  A cu_q that
  * descends sets bit 5 too, and the call writes no output at all.
- * Numerics: codes are used exactly; a query element within 1.13 x 2^-8 of its value (a bf16 value
- * exactly) down to 2^-10 of the row's largest element, within 2^-17 of that below; a softmax weight
- * (times its row's scale) within 1.13 x 2^-8 of its value (2^-9.6 rms), or 1.13 x 2^-17 of the largest of
- * its query where that is more.  The largest is one nearby: a weight of less than 2^-20 of an earlier
- * row's may count as 0 in the 2176 rows behind that (256 if it stood 2^8 above those before it), and after
- * them is held against the largest of its own 128 rows, down to 2^-36 of the query's largest.  So a
- * long tail of small weights behind a large one arrives.  Products are exact, sums, maxima and
- * normalisation in f32.  A row's scale below 2^-64 counts as
- * 2^-64 in the output (the scores use it as it is), and a weight times its row's scale below 2^-110 of
- * the largest as 0.  A query row that is not finite, or has an element past 2^126, gives NaN.
+ * Numerics: codes are used exactly.  Queries and softmax weights are sums of 8-bit terms, as many as the
+ * types ask for.  A bf16 query element counts exactly down to 2^-10 of the row's largest element, within
+ * 2^-17 of that below; an f32 one (three terms) within 2^-11 of its value down to there, within 2^-20 of the
+ * largest below.  A weight (times its row's scale) counts, for bf16 outputs, within 1.13 x 2^-8 of its
+ * value (2^-9.6 rms) or 1.13 x 2^-17 of the largest of its query where that is more; for f32 outputs
+ * (three terms) within 2^-11 of its value or 2^-20 of the largest.  The largest is one nearby: a weight of
+ * less than 2^-20 of an earlier row's may count as 0 in the 2176 rows behind that (256 if it stood 2^8
+ * above those before it), and after them is held against the largest of its own 128 rows, down to 2^-36 of
+ * the query's largest.  So a long tail of small weights behind a large one arrives.  Products are exact,
+ * sums, maxima and normalisation in f32.  A row's scale below 2^-64 counts as 2^-64 in the output (the
+ * scores use it as it is), and a weight times its row's scale below 2^-110 of the largest as 0.  A query
+ * row that is not finite, or has an element past 2^126, gives NaN.
  * Results do not depend on timing; they depend on how the tiles are split, so the same row may differ
  * in the last bits between batches.
  * Errors: MEMQ_ERR_SHAPE (also a workspace too small), MEMQ_ERR_NULL, MEMQ_ERR_ALIGN,

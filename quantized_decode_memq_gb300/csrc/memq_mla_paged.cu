@@ -16,14 +16,18 @@
 //
 // kind::f8f6f4 multiplies 8-bit operands exactly and adds in f32, so the operands that are not
 // codes are sums of two 8-bit terms, each with its own product into the same accumulator (twice
-// the operations at twice the 16-bit rate):
-//   q = 2^e (hi + lo), both E4M3, e per row: a relative 2^-8 (a bf16 value exactly) down to 2^-10 of
-//       the row's largest; below that an absolute 2^-17 of the largest;
+// the operations at twice the 16-bit rate), or of three:
+//   q = 2^e (hi + lo), both E4M3, e per row: a bf16 value exactly down to 2^-10 of the row's largest,
+//       below that an absolute 2^-17 of it.  Of an f32 query hi + mid (E4M3) + lo (E5M2): its f16 form, 2^-11,
+//       down to 2^-10 of the largest, an absolute 2^-20 below.
 //   p = hi (E4M3) + lo (E5M2), with p in (0, 2^8.8] and 8 at the reference: a relative 1.13 x 2^-8 at most
 //       (about 2^-9.6 rms) down to 2^-6, an absolute 2^-14 below that, steps of 2^-16 from 2^-14 on, and
-//       0 below 2^-17: E5M2 carries small weights that a second E4M3 term would flush.  Both codes are bit
-//       fields of f16 numbers: E4M3 of v is bits 14..7 of f16(v / 256), E5M2 of v the high byte of
-//       f16(v), so the split needs one conversion per pair of weights and integer operations.
+//       0 below 2^-17: E5M2 carries small weights that a second E4M3 term would flush.  For f32 outputs a third
+//       term, E5M2 too: a relative 2^-11 down to 2^-6, an absolute 2^-17 below.
+//   8 sequences of 8 tokens over 8192 rows (rank 512, rope 64), us: bf16 85, f32 outputs 119, f32 queries 128,
+//   both 145; relative error of 2048 rows against 64 bits with both 3.5e-4.
+// The codes are bit fields of f16 numbers: E4M3 of v is bits 14..7 of f16(v / 256), E5M2 of v the high byte
+// of f16(v), so a split needs one conversion per pair of numbers and integer operations.
 // The key's scale is folded into its weight (p_j = 2^8 exp2(s_j + log2 scales_j - R - 7)), so R, the
 // running reference, bounds what the 8-bit terms must hold; the sum of weights is kept apart in f32.
 // R moves, and the accumulators are rescaled, only when a score exceeds it by 5.8, so that a tile needs one
@@ -49,8 +53,8 @@
 // 128, where both do).  So both query terms are one product of 128 columns, S_hi and S_lo, which the
 // softmax warps add; the accumulators of the outputs leave no room in TMEM for the same there.  At
 // rank 512, rope 64: 18 x 64 + 32 x 48 cycles, and 576 for the copies that fill the ring; a tile takes
-// 3480.  64 heads, rank 512, rope 64, bf16: 2048 new tokens over 8192 rows 1.71 ms, 1.20 PFLOP/s (61% of the
-// bf16 peak; moves of the references take 0.1 ms of it); 48 single tokens over up to 16384 rows 91 us, 4.9 TB/s
+// 3480.  64 heads, rank 512, rope 64, bf16: 2048 new tokens over 8192 rows 1.69 ms, 1.21 PFLOP/s (62% of the
+// bf16 peak; moves of the references take 0.1 ms of it); 48 single tokens over up to 16384 rows 89 us, 4.9 TB/s
 // once it runs, of which starts and partial accumulators take 30; 8 tokens over 32768 rows 49 us.
 //
 // Codes of a cached row are finite by the cache's contract (a row that was not finite carries a
@@ -93,7 +97,8 @@ constexpr int kStart = 5;
 constexpr float kUnset = -1e30f;  // the reference before the first visible key
 // log2 of how far a score may exceed the reference, before kOver more: weights end at 2^8.8, E4M3's largest is
 // 448.  Less slack keeps more bits of small weights and moves the references more often (2048 tokens over 8192
-// rows, slack 4 / 5 / 6 us: 1737 / 1707 / 1676).
+// rows, slack 4 / 5 / 6 us: 1737 / 1707 / 1676; wider scores cost more, twice as wide 2140, at 7 without
+// looks 1780).
 constexpr float kSlack = 5.0f;
 constexpr float kOver = 0.8f;
 // References come down on a look, to a tile's maxima that lie more than kKeep (log2) below them, but no more
@@ -128,7 +133,7 @@ struct PagedArgs {
     int group;  // tokens per item
     int heads_per, head_blocks;
     int slots;
-    int q_bf16, out_bf16;
+    int out_bf16;
     float scale_log2;
 };
 
@@ -156,10 +161,11 @@ struct Control {
 };
 static_assert(sizeof(Control) <= 2048, "the control block has 2 KB of shared memory");
 
-// Shared memory, from a 1024-byte boundary: Q terms (per 128 latent dims hi, lo; rope hi, lo), P terms, the rope
-// piece, the ring, the scales of two tiles, the control block.
-__host__ __device__ constexpr int smem_ring_off(int rank, int rope) {
-    return rank * 128 + 128 * rope + 2 * kKeys * kRows + kKeys * rope;
+// Shared memory, from a 1024-byte boundary: Q terms (per 128 latent dims hi, lo; rope hi, lo; of f32 queries the third
+// terms, per 128 latent dims and rope), P terms, the rope piece, the ring, the scales of two tiles, the control block.
+__host__ __device__ constexpr int smem_weights_off(bool q3, int rank, int rope) { return (q3 ? 3 : 2) * kRows * (rank + rope); }
+__host__ __device__ constexpr int smem_ring_off(bool q3, bool p3, int rank, int rope) {
+    return smem_weights_off(q3, rank, rope) + (p3 ? 3 : 2) * kKeys * kRows + kKeys * rope;
 }
 __host__ __device__ constexpr int smem_tail() { return 2 * kKeys * 4 + 2048; }
 
@@ -264,12 +270,34 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) { return (w + 0x7c7c7
 __device__ __forceinline__ int q_lat_at(int r, int e) { return (e >> 7) * (2 * kRows * 128) + swizzled(r, e & 127, 128); }
 __device__ __forceinline__ int q_pe_at(const PagedArgs &a, int r, int e) { return 2 * a.rank * kRows + swizzled(r, e, a.rope); }
 constexpr int kLatLo = kRows * 128;
+// The same of the third terms.
+__device__ __forceinline__ int q3_lat_at(const PagedArgs &a, int r, int e) {
+    return 2 * kRows * (a.rank + a.rope) + (e >> 7) * (kRows * 128) + swizzled(r, e & 127, 128);
+}
+__device__ __forceinline__ int q3_pe_at(const PagedArgs &a, int r, int e) {
+    return 2 * kRows * (a.rank + a.rope) + a.rank * kRows + swizzled(r, e, a.rope);
+}
+
+// 256 times the two f16 numbers of a, which are small enough; E5M2 codes of the four of a and b, the high
+// bytes of which are rounded.
+__device__ __forceinline__ uint32_t times256(uint32_t a) { return mul_f16x2(a, 0x5c005c00u); }
+__device__ __forceinline__ uint32_t e5m2_bits(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
+// To the nearest multiple of three fraction bits.
+__device__ __forceinline__ uint32_t round3(uint32_t f) { return (f + 0x00400040u) & 0xff80ff80u; }
 
 // hi and lo terms of four query elements, given as two pairs of f16 in (-1, 1].
 __device__ __forceinline__ void split4(uint32_t f0, uint32_t f1, uint32_t &hi, uint32_t &lo) {
-    const uint32_t h0 = (f0 + 0x00400040u) & 0xff80ff80u, h1 = (f1 + 0x00400040u) & 0xff80ff80u;
-    hi = e4m3_bits(h0, h1);  // to the nearest multiple of three fraction bits
+    const uint32_t h0 = round3(f0), h1 = round3(f1);
+    hi = e4m3_bits(h0, h1);
     lo = e4m3_bits(sub_f16x2(f0, h0) + 0x00400040u, sub_f16x2(f1, h1) + 0x00400040u);
+}
+// Three terms hold the eleven bits of an f16 number exactly, four, four and three of them, down to 2^-10.
+__device__ __forceinline__ void split4(uint32_t f0, uint32_t f1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    const uint32_t h0 = round3(f0), h1 = round3(f1), r0 = sub_f16x2(f0, h0), r1 = sub_f16x2(f1, h1);
+    const uint32_t m0 = round3(r0), m1 = round3(r1);
+    hi = e4m3_bits(h0, h1);
+    mid = e4m3_bits(m0, m1);
+    lo = e5m2_bits(times256(sub_f16x2(r0, m0)) + 0x00800080u, times256(sub_f16x2(r1, m1)) + 0x00800080u);
 }
 __device__ __forceinline__ uint32_t scaled_pair(uint32_t a, uint32_t b, uint64_t by) {
     const float2 x = unpack2(mul2(bits2(a, b), by));
@@ -287,9 +315,9 @@ __device__ __forceinline__ void split_parked(uint8_t *hi, uint8_t *lo, uint64_t 
     *h = th;
     *l = tl;
 }
-__device__ __forceinline__ void split_f32(uint8_t *hi, uint8_t *lo, uint4 v, uint64_t by) {
+__device__ __forceinline__ void split_f32(uint8_t *hi, uint8_t *mid, uint8_t *lo, uint4 v, uint64_t by) {
     split4(scaled_pair(v.x, v.y, by), scaled_pair(v.z, v.w, by), *reinterpret_cast<uint32_t *>(hi),
-           *reinterpret_cast<uint32_t *>(lo));
+           *reinterpret_cast<uint32_t *>(mid), *reinterpret_cast<uint32_t *>(lo));
 }
 
 // Maxima of |x| as bits: infinities and NaN lie above all numbers.
@@ -450,8 +478,9 @@ __device__ __forceinline__ void stage_f32(const PagedArgs &a, Control *ctl, uint
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint8_t *hi = smem + q_lat_at(r + k, c * 128 + (q + 8 * j) * 4);
-                split_f32(hi, hi + kLatLo, v[k][j], by[k]);
+                const int e = c * 128 + (q + 8 * j) * 4;
+                uint8_t *hi = smem + q_lat_at(r + k, e);
+                split_f32(hi, hi + kLatLo, smem + q3_lat_at(a, r + k, e), v[k][j], by[k]);
                 v[k][j] = next[k][j];
             }
     }
@@ -459,19 +488,21 @@ __device__ __forceinline__ void stage_f32(const PagedArgs &a, Control *ctl, uint
     for (int k = 0; k < 2; ++k)
         for (int u = q; u * 4 < a.rope; u += 8) {
             uint8_t *hi = smem + q_pe_at(a, r + k, u * 4);
-            split_f32(hi, hi + kRows * a.rope, live[k] ? __ldcg(pe[k] + (u - q)) : zero, by[k]);
+            split_f32(hi, hi + kRows * a.rope, smem + q3_pe_at(a, r + k, u * 4),
+                      live[k] ? __ldcg(pe[k] + (u - q)) : zero, by[k]);
         }
 }
 
+template <bool F32>
 __device__ __forceinline__ void stage_q(const PagedArgs &a, Control *ctl, uint8_t *smem, int64_t row0, int rows,
                                         int tid, bool first) {
     // rows r and r + 1; the warp's other rows lie 2 and 4 apart, so that the swizzle keeps them off
     // each other's banks
     const int r = (tid >> 5) * 8 + ((tid >> 3) & 1) * 4 + ((tid >> 4) & 1) * 2, q = tid & 7;
-    if (a.q_bf16)
-        stage_bf16(a, ctl, smem, row0, rows, r, q, first);
-    else
+    if (F32)
         stage_f32(a, ctl, smem, row0, rows, r, q, first);
+    else
+        stage_bf16(a, ctl, smem, row0, rows, r, q, first);
 }
 
 // Sum over the 32 lanes of v[c], for every c, in lane c (a fixed tree).
@@ -502,6 +533,8 @@ __device__ __forceinline__ float column_maxima(float (&v)[32], int lane) {
     return v[0];
 }
 
+// Q3: f32 queries, three terms of them.  P3: f32 outputs, three terms of the weights.
+template <bool Q3, bool P3>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap map_lat, const __grid_constant__ CUtensorMap map_rope,
                       const PagedArgs a) {
@@ -509,9 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFullMask, tid >> 5, 0);  // uniform
     const int pieces = a.rank / 128;
-    uint8_t *weights = smem + a.rank * 128 + 128 * a.rope;
-    uint8_t *rope_k = weights + 2 * kKeys * kRows;
-    uint8_t *ring = smem + smem_ring_off(a.rank, a.rope);
+    uint8_t *weights = smem + smem_weights_off(Q3, a.rank, a.rope);
+    uint8_t *ring = smem + smem_ring_off(Q3, P3, a.rank, a.rope);
+    uint8_t *rope_k = ring - kKeys * a.rope;
     float *tile_scale = reinterpret_cast<float *>(ring + a.slots * kPiece);
     Control *ctl = reinterpret_cast<Control *>(tile_scale + 2 * kKeys);
 
@@ -686,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     next_item(a, it);
                     // The softmax warps are about two tiles behind: the next query rows come into L2.
                     const int64_t row0 = item_row0(a, it);
-                    const int64_t size = a.q_bf16 ? 2 : 4, rows = item_rows(a, it);
+                    const int64_t size = Q3 ? 4 : 2, rows = item_rows(a, it);
                     prefetch_l2(static_cast<const uint8_t *>(a.q_lat) + row0 * a.rank * size, rows * a.rank * size, lane);
                     if (a.rope) prefetch_l2(static_cast<const uint8_t *>(a.q_pe) + row0 * a.rope * size, rows * a.rope * size, lane);
                 }
@@ -705,14 +738,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             // work in hand, so a barrier is tested while the products before it are being issued and
             // its latency stays hidden.
             if (elect_one()) {
-                constexpr uint32_t idesc_s = f8_idesc(kKeys, 2 * kRows, kE4M3, kE4M3, false, false);
+                // Products into one accumulator have one shape, so that they run in order: n = 128 for two query
+                // terms, n = 64 for three.
+                constexpr uint32_t idesc_s = f8_idesc(kKeys, Q3 ? kRows : 2 * kRows, kE4M3, kE4M3, false, false);
+                constexpr uint32_t idesc_s3 = f8_idesc(kKeys, kRows, kE4M3, kE5M2, false, false);
                 constexpr uint32_t idesc_hi = f8_idesc(128, kRows, kE4M3, kE4M3, true, true);
                 constexpr uint32_t idesc_lo = f8_idesc(128, kRows, kE4M3, kE5M2, true, true);
                 const uint32_t q_u = smem_u32(smem), p_u = smem_u32(weights);
                 // descriptors; a step along an operand adds its bytes / 16
                 const uint64_t d_ring = smem_desc(smem_u32(ring), 128), d_rope = smem_desc(smem_u32(rope_k), a.rope);
                 const uint64_t d_q = smem_desc(q_u, 128), d_qr = smem_desc(q_u + 2 * a.rank * kRows, a.rope);
-                const uint64_t d_p[2] = {smem_desc(p_u, 64), smem_desc(p_u + kKeys * kRows, 64)};
+                const uint64_t d_p[3] = {smem_desc(p_u, 64), smem_desc(p_u + kKeys * kRows, 64),
+                                         smem_desc(p_u + 2 * kKeys * kRows, 64)};
+                const uint32_t q3_u = q_u + 2 * kRows * (a.rank + a.rope);
+                const uint64_t d_q3 = smem_desc(q3_u, 128), d_qr3 = smem_desc(q3_u + a.rank * kRows, a.rope);
                 // Pieces of the next tile's scores that may be awaited before this tile's pieces are free.
                 const int lead = min(pieces, a.slots - pieces);
                 ThreadWaiter wait;
@@ -722,6 +761,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t item_count = 0;
                 bool ready = false;  // the ring slot that the scores read next was seen full
 
+                // One step of K: all query terms q (the second `lo` descriptor steps behind the first), q3.
+                const auto score = [&](uint32_t d, uint64_t k, uint64_t q, uint32_t lo, uint64_t q3, bool acc) {
+                    mma_f8(d, k, q, idesc_s, acc);
+                    if (Q3) {
+                        mma_f8(d + kRows, k, q + lo, idesc_s, acc);
+                        mma_f8(d + kRows, k, q3, idesc_s3, true);
+                    }
+                };
                 // Scores of one tile: pieces [c0, c1), the rope part before piece 0.
                 const auto scores = [&](int c0, int c1) {
                     const uint32_t d = tmem + kScoreCol + (tile_s & 1) * (2 * kRows);
@@ -731,14 +778,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ready = mbar_test(&ctl->full[slot_s], lap_s & 1);
 #pragma unroll 1
                         for (int k = 0; k < a.rope / 32; ++k)
-                            mma_f8(d, d_rope + k * 2, d_qr + k * 2, idesc_s, k != 0);
+                            score(d, d_rope + k * 2, d_qr + k * 2, kRows * a.rope / 16, d_qr3 + k * 2, k != 0);
                         if (!wait.dead) tc_commit(&ctl->rope_free);
                     }
 #pragma unroll 1
                     for (int c = c0; c < c1; ++c) {
                         if (!ready) wait(&ctl->full[slot_s], lap_s & 1);
                         tc_fence_after();
-                        const uint64_t ka = d_ring + slot_s * (kPiece / 16), qa = d_q + c * (2 * kRows * 8);
+                        const uint64_t ka = d_ring + slot_s * (kPiece / 16), qa = d_q + c * (2 * kRows * 8), qa3 = d_q3 + c * (kRows * 8);
                         if (++slot_s == static_cast<uint32_t>(a.slots)) {
                             slot_s = 0;
                             ++lap_s;
@@ -746,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ready = mbar_test(&ctl->full[slot_s], lap_s & 1);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f8(d, ka + k * 2, qa + k * 2, idesc_s, a.rope || c != 0 || k != 0);
+                            score(d, ka + k * 2, qa + k * 2, kLatLo / 16, qa3 + k * 2, a.rope || c != 0 || k != 0);
                     }
                     if (c1 == pieces) tc_commit(&ctl->score_full[tile_s++ & 1]);
                 };
@@ -769,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     --left;
                     const bool same = left > 0;
                     more = same || pos < run_hi;
-                    if (more && same) scores(0, lead);
+                    if (more && same && lead > 0) scores(0, lead);
                     wait(&ctl->weights_ready, i & 1);
                     if (wait.dead) break;
                     tc_fence_after();
@@ -780,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 4; ++k) {
                             mma_f8(tmem + c * kRows, va + k * 256, d_p[0] + k * 128, idesc_hi, !first || k != 0);
                             mma_f8(tmem + c * kRows, va + k * 256, d_p[1] + k * 128, idesc_lo, true);
+                            if (P3) mma_f8(tmem + c * kRows, va + k * 256, d_p[2] + k * 128, idesc_lo, true);
                         }
                         tc_commit(&ctl->freed[slot_o]);
                         if (++slot_o == static_cast<uint32_t>(a.slots)) slot_o = 0;
@@ -821,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         named_bar_sync(3, kSoftmaxWarps * 32);  // nobody reads the row scales any more
                         next = ctl->next;
                     }
-                    stage_q(a, ctl, smem, item_row0(a, next), item_rows(a, next), tid, !have);
+                    stage_q<Q3>(a, ctl, smem, item_row0(a, next), item_rows(a, next), tid, !have);
                     fence_async_smem();
                     named_bar_sync(3, kSoftmaxWarps * 32);
                     if (lane == 0) mbar_arrive(&ctl->q_ready);
@@ -868,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int dim = p * 128 + key;
 #pragma unroll
                         for (int c = 0; c < 32; ++c) o[c] *= norm[c];
-                        if (!whole || !a.out_bf16) {
+                        if (!whole || P3) {
                             float *dst = whole ? static_cast<float *>(a.out) + row0 * a.rank
                                                : a.part + static_cast<int64_t>(here) * kRows * a.rank;
 #pragma unroll
@@ -1042,29 +1090,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_wait_st();
                         }
                     }
-                    uint32_t hi[8], lo[8];
+                    uint32_t hi[8], mid[8], lo[8];  // lo: P3
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
-                        uint32_t h[2], l[2];
+                        uint32_t x[2];
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const float p0 = ex2(s[c + 2 * q]), p1 = ex2(s[c + 2 * q + 1]);
                             sums[c / 2 + q] = fma2(pack2(p0, p1), inv, sums[c / 2 + q]);
-                            const uint32_t x = f32x2_to_f16x2(p0, p1);
-                            h[q] = x + 0x00400040u;  // to the nearest multiple of three fraction bits
-                            l[q] = mul_f16x2(sub_f16x2(x, h[q] & 0xff80ff80u), 0x5c005c00u) + 0x00800080u;  // times 256
+                            x[q] = f32x2_to_f16x2(p0, p1);
+                        }
+                        uint32_t h[2], m[2], l[2];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            h[q] = x[q] + 0x00400040u;  // to the nearest multiple of three fraction bits
+                            const uint32_t rest = times256(sub_f16x2(x[q], h[q] & 0xff80ff80u));
+                            m[q] = rest + 0x00800080u;
+                            if (P3) l[q] = sub_f16x2(rest, m[q] & 0xff00ff00u) + 0x00800080u;
                             h[q] <<= 1;
                         }
                         hi[c / 4] = __byte_perm(h[0], h[1], 0x7531);
-                        lo[c / 4] = __byte_perm(l[0], l[1], 0x7531);
+                        mid[c / 4] = e5m2_bits(m[0], m[1]);
+                        if (P3) lo[c / 4] = e5m2_bits(l[0], l[1]);
                     }
                     if (tile >= 1) wait(&ctl->out_done, (tile - 1) & 1);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const int at = swizzled(key, (half * 2 + q) * 16, 64);
-                        *reinterpret_cast<uint4 *>(weights + at) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-                        *reinterpret_cast<uint4 *>(weights + kKeys * kRows + at) =
-                            make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+                        uint8_t *at = weights + swizzled(key, (half * 2 + q) * 16, 64);
+                        const auto put = [&](int term, const uint32_t(&v)[8]) {
+                            *reinterpret_cast<uint4 *>(at + term * kKeys * kRows) =
+                                make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        };
+                        put(0, hi);
+                        put(1, mid);
+                        if (P3) put(2, lo);
                     }
                     if (!in) {  // rows past the end: zero weights must meet finite codes
                         uint32_t sl = slot;
@@ -1255,6 +1314,11 @@ bool encode_rows(CUtensorMap *map, const void *base, uint64_t width, uint64_t n,
 
 constexpr int kMaxDevices = 64;
 
+template <bool Q3, bool P3>
+cudaError_t allow_smem(int bytes) {
+    return cudaFuncSetAttribute(attn_paged_kernel<Q3, P3>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // SM count and opt-in shared memory of the current device, after allowing the kernel all of it
 // (queried once per device).
 bool device_info(int &sms, int &smem) {
@@ -1267,7 +1331,8 @@ bool device_info(int &sms, int &smem) {
     }
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        allow_smem<false, false>(smem) != cudaSuccess || allow_smem<false, true>(smem) != cudaSuccess ||
+        allow_smem<true, false>(smem) != cudaSuccess || allow_smem<true, true>(smem) != cudaSuccess)
         return false;
     if (dev < kMaxDevices) {
         smem_cache[dev].store(smem, std::memory_order_relaxed);
@@ -1358,10 +1423,10 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     a.head_blocks = (nh + kRows - 1) / kRows;
     a.heads_per = (nh + a.head_blocks - 1) / a.head_blocks;
     a.group = a.head_blocks > 1 ? 1 : kRows / nh;
-    a.q_bf16 = q_dtype == MEMQ_BF16;
     a.out_bf16 = out_dtype == MEMQ_BF16;
     a.scale_log2 = scale * kLog2e;
-    const int fixed = smem_ring_off(kv_rank, d_rope) + smem_tail();
+    const bool q3 = q_dtype == MEMQ_F32, p3 = out_dtype == MEMQ_F32;
+    const int fixed = smem_ring_off(q3, p3, kv_rank, d_rope) + smem_tail();
     a.slots = std::min(kMaxSlots, (smem - fixed) / kPiece);
     if (a.slots < kv_rank / 128) return MEMQ_ERR_LAUNCH;
     const uint64_t width = static_cast<uint64_t>(kv_rank + d_rope), pool = static_cast<uint64_t>(n_pages) * page_size;
@@ -1381,7 +1446,9 @@ extern "C" int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_paged_kernel, lat, rope, a) != cudaSuccess) return MEMQ_ERR_LAUNCH;
+    const auto kernel = q3 ? (p3 ? attn_paged_kernel<true, true> : attn_paged_kernel<true, false>)
+                           : (p3 ? attn_paged_kernel<false, true> : attn_paged_kernel<false, false>);
+    if (cudaLaunchKernelEx(&cfg, kernel, lat, rope, a) != cudaSuccess) return MEMQ_ERR_LAUNCH;
     const int64_t items = n_tok * a.head_blocks;  // at least the number of items
     const unsigned x = static_cast<unsigned>(std::min<int64_t>(items, grid));
     // About eight CTAs an SM over all items, and no more than an item's rows have units of 128 dims.
