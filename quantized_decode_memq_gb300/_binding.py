@@ -35,6 +35,8 @@ class Container(enum.IntEnum):
 
 
 class Dtype(enum.IntEnum):
+    """Element types of the C entry points that take one (memq_dtype)."""
+
     F32 = 0
     BF16 = 1
 
@@ -590,7 +592,7 @@ def memq_mla_attn_gathered(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, idx: 
     return out
 
 
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+_DTYPES = {torch.float32: Dtype.F32, torch.bfloat16: Dtype.BF16}
 
 
 def _float(name: str, t: torch.Tensor, dtype=None, shape=None):

@@ -148,3 +148,15 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     b._here("f", On(0), None, On(0))
     with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
         b._here("f", On(0), None, On(1))
+
+
+def test_dtype_is_the_headers_enum():
+    import os
+    import re
+    import quantized_decode_memq_gb300 as m
+    from quantized_decode_memq_gb300 import _binding, build
+    with open(os.path.join(build.INCLUDE, "memq.h")) as f:
+        body = re.search(r"typedef enum memq_dtype \{(.*?)\}", f.read()).group(1)
+    assert {k: int(v) for k, v in re.findall(r"MEMQ_(\w+) = (\d+)", body)} == {d.name: int(d) for d in m.Dtype}
+    assert _binding._DTYPES == {torch.float32: m.Dtype.F32, torch.bfloat16: m.Dtype.BF16}
+    assert all(isinstance(d, m.Dtype) for d in _binding._DTYPES.values())
