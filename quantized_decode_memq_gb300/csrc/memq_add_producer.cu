@@ -229,7 +229,8 @@ extern "C" int memq_add_rmsnorm_q8_1(const float *x, const float *res, const flo
     const int nwarps = ((nf4 + v - 1) / v + 31) / 32;
     // A cluster of eight shares a row that is wider than 8192 (us, 8 CTAs a row against 2: 8 rows of
     // 17408 4.3 / 5.3, 64 6.9 / 7.2, 512 31.4 / 45.5), and one wider than 4096 while there are SMs for it
-    // (8 / 1: 1 row of 5120 3.2 / 3.4, 8 of 8192 3.4 / 4.3, but 2048 of 5120 44.2 / 30.1).
+    // (8 / 1: 1 row of 5120 3.2 / 3.5, 19 of 5120 3.3 / 3.6, 19 of 8192 3.8 / 4.6, where an SM has one CTA; past
+    // two each the cluster loses: 40 of 8192 4.7 / 4.9, 76 5.0 / 4.6, 152 8.2 / 4.7).
     const bool split = v == 16 || (v == 8 && rows * kMaxCluster <= sms);
     const int per_cta = split ? (nwarps + kMaxCluster - 1) / kMaxCluster : nwarps;
     const int ctas = (nwarps + per_cta - 1) / per_cta;
@@ -238,8 +239,8 @@ extern "C" int memq_add_rmsnorm_q8_1(const float *x, const float *res, const flo
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     // Up to 4096 columns, threads share a summing thread's slices only while two CTAs an SM serve all rows:
-    // more rows have the loads in flight without it (us, shared / not: 160 x 4096 5.2 / 5.8, 3000 x 4096
-    // 43.7 / 31.7).
+    // more rows have the loads in flight without it (us, shared / not: 160 x 4096 4.6 / 6.0, 304 x 4096 4.7 /
+    // 4.5, 305 x 4096 6.8 / 6.4, 500 x 4096 8.1 / 6.5; 250 x 2048 5.0 / 5.5, 912 x 2048 8.0 / 7.5).
     const bool few = rows <= 2 * sms;
     // Up to 8192 columns, w is loaded after the sum once many rows follow one another on an SM: other rows
     // hide its latency, and the first loads go out ahead of it (us, after the sum / before: 1000 x 7168
