@@ -705,9 +705,10 @@ def memq_mla_attn_paged(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, scales: 
     q_lat f32 or bf16 [n_tok, nh, kv_rank]; q_pe the same type [n_tok, nh, d_rope], or None (d_rope
     0); cache, scales as memq_mla_cache_append writes them; block_table int32 [n_seq, max_pages];
     kv_len int32 [n_seq]; cu_q int32 [n_seq + 1] -> out [n_tok, nh, kv_rank], bf16 unless an f32
-    `out` is given.  The types choose the precision of the products: f32 queries, and the weights of f32
-    outputs, count to 2^-11, the weights of bf16 outputs to 2^-8; bf16 is faster.  workspace: uint8 scratch of at least memq_mla_attn_paged_workspace(kv_rank)
-    bytes, one per call that may run at the same time; a new one is taken when it is None."""
+    `out` is given.  The types choose the precision of the products: f32 queries, and the weights of
+    f32 outputs, count to 2^-11, the weights of bf16 outputs to 2^-8; bf16 is faster.  workspace:
+    uint8 scratch of at least memq_mla_attn_paged_workspace(kv_rank) bytes, one per call that may run
+    at the same time; a new one is taken when it is None."""
     fn = "memq_mla_attn_paged"
     q_kind = _float("q_lat", q_lat)
     if q_lat.dim() != 3:
