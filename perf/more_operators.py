@@ -265,7 +265,7 @@ def _plan(s):
     slot = table[b, (pos // page).clamp(max=table.shape[1] - 1)].long() * page + pos % page
     minus = torch.full_like(tok, -1)
     out = {"slots": torch.where(live & granted[b], slot, minus), "positions": torch.where(live, pos, minus),
-           "cu_q": cu, "kv_len": keep + torch.where(granted, new, torch.zeros_like(new)),
+           "cu_q": cu, "kv_len": torch.where(granted, keep + new, cached),
            "granted": granted, "n_free": (stack - pop.sum()).view(1)}
     out = {k: v.to(torch.int32) for k, v in out.items()}
     return dict(out, table=table, free=free)
@@ -457,7 +457,7 @@ def _exact_plan(s, case):
             positions.append(i)
             slots.append(table[b][i // page] * page + i % page if ok else -1)
         cu.append(cu[-1] + new)
-        kv_len.append(keep + new if ok else keep)
+        kv_len.append(keep + new if ok else cached)
         granted.append(int(ok))
     slots += [-1] * (n_tok - len(slots))
     positions += [-1] * (n_tok - len(positions))
