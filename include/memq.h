@@ -14,7 +14,9 @@
  * memq_repack_e4m3[_blk128]_q8_0, the t <= 8 MLA decode attention kernels memq_mla_absorb_q,
  * memq_mla_attn_gathered and memq_mla_decompress_v, the producer with the residual stream's addition
  * in front, memq_add_rmsnorm_q8_1, and latent attention over an 8-bit paged cache:
- * memq_mla_cache_append, memq_mla_cache_read and memq_mla_attn_paged.
+ * memq_mla_cache_append, memq_mla_cache_read and memq_mla_attn_paged.  Of a serving step over paged caches:
+ * the block tables and slots, memq_page_plan, the 8-bit cache of keys and values and the attention of grouped
+ * heads over it, memq_kv_cache_append, memq_kv_cache_read and memq_attn_paged, and the sampler memq_sample.
  *
  * The operations are the ones defined on the memra-engine 0.125.0 source pages:
  * q8_fuse_gate.rs (module doc: the `rms_norm` -> `quantize_q8_1` chain and the fused
@@ -410,6 +412,144 @@ int memq_mla_attn_paged(int q_dtype, const void *q_lat, const void *q_pe, const 
  * when the device cannot be queried. */
 int64_t memq_mla_attn_paged_workspace(int kv_rank);
 
+/*
+ * memq_page_plan -- the bookkeeping of one serving step over a paged cache: from every request's
+ * lengths, which pages go back, which are taken, and where each new token's row lies.  Request b has
+ * cached[b] rows, keeps the first keep[b] of them (0: the request is finished or replaced; fewer than
+ * cached[b]: rejected drafts) and gets new_tok[b] more.  With pages(n) = ceil(n / page_size):
+ *     have = pages(cached[b]);  need = pages(keep[b] + new_tok[b])
+ *     have > need: the pages of columns need .. have - 1 of its table go on the stack of free pages
+ *     have < need: columns have .. need - 1 get pages from the stack's top
+ * All pages that go back are pushed first, in (request, column) order, then pages are popped in the same
+ * order.  A request is served (granted[b] = 1) when the pops up to and including its own fit on the stack,
+ * and those that need none always are; keep + new_tok may not pass max_pages * page_size.  One that is not
+ * served keeps its rows and pages as they were, and its new tokens get no slots.
+ *   cached, keep, new_tok   device int32 [n_seq]; keep may be NULL (every request keeps its rows)
+ *   block_table  device int32 [n_seq][max_pages], updated; entries from need on are left as they are
+ *   free_pages   device int32 [n_pages]: a stack of page indices, its top at *n_free - 1; updated
+ *   n_free       device, one int32;  n_free_out  its new value
+ *   kv_len       device int32 [n_seq]: keep + new_tok, or cached for a request that was not served: what
+ *                memq_mla_attn_paged and memq_attn_paged take
+ *   cu_q         device int32 [n_seq + 1]: prefix sums of new_tok, of requests that were not served too
+ *   slots        device int32 [n_tok]: page * page_size + offset of each new token's row, what the caches'
+ *                append calls take; -1 for those of requests not served and from cu_q[n_seq] on
+ *   positions    device int32 [n_tok]: keep[b] + i of each request's i-th new token; -1 from cu_q[n_seq] on
+ *   granted      device int32 [n_seq]
+ * kv_len may be cached itself, and n_free_out n_free; other outputs must not overlap inputs.
+ *   1 <= n_seq <= 4096;  n_tok <= 2^24;  page_size a power of two, 16 to 1024;  n_pages * page_size < 2^31;
+ *   max_pages * page_size <= 2^30.  n_seq == 0 with n_tok == 0 is a no-op that accepts NULL pointers.
+ * Nothing outside the arrays is read or written whatever the lengths say: a cached, keep, new_tok or n_free out
+ * of range is clamped, new tokens past n_tok are not served, a page index outside the pool gives slot
+ * -1, and pages that would pass the stack's end are dropped; each sets bit 5 of the device fault word.
+ * Errors: MEMQ_ERR_SHAPE, MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
+ */
+int memq_page_plan(const int32_t *cached, const int32_t *keep, const int32_t *new_tok,
+                   int32_t *block_table, int32_t *free_pages, const int32_t *n_free, int32_t *kv_len,
+                   int32_t *n_free_out, int32_t *cu_q, int32_t *slots, int32_t *positions,
+                   int32_t *granted, int n_seq, int64_t n_tok, int max_pages, int page_size,
+                   int64_t n_pages, void *stream);
+
+/*
+ * The paged cache of keys and values, for heads in groups that share a kv head.  Of keys and of values
+ * there is a pool of n_pages pages; row s (its slot, page * page_size + offset) caches one token:
+ *   cache   device, uint8 E4M3 codes [n_pages][n_kv][page_size][d], 16-byte aligned
+ *   scales  device, f32 [n_pages][n_kv][page_size / 16]: the 16 rows of a block share a scale per kv
+ *           head; element = scale * e4m3(code)
+ * d is 64 or 128; 1 <= n_kv <= 1024; page_size a power of two, 16 to 1024; n_pages * page_size * n_kv < 2^31.
+ *
+ * memq_kv_cache_append: writes the rows k[r], v[r] (r < n) to slots[r].  A block's scale is the least power
+ * of two (2^-100 at least) with |x| <= 448 * scale for all rows that the call writes there, and codes are
+ * e4m3(x / scale), to nearest, ties to even.  Rows of a block are filled in order: a call that writes
+ * its offset 0 starts it afresh; one that does not leaves the scale no smaller than it was, and when it
+ * grows, the codes of the block's other rows are brought to it (exactly, but for codes that fall below E4M3's
+ * normal range, which are rounded).  A token with an infinity or a NaN in a head's k or v is stored there as
+ * NaN keys and zero values, so that queries that see it are NaN and all others are not touched by it.
+ *   dtype         a memq_dtype: the type of k and v
+ *   k, v          device, [n][n_kv][d], 16-byte aligned, rows k_stride and v_stride elements apart (a multiple of
+ *                 16 bytes, >= 0): parts of a wider projection are taken as they lie
+ *   slots         device int32 [n]: a negative slot skips its row; one >= n_pages * page_size skips it too
+ *                 and sets bit 5 of the device fault word.  Rows of the same block must be next to one another,
+ *                 as memq_page_plan makes them (rows of a block that are not leave a mixture of them); of rows
+ *                 with the same slot the last one counts.
+ * memq_kv_cache_read: out[r][h][i] = scale * e4m3(code) of the row slots[r], of one of the two pools, rounded
+ * once to the output's type; a negative slot gives a row of zeros, one outside the pool too, with bit 5 set.
+ *   out           device, dtype [n][n_kv][d], 16-byte aligned
+ * 0 <= n <= 2^24 (0 = no-op).  Errors: MEMQ_ERR_SHAPE, MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
+ */
+int memq_kv_cache_append(int dtype, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                         const int32_t *slots, uint8_t *k_cache, float *k_scales, uint8_t *v_cache,
+                         float *v_scales, int64_t n, int n_kv, int d, int64_t n_pages, int page_size,
+                         void *stream);
+int memq_kv_cache_read(int dtype, const uint8_t *cache, const float *scales, const int32_t *slots,
+                       void *out, int64_t n, int n_kv, int d, int64_t n_pages, int page_size, void *stream);
+
+/*
+ * memq_attn_paged -- causal attention of each sequence's new tokens over its rows of the paged cache of
+ * keys and values.  Sequences, lengths and block table as in memq_mla_attn_paged: sequence b has the query
+ * tokens cu_q[b] .. cu_q[b + 1] - 1, its last t_b tokens, and kv_len[b] cached rows, theirs included; token i
+ * of the t_b sees the rows j <= kv_len[b] - t_b + i.  Query head h reads kv head h / (nh / n_kv):
+ *     s_j = scale * (q . k_j);   out = sum_j softmax(s)_j * v_j
+ * A token that sees no row gets zeros.  Rows of q and out that belong to no sequence are neither read nor
+ * written.
+ *   q_dtype      a memq_dtype: the type of q, [n_tok][nh][d] (device, 16-byte aligned), rows q_stride elements
+ *                apart (a multiple of 16 bytes, >= 0)
+ *   k_cache, k_scales, v_cache, v_scales   the pools; scales finite and >= 0; a value's codes in visible rows are
+ *                not NaN (what memq_kv_cache_append writes); rows past a sequence's end may hold anything
+ *   block_table, kv_len, cu_q   as memq_mla_attn_paged
+ *   out_dtype    a memq_dtype: the type of out, [n_tok][nh][d] (device, 16-byte aligned)
+ *   workspace    device, 16-byte aligned, at least memq_attn_paged_workspace(d) bytes; scratch of this
+ *                call alone, neither initialised nor kept
+ *   n_kv divides nh <= 1024;  n_tok <= 2^24;  n_tok * nh < 2^31;  n_seq <= 4096;  max_pages * page_size <= 2^30;
+ *   scale * log2(e) finite.  n_tok == 0 or n_seq == 0 is a no-op that accepts NULL pointers.
+ * Lengths are read on the device only, so a captured call serves other lengths of the same arrays; lengths,
+ * offsets and pages out of range are contained as in memq_mla_attn_paged (bit 5), and a bounded wait that
+ * expires sets bit 6.
+ * Numerics: codes are used exactly, sums, maxima and normalisation are f32.  A query element is rounded to
+ * eleven bits (exact for bf16) down to 2^-29 of its row's largest, an f32 one to 22; a weight times its
+ * values' scale, for bf16 outputs, to eleven bits, in steps of 2^-38 of the largest such product of the row where
+ * those are coarser; to 22 bits for f32 outputs.  A scale of values below 2^-100 counts as 2^-100.  A
+ * query row that is not finite gives NaN.
+ * Results do not depend on timing; they depend on how the keys are split, so the same row may differ in
+ * the last bits between batches.
+ * Errors: MEMQ_ERR_SHAPE (also a workspace too small), MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
+ */
+int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, const uint8_t *k_cache,
+                    const float *k_scales, const uint8_t *v_cache, const float *v_scales,
+                    const int32_t *block_table, const int32_t *kv_len, const int32_t *cu_q, int out_dtype,
+                    void *out, void *workspace, int64_t workspace_bytes, int64_t n_tok, int n_seq, int nh,
+                    int n_kv, int d, int64_t n_pages, int page_size, int max_pages, float scale,
+                    void *stream);
+/* Workspace bytes of memq_attn_paged on the current device; -1 for an unsupported d or when the device
+ * cannot be queried. */
+int64_t memq_attn_paged_workspace(int d);
+
+/*
+ * memq_sample -- one token for each row of logits, from a given random number.  In descending order of
+ * l (equal ones by index), with w_i = exp((l_i - max l) / temperature):
+ *   top_k   keeps the first k tokens (k <= 0 or k >= vocab: all)
+ *   top_p   of those the shortest prefix that has at least p of their weight (p >= 1 or NaN: all; p <= 0: the
+ *           first token)
+ *   min_p   of those the ones with w_i >= min_p (<= 0 or NaN: all; 1 at most), and the first token in any case
+ * and out = the first kept token in the order of indices whose cumulative weight is above u times the kept
+ * tokens' weight (u < 0 or NaN counts as 0, u >= 1 gives the last kept token).  temperature <= 0 or NaN: the largest
+ * logit, the first of equal ones.
+ *   dtype    a memq_dtype: the type of the logits
+ *   logits   device, [rows][vocab], rows `stride` elements apart (>= 0), aligned to an element
+ *   temperature, top_p, min_p, u   device, f32 [rows];  top_k   device int32 [rows]; each but u may be NULL
+ *            (temperature 1, no cut)
+ *   out      device int32 [rows]
+ *   0 <= rows <= 2^20 (0 = no-op);  1 <= vocab <= 360000
+ * NaN logits and those of -infinity are never drawn; in a row without others the first of the largest is given
+ * (NaN below -infinity).  Several of +infinity share the weight.  -0 equals 0.
+ * Numerics: a weight is formed to within 2^-41 of the largest one's and sums are exact, so that a token's
+ * cumulative weight is known to about vocab^(1/2) 2^-42; a weight below 2^-60 counts as 0.  Results do not depend
+ * on timing or on the other rows.
+ * Errors: MEMQ_ERR_SHAPE, MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
+ */
+int memq_sample(int dtype, const void *logits, int64_t stride, const float *temperature,
+                const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                int32_t *out, int64_t rows, int64_t vocab, void *stream);
+
 /* Human-readable name of a memq_status value (static storage; never NULL). */
 const char *memq_status_string(int status);
 
@@ -424,7 +564,8 @@ const char *memq_status_string(int status);
  * memq_mla_absorb_q / memq_mla_decompress_v.  That CTA stopped streaming, waited (bounded) for
  * its copies in flight and returned; the call's outputs are invalid.  Bit 4: a bounded wait of
  * memq_mla_attn_paged expired; the call's outputs are invalid.  Bit 5: a slot, page index or cached
- * length given to the paged cache's calls was out of range (see there).
+ * length given to the paged caches' calls or the page plan was out of range (see there).  Bit 6: a bounded wait of
+ * memq_attn_paged expired; the call's outputs are invalid.
  * Returns MEMQ_ERR_NULL for a NULL fault_out, MEMQ_ERR_DEVICE if the copy fails.
  */
 int memq_device_fault(void *stream, uint32_t *fault_out);

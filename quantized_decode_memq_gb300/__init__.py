@@ -18,7 +18,10 @@ Q8_0 once at load).  The MLA decode attention kernels ``memq_mla_absorb_q``,
 ``memq_mla_attn_gathered`` and ``memq_mla_decompress_v``: mla_decode_arm_gate.rs (module doc).
 ``memq_add_rmsnorm_q8_1`` puts the residual stream's addition in front of stage 1;
 ``memq_mla_cache_append``, ``memq_mla_cache_read`` and ``memq_mla_attn_paged`` keep the latent cache
-in 8 bits and in pages and attend to it, causally, from any number of new tokens.
+in 8 bits and in pages and attend to it, causally, from any number of new tokens;
+``memq_kv_cache_append``, ``memq_kv_cache_read`` and ``memq_attn_paged`` do the same for keys and values of
+grouped heads, with a scale for every 16 tokens of a head, ``memq_page_plan`` keeps the block tables and
+``memq_sample`` draws the next tokens.
 """
 from __future__ import annotations
 
@@ -33,6 +36,8 @@ from ._binding import (  # noqa: F401
     lib,
     lib_path,
     memq_add_rmsnorm_q8_1,
+    memq_attn_paged,
+    memq_attn_paged_workspace,
     memq_decode_step_host,
     memq_device_fault,
     memq_gemv_e4m3,
@@ -41,6 +46,8 @@ from ._binding import (  # noqa: F401
     memq_gemv_e4m3_group,
     memq_gemv_q8_0,
     memq_gemv_q8_0_group,
+    memq_kv_cache_append,
+    memq_kv_cache_read,
     memq_mla_absorb_q,
     memq_mla_attn_gathered,
     memq_mla_attn_paged,
@@ -48,12 +55,14 @@ from ._binding import (  # noqa: F401
     memq_mla_cache_append,
     memq_mla_cache_read,
     memq_mla_decompress_v,
+    memq_page_plan,
     memq_rmsnorm_q8_1,
     memq_rmsnorm_q8_1_gemv_e4m3,
     memq_rmsnorm_q8_1_gemv_e4m3_blk128,
     memq_rmsnorm_q8_1_gemv_q8_0,
     memq_repack_e4m3_blk128_q8_0,
     memq_repack_e4m3_q8_0,
+    memq_sample,
     memq_silu_mul_q8_1,
     memq_status_string,
     memq_version,

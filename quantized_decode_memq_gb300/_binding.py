@@ -95,6 +95,15 @@ def lib() -> ctypes.CDLL:
                                               I32, I32, I32, I64, I32, I32, ctypes.c_float, P]
             L.memq_mla_attn_paged_workspace.argtypes = [I32]
             L.memq_mla_attn_paged_workspace.restype = I64
+            L.memq_page_plan.argtypes = [P] * 12 + [I32, I64, I32, I32, I64, P]
+            L.memq_kv_cache_append.argtypes = [I32, P, I64, P, I64, P, P, P, P, P, I64, I32, I32, I64,
+                                               I32, P]
+            L.memq_kv_cache_read.argtypes = [I32, P, P, P, P, I64, I32, I32, I64, I32, P]
+            L.memq_attn_paged.argtypes = [I32, P, I64, P, P, P, P, P, P, P, I32, P, P, I64, I64, I32, I32,
+                                          I32, I32, I64, I32, I32, ctypes.c_float, P]
+            L.memq_attn_paged_workspace.argtypes = [I32]
+            L.memq_attn_paged_workspace.restype = I64
+            L.memq_sample.argtypes = [I32, P, I64, P, P, P, P, P, P, I64, I64, P]
             L.memq_device_fault.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
             L.memq_status_string.argtypes = [I32]
             L.memq_status_string.restype = ctypes.c_char_p
@@ -745,5 +754,228 @@ def memq_mla_attn_paged(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, scales: 
                                    _ptr(block_table), _ptr(kv_len), _ptr(cu_q), o_kind, _ptr(out),
                                    _ptr(workspace), need, n_tok, n_seq, nh, kv_rank,
                                    d_rope, pages, page_size, max_pages, scale, st)
+    _check(fn, rc)
+    return out
+
+
+def _i32(name: str, t, shape, device):
+    """An int32 CUDA tensor of the shape, a new one for None."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    return _cuda(name, t, torch.int32, shape)
+
+
+def memq_page_plan(cached: torch.Tensor, new_tok: torch.Tensor, block_table: torch.Tensor,
+                   free_pages: torch.Tensor, n_free: torch.Tensor, page_size: int, n_tok: int, *, keep=None,
+                   kv_len=None, n_free_out=None, cu_q=None, slots=None, positions=None, granted=None,
+                   stream=None):
+    """Pages, slots and offsets of one step from the requests' lengths, on the device.
+
+    cached, new_tok, keep int32 [n_seq] (keep None: every request keeps its rows); block_table int32 [n_seq,
+    max_pages] and free_pages int32 [n_pages] (a stack, its top at n_free - 1) are updated in place; n_free
+    int32 [1]; n_tok: room for new tokens, of all requests.
+    Returns (slots [n_tok], positions [n_tok], cu_q [n_seq + 1], kv_len [n_seq], granted [n_seq],
+    n_free_out [1]), all int32.  kv_len may be cached itself and n_free_out n_free (both in place)."""
+    fn = "memq_page_plan"
+    _cuda("cached", cached, torch.int32)
+    if cached.dim() != 1:
+        raise ValueError(f"{fn}: cached must be [n_seq]")
+    n_seq = cached.shape[0]
+    _cuda("new_tok", new_tok, torch.int32, (n_seq,))
+    if keep is not None:
+        _cuda("keep", keep, torch.int32, (n_seq,))
+    _cuda("block_table", block_table, torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != n_seq:
+        raise ValueError(f"{fn}: block_table must be [{n_seq}, max_pages]")
+    _cuda("free_pages", free_pages, torch.int32)
+    if free_pages.dim() != 1:
+        raise ValueError(f"{fn}: free_pages must be [n_pages]")
+    _cuda("n_free", n_free, torch.int32, (1,))
+    if n_tok < 0:
+        raise ValueError(f"{fn}: n_tok must not be negative")
+    dev = cached.device
+    slots = _i32("slots", slots, (n_tok,), dev)
+    positions = _i32("positions", positions, (n_tok,), dev)
+    cu_q = _i32("cu_q", cu_q, (n_seq + 1,), dev)
+    kv_len = _i32("kv_len", kv_len, (n_seq,), dev)
+    granted = _i32("granted", granted, (n_seq,), dev)
+    n_free_out = _i32("n_free_out", n_free_out, (1,), dev)
+    _here(fn, cached, new_tok, keep, block_table, free_pages, n_free, slots, positions, cu_q, kv_len, granted,
+          n_free_out)
+    rc = lib().memq_page_plan(_ptr(cached), _ptr(keep), _ptr(new_tok), _ptr(block_table), _ptr(free_pages),
+                              _ptr(n_free), _ptr(kv_len), _ptr(n_free_out), _ptr(cu_q), _ptr(slots),
+                              _ptr(positions), _ptr(granted), n_seq, n_tok, block_table.shape[1], page_size,
+                              free_pages.shape[0], _stream(stream))
+    _check(fn, rc)
+    return slots, positions, cu_q, kv_len, granted, n_free_out
+
+
+def _rows(name: str, t, dtype=None, shape=None):
+    """An f32 or bf16 CUDA tensor [n, heads, d] whose token rows are whole and any distance apart; its
+    memq_dtype and that distance."""
+    kind = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if kind is None or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'torch.float32 or torch.bfloat16'}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape or '[n, heads, d]'}")
+    n, heads, d = t.shape
+    if n == 0 or heads == 0 or d == 0:
+        return kind, heads * d
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}: the heads of a token must lie next to one another")
+    return kind, s0 if n > 1 else heads * d
+
+
+def _kv_pool(fn: str, name: str, cache, scales, shape=None):
+    """The pool's (n_pages, n_kv, page_size, d)."""
+    _cuda(name + "_cache", cache, torch.uint8, shape)
+    if cache.dim() != 4:
+        raise ValueError(f"{fn}: {name}_cache must be [n_pages, n_kv, page_size, d]")
+    pages, n_kv, page_size, _ = cache.shape
+    _cuda(name + "_scales", scales, torch.float32, (pages, n_kv, page_size // 16))
+    return cache.shape
+
+
+def memq_kv_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, *, stream=None):
+    """Quantise keys and values into the paged cache: token r goes to pool row slots[r].
+
+    k, v f32 or bf16 [n, n_kv, d], each token's heads next to one another (views of a wider projection are
+    taken as they lie); slots int32 [n], negative = skip, rows of the same 16-token block next to one another;
+    k_cache, v_cache uint8 (E4M3 codes) [n_pages, n_kv, page_size, d] and k_scales, v_scales f32 [n_pages, n_kv,
+    page_size / 16] are written in place."""
+    fn = "memq_kv_cache_append"
+    kind, k_stride = _rows("k", k)
+    n, n_kv, d = k.shape
+    _, v_stride = _rows("v", v, k.dtype, k.shape)
+    pages, heads, page_size, width = _kv_pool(fn, "k", k_cache, k_scales)
+    if (heads, width) != (n_kv, d):
+        raise ValueError(f"{fn}: the cache holds {heads} heads of {width}, k has {n_kv} of {d}")
+    _kv_pool(fn, "v", v_cache, v_scales, k_cache.shape)
+    _cuda("slots", slots, torch.int32, (n,))
+    _here(fn, k, v, slots, k_cache, v_cache, k_scales, v_scales)
+    rc = lib().memq_kv_cache_append(kind, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), _ptr(k_cache),
+                                    _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), n, n_kv, d, pages, page_size,
+                                    _stream(stream))
+    _check(fn, rc)
+
+
+def memq_kv_cache_read(cache: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, *, out=None,
+                       dtype=torch.bfloat16, stream=None):
+    """The values of the pool rows named by slots (int32 [n], repeats allowed, negative = zeros), of keys or
+    of values: f32 or bf16 [n, n_kv, d], in `out` or a new tensor of `dtype`."""
+    fn = "memq_kv_cache_read"
+    pages, n_kv, page_size, d = _kv_pool(fn, "kv", cache, scales)
+    _cuda("slots", slots, torch.int32)
+    if slots.dim() != 1:
+        raise ValueError(f"{fn}: slots must be [n]")
+    n = slots.shape[0]
+    if out is None:
+        out = torch.empty((n, n_kv, d), dtype=dtype, device=cache.device)
+    kind = _float("out", out, None, (n, n_kv, d))
+    _here(fn, cache, scales, slots, out)
+    rc = lib().memq_kv_cache_read(kind, _ptr(cache), _ptr(scales), _ptr(slots), _ptr(out), n, n_kv, d, pages,
+                                  page_size, _stream(stream))
+    _check(fn, rc)
+    return out
+
+
+_attn_workspace_bytes = {}  # by (device, d): fixed by the device's SM count
+
+
+def memq_attn_paged_workspace(d: int) -> int:
+    """Workspace bytes of memq_attn_paged on the current device."""
+    key = (_cur_device() if _cur_device is not None else torch.cuda.current_device(), d)
+    n = _attn_workspace_bytes.get(key)
+    if n is None:
+        n = lib().memq_attn_paged_workspace(d)
+        if n < 0:
+            raise ValueError(f"memq_attn_paged: d must be 64 or 128, got {d}")
+        _attn_workspace_bytes[key] = n
+    return n
+
+
+def memq_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                    v_scales: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor,
+                    scale: float, *, out=None, workspace=None, stream=None):
+    """Causal attention of each sequence's new tokens over its rows of the paged cache of keys and values.
+
+    q f32 or bf16 [n_tok, nh, d], each token's heads next to one another; caches and scales as
+    memq_kv_cache_append writes them, n_kv dividing nh; block_table int32 [n_seq, max_pages]; kv_len int32 [n_seq];
+    cu_q int32 [n_seq + 1] -> out [n_tok, nh, d], of q's type unless an `out` is given.  The types choose the
+    precision of the products: f32 queries, and the weights of f32 outputs, count to 22 bits, otherwise eleven;
+    bf16 is faster.  workspace: uint8 scratch of at least memq_attn_paged_workspace(d) bytes, one per call
+    that may run at the same time; a new one is taken when it is None."""
+    fn = "memq_attn_paged"
+    q_kind, q_stride = _rows("q", q)
+    n_tok, nh, d = q.shape
+    pages, n_kv, page_size, width = _kv_pool(fn, "k", k_cache, k_scales)
+    if width != d:
+        raise ValueError(f"{fn}: the cache's heads have {width} elements, q's {d}")
+    _kv_pool(fn, "v", v_cache, v_scales, k_cache.shape)
+    _cuda("block_table", block_table, torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError(f"{fn}: block_table must be [n_seq, max_pages]")
+    n_seq, max_pages = block_table.shape
+    _cuda("kv_len", kv_len, torch.int32, (n_seq,))
+    _cuda("cu_q", cu_q, torch.int32, (n_seq + 1,))
+    if out is None:
+        out = torch.empty((n_tok, nh, d), dtype=q.dtype, device=q.device)
+    o_kind = _float("out", out, None, (n_tok, nh, d))
+    _here(fn, q, k_cache, v_cache, k_scales, v_scales, block_table, kv_len, cu_q, out, workspace)
+    st = _stream(stream)
+    if workspace is None:
+        need = memq_attn_paged_workspace(d)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:  # memory of the stream that uses it
+            with torch.cuda.stream(torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _cuda("workspace", workspace, torch.uint8)
+        need = workspace.numel()
+    rc = lib().memq_attn_paged(q_kind, _ptr(q), q_stride, _ptr(k_cache), _ptr(k_scales), _ptr(v_cache),
+                               _ptr(v_scales), _ptr(block_table), _ptr(kv_len), _ptr(cu_q), o_kind, _ptr(out),
+                               _ptr(workspace), need, n_tok, n_seq, nh, n_kv, d, pages, page_size, max_pages,
+                               scale, st)
+    _check(fn, rc)
+    return out
+
+
+def memq_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=None, top_k=None, top_p=None, min_p=None,
+                out=None, stream=None):
+    """One token for each row of logits: temperature, then top-k, top-p of what is left, min-p of the largest
+    weight, then the draw with u in [0, 1) over the kept tokens in the order of their indices.
+
+    logits f32 or bf16 [rows, vocab], rows any distance apart; u, temperature, top_p, min_p f32 [rows]; top_k
+    int32 [rows]; None leaves a cut out (temperature 1).  temperature <= 0: the first largest logit.  Returns int32
+    [rows]."""
+    fn = "memq_sample"
+    kind = _DTYPES.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
+    if kind is None:
+        raise TypeError(f"{fn}: logits must be a torch.float32 or torch.bfloat16 tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dim() != 2:
+        raise ValueError(f"{fn}: logits must be [rows, vocab]")
+    rows, vocab = logits.shape
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a row must lie next to one another")
+    _cuda("u", u, torch.float32, (rows,))
+    for name, t in (("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
+        if t is not None:
+            _cuda(name, t, torch.float32, (rows,))
+    if top_k is not None:
+        _cuda("top_k", top_k, torch.int32, (rows,))
+    out = _i32("out", out, (rows,), logits.device)
+    _here(fn, logits, u, temperature, top_k, top_p, min_p, out)
+    rc = lib().memq_sample(kind, _ptr(logits), logits.stride(0) if rows > 1 else vocab, _ptr(temperature),
+                           _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(out), rows, vocab,
+                           _stream(stream))
     _check(fn, rc)
     return out

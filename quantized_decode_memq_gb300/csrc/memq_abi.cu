@@ -10,6 +10,9 @@ int memq_internal_fault_q8_0(unsigned int *out, bool clear);
 int memq_internal_fault_mla(unsigned int *out, bool clear);
 int memq_internal_fault_cache(unsigned int *out, bool clear);
 int memq_internal_fault_paged(unsigned int *out, bool clear);
+int memq_internal_fault_plan(unsigned int *out, bool clear);
+int memq_internal_fault_kv(unsigned int *out, bool clear);
+int memq_internal_fault_attn(unsigned int *out, bool clear);
 int memq_internal_step_host_e4m3(const float *x_host, float *x_dev, const float *wn, float eps,
                                  const void *w, const float *aux, int8_t *qs, float *d, float *z,
                                  float *y_dev, float *y_host, int64_t out_f, int64_t in_f, int m,
@@ -45,12 +48,13 @@ extern "C" int memq_decode_step_host(int container, const float *x_host, float *
 extern "C" int memq_device_fault(void *stream, uint32_t *fault_out) {
     if (!fault_out) return MEMQ_ERR_NULL;
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MEMQ_ERR_DEVICE;
-    unsigned int a = 0, b = 0, c = 0, e = 0, f = 0, g = 0;
+    unsigned int a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, h = 0, i = 0, j = 0;
     if (memq_internal_fault_e4m3(&a, true) || memq_internal_fault_blk128(&b, true) ||
         memq_internal_fault_q8_0(&c, true) || memq_internal_fault_mla(&e, true) ||
-        memq_internal_fault_cache(&f, true) || memq_internal_fault_paged(&g, true))
+        memq_internal_fault_cache(&f, true) || memq_internal_fault_paged(&g, true) ||
+        memq_internal_fault_plan(&h, true) || memq_internal_fault_kv(&i, true) || memq_internal_fault_attn(&j, true))
         return MEMQ_ERR_DEVICE;
-    *fault_out = a | b | c | e | f | g;
+    *fault_out = a | b | c | e | f | g | h | i | j;
     return MEMQ_OK;
 }
 

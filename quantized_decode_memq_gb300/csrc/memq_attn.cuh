@@ -1,0 +1,88 @@
+// memq_attn.cuh -- what the kernels of memq_attn_paged share: their arguments, the sequences' sizes, the
+// partial results that they leave in the workspace.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "memq.h"
+#include "memq_dev.cuh"
+#include "memq_tc.cuh"
+
+namespace memq {
+
+constexpr unsigned int kAttnFaultWait = 64;   // a bounded wait expired
+constexpr unsigned int kAttnFaultInput = 32;  // a length or page index was out of range
+
+constexpr int kAttnBlock = 16;  // keys that share a scale
+constexpr int kAttnMaxSeqs = 4096;
+constexpr int kAttnMaxCached = 1 << 30;  // rows a sequence
+constexpr int kAttnMaxGrid = 256;
+constexpr float kAttnUnset = -1e30f;  // a reference before the first visible key
+constexpr float kAttnLog2e = 1.4426950408889634f;
+// Weights are 2^kAttnTop at the reference: f16 keeps eleven bits of them down to 2^-14 and steps of 2^-24
+// below.  The reference moves when a score exceeds it by kAttnSlack (65504 is the largest f16).
+constexpr float kAttnTop = 13.f;
+constexpr float kAttnSlack = 2.f;
+constexpr float kAttnLeastScale = 0x1p-100f;  // a smaller scale of values counts as this
+constexpr float kAttnLeastLog = -60.f;  // smaller value scales (log2) count as this in the reference
+
+// A piece of an item's rows whose keys were shared among several runs, noted by the run that holds its
+// first key (`rows` is 0 otherwise): the other pieces are those of the runs up to `last`.
+struct __align__(16) AttnOwner {
+    int start;        // the sequence's first token
+    int row0;         // the item's first row among the t * group rows of (sequence, kv head)
+    int last;
+    short head, rows;
+};
+static_assert(sizeof(AttnOwner) == 16, "one load");
+
+struct AttnArgs {
+    const void *q;
+    int64_t q_stride;  // elements from one token's row to the next
+    const float *k_scales, *v_scales;
+    const int32_t *table, *kv_len, *cu_q;
+    void *out;
+    AttnOwner *owner;  // one a run
+    float2 *stats;     // [2 * run + piece][row] (reference, sum of weights)
+    float *part;       // [2 * run + piece][row][d]
+    int n_tok, n_seq, nh, n_kv, group, n_pages, page_shift, max_pages;
+    int rows_from, rows_to;  // sequences with t * group in this range are served
+    int out_bf16;
+    float scale_log2;
+};
+
+struct AttnSeq {
+    int start, t, kv;
+};
+
+// The sequence's lengths, clamped to what the arrays hold.
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int c0, int c1, int kv) {
+    AttnSeq s;
+    s.start = min(max(c0, 0), a.n_tok);
+    s.t = min(max(c1, s.start), a.n_tok) - s.start;
+    s.kv = static_cast<int>(
+        min(static_cast<long long>(max(kv, 0)), static_cast<long long>(a.max_pages) << a.page_shift));
+    return s;
+}
+
+// Row `row` of the pool's [page][kv head][offset] rows that holds key `key` (a multiple of 16) of a
+// sequence and head.
+__device__ __forceinline__ int attn_page(const AttnArgs &a, const int32_t *table, int key, unsigned int *fault) {
+    int page = __ldcg(table + (key >> a.page_shift));
+    if (page < 0 || page >= a.n_pages) {
+        atomicOr(fault, kAttnFaultInput);
+        page = 0;
+    }
+    return page;
+}
+
+// out element offset of row `rr` of a (sequence, kv head).
+__device__ __forceinline__ int64_t attn_out_at(const AttnArgs &a, int start, int head, int rr, int d) {
+    const int tok = rr / a.group;
+    return ((static_cast<int64_t>(start) + tok) * a.nh + head * a.group + (rr - tok * a.group)) * d;
+}
+
+}  // namespace memq

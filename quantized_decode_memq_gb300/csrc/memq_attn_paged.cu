@@ -1,0 +1,724 @@
+// memq_attn_paged.cu -- memq_attn_paged: causal attention of a chunk of new tokens per sequence over a
+// paged E4M3 cache of keys and values, heads in groups that share a kv head.
+//
+//   s_j = scale * ks_j * (q . k_j)          j <= position of the query's token
+//   out = sum_j softmax(s)_j * vs_j * v_j   k_j, v_j codes, ks_j, vs_j the scales of their 16 tokens
+//
+// Codes are exact in f16 (cvt.rn.f16x2.e4m3x2), so both products are f16 products with f32 sums.  What is not
+// a code is rounded to f16: a query row after a power of two that brings its largest element below 2^15 (of an
+// f32 query the remainder, too, in a second product), and a weight, scaled by its values' scale,
+//   p_j = 2^13 exp2(s_j + log2 vs_j - R)
+// under a running reference R of the row that is never more than 2 (log2) behind the largest so far: eleven bits
+// down to 2^-27 of the largest, steps of 2^-38 of it below; for f32 outputs the remainder is a second product.  The
+// sum of weights is kept apart in f32, from p_j / vs_j.
+//
+// The single-token kernel: its time is the cache's bytes, so it is built around a stream.  A warp holds 16
+// query rows (heads of a group, times tokens) as fragments of m16n8k16 products and runs through 32 keys a
+// time; it works alone, with its own ring of TMA copies.  What of the list of all (sequence, kv head, 16
+// rows, 32 keys) tiles a warp serves is one run of equal length, derived from the lengths on the device; the items
+// that two or more warps share leave f32 pieces in the workspace, which a second kernel adds in order.
+// The order of an inner product's terms is free, so lane (g, c) = (lane / 4, lane % 4) of a fragment takes 32 (or
+// 16) consecutive bytes of key g, and of the values the 16 (8) columns from 16 g on: both are read from shared
+// memory 16 bytes at once, and no code is moved between lanes.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "memq_attn.cuh"
+
+namespace memq {
+namespace {
+
+__device__ unsigned int g_attn_fault = 0;
+
+constexpr int kRows = 16;   // query rows of a warp
+constexpr int kKeys = 32;   // keys of a tile
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kWindow = 16;  // tiles whose pages and scales are looked up at once: two blocks a lane pair
+constexpr int kStart = 2;    // tiles that starting an item counts as
+
+template <int D>
+struct Ring {
+    static constexpr int kTile = 2 * kKeys * D;                  // bytes: keys, then values
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kWarpBytes = kStages * kTile;
+    static constexpr int kBytes = kWarps * kWarpBytes;
+};
+
+struct Run {
+    int seq, head, tile_row, tile;  // where it begins
+    int valid;
+};
+
+struct Control {
+    uint64_t full[kWarps][6];
+    long long warp_sum[kWarps];
+};
+
+__host__ __device__ constexpr int smem_bytes(int ring) { return ring + 1024 + static_cast<int>(sizeof(Control)); }
+
+__device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
+
+// Two f32 -> f16x2 and what is left of them.
+__device__ __forceinline__ uint32_t rest_f16x2(float a, float b, uint32_t hi) {
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return f32x2_to_f16x2(a - h.x, b - h.y);
+}
+
+template <int D, bool Q2, bool P2>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const AttnArgs a,
+                     const int box) {
+    constexpr int kSteps = D / 16;  // k16 steps of q . k; n8 columns of the values per thread group
+    constexpr int kStages = Ring<D>::kStages;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFullMask, tid >> 5, 0);
+    const int g = lane >> 2, c = lane & 3;
+    uint8_t *ring = smem + warp * Ring<D>::kWarpBytes;
+    Control *ctl = reinterpret_cast<Control *>(smem + Ring<D>::kBytes);
+
+    griddep_launch_dependents();
+    if (tid == 0) {
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
+        for (int w = 0; w < kWarps; ++w)
+            for (int i = 0; i < kStages; ++i) mbar_init(&ctl->full[w][i], 1);
+        mbar_init_fence();
+    }
+    griddep_wait();
+
+    // ------------------------------------------------------------------ the runs
+    long long *first = reinterpret_cast<long long *>(smem);  // units before each sequence
+    const int per_seq = (a.n_seq + kThreads - 1) / kThreads;
+    bool descends = false;
+    long long sum = 0;
+    for (int i = 0; i < per_seq; ++i) {
+        const int b = tid * per_seq + i;
+        if (b >= a.n_seq) break;
+        const int c0 = __ldcg(a.cu_q + b), c1 = __ldcg(a.cu_q + b + 1), kv = __ldcg(a.kv_len + b);
+        if (c0 < 0 || c0 > c1 || c1 > a.n_tok || kv < 0 || kv > (static_cast<long long>(a.max_pages) << a.page_shift))
+            atomicOr(&g_attn_fault, kAttnFaultInput);
+        descends = descends || c0 > c1;
+        const AttnSeq s = attn_seq(a, c0, c1, kv);
+        const int rows = s.t * a.group;
+        first[b] = sum;
+        if (rows >= a.rows_from && rows <= a.rows_to)
+            sum += static_cast<long long>(a.n_kv) * ((rows + kRows - 1) / kRows) * (tiles_of(s.kv) + kStart);
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) ctl->warp_sum[warp] = incl;
+    const bool nothing = __syncthreads_or(descends);
+    long long before = incl - sum, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += ctl->warp_sum[w];
+        total += ctl->warp_sum[w];
+    }
+    for (int i = 0; i < per_seq; ++i) {
+        const int b = tid * per_seq + i;
+        if (b >= a.n_seq) break;
+        first[b] += before;
+    }
+    __syncthreads();
+    const int run = blockIdx.x * kWarps + warp, runs = gridDim.x * kWarps;
+    const long long per = max(static_cast<long long>(kStart + 1), (total + runs - 1) / runs);
+    long long pos = nothing ? total : run * per;
+    const long long run_hi = min(total, pos + per);
+    int seq = 0;
+    if (pos < run_hi) {
+        int hi = a.n_seq;  // first[seq] <= pos < first[hi]
+        while (hi - seq > 1) {
+            const int mid = (seq + hi) >> 1;
+            if (first[mid] <= pos) seq = mid; else hi = mid;
+        }
+    }
+    long long seq_pos = pos < run_hi ? first[seq] : 0;
+    fence_async_smem();
+    __syncthreads();  // copies may go where the sums lie
+    if (lane == 0) a.owner[run].rows = 0;
+    if (pos >= run_hi) return;
+
+    AttnSeq s = attn_seq(a, __ldcg(a.cu_q + seq), __ldcg(a.cu_q + seq + 1), __ldcg(a.kv_len + seq));
+    int rows = s.t * a.group, row_tiles = (rows + kRows - 1) / kRows, units = tiles_of(s.kv) + kStart;
+    long long at = pos - seq_pos;
+    int head = static_cast<int>(at / (static_cast<long long>(row_tiles) * units));
+    at -= static_cast<long long>(head) * row_tiles * units;
+    int row_tile = static_cast<int>(at / units);
+    int off = max(0, static_cast<int>(at - static_cast<long long>(row_tile) * units) - kStart);
+    long long item_pos = pos - (at - static_cast<long long>(row_tile) * units);  // of the item's first unit
+    uint32_t sent = 0, taken = 0;  // tiles of the ring
+
+    bool dead = false;
+    while (item_pos + kStart + off < run_hi && !dead) {
+        const int n_all = units - kStart;
+        const int end = static_cast<int>(min(static_cast<long long>(n_all), run_hi - item_pos - kStart));
+        // keys that the tile's last row sees; tiles behind them are passed over
+        const int row0 = row_tile * kRows, n_rows = min(kRows, rows - row0);
+        const int tok_lo = row0 / a.group, tok_hi = (row0 + n_rows - 1) / a.group;
+        const int vis = max(0, s.kv - s.t + tok_hi + 1), all_see = max(0, s.kv - s.t + tok_lo + 1);
+        const int t1 = min(end, (vis + kKeys - 1) / kKeys);
+        const int32_t *table = a.table + static_cast<int64_t>(seq) * a.max_pages;
+
+        // ---- pages and scales: lane l serves block l of a window of 32 blocks
+        const auto page_at = [&](int tile) {
+            const int key = tile * kKeys + lane * kAttnBlock;
+            return key < vis && tile < t1 ? attn_page(a, table, key, &g_attn_fault) : -1;
+        };
+        const auto row_at = [&](int page, int tile) {
+            const int key = tile * kKeys + lane * kAttnBlock;
+            return page < 0 ? -1
+                            : static_cast<int>(((static_cast<int64_t>(page) * a.n_kv + head) << a.page_shift) +
+                                               (key & ((1 << a.page_shift) - 1)));
+        };
+        const auto scale_at = [&](const float *scales, int row) { return row < 0 ? 1.f : __ldcg(scales + (row >> 4)); };
+        int win = off;
+        int row_now = row_at(page_at(win), win);
+        float ks_now = scale_at(a.k_scales, row_now), vs_now = scale_at(a.v_scales, row_now);
+        int row_next = row_at(page_at(win + kWindow), win + kWindow);
+        float ks_next = scale_at(a.k_scales, row_next), vs_next = scale_at(a.v_scales, row_next);
+        int page_later = page_at(win + 2 * kWindow);
+
+        const auto send = [&](int tile) {  // the copies of a tile; all lanes
+            const int i = 2 * (tile - win);
+            const int r0 = __shfl_sync(kFullMask, i < 32 ? row_now : row_next, i & 31);
+            const int r1 = __shfl_sync(kFullMask, i < 32 ? row_now : row_next, (i + 1) & 31);
+            if (lane == 0) {
+                const uint32_t slot = sent % kStages;
+                uint64_t *bar = &ctl->full[warp][slot];
+                uint8_t *dst = ring + slot * Ring<D>::kTile;
+                const bool two = box < kKeys;
+                const int boxes = two ? (r1 >= 0 ? 2 : 1) : 1;
+                mbar_arrive_expect_tx(bar, 2 * boxes * box * D);
+                tma_load_2d_plain(dst, &k_map, 0, r0, bar);
+                tma_load_2d_plain(dst + kKeys * D, &v_map, 0, r0, bar);
+                if (boxes == 2) {
+                    tma_load_2d_plain(dst + kAttnBlock * D, &k_map, 0, r1, bar);
+                    tma_load_2d_plain(dst + (kKeys + kAttnBlock) * D, &v_map, 0, r1, bar);
+                }
+            }
+            ++sent;
+        };
+        int next_send = off;
+        for (; next_send < min(t1, off + kStages); ++next_send) send(next_send);
+
+        // ---- the query rows
+        uint32_t q_hi[kSteps][4], q_lo[Q2 ? kSteps : 1][4];
+        float factor[2];  // of the scores, by row
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = g + 8 * k;
+            float x[D / 4];
+            const bool live = r < n_rows;
+            const int rr = row0 + (live ? r : 0), tok = rr / a.group;
+            const int64_t from = (static_cast<int64_t>(s.start) + tok) * a.q_stride +
+                                 (head * a.group + rr - tok * a.group) * D + c * (D / 4);
+            if (Q2) {
+                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + from);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const float4 v = live ? __ldcg(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[4 * i] = v.x;
+                    x[4 * i + 1] = v.y;
+                    x[4 * i + 2] = v.z;
+                    x[4 * i + 3] = v.w;
+                }
+            } else {
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + from);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 v = live ? __ldcg(src + i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                    }
+                }
+            }
+            uint32_t top = 0;  // as bits, infinities and NaN lie above all numbers
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+            top = max(top, __shfl_xor_sync(kFullMask, top, 1));
+            top = max(top, __shfl_xor_sync(kFullMask, top, 2));
+            // the largest comes to [2^14, 2^15); tiny rows keep a normal factor
+            const int e = max(static_cast<int>(top >> 23), 32);
+            const float inv = __uint_as_float(static_cast<uint32_t>(min(254, 127 + 14 - (e - 127))) << 23);
+            const float back = __uint_as_float(static_cast<uint32_t>(max(1, 127 - 14 + (e - 127))) << 23);
+            factor[k] = top < 0x7f800000u ? back * a.scale_log2 : NAN;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float u = x[4 * j + 2 * i] * inv, v = x[4 * j + 2 * i + 1] * inv;
+                    const uint32_t h = f32x2_to_f16x2(u, v);
+                    q_hi[j][2 * i + k] = h;
+                    if (Q2) q_lo[j][2 * i + k] = rest_f16x2(u, v, h);
+                }
+        }
+
+        float o[kSteps * 2][4];  // column group j: columns of this thread 16 (2 c + i) + j
+#pragma unroll
+        for (int j = 0; j < kSteps * 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+        float ref[2] = {kAttnUnset, kAttnUnset}, total_w[2] = {0.f, 0.f};
+        float lv_now = 0.f, inv_now = 1.f;
+        int lim[2];  // keys that a row sees
+#pragma unroll
+        for (int k = 0; k < 2; ++k) lim[k] = min(vis, max(0, s.kv - s.t + (row0 + g + 8 * k) / a.group + 1));
+
+        for (int tile = off; tile < t1; ++tile) {
+            if (tile - win == kWindow) {
+                win = tile;
+                row_now = row_next;
+                ks_now = ks_next;
+                vs_now = vs_next;
+                row_next = row_at(page_later, win + kWindow);
+                ks_next = scale_at(a.k_scales, row_next);
+                vs_next = scale_at(a.v_scales, row_next);
+                page_later = page_at(win + 2 * kWindow);
+            }
+            const uint32_t slot = taken % kStages;
+            if (!warp_wait_bounded(&ctl->full[warp][slot], (taken / kStages) & 1)) {
+                if (lane == 0) atomicOr(&g_attn_fault, kAttnFaultWait);
+                dead = true;
+                break;
+            }
+            ++taken;
+            const uint8_t *kt = ring + slot * Ring<D>::kTile, *vt = kt + kKeys * D;
+            const int key0 = tile * kKeys;
+            const bool masked = key0 + kKeys > all_see;
+
+            // ---- scores of 4 x 8 keys
+            float sc[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int row = n * 8 + g;
+                uint32_t w[D / 16];
+                if (D == 128) {
+                    const uint4 u = lds128(kt + row * 128 + ((2 * c ^ (row & 7)) << 4));
+                    const uint4 v = lds128(kt + row * 128 + (((2 * c + 1) ^ (row & 7)) << 4));
+                    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+                    w[D / 16 - 4] = v.x; w[D / 16 - 3] = v.y; w[D / 16 - 2] = v.z; w[D / 16 - 1] = v.w;
+                } else {
+                    const uint4 u = lds128(kt + row * 64 + ((c ^ (row >> 1 & 3)) << 4));
+                    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) {
+                    uint32_t b0, b1;
+                    e4m3x4_to_f16x2x2(w[j], b0, b1);
+                    mma_f16_16816(sc[n], q_hi[j][0], q_hi[j][1], q_hi[j][2], q_hi[j][3], b0, b1);
+                    if (Q2) mma_f16_16816(sc[n], q_lo[Q2 ? j : 0][0], q_lo[Q2 ? j : 0][1], q_lo[Q2 ? j : 0][2], q_lo[Q2 ? j : 0][3], b0, b1);
+                }
+            }
+            // ---- their maxima, with the values' scales
+            float lv[2], inv_vs[2];
+            const int i0 = 2 * (tile - win);
+            if (tile == win) {  // log2 and reciprocal of the window's value scales; exact for powers of two
+                const float v = vs_now < kAttnLeastScale ? kAttnLeastScale : vs_now;
+                const uint32_t bits = __float_as_uint(v);
+                lv_now = static_cast<float>(static_cast<int>(bits >> 23) - 127) +
+                         __log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+                if (!(v < INFINITY)) lv_now = v;
+                inv_now = __frcp_rn(v);
+            }
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const float ks = __shfl_sync(kFullMask, ks_now, i0 + b);
+                lv[b] = __shfl_sync(kFullMask, lv_now, i0 + b);
+                inv_vs[b] = __shfl_sync(kFullMask, inv_now, i0 + b);
+                const float least = fmaxf(lv[b], kAttnLeastLog);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float f = factor[k] * ks;
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float &x = sc[2 * b + n][2 * k + i];
+                            x *= f;
+                            if (masked && key0 + b * 16 + n * 8 + 2 * c + i >= lim[k]) x = -INFINITY;
+                            m = fmaxf(m, x);
+                        }
+                    top[k] = fmaxf(top[k], m + least);
+                }
+            }
+            const bool move = top[0] > ref[0] + kAttnSlack || top[1] > ref[1] + kAttnSlack;
+            if (__any_sync(kFullMask, move)) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float m = fmaxf(top[k], __shfl_xor_sync(kFullMask, top[k], 1));
+                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 2));
+                    const float to = fmaxf(ref[k], m), by = ex2(ref[k] - to);
+                    ref[k] = to;
+                    total_w[k] *= by;
+#pragma unroll
+                    for (int j = 0; j < kSteps * 2; ++j) {
+                        o[j][2 * k] *= by;
+                        o[j][2 * k + 1] *= by;
+                    }
+                }
+            }
+            // ---- weights
+            uint32_t p_hi[2][4], p_lo[P2 ? 2 : 1][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float shift = lv[b] - ref[k] + kAttnTop;
+                    const float back = inv_vs[b];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float p0 = ex2(sc[2 * b + n][2 * k] + shift), p1 = ex2(sc[2 * b + n][2 * k + 1] + shift);
+                        total_w[k] = fmaf(p0 + p1, back, total_w[k]);
+                        const uint32_t h = f32x2_to_f16x2(p0, p1);
+                        p_hi[b][2 * n + k] = h;
+                        if (P2) p_lo[P2 ? b : 0][2 * n + k] = rest_f16x2(p0, p1, h);
+                    }
+                }
+            // ---- values
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t w[4][D / 32];  // keys 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = b * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
+                    if (D == 128) {
+                        const uint4 u = lds128(vt + row * 128 + ((g ^ (row & 7)) << 4));
+                        w[i][0] = u.x; w[i][1] = u.y; w[i][D / 32 - 2] = u.z; w[i][D / 32 - 1] = u.w;
+                    } else {
+                        const uint2 u = lds64(vt + row * 64 + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8);
+                        w[i][0] = u.x; w[i][1] = u.y;
+                    }
+                    if (masked && key0 + row >= vis) {  // zero weights must meet finite codes
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j) w[i][j] = 0;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    uint32_t lo[4], hi[4];
+                    e4m3x4_to_f16x2x2(__byte_perm(w[0][j], w[1][j], 0x5140), lo[0], lo[1]);
+                    e4m3x4_to_f16x2x2(__byte_perm(w[0][j], w[1][j], 0x7362), lo[2], lo[3]);
+                    e4m3x4_to_f16x2x2(__byte_perm(w[2][j], w[3][j], 0x5140), hi[0], hi[1]);
+                    e4m3x4_to_f16x2x2(__byte_perm(w[2][j], w[3][j], 0x7362), hi[2], hi[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mma_f16_16816(o[4 * j + i], p_hi[b][0], p_hi[b][1], p_hi[b][2], p_hi[b][3], lo[i], hi[i]);
+                        if (P2) mma_f16_16816(o[4 * j + i], p_lo[P2 ? b : 0][0], p_lo[P2 ? b : 0][1], p_lo[P2 ? b : 0][2], p_lo[P2 ? b : 0][3], lo[i], hi[i]);
+                    }
+                }
+            }
+            __syncwarp();  // all lanes have read the slot
+            if (next_send < t1) send(next_send++);
+        }
+        if (dead) break;
+
+        // ---- the way out: columns 16 (2 c + i) + j of rows g and g + 8 (D = 128)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            total_w[k] += __shfl_xor_sync(kFullMask, total_w[k], 1);
+            total_w[k] += __shfl_xor_sync(kFullMask, total_w[k], 2);
+        }
+        const bool whole = off == 0 && end == n_all;
+        const int piece = 2 * run + (off == 0 ? 1 : 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = g + 8 * k;
+            if (r >= n_rows) continue;
+            constexpr int kCols = D / 8;  // columns of one n8 index
+            if (whole) {
+                const float n = total_w[k] == 0.f ? 0.f : __fdiv_rn(1.f, total_w[k]);
+                const int64_t to = attn_out_at(a, s.start, head, row0 + r, D) + c * 2 * kCols;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (a.out_bf16) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to + i * kCols);
+#pragma unroll
+                        for (int j = 0; j < kCols / 8; ++j) {
+                            __nv_bfloat162 v[4];
+#pragma unroll
+                            for (int m = 0; m < 4; ++m)
+                                v[m] = __floats2bfloat162_rn(o[8 * j + 2 * m][2 * k + i] * n, o[8 * j + 2 * m + 1][2 * k + i] * n);
+                            dst[j] = *reinterpret_cast<uint4 *>(v);
+                        }
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to + i * kCols);
+#pragma unroll
+                        for (int j = 0; j < kCols / 4; ++j)
+                            dst[j] = make_float4(o[4 * j][2 * k + i] * n, o[4 * j + 1][2 * k + i] * n,
+                                                 o[4 * j + 2][2 * k + i] * n, o[4 * j + 3][2 * k + i] * n);
+                    }
+                }
+            } else {
+                if (c == 0) a.stats[piece * kRows + r] = make_float2(ref[k], total_w[k]);
+                float *to = a.part + (static_cast<int64_t>(piece) * kRows + r) * D + c * 2 * kCols;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < kCols / 4; ++j)
+                        reinterpret_cast<float4 *>(to + i * kCols)[j] =
+                            make_float4(o[4 * j][2 * k + i], o[4 * j + 1][2 * k + i], o[4 * j + 2][2 * k + i],
+                                        o[4 * j + 3][2 * k + i]);
+            }
+        }
+        if (!whole && off == 0 && lane == 0) {
+            AttnOwner own;
+            own.start = s.start;
+            own.row0 = row0;
+            own.last = static_cast<int>((item_pos + units - 1) / per);
+            own.head = static_cast<short>(head);
+            own.rows = static_cast<short>(n_rows);
+            a.owner[run] = own;
+        }
+
+        // ---- the next item
+        item_pos += units;
+        off = 0;
+        if (item_pos + kStart >= run_hi) break;
+        if (++row_tile == row_tiles) {
+            row_tile = 0;
+            if (++head == a.n_kv) {
+                head = 0;
+                do {
+                    if (++seq >= a.n_seq) return;  // not with lengths that stand still
+                    s = attn_seq(a, __ldcg(a.cu_q + seq), __ldcg(a.cu_q + seq + 1), __ldcg(a.kv_len + seq));
+                    rows = s.t * a.group;
+                } while (rows == 0 || rows < a.rows_from || rows > a.rows_to);
+                row_tiles = (rows + kRows - 1) / kRows;
+                units = tiles_of(s.kv) + kStart;
+            }
+        }
+    }
+    if (dead) {  // copies in flight land before shared memory is given up, each wait bounded
+        for (uint32_t i = taken; i != sent; ++i)
+            (void)warp_wait_bounded(&ctl->full[warp][i % kStages], (i / kStages) & 1);
+    }
+}
+
+// Adds the pieces of the items that several runs shared, in the runs' order.  CTA x serves the item that run x
+// began; a warp a row at a time.
+template <int D>
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, int runs) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int x = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint4 raw = __ldcg(reinterpret_cast<const uint4 *>(a.owner + x));
+    const AttnOwner own = *reinterpret_cast<const AttnOwner *>(&raw);
+    const int parts = min(own.last, runs - 1) - x + 1;
+    constexpr int E = D / 32;
+    for (int r = warp; r < own.rows; r += kWarps) {
+        const auto slot_of = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * x + 1 : 2 * (x + k)) * kRows + r; };
+        float top = kAttnUnset;
+        for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(a.stats + slot_of(k)).x);
+        top = warp_max(top);
+        float acc[E], total = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0.f;
+        for (int k0 = 0; k0 < parts; k0 += 32) {
+            float w = 0.f, l = 0.f;
+            if (k0 + lane < parts) {
+                const float2 st = __ldcg(a.stats + slot_of(k0 + lane));
+                w = ex2(st.x - top);
+                l = st.y * w;
+            }
+            total += warp_sum(l);
+            const int n = min(32, parts - k0);
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const float by = __shfl_sync(kFullMask, w, k);
+                const float *src = a.part + slot_of(k0 + k) * D + lane * E;
+                if (E == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                    acc[0] = fmaf(v.x, by, acc[0]);
+                    acc[1] = fmaf(v.y, by, acc[1]);
+                    acc[E - 2] = fmaf(v.z, by, acc[E - 2]);
+                    acc[E - 1] = fmaf(v.w, by, acc[E - 1]);
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                    acc[0] = fmaf(v.x, by, acc[0]);
+                    acc[1] = fmaf(v.y, by, acc[1]);
+                }
+            }
+        }
+        const float n = total == 0.f ? 0.f : __fdiv_rn(1.f, total);
+        const int64_t to = attn_out_at(a, own.start, own.head, own.row0 + r, D) + lane * E;
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            if (a.out_bf16)
+                *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + to + i) =
+                    __floats2bfloat162_rn(acc[i] * n, acc[i + 1] * n);
+            else
+                *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + to + i) = make_float2(acc[i] * n, acc[i + 1] * n);
+        }
+    }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static const EncodeTiledFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiledFn>(nullptr);
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// Rows of d codes; a box of `rows` whole rows, swizzled over a row.
+bool encode_rows(CUtensorMap *map, const void *base, int d, uint64_t n, uint32_t rows) {
+    const EncodeTiledFn enc = encode_tiled();
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), n};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(d), rows}, step[2] = {1, 1};
+    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+
+template <int D, bool Q2, bool P2>
+bool allow() {
+    return cudaFuncSetAttribute(attn_rows_kernel<D, Q2, P2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem_bytes(Ring<D>::kBytes)) == cudaSuccess;
+}
+
+// SM count of the current device, after allowing the kernels their shared memory (once per device).
+bool device_info(int &sms) {
+    static std::atomic<int> cache[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < kMaxDevices && (sms = cache[dev].load(std::memory_order_acquire)) > 0) return true;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !allow<64, false, false>() ||
+        !allow<64, false, true>() || !allow<64, true, false>() || !allow<64, true, true>() || !allow<128, false, false>() ||
+        !allow<128, false, true>() || !allow<128, true, false>() || !allow<128, true, true>())
+        return false;
+    if (dev < kMaxDevices) cache[dev].store(sms, std::memory_order_release);
+    return true;
+}
+
+bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+int64_t owner_bytes(int runs) { return (static_cast<int64_t>(runs) * sizeof(AttnOwner) + 255) / 256 * 256; }
+int64_t stat_bytes(int runs) { return static_cast<int64_t>(2) * runs * kRows * sizeof(float2); }
+int64_t part_bytes(int runs, int d) { return static_cast<int64_t>(2) * runs * kRows * d * sizeof(float); }
+
+}  // namespace
+}  // namespace memq
+
+// Internal: this translation unit's device fault word (not part of the public header).
+int memq_internal_fault_attn(unsigned int *out, bool clear) {
+    if (cudaMemcpyFromSymbol(out, memq::g_attn_fault, sizeof(unsigned int)) != cudaSuccess) return 1;
+    if (!clear) return 0;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(memq::g_attn_fault, &zero, sizeof(zero)) == cudaSuccess ? 0 : 1;
+}
+
+extern "C" int64_t memq_attn_paged_workspace(int d) {
+    using namespace memq;
+    if (d != 64 && d != 128) return -1;
+    int sms = 0;
+    if (!device_info(sms)) return -1;
+    const int runs = std::min(sms, kAttnMaxGrid) * kWarps;
+    return owner_bytes(runs) + stat_bytes(runs) + part_bytes(runs, d);
+}
+
+extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, const uint8_t *k_cache,
+                               const float *k_scales, const uint8_t *v_cache, const float *v_scales,
+                               const int32_t *block_table, const int32_t *kv_len, const int32_t *cu_q, int out_dtype,
+                               void *out, void *workspace, int64_t workspace_bytes, int64_t n_tok, int n_seq, int nh,
+                               int n_kv, int d, int64_t n_pages, int page_size, int max_pages, float scale, void *stream) {
+    using namespace memq;
+    if ((q_dtype != MEMQ_F32 && q_dtype != MEMQ_BF16) || (out_dtype != MEMQ_F32 && out_dtype != MEMQ_BF16))
+        return MEMQ_ERR_SHAPE;
+    if (n_tok < 0 || n_tok > (1 << 24) || n_seq < 0 || n_seq > kAttnMaxSeqs || nh < 1 || nh > 1024 || n_kv < 1 ||
+        nh % n_kv != 0 || n_tok * nh > 0x7fffffffLL || (d != 64 && d != 128) || page_size < 16 || page_size > 1024 ||
+        (page_size & (page_size - 1)) != 0 || n_pages < 0 || n_pages > 0x7fffffffLL / page_size / n_kv || max_pages < 0 ||
+        max_pages > kAttnMaxCached / page_size || !std::isfinite(scale * kAttnLog2e) || q_stride < 0 ||
+        q_stride > (int64_t{1} << 38))
+        return MEMQ_ERR_SHAPE;
+    if (n_tok == 0 || n_seq == 0) return MEMQ_OK;  // no query rows
+    if (n_pages < 1 || max_pages < 1) return MEMQ_ERR_SHAPE;
+    if (!q || !k_cache || !k_scales || !v_cache || !v_scales || !block_table || !kv_len || !cu_q || !out || !workspace)
+        return MEMQ_ERR_NULL;
+    const int64_t size = q_dtype == MEMQ_F32 ? 4 : 2;
+    if (misaligned(q, 16) || (n_tok > 1 && (q_stride * size) % 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) ||
+        misaligned(k_scales, 4) || misaligned(v_scales, 4) || misaligned(block_table, 4) || misaligned(kv_len, 4) ||
+        misaligned(cu_q, 4) || misaligned(out, 16) || misaligned(workspace, 16))
+        return MEMQ_ERR_ALIGN;
+    int sms = 0;
+    if (!device_info(sms)) return MEMQ_ERR_LAUNCH;
+    const int grid = std::min(sms, kAttnMaxGrid), runs = grid * kWarps;
+    if (workspace_bytes < owner_bytes(runs) + stat_bytes(runs) + part_bytes(runs, d)) return MEMQ_ERR_SHAPE;
+
+    AttnArgs a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.table = block_table;
+    a.kv_len = kv_len;
+    a.cu_q = cu_q;
+    a.out = out;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.owner = reinterpret_cast<AttnOwner *>(ws);
+    a.stats = reinterpret_cast<float2 *>(ws + owner_bytes(runs));
+    a.part = reinterpret_cast<float *>(ws + owner_bytes(runs) + stat_bytes(runs));
+    a.n_tok = static_cast<int>(n_tok);
+    a.n_seq = n_seq;
+    a.nh = nh;
+    a.n_kv = n_kv;
+    a.group = nh / n_kv;
+    a.n_pages = static_cast<int>(n_pages);
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.max_pages = max_pages;
+    a.rows_from = 1;
+    a.rows_to = 0x7fffffff;
+    a.out_bf16 = out_dtype == MEMQ_BF16;
+    a.scale_log2 = scale * kAttnLog2e;
+    const int box = std::min(page_size, kKeys);
+    const uint64_t pool = static_cast<uint64_t>(n_pages) * page_size * n_kv;
+    CUtensorMap k_map, v_map;
+    if (!encode_rows(&k_map, k_cache, d, pool, box) || !encode_rows(&v_map, v_cache, d, pool, box)) return MEMQ_ERR_LAUNCH;
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(d == 128 ? Ring<128>::kBytes : Ring<64>::kBytes));
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const bool q2 = q_dtype == MEMQ_F32, p2 = out_dtype == MEMQ_F32;
+    using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const AttnArgs, const int);
+    static constexpr Kernel kKernels[2][2][2] = {
+        {{attn_rows_kernel<64, false, false>, attn_rows_kernel<64, false, true>},
+         {attn_rows_kernel<64, true, false>, attn_rows_kernel<64, true, true>}},
+        {{attn_rows_kernel<128, false, false>, attn_rows_kernel<128, false, true>},
+         {attn_rows_kernel<128, true, false>, attn_rows_kernel<128, true, true>}}};
+    if (cudaLaunchKernelEx(&cfg, kKernels[d == 128][q2][p2], k_map, v_map, a, box) != cudaSuccess) return MEMQ_ERR_LAUNCH;
+    cfg.gridDim = dim3(static_cast<unsigned>(runs));
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, a, runs) == cudaSuccess
+               ? MEMQ_OK
+               : MEMQ_ERR_LAUNCH;
+}

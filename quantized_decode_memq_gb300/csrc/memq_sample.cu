@@ -1,0 +1,787 @@
+// memq_sample.cu -- memq_sample: one token a row of logits, from a given random number.
+//
+//   w_i = exp((l_i - max) / T), tokens in descending order of l, equal ones by index
+//   top-k: the first k;  top-p: of those the shortest prefix with at least p of their weight;
+//   min-p: of those the ones with w_i >= min_p;  then, in the order of indices, the first token whose
+//   cumulative weight is above u times the total.
+//
+// What is kept is always a prefix of the order, so no row is sorted: a cut (a key and, among equal ones, an
+// index) is found, and the draw runs over the kept tokens by index.
+//
+// A draw and a cut compare sums with a border, and with 1e5 tokens some border is near, so weights are formed to
+// about 2^-41 and summed as 64-bit integers in units of 2^-44: sums do not depend on their order, and a token's
+// probability is exact to 2^-41 of the largest one's.  (l - max) / T is a pair of f32, 2^-x a table of 512 powers
+// times a polynomial, both in integers; below 2^-24 of the largest the hardware's exp2 is exact enough.
+//
+// A cluster of CTAs keeps a row in shared memory, so it is read once; the number of CTAs is chosen to fill
+// the GPU with few rows and to let a row fit with many.  Then, by what the row asks for:
+//   greedy          the first of the largest
+//   top-k           The k-th largest of all is not below t if every one of the C CTAs has ceil(k / C) threads whose
+//                   largest is t or more; what is t or more (usually little over k) is gathered and sorted by one CTA.
+//   top-p           A histogram of x over 2048 steps of 2^-6 bounds the weight above every step; only the
+//                   steps between which the cut must lie (1 or 2% of the weight) are gathered and sorted; finer
+//                   steps when they hold too much.
+//   neither         One pass of weights, the draw from the warps' sums.
+// Rows that defeat this (thousands of equal logits at the cut) are cut by bisection over keys, then over indices.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "memq.h"
+#include "memq_dev.cuh"
+#include "memq_tc.cuh"
+
+namespace memq {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCtas = 8;
+constexpr int kCap = 2048;   // tokens that are sorted
+constexpr int kBins = 2048;
+constexpr int kTable = 512;
+constexpr int kUnitLog = 44;  // weights are integers in units of 2^-44
+constexpr uint32_t kLeastKey = 0x007fffffu;  // of -infinity; NaN has key 0
+constexpr int64_t kMaxVocab = 360000;
+
+struct SampleArgs {
+    const void *logits;
+    int64_t stride;
+    const float *temperature, *top_p, *min_p, *u;
+    const int32_t *top_k;
+    int32_t *out;
+    int vocab, slice;  // tokens of a row, of a CTA
+};
+
+struct __align__(16) Shared {
+    unsigned long long table[kTable];    // 2^(-j / 512) in units of 2^-62
+    unsigned long long list[kCap];       // sorted tokens: key << 32 | ~index, largest first
+    unsigned long long weight[kCap];
+    unsigned long long sums[kMaxCtas][kWarps];  // of every CTA's warps
+    unsigned long long pair[kMaxCtas][2];
+    unsigned long long warp64[2][kWarps];
+    uint32_t hist[kBins];
+    uint32_t from_cta[kMaxCtas];
+    uint32_t warp32[kWarps];
+    unsigned long long cut;      // key << 32 | ~index of the last token that is kept
+    uint32_t count;              // tokens in this CTA's list
+    int window[2];
+    uint32_t found;
+};
+
+// ------------------------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cta_count() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// Nothing is stored to another CTA before it has begun.
+__device__ __forceinline__ void cluster_arrive_entry() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_entry() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `p` in CTA `rank`'s shared memory.
+template <typename T>
+__device__ __forceinline__ T *in_cta(T *p, uint32_t rank) {
+    uint64_t r;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<T *>(r);
+}
+
+// ------------------------------------------------------------------------------ weights
+struct Scale {
+    float top;     // the largest logit
+    float hi, lo;  // log2(e) / T
+};
+
+// x = (top - l) log2(e) / T, rounded to f32: monotone in l, so its steps are ranges of the order.
+__device__ __forceinline__ float coarse(const Scale &s, float l) { return l == s.top ? 0.f : (s.top - l) * s.hi; }
+
+// 2^-x in units of 2^-kUnitLog.
+__device__ __forceinline__ unsigned long long weight_of(const Scale &s, const unsigned long long *table, float l) {
+    if (l == s.top) return 1ull << kUnitLog;
+    // the difference, exactly: dh + dl
+    const float dh = __fsub_rn(s.top, l), bb = __fsub_rn(dh, s.top);
+    const float dl = __fsub_rn(__fsub_rn(s.top, __fsub_rn(dh, bb)), __fadd_rn(l, bb));
+    const float yh = __fmul_rn(dh, s.hi);
+    if (!(yh < 24.f)) {
+        const float w = ex2(static_cast<float>(kUnitLog) - yh);
+        return yh < 60.f ? static_cast<unsigned long long>(__float2uint_rn(w)) : 0ull;
+    }
+    const float yl = __fmaf_rn(dh, s.hi, -yh) + __fmaf_rn(dh, s.lo, dl * s.hi);
+    // the nearest multiple n of 2^-9
+    const float big = 0x1.8p23f / kTable;
+    const float t = __fadd_rn(yh, big);
+    const int n = __float_as_int(t) - __float_as_int(big);
+    const float rh = __fsub_rn(yh, __fsub_rn(t, big));
+    // r = rh + yl as a pair
+    const float r = __fadd_rn(rh, yl), rb = __fsub_rn(r, rh);
+    const float rl = __fadd_rn(__fsub_rn(rh, __fsub_rn(r, rb)), __fsub_rn(yl, rb));
+    // z = r ln 2, |z| < 2^-10.5; 1 - 2^-r = z - z^2/2 + z^3/6 - z^4/24
+    const float kLn2 = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
+    const float zh = __fmul_rn(r, kLn2);
+    const float zl = __fmaf_rn(r, kLn2, -zh) + __fmaf_rn(r, kLn2Lo, rl * kLn2);
+    const float q = zh * zh * __fmaf_rn(zh, __fmaf_rn(zh, 1.f / 24.f, -1.f / 6.f), 0.5f);
+    const long long a = static_cast<long long>(__float2int_rn(zh * 0x1p41f)) + __float2int_rn((zl - q) * 0x1p41f);
+    const int j = n & (kTable - 1), e = n >> 9;
+    const unsigned long long p = table[j];
+    const long long down = (static_cast<long long>(static_cast<uint32_t>((p + 0x40000000ull) >> 31)) * a) >> 10;
+    const unsigned long long w = p - static_cast<unsigned long long>(down);
+    const int shift = 62 - kUnitLog + e;
+    return (w + (1ull << (shift - 1))) >> shift;
+}
+
+// ------------------------------------------------------------------------------ reductions
+__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+
+template <bool BF16>
+struct Row {
+    const uint8_t *data;  // this CTA's tokens
+    int len, first;       // their number, the first one's index
+    __device__ __forceinline__ float at(int i) const {
+        float v;
+        if (BF16)
+            v = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(data)[i]) << 16);
+        else
+            v = reinterpret_cast<const float *>(data)[i];
+        return v + 0.f;  // one zero
+    }
+};
+__device__ __forceinline__ uint32_t key_of(float v) { return v == v ? order_bits(v) : 0u; }
+__device__ __forceinline__ unsigned long long place_of(uint32_t key, int index) {
+    return static_cast<unsigned long long>(key) << 32 | static_cast<uint32_t>(~index);
+}
+
+// Sum over the cluster of two 64-bit numbers a thread; all threads get the totals.
+__device__ __forceinline__ void cluster_sum(Shared &sh, uint32_t rank, uint32_t ctas, unsigned long long &a,
+                                            unsigned long long &b) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    a = warp_sum64(a);
+    b = warp_sum64(b);
+    if (lane == 0) {
+        sh.warp64[0][warp] = a;
+        sh.warp64[1][warp] = b;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        a = warp_sum64(lane < kWarps ? sh.warp64[0][lane] : 0);
+        b = warp_sum64(lane < kWarps ? sh.warp64[1][lane] : 0);
+        if (lane < static_cast<int>(ctas)) {
+            unsigned long long *to = in_cta(&sh.pair[rank][0], lane);
+            to[0] = a;
+            to[1] = b;
+        }
+    }
+    cluster_sync();
+    a = b = 0;
+    for (uint32_t r = 0; r < ctas; ++r) {
+        a += sh.pair[r][0];
+        b += sh.pair[r][1];
+    }
+    cluster_sync();  // the pairs may be written again
+}
+
+// Sorts n places (padded with zeros to a power of two), largest first.
+__device__ __forceinline__ int sort_list(Shared &sh, int n) {
+    int size = 32;
+    while (size < n) size <<= 1;
+    for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
+    __syncthreads();
+    for (int k = 2; k <= size; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+                const int i = (t / j) * 2 * j + (t & (j - 1)), o = i + j;
+                const unsigned long long a = sh.list[i], b = sh.list[o];
+                if ((a < b) == ((i & k) == 0)) {
+                    sh.list[i] = b;
+                    sh.list[o] = a;
+                }
+            }
+            __syncthreads();
+        }
+    return size;
+}
+
+// Inclusive prefix sums of sh.weight[0 .. n), by the whole CTA.
+__device__ __forceinline__ void scan_weights(Shared &sh, int n) {
+    const int per = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * per;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned long long s = 0;
+    for (int i = i0; i < min(n, i0 + per); ++i) s += sh.weight[i];
+    unsigned long long incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long up = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) sh.warp64[0][warp] = incl;
+    __syncthreads();
+    unsigned long long run = incl - s;
+    for (int w = 0; w < warp; ++w) run += sh.warp64[0][w];
+    for (int i = i0; i < min(n, i0 + per); ++i) sh.weight[i] = run += sh.weight[i];
+    __syncthreads();
+}
+
+// Gathers the CTAs' lists in the first one's, after a cluster barrier; the number of them.  Its lists lie
+// from its own on; the others' are read from their shared memory.
+__device__ __forceinline__ int gather_lists(Shared &sh, uint32_t ctas) {
+    int n = static_cast<int>(sh.count);
+    for (uint32_t r = 1; r < ctas; ++r) {
+        const Shared *other = in_cta(&sh, r);
+        const int m = static_cast<int>(other->count);
+        for (int i = threadIdx.x; i < m; i += kThreads) sh.list[n + i] = other->list[i];
+        n += m;
+    }
+    __syncthreads();
+    return n;
+}
+
+__device__ __forceinline__ float value_of(unsigned long long place) { return unorder_bits(static_cast<uint32_t>(place >> 32)); }
+__device__ __forceinline__ int index_of(unsigned long long place) { return static_cast<int>(~static_cast<uint32_t>(place)); }
+
+// The least sum that reaches p of `total`, and u of `total` to be passed.
+__device__ __forceinline__ unsigned long long reach(double p, unsigned long long total) {
+    return static_cast<unsigned long long>(ceil(p * static_cast<double>(total)));
+}
+__device__ __forceinline__ unsigned long long below(double u, unsigned long long total) {
+    const unsigned long long t = static_cast<unsigned long long>(u * static_cast<double>(total));
+    return min(t, total - 1);
+}
+
+// Of the sorted list's first n tokens: how many hold `need` of weight, at least one.  sh.weight has their sums.
+__device__ __forceinline__ int first_reaching(const Shared &sh, int n, unsigned long long need) {
+    int lo = 0, hi = n - 1;  // the first i with weight[i] >= need, the last at most
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.weight[mid] >= need) hi = mid; else lo = mid + 1;
+    }
+    return lo + 1;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cta_rank(), ctas = cta_count();
+    const int row_i = blockIdx.x / static_cast<int>(ctas);
+    constexpr int kSize = BF16 ? 2 : 4;
+    cluster_arrive_entry();
+    griddep_launch_dependents();
+    griddep_wait();
+
+    // ------------------------------------------------------------------ the row into shared memory
+    Row<BF16> row;
+    row.first = min(a.vocab, static_cast<int>(rank) * a.slice);
+    row.len = min(a.vocab, row.first + a.slice) - row.first;
+    const uint8_t *src = static_cast<const uint8_t *>(a.logits) + (row_i * a.stride + row.first) * kSize;
+    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+    uint8_t *dst = smem + sizeof(Shared) + skew;
+    row.data = dst;
+    float top = -INFINITY;  // of this thread's tokens
+    bool any = false;       // one is a number
+    {
+        const int bytes = row.len * kSize, head = min(bytes, (16 - skew) & 15);
+        const int body = (bytes - head) / 16, tail0 = head + body * 16;
+        const auto look = [&](float v) {
+            if (v == v) {
+                top = fmaxf(top, v);
+                any = true;
+            }
+        };
+        const auto one = [&](int at) {
+            if (BF16) {
+                const uint16_t w = __ldcg(reinterpret_cast<const uint16_t *>(src + at));
+                *reinterpret_cast<uint16_t *>(dst + at) = w;
+                look(__uint_as_float(static_cast<uint32_t>(w) << 16));
+            } else {
+                const float w = __ldcg(reinterpret_cast<const float *>(src + at));
+                *reinterpret_cast<float *>(dst + at) = w;
+                look(w);
+            }
+        };
+        if (tid * kSize < head) one(tid * kSize);
+        if (tail0 + tid * kSize < bytes) one(tail0 + tid * kSize);
+        const uint4 *from = reinterpret_cast<const uint4 *>(src + head);
+        uint4 *to = reinterpret_cast<uint4 *>(dst + head);
+#pragma unroll 8
+        for (int i = tid; i < body; i += kThreads) {
+            const uint4 v = __ldcg(from + i);
+            to[i] = v;
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (BF16) {
+                    look(__uint_as_float(w[j] << 16));
+                    look(__uint_as_float(w[j] & 0xffff0000u));
+                } else {
+                    look(__uint_as_float(w[j]));
+                }
+            }
+        }
+    }
+    for (int j = tid; j < kTable; j += kThreads)
+        sh.table[j] = static_cast<unsigned long long>(rint(exp2(-j / static_cast<double>(kTable)) * 0x1p62));
+    if (tid == 0) sh.count = 0;
+    cluster_wait_entry();
+    const uint32_t my_top = any ? key_of(top + 0.f) : 0u;
+    {
+        const uint32_t m = __reduce_max_sync(kFullMask, my_top);
+        if (lane == 0) sh.warp32[warp] = m;
+        __syncthreads();
+        if (warp == 0) {
+            const uint32_t c = __reduce_max_sync(kFullMask, lane < kWarps ? sh.warp32[lane] : 0u);
+            if (lane < static_cast<int>(ctas)) *in_cta(&sh.from_cta[rank], lane) = c;
+        }
+        cluster_sync();
+    }
+    uint32_t top_key = 0;
+    for (uint32_t r = 0; r < ctas; ++r) top_key = max(top_key, sh.from_cta[r]);
+
+    const float temperature = a.temperature ? __ldcg(a.temperature + row_i) : 1.f;
+    int k = a.top_k ? __ldcg(a.top_k + row_i) : 0;
+    if (k <= 0 || k > a.vocab) k = a.vocab;
+    double p = a.top_p ? static_cast<double>(__ldcg(a.top_p + row_i)) : 1.0;
+    if (!(p < 1.0)) p = 1.0;
+    if (p <= 0.0) {
+        p = 1.0;
+        k = 1;
+    }
+    const float floor_p = a.min_p ? fminf(fmaxf(__ldcg(a.min_p + row_i), 0.f), 1.f) : 0.f;
+    const unsigned long long least = max(1ull, static_cast<unsigned long long>(ceil(static_cast<double>(floor_p) * (1ull << kUnitLog))));
+    const float u_in = __ldcg(a.u + row_i);
+    const double u = u_in > 0.f ? static_cast<double>(fminf(u_in, 1.f)) : 0.0;
+
+    // ------------------------------------------------------------------ greedy
+    if (!(temperature > 0.f) || k == 1 || top_key <= kLeastKey) {
+        uint32_t best = 0xffffffffu;
+        for (int i = tid; i < row.len; i += kThreads)
+            if (key_of(row.at(i)) == top_key) {
+                best = static_cast<uint32_t>(row.first + i);
+                break;
+            }
+        best = __reduce_min_sync(kFullMask, best);
+        cluster_sync();  // the tops have been read
+        if (lane == 0) sh.warp32[warp] = best;
+        __syncthreads();
+        if (warp == 0) {
+            best = __reduce_min_sync(kFullMask, lane < kWarps ? sh.warp32[lane] : 0xffffffffu);
+            if (lane == 0) *in_cta(&sh.from_cta[rank], 0) = best;
+        }
+        cluster_sync();
+        if (rank == 0 && tid == 0) {
+            for (uint32_t r = 1; r < ctas; ++r) best = min(best, sh.from_cta[r]);
+            a.out[row_i] = static_cast<int>(best);
+        }
+        return;
+    }
+    Scale s;
+    s.top = unorder_bits(top_key);
+    {
+        const double c = 1.4426950408889634074 / static_cast<double>(fmaxf(temperature, 1e-30f));
+        s.hi = static_cast<float>(c);
+        s.lo = static_cast<float>(c - static_cast<double>(s.hi));
+    }
+
+    // ------------------------------------------------------------------ top-k: few tokens, sorted
+    const int each = (k + static_cast<int>(ctas) - 1) / static_cast<int>(ctas);
+    unsigned long long cut_k = 0;  // what is kept has this place or a higher one; 0: everything
+    if (k < a.vocab && each <= kThreads / 2 && k <= kCap / 2) {
+        // a key that `each` threads' largest reach, near the highest such
+        uint32_t lo = 0, hi = 0xffffffffu;
+        for (int bit = 0; bit < 32; ++bit) {
+            const uint32_t mid = lo + (hi - lo) / 2 + 1;
+            const int n = __syncthreads_count(my_top >= mid);
+            if (n >= each) lo = mid; else hi = mid - 1;
+            if (n >= each && n <= each + each / 8) break;
+            if (lo == hi) break;
+        }
+        cluster_sync();  // the tops have been read
+        if (tid < static_cast<int>(ctas)) *in_cta(&sh.from_cta[rank], tid) = lo;
+        cluster_sync();
+        uint32_t bound = 0xffffffffu;
+        for (uint32_t r = 0; r < ctas; ++r) bound = min(bound, sh.from_cta[r]);
+        for (int i = tid; i < row.len; i += kThreads) {
+            const uint32_t key = key_of(row.at(i));
+            if (key >= bound) {
+                const uint32_t at = atomicAdd(&sh.count, 1u);
+                if (at < kCap) sh.list[at] = place_of(key, row.first + i);
+            }
+        }
+        __syncthreads();
+        if (tid < static_cast<int>(ctas)) *in_cta(&sh.pair[rank][0], tid) = sh.count;
+        cluster_sync();
+        unsigned long long n_all = 0;
+        for (uint32_t r = 0; r < ctas; ++r) n_all += sh.pair[r][0];
+        if (n_all <= kCap) {
+            if (rank == 0) {
+                const int n = gather_lists(sh, ctas);
+                sort_list(sh, n);
+                const int m = min(n, k);
+                for (int i = tid; i < m; i += kThreads) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
+                __syncthreads();
+                scan_weights(sh, m);
+                int kept = m;
+                if (p < 1.0) kept = first_reaching(sh, m, reach(p, sh.weight[m - 1]));
+                __syncthreads();
+                // min-p, and the order of indices: a token's place there is its rank among the kept
+                int mine = 0;
+                for (int i = tid; i < kept; i += kThreads) {
+                    const unsigned long long w = sh.weight[i] - (i ? sh.weight[i - 1] : 0ull);
+                    mine += i == 0 || w >= least;
+                }
+                // weights fall along the list, so those that pass are its first ones
+                mine = __reduce_add_sync(kFullMask, mine);
+                if (lane == 0) sh.warp32[warp] = mine;
+                __syncthreads();
+                kept = 0;
+                for (int w = 0; w < kWarps; ++w) kept += static_cast<int>(sh.warp32[w]);
+                const unsigned long long goal = below(u, sh.weight[kept - 1]);
+                // sums by index, in turn of the sorted list: the first with sum > goal
+                for (int i = tid; i < kept; i += kThreads) {
+                    const uint32_t mine_i = static_cast<uint32_t>(index_of(sh.list[i]));
+                    unsigned long long before = 0;
+                    for (int j = 0; j < kept; ++j) {
+                        const unsigned long long w = sh.weight[j] - (j ? sh.weight[j - 1] : 0ull);
+                        before += static_cast<uint32_t>(index_of(sh.list[j])) < mine_i ? w : 0ull;
+                    }
+                    const unsigned long long w = sh.weight[i] - (i ? sh.weight[i - 1] : 0ull);
+                    if (before <= goal && goal < before + w) a.out[row_i] = static_cast<int>(mine_i);
+                }
+            }
+            cluster_sync();  // the lists have been read
+            return;
+        }
+        __syncthreads();
+        if (tid == 0) sh.count = 0;
+        cluster_sync();
+    }
+    const auto in_k = [&](uint32_t key, int index) { return place_of(key, index) >= cut_k; };
+
+    // ------------------------------------------------------------------ top-k by bisection
+    if (k < a.vocab) {
+        uint32_t lo = 0, hi = top_key;  // the largest key that k tokens reach
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2 + 1;
+            unsigned long long n = 0, none = 0;
+            for (int i = tid; i < row.len; i += kThreads) n += key_of(row.at(i)) >= mid;
+            cluster_sum(sh, rank, ctas, n, none);
+            if (n >= static_cast<unsigned long long>(k)) lo = mid; else hi = mid - 1;
+        }
+        unsigned long long above = 0, none = 0;
+        for (int i = tid; i < row.len; i += kThreads) above += key_of(row.at(i)) > lo;
+        cluster_sum(sh, rank, ctas, above, none);
+        int from = 0, to = a.vocab - 1;  // the least index up to which enough equal ones lie
+        while (from < to) {
+            const int mid = (from + to) >> 1;
+            unsigned long long n = 0;
+            none = 0;
+            for (int i = tid; i < row.len; i += kThreads) n += key_of(row.at(i)) == lo && row.first + i <= mid;
+            cluster_sum(sh, rank, ctas, n, none);
+            if (above + n >= static_cast<unsigned long long>(k)) to = mid; else from = mid + 1;
+        }
+        cut_k = place_of(lo, from);
+    }
+
+    // ------------------------------------------------------------------ top-p
+    unsigned long long cut = cut_k;
+    if (p < 1.0) {
+        // steps of x = coarse(): [x0 + b / per, x0 + (b + 1) / per), the last open; below x0 all are kept
+        float x0 = 0.f, per = 64.f;
+        float x_from = 0.f, x_to = INFINITY;  // the cut lies at from <= x < to
+        unsigned long long total = 0, sure = 0;  // weight of all, and of what is surely kept
+        bool sorted = false;
+        for (int level = 0; level < 3 && !sorted; ++level) {
+            for (int b = tid; b < kBins; b += kThreads) sh.hist[b] = 0;
+            __syncthreads();
+            for (int i = tid; i < row.len; i += kThreads) {
+                const float v = row.at(i);
+                const uint32_t key = key_of(v);
+                if (key <= kLeastKey || !in_k(key, row.first + i)) continue;
+                const float x = coarse(s, v);
+                if (x < x_from || x >= x_to) continue;
+                atomicAdd(&sh.hist[min(kBins - 1, static_cast<int>(fminf((x - x0) * per, 1e6f)))], 1u);
+            }
+            cluster_sync();
+            // Bounds of the weight up to each step; all CTAs form them alike.
+            const int b0 = tid * (kBins / kThreads);
+            float lo_sum = 0.f, hi_sum = 0.f;
+            uint32_t cnt[kBins / kThreads];
+#pragma unroll
+            for (int j = 0; j < kBins / kThreads; ++j) cnt[j] = 0;
+            for (uint32_t r = 0; r < ctas; ++r) {
+                const uint4 h = *reinterpret_cast<const uint4 *>(&in_cta(&sh, r)->hist[b0]);
+                cnt[0] += h.x;
+                cnt[1] += h.y;
+                cnt[2] += h.z;
+                cnt[3] += h.w;
+            }
+            static_assert(kBins / kThreads == 4, "one load");
+            float lows[4], highs[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int b = b0 + j;
+                const float x = x0 + b / per;
+                highs[j] = cnt[j] * ex2(-x) * 1.00001f;
+                lows[j] = b == kBins - 1 ? 0.f : cnt[j] * ex2(-(x0 + (b + 1) / per)) * 0.99999f;
+                hi_sum += highs[j];
+                lo_sum += lows[j];
+            }
+            // what is surely kept already counts as it is
+            const float base = static_cast<float>(sure) * 0x1p-44f;
+            float hi_run = hi_sum, lo_run = lo_sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float x = __shfl_up_sync(kFullMask, hi_run, o), y = __shfl_up_sync(kFullMask, lo_run, o);
+                if (lane >= o) {
+                    hi_run += x;
+                    lo_run += y;
+                }
+            }
+            if (lane == 31) {
+                sh.warp64[0][warp] = __float_as_uint(hi_run);
+                sh.warp64[1][warp] = __float_as_uint(lo_run);
+            }
+            if (tid == 0) {
+                sh.window[0] = kBins - 1;
+                sh.window[1] = kBins - 1;
+                sh.count = 0;
+            }
+            __syncthreads();
+            float hi_all = 0.f, lo_all = 0.f;
+            hi_run -= hi_sum;
+            lo_run -= lo_sum;
+            for (int w = 0; w < kWarps; ++w) {
+                const float x = __uint_as_float(static_cast<uint32_t>(sh.warp64[0][w]));
+                const float y = __uint_as_float(static_cast<uint32_t>(sh.warp64[1][w]));
+                if (w < warp) {
+                    hi_run += x;
+                    lo_run += y;
+                }
+                hi_all += x;
+                lo_all += y;
+            }
+            // on the first level the total is bounded too; later it is known
+            // (sums of f32 in another order differ by far less than 1e-5)
+            const float want_lo = static_cast<float>(p) * (level ? static_cast<float>(total) * 0x1p-44f : lo_all) * 0.99999f;
+            const float want_hi = static_cast<float>(p) * (level ? static_cast<float>(total) * 0x1p-44f : hi_all) * 1.00001f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                hi_run += highs[j];
+                lo_run += lows[j];
+                if (base + hi_run >= want_lo) atomicMin(&sh.window[0], b0 + j);
+                if (base + lo_run >= want_hi) atomicMin(&sh.window[1], b0 + j);
+            }
+            __syncthreads();
+            const float w_from = x0 + sh.window[0] / per;
+            const float w_to = sh.window[1] == kBins - 1 ? x_to : x0 + (sh.window[1] + 1) / per;
+            // Exact weights of what lies above the window, and of everything; the window's tokens.
+            unsigned long long above = 0, all = 0;
+            for (int i = tid; i < row.len; i += kThreads) {
+                const float v = row.at(i);
+                const uint32_t key = key_of(v);
+                if (key <= kLeastKey || !in_k(key, row.first + i)) continue;
+                const float x = coarse(s, v);
+                if (level == 0 || x < w_to) {
+                    const unsigned long long w = weight_of(s, sh.table, v);
+                    all += w;
+                    if (x < w_from) above += w;
+                }
+                if (x >= w_from && x < w_to) {
+                    const uint32_t at = atomicAdd(&sh.count, 1u);
+                    if (at < kCap) sh.list[at] = place_of(key, row.first + i);
+                }
+            }
+            cluster_sum(sh, rank, ctas, above, all);
+            if (level == 0) total = all;
+            sure = above;
+            if (tid < static_cast<int>(ctas)) *in_cta(&sh.pair[rank][0], tid) = sh.count;
+            cluster_sync();
+            unsigned long long n_all = 0;
+            for (uint32_t r = 0; r < ctas; ++r) n_all += sh.pair[r][0];
+            if (n_all <= kCap) {
+                if (rank == 0) {
+                    const int n = gather_lists(sh, ctas);
+                    sort_list(sh, n);
+                    for (int i = tid; i < n; i += kThreads) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
+                    __syncthreads();
+                    scan_weights(sh, n);
+                    const unsigned long long need = reach(p, total);
+                    if (tid < static_cast<int>(ctas)) {
+                        // the steps are f32: that the cut lies between them is seen here
+                        const bool in = n > 0 && need > sure && need <= sure + sh.weight[n - 1];
+                        *in_cta(&sh.found, tid) = in;
+                        *in_cta(&sh.cut, tid) = in ? sh.list[first_reaching(sh, n, need - sure) - 1] : 0ull;
+                    }
+                }
+                cluster_sync();
+                sorted = sh.found != 0;
+                cut = max(cut, sh.cut);
+                if (!sorted) break;
+            } else {
+                x_from = w_from;
+                x_to = w_to;
+                x0 = w_from;
+                const float wide = (w_to < 48.f ? w_to : fmaxf(48.f, w_from + 1.f)) - w_from;
+                per = fminf(kBins / fmaxf(wide, 0x1p-20f), 0x1p28f);
+                cluster_sync();
+            }
+        }
+        if (!sorted) {  // thousands of equal tokens: bisection over keys, by weight
+            const unsigned long long need = reach(p, total);
+            uint32_t lo = kLeastKey, hi = top_key;
+            while (lo < hi) {
+                const uint32_t mid = lo + (hi - lo) / 2 + 1;
+                unsigned long long w = 0, none = 0;
+                for (int i = tid; i < row.len; i += kThreads) {
+                    const float v = row.at(i);
+                    const uint32_t key = key_of(v);
+                    if (key >= mid && in_k(key, row.first + i)) w += weight_of(s, sh.table, v);
+                }
+                cluster_sum(sh, rank, ctas, w, none);
+                if (w >= need) lo = mid; else hi = mid - 1;
+            }
+            unsigned long long above = 0, none = 0;
+            for (int i = tid; i < row.len; i += kThreads) {
+                const float v = row.at(i);
+                const uint32_t key = key_of(v);
+                if (key > lo && in_k(key, row.first + i)) above += weight_of(s, sh.table, v);
+            }
+            cluster_sum(sh, rank, ctas, above, none);
+            const unsigned long long one = max(1ull, weight_of(s, sh.table, unorder_bits(lo)));
+            const unsigned long long ties = need > above ? (need - above + one - 1) / one : 1ull;
+            int from = 0, to = a.vocab - 1;
+            while (from < to) {
+                const int mid = (from + to) >> 1;
+                unsigned long long n = 0;
+                none = 0;
+                for (int i = tid; i < row.len; i += kThreads)
+                    n += key_of(row.at(i)) == lo && row.first + i <= mid && in_k(lo, row.first + i);
+                cluster_sum(sh, rank, ctas, n, none);
+                if (n >= ties) to = mid; else from = mid + 1;
+            }
+            cut = max(cut, place_of(lo, from));
+        }
+    }
+
+    // ------------------------------------------------------------------ the draw
+    // A warp's tokens are consecutive, so its sum's place among the others is its place by index.
+    const int seg = (row.len + kWarps - 1) / kWarps, seg0 = min(row.len, warp * seg), seg1 = min(row.len, seg0 + seg);
+    const auto kept_weight = [&](int i) -> unsigned long long {
+        const float v = row.at(i);
+        const uint32_t key = key_of(v);
+        if (key <= kLeastKey || place_of(key, row.first + i) < cut) return 0ull;
+        const unsigned long long w = weight_of(s, sh.table, v);
+        return w >= least || key == top_key ? w : 0ull;
+    };
+    unsigned long long mine = 0;
+    for (int i = seg0 + lane; i < seg1; i += 32) mine += kept_weight(i);
+    mine = warp_sum64(mine);
+    if (lane < static_cast<int>(ctas)) *in_cta(&sh.sums[rank][warp], lane) = mine;
+    cluster_sync();
+    unsigned long long before = 0, all = 0;
+    for (uint32_t r = 0; r < ctas; ++r)
+        for (int w = 0; w < kWarps; ++w) {
+            if (r < rank || (r == rank && w < warp)) before += sh.sums[r][w];
+            all += sh.sums[r][w];
+        }
+    const unsigned long long goal = below(u, all);
+    if (before <= goal && goal < before + mine) {
+        for (int i0 = seg0; i0 < seg1; i0 += 32) {
+            const unsigned long long w = i0 + lane < seg1 ? kept_weight(i0 + lane) : 0ull;
+            unsigned long long incl = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long up = __shfl_up_sync(kFullMask, incl, o);
+                if (lane >= o) incl += up;
+            }
+            const unsigned over = __ballot_sync(kFullMask, before + incl > goal);
+            if (over) {
+                if (lane == 0) a.out[row_i] = row.first + i0 + __ffs(over) - 1;
+                break;
+            }
+            before += __shfl_sync(kFullMask, incl, 31);
+        }
+    }
+}
+
+bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+constexpr int kMaxDevices = 64;
+
+// SM count and opt-in shared memory of the current device, after allowing the kernels all of it.
+bool device_info(int &sms, int &smem) {
+    static std::atomic<int> sm_cache[kMaxDevices], smem_cache[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < kMaxDevices && (sms = sm_cache[dev].load(std::memory_order_acquire)) > 0) {
+        smem = smem_cache[dev].load(std::memory_order_relaxed);
+        return true;
+    }
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(sample_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(sample_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return false;
+    if (dev < kMaxDevices) {
+        smem_cache[dev].store(smem, std::memory_order_relaxed);
+        sm_cache[dev].store(sms, std::memory_order_release);
+    }
+    return true;
+}
+
+}  // namespace
+}  // namespace memq
+
+extern "C" int memq_sample(int dtype, const void *logits, int64_t stride, const float *temperature, const int32_t *top_k,
+                           const float *top_p, const float *min_p, const float *u, int32_t *out, int64_t rows,
+                           int64_t vocab, void *stream) {
+    using namespace memq;
+    if ((dtype != MEMQ_F32 && dtype != MEMQ_BF16) || rows < 0 || rows > (1 << 20) || vocab < 1 || vocab > kMaxVocab ||
+        stride < 0 || stride > (int64_t{1} << 40))
+        return MEMQ_ERR_SHAPE;
+    if (rows == 0) return MEMQ_OK;
+    if (!logits || !u || !out) return MEMQ_ERR_NULL;
+    const int size = dtype == MEMQ_F32 ? 4 : 2;
+    if (misaligned(logits, size) || misaligned(temperature, 4) || misaligned(top_k, 4) || misaligned(top_p, 4) ||
+        misaligned(min_p, 4) || misaligned(u, 4) || misaligned(out, 4))
+        return MEMQ_ERR_ALIGN;
+    int sms = 0, smem = 0;
+    if (!device_info(sms, smem)) return MEMQ_ERR_LAUNCH;
+    SampleArgs a{logits, stride, temperature, top_p, min_p, u, top_k, out, static_cast<int>(vocab), 0};
+    // As many CTAs a row as fill the GPU, no fewer than hold it.
+    const auto slice_of = [&](int ctas) { return static_cast<int>(((vocab + ctas - 1) / ctas + 15) / 16 * 16); };
+    const auto bytes_of = [&](int ctas) { return static_cast<int>(sizeof(Shared)) + slice_of(ctas) * size + 16; };
+    int ctas = 1;
+    while (ctas < kMaxCtas && (bytes_of(ctas) > smem || (rows * ctas * 2 <= sms && slice_of(ctas) > 2048))) ctas *= 2;
+    if (bytes_of(ctas) > smem) return MEMQ_ERR_SHAPE;
+    a.slice = slice_of(ctas);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(bytes_of(ctas));
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, dtype == MEMQ_BF16 ? sample_kernel<true> : sample_kernel<false>, a) == cudaSuccess
+               ? MEMQ_OK
+               : MEMQ_ERR_LAUNCH;
+}
