@@ -42,6 +42,7 @@ static_assert(sizeof(AttnOwner) == 16, "one load");
 struct AttnArgs {
     const void *q;
     int64_t q_stride;  // elements from one token's row to the next
+    const uint8_t *k_cache, *v_cache;
     const float *k_scales, *v_scales;
     const int32_t *table, *kv_len, *cu_q;
     void *out;
@@ -68,8 +69,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int c0, int c1, i
     return s;
 }
 
-// Row `row` of the pool's [page][kv head][offset] rows that holds key `key` (a multiple of 16) of a
-// sequence and head.
+// The page that holds key `key` of a sequence.
 __device__ __forceinline__ int attn_page(const AttnArgs &a, const int32_t *table, int key, unsigned int *fault) {
     int page = __ldcg(table + (key >> a.page_shift));
     if (page < 0 || page >= a.n_pages) {
@@ -77,6 +77,19 @@ __device__ __forceinline__ int attn_page(const AttnArgs &a, const int32_t *table
         page = 0;
     }
     return page;
+}
+
+// log2 of a scale, exact for powers of two; not a number or infinite as it is.
+__device__ __forceinline__ float attn_log2(float v) {
+    const uint32_t bits = __float_as_uint(v);
+    const float l = static_cast<float>(static_cast<int>(bits >> 23) - 127) + __log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+    return v < INFINITY ? l : v;
+}
+
+// What two f32 have beyond their f16x2.
+__device__ __forceinline__ uint32_t attn_rest(float a, float b, uint32_t hi) {
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return f32x2_to_f16x2(a - h.x, b - h.y);
 }
 
 // out element offset of row `rr` of a (sequence, kv head).

@@ -25,6 +25,7 @@
 #include <cmath>
 
 #include "memq_attn.cuh"
+#include "memq_attn_tiles.cuh"
 
 namespace memq {
 namespace {
@@ -59,12 +60,6 @@ struct Control {
 __host__ __device__ constexpr int smem_bytes(int ring) { return ring + 1024 + static_cast<int>(sizeof(Control)); }
 
 __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
-
-// Two f32 -> f16x2 and what is left of them.
-__device__ __forceinline__ uint32_t rest_f16x2(float a, float b, uint32_t hi) {
-    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    return f32x2_to_f16x2(a - h.x, b - h.y);
-}
 
 template <int D, bool Q2, bool P2>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -258,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float u = x[4 * j + 2 * i] * inv, v = x[4 * j + 2 * i + 1] * inv;
                     const uint32_t h = f32x2_to_f16x2(u, v);
                     q_hi[j][2 * i + k] = h;
-                    if (Q2) q_lo[j][2 * i + k] = rest_f16x2(u, v, h);
+                    if (Q2) q_lo[j][2 * i + k] = attn_rest(u, v, h);
                 }
         }
 
@@ -325,10 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i0 = 2 * (tile - win);
             if (tile == win) {  // log2 and reciprocal of the window's value scales; exact for powers of two
                 const float v = vs_now < kAttnLeastScale ? kAttnLeastScale : vs_now;
-                const uint32_t bits = __float_as_uint(v);
-                lv_now = static_cast<float>(static_cast<int>(bits >> 23) - 127) +
-                         __log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
-                if (!(v < INFINITY)) lv_now = v;
+                lv_now = attn_log2(v);
                 inv_now = __frcp_rn(v);
             }
             float top[2] = {-INFINITY, -INFINITY};
@@ -384,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         total_w[k] = fmaf(p0 + p1, back, total_w[k]);
                         const uint32_t h = f32x2_to_f16x2(p0, p1);
                         p_hi[b][2 * n + k] = h;
-                        if (P2) p_lo[P2 ? b : 0][2 * n + k] = rest_f16x2(p0, p1, h);
+                        if (P2) p_lo[P2 ? b : 0][2 * n + k] = attn_rest(p0, p1, h);
                     }
                 }
             // ---- values
@@ -507,10 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Adds the pieces of the items that several runs shared, in the runs' order.  CTA x serves the item that run x
-// began; a warp a row at a time.
+// Adds the pieces of the items that several runs shared, in the runs' order.  CTAs (x, 0 .. gridDim.y - 1) serve the
+// item that run x began; a warp a row at a time.  `stride` rows a piece.
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, int runs) {
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, int runs, int stride) {
     griddep_launch_dependents();
     griddep_wait();
     const int x = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -518,8 +510,8 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, i
     const AttnOwner own = *reinterpret_cast<const AttnOwner *>(&raw);
     const int parts = min(own.last, runs - 1) - x + 1;
     constexpr int E = D / 32;
-    for (int r = warp; r < own.rows; r += kWarps) {
-        const auto slot_of = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * x + 1 : 2 * (x + k)) * kRows + r; };
+    for (int r = blockIdx.y * kWarps + warp; r < own.rows; r += gridDim.y * kWarps) {
+        const auto slot_of = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * x + 1 : 2 * (x + k)) * stride + r; };
         float top = kAttnUnset;
         for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(a.stats + slot_of(k)).x);
         top = warp_max(top);
@@ -597,7 +589,9 @@ constexpr int kMaxDevices = 64;
 template <int D, bool Q2, bool P2>
 bool allow() {
     return cudaFuncSetAttribute(attn_rows_kernel<D, Q2, P2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem_bytes(Ring<D>::kBytes)) == cudaSuccess;
+                                smem_bytes(Ring<D>::kBytes)) == cudaSuccess &&
+           cudaFuncSetAttribute(attn_tiles_kernel<D, Q2, P2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                TileShape<D, Q2>::kBytes) == cudaSuccess;
 }
 
 // SM count of the current device, after allowing the kernels their shared memory (once per device).
@@ -616,9 +610,24 @@ bool device_info(int &sms) {
 
 bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
-int64_t owner_bytes(int runs) { return (static_cast<int64_t>(runs) * sizeof(AttnOwner) + 255) / 256 * 256; }
-int64_t stat_bytes(int runs) { return static_cast<int64_t>(2) * runs * kRows * sizeof(float2); }
-int64_t part_bytes(int runs, int d) { return static_cast<int64_t>(2) * runs * kRows * d * sizeof(float); }
+// Workspace: owners, statistics and pieces of one kernel; both kernels' lie behind one another.
+struct Workspace {
+    int runs, rows;
+    int64_t owners, stats, parts;
+    Workspace(int runs_, int rows_, int d)
+        : runs(runs_), rows(rows_), owners((static_cast<int64_t>(runs) * sizeof(AttnOwner) + 255) / 256 * 256),
+          stats(static_cast<int64_t>(2) * runs * rows * sizeof(float2)),
+          parts(static_cast<int64_t>(2) * runs * rows * d * sizeof(float)) {}
+    int64_t bytes() const { return owners + stats + parts; }
+    void place(AttnArgs &a, uint8_t *at) const {
+        a.owner = reinterpret_cast<AttnOwner *>(at);
+        a.stats = reinterpret_cast<float2 *>(at + owners);
+        a.part = reinterpret_cast<float *>(at + owners + stats);
+    }
+};
+int64_t workspace_need(int grid, int d) { return Workspace(grid * kWarps, kRows, d).bytes() + Workspace(grid, 256, d).bytes(); }
+// Sequences of more query rows than this take the tensor-core kernel.
+constexpr int kRowsKernelMost = 16;
 
 }  // namespace
 }  // namespace memq
@@ -636,8 +645,7 @@ extern "C" int64_t memq_attn_paged_workspace(int d) {
     if (d != 64 && d != 128) return -1;
     int sms = 0;
     if (!device_info(sms)) return -1;
-    const int runs = std::min(sms, kAttnMaxGrid) * kWarps;
-    return owner_bytes(runs) + stat_bytes(runs) + part_bytes(runs, d);
+    return workspace_need(std::min(sms, kAttnMaxGrid), d);
 }
 
 extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, const uint8_t *k_cache,
@@ -666,7 +674,7 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     int sms = 0;
     if (!device_info(sms)) return MEMQ_ERR_LAUNCH;
     const int grid = std::min(sms, kAttnMaxGrid), runs = grid * kWarps;
-    if (workspace_bytes < owner_bytes(runs) + stat_bytes(runs) + part_bytes(runs, d)) return MEMQ_ERR_SHAPE;
+    if (workspace_bytes < workspace_need(grid, d)) return MEMQ_ERR_SHAPE;
 
     AttnArgs a{};
     a.q = q;
@@ -677,10 +685,8 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     a.kv_len = kv_len;
     a.cu_q = cu_q;
     a.out = out;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    a.owner = reinterpret_cast<AttnOwner *>(ws);
-    a.stats = reinterpret_cast<float2 *>(ws + owner_bytes(runs));
-    a.part = reinterpret_cast<float *>(ws + owner_bytes(runs) + stat_bytes(runs));
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
     a.n_tok = static_cast<int>(n_tok);
     a.n_seq = n_seq;
     a.nh = nh;
@@ -699,9 +705,6 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     if (!encode_rows(&k_map, k_cache, d, pool, box) || !encode_rows(&v_map, v_cache, d, pool, box)) return MEMQ_ERR_LAUNCH;
 
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(d == 128 ? Ring<128>::kBytes : Ring<64>::kBytes));
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -709,16 +712,47 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const bool q2 = q_dtype == MEMQ_F32, p2 = out_dtype == MEMQ_F32;
+    const Workspace of_rows(runs, kRows, d), of_tiles(grid, q2 ? 128 : 256, d);
+    const auto join = [&](const AttnArgs &args, const Workspace &w, unsigned share) {
+        cfg.gridDim = dim3(static_cast<unsigned>(w.runs), share);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = 0;
+        return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, args, w.runs, w.rows) ==
+               cudaSuccess;
+    };
+    // One token a sequence, or rows that no sequence can have more of than a warp holds: the stream of keys is
+    // all.  (More tokens than sequences may still lie in short ones: each kernel takes its own.)
+    const bool rows_only = n_tok <= n_seq || n_tok * a.group <= kRowsKernelMost;
+    if (!rows_only) {
+        AttnArgs t = a;
+        t.rows_from = kRowsKernelMost + 1;
+        of_tiles.place(t, static_cast<uint8_t *>(workspace) + of_rows.bytes());
+        a.rows_to = kRowsKernelMost;
+        unsigned int *fault = nullptr;
+        if (cudaGetSymbolAddress(reinterpret_cast<void **>(&fault), g_attn_fault) != cudaSuccess) return MEMQ_ERR_LAUNCH;
+        using Tiles = void (*)(const AttnArgs, unsigned int *);
+        static constexpr Tiles kTiles[2][2][2] = {
+            {{attn_tiles_kernel<64, false, false>, attn_tiles_kernel<64, false, true>},
+             {attn_tiles_kernel<64, true, false>, attn_tiles_kernel<64, true, true>}},
+            {{attn_tiles_kernel<128, false, false>, attn_tiles_kernel<128, false, true>},
+             {attn_tiles_kernel<128, true, false>, attn_tiles_kernel<128, true, true>}}};
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(kTileThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(d == 128 ? (q2 ? TileShape<128, true>::kBytes : TileShape<128, false>::kBytes)
+                                                            : (q2 ? TileShape<64, true>::kBytes : TileShape<64, false>::kBytes));
+        if (cudaLaunchKernelEx(&cfg, kTiles[d == 128][q2][p2], t, fault) != cudaSuccess || !join(t, of_tiles, 8))
+            return MEMQ_ERR_LAUNCH;
+    }
+    of_rows.place(a, static_cast<uint8_t *>(workspace));
     using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const AttnArgs, const int);
     static constexpr Kernel kKernels[2][2][2] = {
         {{attn_rows_kernel<64, false, false>, attn_rows_kernel<64, false, true>},
          {attn_rows_kernel<64, true, false>, attn_rows_kernel<64, true, true>}},
         {{attn_rows_kernel<128, false, false>, attn_rows_kernel<128, false, true>},
          {attn_rows_kernel<128, true, false>, attn_rows_kernel<128, true, true>}}};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(d == 128 ? Ring<128>::kBytes : Ring<64>::kBytes));
     if (cudaLaunchKernelEx(&cfg, kKernels[d == 128][q2][p2], k_map, v_map, a, box) != cudaSuccess) return MEMQ_ERR_LAUNCH;
-    cfg.gridDim = dim3(static_cast<unsigned>(runs));
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, a, runs) == cudaSuccess
-               ? MEMQ_OK
-               : MEMQ_ERR_LAUNCH;
+    return join(a, of_rows, 1) ? MEMQ_OK : MEMQ_ERR_LAUNCH;
 }

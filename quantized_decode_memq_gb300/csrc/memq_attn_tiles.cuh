@@ -1,0 +1,648 @@
+// memq_attn_tiles.cuh -- the tensor-core kernel of memq_attn_paged, for chunks of many query rows.
+//
+// A CTA serves 128 or 256 rows (heads of a group, times tokens) of one kv head, 128 keys a time:
+//   S [128 rows x 128 keys] = Q [128 x d] . K^T     kind::f16, both from shared memory
+//   O [128 rows x d]       += P [128 x 128] . V     P from TMEM, where it takes the place of its scores
+// Both products are f16: the codes are widened to f16 in shared memory (which they cost 64 KB of writes a
+// tile, against 2 x 192 KB that the products read), the query rows and the weights rounded to it.  Two blocks of 128
+// rows take turns: while the weights of one are formed, the tensor cores serve the other.
+//
+// Warps 0-3 and 4-7 form the weights of the two blocks, a thread a row, so that a row's maximum and sum need no
+// exchange; warps 8-11 load codes, a tile ahead in registers, and widen them; one thread of warp 12 issues
+// the products.  An f32 query has two terms, two products, and its 128 rows the shared memory of 256.
+#pragma once
+
+#include "memq_attn.cuh"
+
+namespace memq {
+
+constexpr int kTileKeys = 128;
+constexpr int kTileThreads = 13 * 32;
+constexpr int kWidenWarp = 8, kIssueWarp = 12;
+constexpr int kTileStart = 3;  // tiles that starting an item counts as
+
+struct TileItem {
+    int seq, head, row_tile;
+    AttnSeq s;
+    int rows;           // of the sequence and kv head: t * group
+    int row0, n_rows;   // of the item
+    int vis, tiles;     // keys that its last row sees; tiles, one at least
+};
+
+struct TileControl {
+    uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
+    uint64_t scores[2], weights[2], out_done[2];  // by block of rows
+    uint64_t q_ready, drain;
+    uint32_t tmem;
+    int first_off;
+    long long first_pos;
+    TileItem first;
+    long long warp_sum[16];
+    float4 scale[4][8];   // of a tile's blocks of keys: k's, log2 v's, 1 / v's, and log2 v's for the reference
+    float factor[256];
+};
+
+template <int D, bool Q2>
+struct TileShape {
+    static constexpr int kBlocks = Q2 ? 1 : 2;                  // of 128 rows
+    static constexpr int kRows = kBlocks * 128;
+    static constexpr int kQ = 2 * 128 * D * 2;                  // two blocks, or two terms of one
+    static constexpr int kKv = kTileKeys * D * 2;
+    static constexpr int kBytes = kQ + 4 * kKv + static_cast<int>(sizeof(TileControl));
+    static constexpr int kHalves = D / 64;                      // of 64 elements, a swizzled 128-byte row each
+};
+
+__device__ __forceinline__ void tile_sizes(const AttnArgs &a, int rows_per, TileItem &it) {
+    it.row0 = it.row_tile * rows_per;
+    it.n_rows = min(rows_per, it.rows - it.row0);
+    it.vis = max(0, it.s.kv - it.s.t + (it.row0 + it.n_rows - 1) / a.group + 1);
+    it.tiles = max(1, (it.vis + kTileKeys - 1) / kTileKeys);
+}
+
+__device__ __forceinline__ bool tile_served(const AttnArgs &a, int rows) { return rows >= a.rows_from && rows <= a.rows_to; }
+
+// Order: sequences, blocks of rows, kv heads.
+__device__ __forceinline__ void next_tile_item(const AttnArgs &a, int rows_per, TileItem &it) {
+    if (++it.head < a.n_kv) return;
+    it.head = 0;
+    ++it.row_tile;
+    if (it.row_tile * rows_per >= it.rows) {
+        it.row_tile = 0;
+        do {
+            if (++it.seq >= a.n_seq) {  // not with lengths that stand still: an item without rows and keys
+                it.seq = a.n_seq;
+                it.rows = 0;
+                it.s = AttnSeq{0, 0, 0};
+                break;
+            }
+            it.s = attn_seq(a, __ldcg(a.cu_q + it.seq), __ldcg(a.cu_q + it.seq + 1), __ldcg(a.kv_len + it.seq));
+            it.rows = it.s.t * a.group;
+        } while (it.rows == 0 || !tile_served(a, it.rows));
+    }
+    tile_sizes(a, rows_per, it);
+}
+
+// D[tmem] (+)= A[tmem] B[smem], K = 16; issued by one thread.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        : "memory");
+}
+// Instruction descriptor of kind::f16 with f16 operands and f32 sums, A K-major.
+__host__ __device__ constexpr uint32_t f16_idesc(int n, bool b_mn_major) {
+    return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+// The values' operand: a row is one key and runs along d, in swizzled rows of 64 elements, the next 64 `next` bytes on.
+__device__ __forceinline__ uint64_t values_desc(uint32_t addr, int next) {
+    return (smem_desc(addr, 128) & ~(uint64_t{0x3fff} << 16)) | (static_cast<uint64_t>(next >> 4) << 16);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Waits for a barrier phase; after one wait expired, none is made any more, and the fault word says so.
+struct AttnWaiter {
+    unsigned int *fault;
+    bool dead = false;
+    __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
+        if (!dead && !warp_wait_bounded(bar, parity)) {
+            dead = true;
+            if ((threadIdx.x & 31) == 0) atomicOr(fault, kAttnFaultWait);
+        }
+    }
+};
+
+// Offset of the 16-byte piece `p` of row `r` in swizzled rows of 128 bytes.
+__device__ __forceinline__ int piece_at(int r, int p) { return r * 128 + ((p ^ (r & 7)) << 4); }
+
+// A row of a block -> its f16 terms in shared memory and its scores' factor.  16 lanes serve a row, 8 (4)
+// elements each.
+template <int D, bool Q2>
+__device__ __forceinline__ void stage_queries(const AttnArgs &a, const TileItem &it, uint8_t *q, float *factors, int block,
+                                              int warp, int lane) {
+    constexpr int E = D / 16;
+    const int part = lane & 15;
+    const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+        const int r = warp * 32 + i * 2 + (lane >> 4), rr = it.row0 + block * 128 + r;
+        const bool live = block * 128 + r < it.n_rows;
+        const int tok = live ? rr / a.group : 0;
+        const int64_t from = (static_cast<int64_t>(it.s.start) + tok) * a.q_stride +
+                             (live ? it.head * a.group + rr - tok * a.group : 0) * D + part * E;
+        float x[E];
+        if (Q2) {
+            const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + from);
+#pragma unroll
+            for (int j = 0; j < E / 4; ++j) {
+                const float4 v = live ? __ldcg(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[4 * j] = v.x;
+                x[4 * j + 1] = v.y;
+                x[4 * j + 2] = v.z;
+                x[4 * j + 3] = v.w;
+            }
+        } else {
+            const uint2 *src = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + from);
+#pragma unroll
+            for (int j = 0; j < E / 4; ++j) {
+                const uint2 v = live ? __ldcg(src + j) : make_uint2(0, 0);
+                x[4 * j] = __uint_as_float(v.x << 16);
+                x[4 * j + 1] = __uint_as_float(v.x & 0xffff0000u);
+                x[4 * j + 2] = __uint_as_float(v.y << 16);
+                x[4 * j + 3] = __uint_as_float(v.y & 0xffff0000u);
+            }
+        }
+        uint32_t top = 0;  // as bits, infinities and NaN lie above all numbers
+#pragma unroll
+        for (int j = 0; j < E; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
+        const int e = max(static_cast<int>(top >> 23), 32);
+        const float inv = sign * __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
+        const float back = __uint_as_float(static_cast<uint32_t>(max(1, e - 14)) << 23);
+        if (part == 0) factors[block * 128 + r] = top < 0x7f800000u ? back * fabsf(a.scale_log2) : NAN;
+        uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+            const float u = x[2 * j] * inv, v = x[2 * j + 1] * inv;
+            hi[j] = f32x2_to_f16x2(u, v);
+            if (Q2) lo[j] = attn_rest(u, v, hi[j]);
+        }
+        uint8_t *base = q + (Q2 ? 0 : block) * (128 * D * 2);
+        const int byte = part * E * 2, half = byte >> 7, p = (byte & 127) >> 4;
+        uint8_t *at = base + half * 16384 + piece_at(r, p) + (byte & 15);
+        if (E == 8) {
+            *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[E / 2 - 2], hi[E / 2 - 1]);
+            if (Q2)
+                *reinterpret_cast<uint4 *>(at + 128 * D * 2) = make_uint4(lo[0], lo[1], lo[E / 2 - 2], lo[E / 2 - 1]);
+        } else {
+            *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
+            if (Q2) *reinterpret_cast<uint2 *>(at + 128 * D * 2) = make_uint2(lo[0], lo[1]);
+        }
+    }
+}
+
+template <int D, bool Q2, bool P2>
+__global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnArgs a, unsigned int *fault) {
+    using Shape = TileShape<D, Q2>;
+    constexpr int kBlocks = Shape::kBlocks, kRowsPer = Shape::kRows;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFullMask, tid >> 5, 0);
+    uint8_t *q_smem = smem, *k_smem = smem + Shape::kQ, *v_smem = k_smem + 2 * Shape::kKv;
+    TileControl *ctl = reinterpret_cast<TileControl *>(v_smem + 2 * Shape::kKv);
+
+    griddep_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->k_full[i], 4);
+            mbar_init(&ctl->k_free[i], 1);
+            mbar_init(&ctl->v_full[i], 4);
+            mbar_init(&ctl->v_free[i], 1);
+            mbar_init(&ctl->scores[i], 1);
+            mbar_init(&ctl->weights[i], 4);
+            mbar_init(&ctl->out_done[i], 1);
+        }
+        mbar_init(&ctl->q_ready, kBlocks * 4);
+        mbar_init(&ctl->drain, 1);
+        mbar_init_fence();
+    }
+    if (warp == kIssueWarp) tmem_alloc(&ctl->tmem, 512);
+    griddep_wait();
+
+    // ------------------------------------------------------------------ this CTA's run of tiles
+    // Blocks of rows before each sequence; then a thread counts the tiles of a slice of the blocks.
+    int *first = reinterpret_cast<int *>(smem);  // [n_seq + 1], of at most 2^27 blocks
+    const auto prefix = [&](long long v, long long &total) {  // exclusive, over the CTA
+        long long incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(kFullMask, incl, o);
+            if (lane >= o) incl += up;
+        }
+        __syncthreads();
+        if (lane == 31) ctl->warp_sum[warp] = incl;
+        __syncthreads();
+        long long before = incl - v;
+        total = 0;
+        for (int w = 0; w < kTileThreads / 32; ++w) {
+            if (w < warp) before += ctl->warp_sum[w];
+            total += ctl->warp_sum[w];
+        }
+        return before;
+    };
+    const int per_seq = (a.n_seq + kTileThreads - 1) / kTileThreads;
+    bool descends = false;
+    long long blocks = 0, total_blocks = 0, total = 0;
+    for (int i = 0; i < per_seq; ++i) {
+        const int b = tid * per_seq + i;
+        if (b >= a.n_seq) break;
+        const int c0 = __ldcg(a.cu_q + b), c1 = __ldcg(a.cu_q + b + 1), kv = __ldcg(a.kv_len + b);
+        if (c0 < 0 || c0 > c1 || c1 > a.n_tok || kv < 0 || kv > (static_cast<long long>(a.max_pages) << a.page_shift))
+            atomicOr(fault, kAttnFaultInput);
+        descends = descends || c0 > c1;
+        const int rows = attn_seq(a, c0, c1, kv).t * a.group;
+        first[b] = static_cast<int>(blocks);
+        if (tile_served(a, rows)) blocks += (rows + kRowsPer - 1) / kRowsPer;
+    }
+    const bool nothing = __syncthreads_or(descends);
+    long long before = prefix(blocks, total_blocks);
+    for (int i = 0; i < per_seq; ++i) {
+        const int b = tid * per_seq + i;
+        if (b < a.n_seq) first[b] += static_cast<int>(before);
+    }
+    if (nothing) total_blocks = 0;
+    __syncthreads();
+    const long long slice = (total_blocks + kTileThreads - 1) / kTileThreads;
+    const int lo_block = static_cast<int>(min(total_blocks, tid * slice)),
+              hi_block = static_cast<int>(min(total_blocks, lo_block + slice));
+    long long own = 0, per = 0, run_lo = 0, run_hi = 0;
+    before = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        if (pass == 1 && (run_lo < before || run_lo >= before + own)) break;
+        long long sum = before;
+        TileItem it{};
+        if (lo_block < hi_block) {
+            int lo = 0, hi = a.n_seq;  // the last sequence whose first block is at or before lo_block
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= lo_block) lo = mid; else hi = mid;
+            }
+            it.seq = lo;
+            it.s = attn_seq(a, __ldcg(a.cu_q + lo), __ldcg(a.cu_q + lo + 1), __ldcg(a.kv_len + lo));
+            it.rows = it.s.t * a.group;
+            it.row_tile = lo_block - first[lo];
+            tile_sizes(a, kRowsPer, it);
+        }
+        for (int b = lo_block; b < hi_block; ++b) {
+            const int units = it.tiles + kTileStart;
+            const long long n = static_cast<long long>(units) * a.n_kv;
+            if (pass == 1 && sum <= run_lo && run_lo < sum + n) {
+                const long long at = run_lo - sum;
+                it.head = static_cast<int>(at / units);
+                const int in_item = static_cast<int>(at - static_cast<long long>(it.head) * units);
+                ctl->first = it;
+                ctl->first_off = max(0, in_item - kTileStart);
+                ctl->first_pos = run_lo - in_item;  // of the item's first unit
+            }
+            sum += n;
+            if (b + 1 < hi_block) {
+                it.head = a.n_kv - 1;
+                next_tile_item(a, kRowsPer, it);
+            }
+        }
+        if (pass == 0) {
+            own = sum;
+            before = prefix(own, total);
+            per = max(static_cast<long long>(kTileStart + 1), (total + gridDim.x - 1) / gridDim.x);
+            run_lo = blockIdx.x * per;
+            run_hi = min(total, run_lo + per);
+        }
+    }
+    if (tid == 0) a.owner[blockIdx.x].rows = 0;
+    fence_async_smem();  // the lengths lie where codes will
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(kFullMask, ctl->tmem, 0);
+    const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 384};
+
+    AttnWaiter wait{fault};
+    if (run_lo < run_hi) {
+        TileItem it = ctl->first;
+        int off = ctl->first_off;
+        long long pos = ctl->first_pos;
+        uint32_t tile = 0;                   // key tiles so far, of all items
+        uint32_t turns[2] = {0, 0};          // of a block's scores and weights
+        uint32_t items[2] = {0, 0}, all_items = 0;  // that a block had part in
+        while (pos + kTileStart + off < run_hi && !wait.dead) {
+            const int end = static_cast<int>(min(static_cast<long long>(it.tiles), run_hi - pos - kTileStart));
+            const int t1 = min(end, (it.vis + kTileKeys - 1) / kTileKeys);
+            const int n = max(0, t1 - off);
+            const int live_blocks = it.n_rows > 128 ? 2 : 1;
+
+            if (warp >= kWidenWarp && warp < kIssueWarp && n > 0) {
+                // -------------------------------------------------------- codes -> f16
+                constexpr int kChunks = D / 16, kLoads = kTileKeys / (128 / kChunks);
+                const int ct = tid - kWidenWarp * 32, chunk = ct % kChunks, r0 = ct / kChunks;
+                const int32_t *table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
+                // lane l: first row in the pool of the tile's block l
+                const auto base_at = [&](int j) -> long long {
+                    const int key = j * kTileKeys + (lane & 7) * kAttnBlock;
+                    if (j >= t1 || key >= it.vis) return -1;
+                    const int page = attn_page(a, table, key, fault);
+                    return ((static_cast<long long>(page) * a.n_kv + it.head) << a.page_shift) +
+                           (key & ((1 << a.page_shift) - 1));
+                };
+                const auto load = [&](uint4(&to)[kLoads], const uint8_t *cache, long long base, int j) {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int r = r0 + i * (128 / kChunks);
+                        const long long b = __shfl_sync(kFullMask, base, r >> 4);
+                        to[i] = b >= 0 && j * kTileKeys + r < it.vis
+                                    ? __ldcg(reinterpret_cast<const uint4 *>(cache + (b + (r & 15)) * D) + chunk)
+                                    : make_uint4(0, 0, 0, 0);
+                    }
+                };
+                // 16 codes fill two pieces of a swizzled row; the upper lanes store them in the other order, off the
+                // banks of the lower
+                const auto widen = [&](uint8_t *to, const uint4(&from)[kLoads]) {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int r = r0 + i * (128 / kChunks);
+                        uint8_t *half = to + (chunk >> 2) * 16384;
+                        uint4 x, y;
+                        e4m3x4_to_f16x2x2(from[i].x, x.x, x.y);
+                        e4m3x4_to_f16x2x2(from[i].y, x.z, x.w);
+                        e4m3x4_to_f16x2x2(from[i].z, y.x, y.y);
+                        e4m3x4_to_f16x2x2(from[i].w, y.z, y.w);
+                        const int p = (chunk & 3) * 2, swap = kChunks == 8 ? chunk >> 2 : r & 1;
+                        *reinterpret_cast<uint4 *>(half + piece_at(r, p + swap)) = swap ? y : x;
+                        *reinterpret_cast<uint4 *>(half + piece_at(r, p + 1 - swap)) = swap ? x : y;
+                    }
+                };
+                long long base = base_at(off), base_next = base_at(off + 1);
+                uint4 kc[kLoads], vc[kLoads];
+                load(kc, a.k_cache, base, off);
+                load(vc, a.v_cache, base, off);
+                for (int j = off; j < t1; ++j, ++tile) {
+                    const uint32_t buf = tile & 1, use = tile >> 1;
+                    float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
+                    if (warp == kWidenWarp && lane < 8 && base >= 0) {
+                        sc.x = __ldcg(a.k_scales + (base >> 4));
+                        float v = __ldcg(a.v_scales + (base >> 4));
+                        if (v < kAttnLeastScale) v = kAttnLeastScale;
+                        sc.y = attn_log2(v);
+                        sc.z = __frcp_rn(v);
+                        sc.w = fmaxf(sc.y, kAttnLeastLog);
+                    }
+                    if (tile >= 2) wait(&ctl->k_free[buf], (use - 1) & 1);
+                    if (wait.dead) break;
+                    if (warp == kWidenWarp && lane < 8) ctl->scale[tile & 3][lane] = sc;
+                    widen(k_smem + buf * Shape::kKv, kc);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->k_full[buf]);
+                    base = base_next;
+                    load(kc, a.k_cache, base, j + 1);
+                    if (tile >= 2) wait(&ctl->v_free[buf], (use - 1) & 1);
+                    if (wait.dead) break;
+                    widen(v_smem + buf * Shape::kKv, vc);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->v_full[buf]);
+                    load(vc, a.v_cache, base, j + 1);
+                    base_next = base_at(j + 2);
+                }
+            } else if (warp == kIssueWarp && n > 0) {
+                // -------------------------------------------------------- products
+                constexpr uint32_t kQk = f16_idesc(kTileKeys, false), kPv = f16_idesc(D, true);
+                const uint32_t q_at = smem_u32(q_smem), k_at = smem_u32(k_smem), v_at = smem_u32(v_smem);
+                const auto scores = [&](int b, uint32_t buf) {
+                    if (elect_one()) {
+#pragma unroll
+                        for (int term = 0; term < (Q2 ? 2 : 1); ++term)
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
+                                mma_f16_ss(s_col[b], smem_desc(q_at + (Q2 ? term : b) * (128 * D * 2) + at, 128),
+                                           smem_desc(k_at + buf * Shape::kKv + at, 128), kQk, term > 0 || i > 0);
+                            }
+                        tc_commit(&ctl->scores[b]);
+                    }
+                    __syncwarp();
+                };
+                const auto outputs = [&](int b, uint32_t buf, bool acc) {
+                    if (elect_one()) {
+#pragma unroll
+                        for (int term = 0; term < (P2 ? 2 : 1); ++term)
+#pragma unroll
+                            for (int i = 0; i < kTileKeys / 16; ++i)
+                                mma_f16_ts(o_col[b], s_col[b] + term * 64 + i * 8,
+                                           values_desc(v_at + buf * Shape::kKv + i * 2048, 16384), kPv,
+                                           acc || term > 0 || i > 0);
+                    }
+                    __syncwarp();
+                };
+                const auto commit = [&](uint64_t *bar) {
+                    if (elect_one()) tc_commit(bar);
+                    __syncwarp();
+                };
+                wait(&ctl->q_ready, all_items & 1);
+                wait(&ctl->k_full[tile & 1], (tile >> 1) & 1);
+                tc_fence_after();
+                if (!wait.dead) {
+                    for (int b = 0; b < live_blocks; ++b) scores(b, tile & 1);
+                    commit(&ctl->k_free[tile & 1]);
+                }
+                for (int j = 0; j < n && !wait.dead; ++j, ++tile) {
+                    const uint32_t buf = tile & 1, next = tile + 1;
+                    wait(&ctl->v_full[buf], (tile >> 1) & 1);
+                    for (int b = 0; b < live_blocks; ++b) {
+                        wait(&ctl->weights[b], turns[b] & 1);
+                        ++turns[b];
+                        if (b == 0 && j + 1 < n) wait(&ctl->k_full[next & 1], (next >> 1) & 1);
+                        if (wait.dead) break;
+                        tc_fence_after();
+                        outputs(b, buf, j > 0);
+                        if (j + 1 < n)
+                            scores(b, next & 1);
+                        else
+                            commit(&ctl->out_done[b]);
+                    }
+                    if (wait.dead) break;
+                    commit(&ctl->v_free[buf]);
+                    if (j + 1 < n) commit(&ctl->k_free[next & 1]);
+                }
+            } else if (warp < kBlocks * 4) {
+                // -------------------------------------------------------- weights and the way out
+                const int b = warp >> 2, wq = warp & 3, r = b * 128 + wq * 32 + lane;
+                const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+                const uint32_t at_s = s_col[b] + lanes, at_o = o_col[b] + lanes;
+                float ref = kAttnUnset, total_w = 0.f;
+                const bool mine = b < live_blocks;
+                if (n > 0) {
+                    if (mine) stage_queries<D, Q2>(a, it, q_smem, ctl->factor, b, wq, lane);
+                    fence_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->q_ready);
+                    if (!mine) wait(&ctl->q_ready, all_items & 1);  // never two arrivals in one phase
+                }
+                if (mine && n > 0) {
+                    const float factor = ctl->factor[r];
+                    const int see0 = it.s.kv - it.s.t + 1;
+                    const int lim = min(it.vis, max(0, see0 + (it.row0 + r) / a.group));
+                    const int all_see = max(0, see0 + (it.row0 + b * 128) / a.group);
+                    for (int j = off; j < t1; ++j) {
+                        const float4 *scale = ctl->scale[(tile + (j - off)) & 3];
+                        wait(&ctl->scores[b], turns[b] & 1);
+                        if (wait.dead) break;
+                        tc_fence_after();
+                        const int left = lim - j * kTileKeys;  // keys of the tile that the row sees
+                        const bool masked = (j + 1) * kTileKeys > all_see;
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            float s[32];
+                            tmem_ld32(at_s + c * 32, s);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float4 sc = scale[2 * c + h];
+                                float m = -INFINITY;
+                                if (masked) {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        if (c * 32 + h * 16 + i < left) m = fmaxf(m, s[h * 16 + i]);
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) m = fmaxf(m, s[h * 16 + i]);
+                                }
+                                // (a block of which nothing is seen has -inf, times a scale of 0 a NaN, which is passed over)
+                                top = fmaxf(top, fmaf(m, factor * sc.x, sc.w));
+                            }
+                        }
+                        if (__any_sync(kFullMask, top > ref + kAttnSlack)) {
+                            const float to = fmaxf(ref, top), by = ex2(ref - to);
+                            ref = to;
+                            total_w *= by;
+                            if (j > off) {  // the products so far are done: the scores came behind them
+#pragma unroll 1
+                                for (int c = 0; c < D / 32; ++c) {
+                                    float o[32];
+                                    tmem_ld32(at_o + c * 32, o);
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] *= by;
+                                    tmem_st32(at_o + c * 32, o);
+                                }
+                            }
+                        }
+                        uint32_t rest[P2 ? 64 : 1];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            float s[32];
+                            uint32_t w[16];
+                            tmem_ld32(at_s + c * 32, s);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float4 sc = scale[2 * c + h];
+                                const float f = factor * sc.x, shift = sc.y - ref + kAttnTop;
+                                float sum = 0.f;
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    float p0 = ex2(fmaf(s[h * 16 + i], f, shift)), p1 = ex2(fmaf(s[h * 16 + i + 1], f, shift));
+                                    if (masked) {
+                                        if (c * 32 + h * 16 + i >= left) p0 = 0.f;
+                                        if (c * 32 + h * 16 + i + 1 >= left) p1 = 0.f;
+                                    }
+                                    sum += p0 + p1;
+                                    w[h * 8 + i / 2] = f32x2_to_f16x2(p0, p1);
+                                    if (P2) rest[P2 ? c * 16 + h * 8 + i / 2 : 0] = attn_rest(p0, p1, w[h * 8 + i / 2]);
+                                }
+                                total_w = fmaf(sum, sc.z, total_w);
+                            }
+                            tmem_st16(at_s + c * 16, w);
+                        }
+                        if (P2) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t w[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) w[i] = rest[P2 ? c * 16 + i : 0];
+                                tmem_st16(at_s + 64 + c * 16, w);
+                            }
+                        }
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->weights[b]);
+                        ++turns[b];
+                    }
+                    wait(&ctl->out_done[b], items[b] & 1);
+                    ++items[b];
+                    tc_fence_after();
+                }
+                if (mine && !wait.dead) {
+                    const bool whole = off == 0 && end == it.tiles;
+                    const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (off == 0 ? 1 : 0);
+                    const bool live = r < it.n_rows;
+                    const int64_t to = whole ? attn_out_at(a, it.s.start, it.head, it.row0 + (live ? r : 0), D)
+                                             : (piece * kRowsPer + r) * D;
+                    const float norm = !whole ? 1.f : total_w == 0.f ? 0.f : __fdiv_rn(1.f, total_w);
+                    if (!whole && live) a.stats[piece * kRowsPer + r] = make_float2(ref, total_w);
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        if (n > 0) {
+                            tmem_ld32(at_o + c * 32, o);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                        }
+                        if (!live) continue;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] *= norm;
+                        if (whole && a.out_bf16) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to + c * 32);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                __nv_bfloat162 v[4];
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) v[m] = __floats2bfloat162_rn(o[8 * i + 2 * m], o[8 * i + 2 * m + 1]);
+                                dst[i] = *reinterpret_cast<uint4 *>(v);
+                            }
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>((whole ? static_cast<float *>(a.out) : a.part) + to + c * 32);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                    if (!whole && off == 0 && warp == 0 && lane == 0) {
+                        AttnOwner owner;
+                        owner.start = it.s.start;
+                        owner.row0 = it.row0;
+                        owner.last = static_cast<int>((pos + it.tiles + kTileStart - 1) / per);
+                        owner.head = static_cast<short>(it.head);
+                        owner.rows = static_cast<short>(it.n_rows);
+                        a.owner[blockIdx.x] = owner;
+                    }
+                }
+            }
+            // every warp counts alike
+            if (!(warp >= kWidenWarp)) tile += n;
+            if (n > 0) ++all_items;
+            pos += it.tiles + kTileStart;
+            off = 0;
+            if (pos + kTileStart < run_hi) next_tile_item(a, kRowsPer, it);
+        }
+        if (warp == kIssueWarp && wait.dead) {  // products in flight end before TMEM is given up, the wait bounded
+            if (elect_one()) tc_commit(&ctl->drain);
+            __syncwarp();
+            (void)warp_wait_bounded(&ctl->drain, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kIssueWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace memq
