@@ -500,60 +500,142 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Adds the pieces of the items that several runs shared, in the runs' order.  CTAs (x, 0 .. gridDim.y - 1) serve the
-// item that run x began; a warp a row at a time.  `stride` rows a piece.
+// x-th such item.  Up to kFewParts pieces a warp adds a row's alone, eight rows under way; above, the CTA's warps add
+// every eighth and the eight sums are added in turn (one token over 131071 keys: 152 pieces an item; a warp alone
+// took 55 us).  `stride` rows a piece.
+constexpr int kFewParts = 24;
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, int runs, int stride) {
+    constexpr int E = D / 32;
+    __shared__ int counts[kWarps], found;
+    __shared__ AttnOwner owner;
+    __shared__ float red[2][kWarps];
+    __shared__ float sums[kWarps][D];
     griddep_launch_dependents();
     griddep_wait();
-    const int x = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint4 raw = __ldcg(reinterpret_cast<const uint4 *>(a.owner + x));
-    const AttnOwner own = *reinterpret_cast<const AttnOwner *>(&raw);
-    const int parts = min(own.last, runs - 1) - x + 1;
-    constexpr int E = D / 32;
-    for (int r = blockIdx.y * kWarps + warp; r < own.rows; r += gridDim.y * kWarps) {
-        const auto slot_of = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * x + 1 : 2 * (x + k)) * stride + r; };
-        float top = kAttnUnset;
-        for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(a.stats + slot_of(k)).x);
-        top = warp_max(top);
-        float acc[E], total = 0.f;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) found = -1;
+    // the x-th owner: a thread looks at a few runs next to one another
+    const int per = (runs + kThreads - 1) / kThreads, i0 = tid * per, i1 = min(runs, i0 + per);
+    unsigned mine = 0;  // bit i: run i0 + i is one
+    for (int i = i0; i < i1; ++i) {
+        const uint4 raw = __ldcg(reinterpret_cast<const uint4 *>(a.owner + i));
+        mine |= static_cast<unsigned>(reinterpret_cast<const AttnOwner *>(&raw)->rows != 0) << (i - i0);
+    }
+    const int n_mine = __popc(mine);
+    int incl = n_mine;
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = 0.f;
-        for (int k0 = 0; k0 < parts; k0 += 32) {
-            float w = 0.f, l = 0.f;
-            if (k0 + lane < parts) {
-                const float2 st = __ldcg(a.stats + slot_of(k0 + lane));
-                w = ex2(st.x - top);
-                l = st.y * w;
-            }
-            total += warp_sum(l);
-            const int n = min(32, parts - k0);
-#pragma unroll 8
-            for (int k = 0; k < n; ++k) {
-                const float by = __shfl_sync(kFullMask, w, k);
-                const float *src = a.part + slot_of(k0 + k) * D + lane * E;
-                if (E == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                    acc[0] = fmaf(v.x, by, acc[0]);
-                    acc[1] = fmaf(v.y, by, acc[1]);
-                    acc[E - 2] = fmaf(v.z, by, acc[E - 2]);
-                    acc[E - 1] = fmaf(v.w, by, acc[E - 1]);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                    acc[0] = fmaf(v.x, by, acc[0]);
-                    acc[1] = fmaf(v.y, by, acc[1]);
-                }
-            }
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) counts[warp] = incl;
+    __syncthreads();
+    int before = incl - n_mine;
+    for (int w = 0; w < warp; ++w) before += counts[w];
+    const int x = static_cast<int>(blockIdx.x);
+    if (x >= before && x < before + n_mine) {
+        unsigned m = mine;
+        for (int i = before; i < x; ++i) m &= m - 1;
+        found = i0 + __ffs(m) - 1;
+        const uint4 raw = __ldcg(reinterpret_cast<const uint4 *>(a.owner + found));
+        owner = *reinterpret_cast<const AttnOwner *>(&raw);
+    }
+    __syncthreads();
+    if (found < 0) return;
+    const int run = found, parts = min(owner.last, runs - 1) - run + 1;
+    const auto put = [&](int r, const float(&v)[E], float total) {
         const float n = total == 0.f ? 0.f : __fdiv_rn(1.f, total);
-        const int64_t to = attn_out_at(a, own.start, own.head, own.row0 + r, D) + lane * E;
+        const int64_t to = attn_out_at(a, owner.start, owner.head, owner.row0 + r, D) + lane * E;
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
             if (a.out_bf16)
                 *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + to + i) =
-                    __floats2bfloat162_rn(acc[i] * n, acc[i + 1] * n);
+                    __floats2bfloat162_rn(v[i] * n, v[i + 1] * n);
             else
-                *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + to + i) = make_float2(acc[i] * n, acc[i + 1] * n);
+                *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + to + i) = make_float2(v[i] * n, v[i + 1] * n);
         }
+    };
+    const auto slot_of = [&](int k, int r) { return static_cast<int64_t>(k == 0 ? 2 * run + 1 : 2 * (run + k)) * stride + r; };
+    const auto add = [&](float(&acc)[E], int64_t slot, float by) {
+        const float *src = a.part + slot * D + lane * E;
+        if (E == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+            acc[0] = fmaf(v.x, by, acc[0]);
+            acc[1] = fmaf(v.y, by, acc[1]);
+            acc[E - 2] = fmaf(v.z, by, acc[E - 2]);
+            acc[E - 1] = fmaf(v.w, by, acc[E - 1]);
+        } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+            acc[0] = fmaf(v.x, by, acc[0]);
+            acc[1] = fmaf(v.y, by, acc[1]);
+        }
+    };
+    if (parts <= kFewParts) {
+        for (int r = blockIdx.y * kWarps + warp; r < owner.rows; r += gridDim.y * kWarps) {
+            float2 st = make_float2(kAttnUnset, 0.f);
+            if (lane < parts) st = __ldcg(a.stats + slot_of(lane, r));
+            const float w = ex2(st.x - warp_max(st.x)), total = warp_sum(st.y * w);
+            float acc[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = 0.f;
+            for (int k0 = 0; k0 < parts; k0 += 8) {  // past the last piece: the last again, with weight 0
+#pragma unroll
+                for (int k = k0; k < k0 + 8; ++k) {
+                    const float by = __shfl_sync(kFullMask, w, k & 31);
+                    add(acc, slot_of(min(k, parts - 1), r), k < parts ? by : 0.f);
+                }
+            }
+            put(r, acc, total);
+        }
+        return;
+    }
+    for (int r = blockIdx.y; r < owner.rows; r += gridDim.y) {
+        float top = kAttnUnset;
+        for (int k = tid; k < parts; k += kThreads) top = fmaxf(top, __ldcg(a.stats + slot_of(k, r)).x);
+        top = warp_max(top);
+        if (lane == 0) red[0][warp] = top;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[0][w]);
+        float acc[E], total = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0.f;
+        // warp w adds pieces w, w + 8, ..: 32 of them a turn
+        for (int k0 = warp; k0 < parts; k0 += 32 * kWarps) {
+            const int k = k0 + lane * kWarps;
+            float w = 0.f;
+            if (k < parts) {
+                const float2 st = __ldcg(a.stats + slot_of(k, r));
+                w = ex2(st.x - top);
+                total += st.y * w;
+            }
+            const int n = min(32, (parts - k0 + kWarps - 1) / kWarps);
+            for (int i0 = 0; i0 < n; i0 += 16) {
+#pragma unroll
+                for (int i = i0; i < i0 + 16; ++i) {
+                    const float by = __shfl_sync(kFullMask, w, i & 31);
+                    add(acc, slot_of(min(k0 + i * kWarps, parts - 1), r), i < n ? by : 0.f);
+                }
+            }
+        }
+        total = warp_sum(total);
+        if (lane == 0) red[1][warp] = total;
+#pragma unroll
+        for (int i = 0; i < E; ++i) sums[warp][lane * E + i] = acc[i];
+        __syncthreads();
+        if (warp == 0) {
+            total = 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = 0.f;
+            for (int w = 0; w < kWarps; ++w) {
+                total += red[1][w];
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[i] += sums[w][lane * E + i];
+            }
+            put(r, acc, total);
+        }
+        __syncthreads();  // the shared arrays are free for the next row
     }
 }
 
@@ -713,8 +795,11 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     cfg.numAttrs = 1;
     const bool q2 = q_dtype == MEMQ_F32, p2 = out_dtype == MEMQ_F32;
     const Workspace of_rows(runs, kRows, d), of_tiles(grid, q2 ? 128 : 256, d);
-    const auto join = [&](const AttnArgs &args, const Workspace &w, unsigned share) {
-        cfg.gridDim = dim3(static_cast<unsigned>(w.runs), share);
+    const auto join = [&](const AttnArgs &args, const Workspace &w) {
+        // at least as many as items, of which a run begins one at most; about eight CTAs an SM over all
+        const int64_t items = n_kv * (n_tok * a.group / w.rows + std::min<int64_t>(n_seq, n_tok));
+        const unsigned x = static_cast<unsigned>(std::min<int64_t>(items, w.runs));
+        cfg.gridDim = dim3(x, std::max(1u, std::min(w.rows / 8u * 2u, 8u * static_cast<unsigned>(grid) / x)));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, args, w.runs, w.rows) ==
@@ -740,7 +825,7 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
         cfg.blockDim = dim3(kTileThreads);
         cfg.dynamicSmemBytes = static_cast<size_t>(d == 128 ? (q2 ? TileShape<128, true>::kBytes : TileShape<128, false>::kBytes)
                                                             : (q2 ? TileShape<64, true>::kBytes : TileShape<64, false>::kBytes));
-        if (cudaLaunchKernelEx(&cfg, kTiles[d == 128][q2][p2], t, fault) != cudaSuccess || !join(t, of_tiles, 8))
+        if (cudaLaunchKernelEx(&cfg, kTiles[d == 128][q2][p2], t, fault) != cudaSuccess || !join(t, of_tiles))
             return MEMQ_ERR_LAUNCH;
     }
     of_rows.place(a, static_cast<uint8_t *>(workspace));
@@ -754,5 +839,5 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(d == 128 ? Ring<128>::kBytes : Ring<64>::kBytes));
     if (cudaLaunchKernelEx(&cfg, kKernels[d == 128][q2][p2], k_map, v_map, a, box) != cudaSuccess) return MEMQ_ERR_LAUNCH;
-    return join(a, of_rows, 1) ? MEMQ_OK : MEMQ_ERR_LAUNCH;
+    return join(a, of_rows) ? MEMQ_OK : MEMQ_ERR_LAUNCH;
 }

@@ -8,8 +8,8 @@
 // rows take turns: while the weights of one are formed, the tensor cores serve the other.
 //
 // Warps 0-3 and 4-7 form the weights of the two blocks, a thread a row, so that a row's maximum and sum need no
-// exchange; warps 8-11 load codes, a tile ahead in registers, and widen them; one thread of warp 12 issues
-// the products.  An f32 query has two terms, two products, and its 128 rows the shared memory of 256.
+// exchange; warps 8-11 and 13-15 load codes of keys and of values, a tile ahead in registers, and widen them; one thread
+// of warp 12 issues the products.  An f32 query has two terms, two products, and its 128 rows the shared memory of 256.
 #pragma once
 
 #include "memq_attn.cuh"
@@ -17,7 +17,10 @@
 namespace memq {
 
 constexpr int kTileKeys = 128;
-constexpr int kTileThreads = 13 * 32;
+constexpr int kTileThreads = 16 * 32;
+// Registers a thread: 128 at launch; the two warpgroups that hold scores take 168, the others give theirs.
+constexpr int kRegsWeights = 168, kRegsOthers = 88;
+static_assert(2 * kRegsWeights + 2 * kRegsOthers <= 4 * 128, "a split beyond the launch's registers never comes");
 constexpr int kWidenWarp = 8, kIssueWarp = 12;
 constexpr int kTileStart = 3;  // tiles that starting an item counts as
 
@@ -41,6 +44,15 @@ struct TileControl {
     float4 scale[4][8];   // of a tile's blocks of keys: k's, log2 v's, 1 / v's, and log2 v's for the reference
     float factor[256];
 };
+
+template <int R>
+__device__ __forceinline__ void set_registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void set_registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
 
 template <int D, bool Q2>
 struct TileShape {
@@ -82,6 +94,41 @@ __device__ __forceinline__ void next_tile_item(const AttnArgs &a, int rows_per, 
     tile_sizes(a, rows_per, it);
 }
 
+// The items of a run, as each warp walks them.
+struct TileRun {
+    const AttnArgs &a;
+    int rows_per;
+    long long lo, hi;
+    TileItem it;
+    int off, end, t1, n;  // first tile, where the run's part ends, where what is seen ends, tiles to do
+    long long pos;        // of the item's first unit
+    bool live;
+    __device__ __forceinline__ TileRun(const AttnArgs &args, int rows, long long run_lo, long long run_hi)
+        : a(args), rows_per(rows), lo(run_lo), hi(run_hi), live(false) {}
+    __device__ __forceinline__ void start(const TileItem &first, int first_off, long long first_pos) {
+        it = first;
+        off = first_off;
+        pos = first_pos;
+        sizes();
+    }
+    __device__ __forceinline__ void sizes() {
+        live = pos + kTileStart + off < hi;
+        end = static_cast<int>(min(static_cast<long long>(it.tiles), hi - pos - kTileStart));
+        t1 = min(end, (it.vis + kTileKeys - 1) / kTileKeys);
+        n = max(0, t1 - off);
+    }
+    __device__ __forceinline__ bool more() const { return live; }
+    __device__ __forceinline__ bool whole() const { return off == 0 && end == it.tiles; }
+    __device__ __forceinline__ void next() {
+        pos += it.tiles + kTileStart;
+        off = 0;
+        live = pos + kTileStart < hi;
+        if (!live) return;
+        next_tile_item(a, rows_per, it);
+        sizes();
+    }
+};
+
 // D[tmem] (+)= A[tmem] B[smem], K = 16; issued by one thread.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile(
@@ -113,6 +160,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+// Eight columns of a warp's lanes times a number of each lane's.
+__device__ __forceinline__ void tmem_scale8(uint32_t addr, float by) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        asm volatile("" : "+r"(r[i]));
+        r[i] = __float_as_uint(__uint_as_float(r[i]) * by);
+    }
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // Waits for a barrier phase; after one wait expired, none is made any more, and the fault word says so.
@@ -212,7 +276,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->k_full[i], 4);
             mbar_init(&ctl->k_free[i], 1);
-            mbar_init(&ctl->v_full[i], 4);
+            mbar_init(&ctl->v_full[i], 3);
             mbar_init(&ctl->v_free[i], 1);
             mbar_init(&ctl->scores[i], 1);
             mbar_init(&ctl->weights[i], 4);
@@ -324,316 +388,316 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
     const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 384};
 
     AttnWaiter wait{fault};
-    if (run_lo < run_hi) {
-        TileItem it = ctl->first;
-        int off = ctl->first_off;
-        long long pos = ctl->first_pos;
-        uint32_t tile = 0;                   // key tiles so far, of all items
-        uint32_t turns[2] = {0, 0};          // of a block's scores and weights
-        uint32_t items[2] = {0, 0}, all_items = 0;  // that a block had part in
-        while (pos + kTileStart + off < run_hi && !wait.dead) {
-            const int end = static_cast<int>(min(static_cast<long long>(it.tiles), run_hi - pos - kTileStart));
-            const int t1 = min(end, (it.vis + kTileKeys - 1) / kTileKeys);
-            const int n = max(0, t1 - off);
-            const int live_blocks = it.n_rows > 128 ? 2 : 1;
-
-            if (warp >= kWidenWarp && warp < kIssueWarp && n > 0) {
-                // -------------------------------------------------------- codes -> f16
-                constexpr int kChunks = D / 16, kLoads = kTileKeys / (128 / kChunks);
-                const int ct = tid - kWidenWarp * 32, chunk = ct % kChunks, r0 = ct / kChunks;
-                const int32_t *table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
-                // lane l: first row in the pool of the tile's block l
-                const auto base_at = [&](int j) -> long long {
-                    const int key = j * kTileKeys + (lane & 7) * kAttnBlock;
-                    if (j >= t1 || key >= it.vis) return -1;
-                    const int page = attn_page(a, table, key, fault);
-                    return ((static_cast<long long>(page) * a.n_kv + it.head) << a.page_shift) +
-                           (key & ((1 << a.page_shift) - 1));
-                };
-                const auto load = [&](uint4(&to)[kLoads], const uint8_t *cache, long long base, int j) {
+    TileRun run{a, kRowsPer, run_lo, run_hi};
+    if (run_lo < run_hi) run.start(ctl->first, ctl->first_off, ctl->first_pos);
+    __syncwarp();
+    if (warp < 8)  // whole warpgroups, one instruction each
+        set_registers_up<kRegsWeights>();
+    else
+        set_registers_down<kRegsOthers>();
+    if (warp < 8) {
+        // ------------------------------------------------------------ weights and the way out
+        const int b = warp >> 2, wq = warp & 3, r = b * 128 + wq * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+        const uint32_t at_s = s_col[b] + lanes, at_o = o_col[b] + lanes;
+        uint32_t tile = 0, turns = 0, items = 0, all_items = 0;
+        for (; b < kBlocks && run.more() && !wait.dead; run.next()) {
+            const TileItem &it = run.it;
+            const int n = run.n;
+            const bool mine = b == 0 || it.n_rows > 128;
+            float ref = kAttnUnset, total_w = 0.f;
+            if (n > 0) {
+                if (mine) stage_queries<D, Q2>(a, it, q_smem, ctl->factor, b, wq, lane);
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->q_ready);
+                if (!mine) wait(&ctl->q_ready, all_items & 1);  // never two arrivals in one phase
+                ++all_items;
+            }
+            if (mine && n > 0) {
+                const float factor = ctl->factor[r];
+                const int see0 = it.s.kv - it.s.t + 1;
+                const int lim = min(it.vis, max(0, see0 + (it.row0 + r) / a.group));
+                const int all_see = max(0, see0 + (it.row0 + b * 128) / a.group);
+                for (int j = 0; j < n; ++j) {
+                    const float4 *scale = ctl->scale[(tile + j) & 3];
+                    const int key0 = (run.off + j) * kTileKeys;
+                    wait(&ctl->scores[b], turns & 1);
+                    if (wait.dead) break;
+                    tc_fence_after();
+                    const bool masked = key0 + kTileKeys > all_see;
+                    const int left = masked ? lim - key0 : kTileKeys;  // keys of the tile that the row sees
+                    uint32_t raw[4][32];
 #pragma unroll
-                    for (int i = 0; i < kLoads; ++i) {
-                        const int r = r0 + i * (128 / kChunks);
-                        const long long b = __shfl_sync(kFullMask, base, r >> 4);
-                        to[i] = b >= 0 && j * kTileKeys + r < it.vis
-                                    ? __ldcg(reinterpret_cast<const uint4 *>(cache + (b + (r & 15)) * D) + chunk)
-                                    : make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < 4; ++c) tmem_ld32_nowait(at_s + c * 32, raw[c]);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32_done(raw[c]);
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c * 32 + i >= left) raw[c][i] = 0xff800000u;
                     }
-                };
-                // 16 codes fill two pieces of a swizzled row; the upper lanes store them in the other order, off the
-                // banks of the lower
-                const auto widen = [&](uint8_t *to, const uint4(&from)[kLoads]) {
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < kLoads; ++i) {
-                        const int r = r0 + i * (128 / kChunks);
-                        uint8_t *half = to + (chunk >> 2) * 16384;
-                        uint4 x, y;
-                        e4m3x4_to_f16x2x2(from[i].x, x.x, x.y);
-                        e4m3x4_to_f16x2x2(from[i].y, x.z, x.w);
-                        e4m3x4_to_f16x2x2(from[i].z, y.x, y.y);
-                        e4m3x4_to_f16x2x2(from[i].w, y.z, y.w);
-                        const int p = (chunk & 3) * 2, swap = kChunks == 8 ? chunk >> 2 : r & 1;
+                    for (int c = 0; c < 4; ++c) {
+                        float m[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)  // 0 to 3: the chunk's first block of keys
+                            m[i] = fmaxf(fmaxf(__uint_as_float(raw[c][4 * i]), __uint_as_float(raw[c][4 * i + 1])),
+                                         fmaxf(__uint_as_float(raw[c][4 * i + 2]), __uint_as_float(raw[c][4 * i + 3])));
+                        const float4 s0 = scale[2 * c], s1 = scale[2 * c + 1];
+                        // (a block of which nothing is seen has -inf, times a scale of 0 a NaN, which is passed over)
+                        top = fmaxf(top, fmaxf(fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), factor * s0.x, s0.w),
+                                               fmaf(fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7])), factor * s1.x, s1.w)));
+                    }
+                    if (__any_sync(kFullMask, top > ref + kAttnSlack)) {
+                        const float to = fmaxf(ref, top), by = ex2(ref - to);
+                        ref = to;
+                        total_w *= by;
+                        if (j > 0) {  // the products so far are done: the scores came behind them
+#pragma unroll 1
+                            for (int c = 0; c < D / 8; ++c) tmem_scale8(at_o + c * 8, by);
+                        }
+                    }
+                    float sums[8];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16], rest[P2 ? 16 : 1];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 sc = scale[2 * c + h];
+                            const float f = factor * sc.x, shift = sc.y - ref + kAttnTop;
+                            const uint64_t f2 = pack2(f, f), shift2 = pack2(shift, shift);
+                            uint64_t sum[2] = {0, 0};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int k = h * 16 + 2 * i;
+                                const float2 x = unpack2(fma2(bits2(raw[c][k], raw[c][k + 1]), f2, shift2));
+                                float p0 = ex2(x.x), p1 = ex2(x.y);
+                                if (masked) {  // (a scale of 0 makes a NaN of -inf)
+                                    if (c * 32 + k >= left) p0 = 0.f;
+                                    if (c * 32 + k + 1 >= left) p1 = 0.f;
+                                }
+                                sum[i & 1] = add2(sum[i & 1], pack2(p0, p1));
+                                w[h * 8 + i] = f32x2_to_f16x2(p0, p1);
+                                if (P2) rest[P2 ? h * 8 + i : 0] = attn_rest(p0, p1, w[h * 8 + i]);
+                            }
+                            const float2 t = unpack2(add2(sum[0], sum[1]));
+                            sums[2 * c + h] = (t.x + t.y) * sc.z;
+                        }
+                        tmem_st16(at_s + c * 16, w);
+                        if (P2) tmem_st16(at_s + 64 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(rest));
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->weights[b]);
+                    total_w += ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
+                    ++turns;
+                }
+                wait(&ctl->out_done[b], items & 1);
+                ++items;
+                tc_fence_after();
+            }
+            tile += n;
+            if (mine && !wait.dead) {
+                const bool whole = run.whole();
+                const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (run.off == 0 ? 1 : 0);
+                const bool live = r < it.n_rows;
+                const int64_t to = whole ? attn_out_at(a, it.s.start, it.head, it.row0 + (live ? r : 0), D)
+                                         : (piece * kRowsPer + r) * D;
+                const float norm = !whole ? 1.f : total_w == 0.f ? 0.f : __fdiv_rn(1.f, total_w);
+                if (!whole && live) a.stats[piece * kRowsPer + r] = make_float2(ref, total_w);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    if (n > 0) {
+                        tmem_ld32(at_o + c * 32, o);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                    }
+                    if (!live) continue;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= norm;
+                    if (whole && a.out_bf16) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to + c * 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            __nv_bfloat162 v[4];
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) v[m] = __floats2bfloat162_rn(o[8 * i + 2 * m], o[8 * i + 2 * m + 1]);
+                            dst[i] = *reinterpret_cast<uint4 *>(v);
+                        }
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>((whole ? static_cast<float *>(a.out) : a.part) + to + c * 32);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+                if (!whole && run.off == 0 && warp == 0 && lane == 0) {
+                    AttnOwner owner;
+                    owner.start = it.s.start;
+                    owner.row0 = it.row0;
+                    owner.last = static_cast<int>((run.pos + it.tiles + kTileStart - 1) / per);
+                    owner.head = static_cast<short>(it.head);
+                    owner.rows = static_cast<short>(it.n_rows);
+                    a.owner[blockIdx.x] = owner;
+                }
+            }
+        }
+    } else if (warp != kIssueWarp) {
+        // ------------------------------------------------------------ codes -> f16
+        // The lower four warps widen keys, three of the upper values.  16 codes are a thread's load.
+        constexpr int kChunks = D / 16;
+        const bool keys = warp < kIssueWarp;
+        const int ct = keys ? tid - kWidenWarp * 32 : tid - (kIssueWarp + 1) * 32;
+        const int chunk = ct % kChunks, r0 = ct / kChunks, step = (keys ? 128 : 96) / kChunks;
+        constexpr int kLoads = (kTileKeys * kChunks + 95) / 96;
+        const uint8_t *cache = keys ? a.k_cache : a.v_cache;
+        uint8_t *to_smem = keys ? k_smem : v_smem;
+        uint64_t *full = keys ? ctl->k_full : ctl->v_full, *freed = keys ? ctl->k_free : ctl->v_free;
+        const bool scaling = warp == kWidenWarp && lane < 8;
+        uint32_t tile = 0;
+        for (; run.more() && !wait.dead; run.next()) {
+            const TileItem &it = run.it;
+            if (run.n == 0) continue;
+            const int32_t *table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
+            // Lane l (of 8) serves the tile's block l: its page, three tiles ahead of the codes' use; its first row in
+            // the pool, two; its scales, one.
+            const auto page_at = [&](int j) {
+                const int key = j * kTileKeys + (lane & 7) * kAttnBlock;
+                return j < run.t1 && key < it.vis ? attn_page(a, table, key, fault) : -1;
+            };
+            const auto base_at = [&](int page, int j) -> int {
+                const int key = j * kTileKeys + (lane & 7) * kAttnBlock;
+                return page < 0 ? -1 : ((page * a.n_kv + it.head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+            };
+            const auto scale_at = [&](const float *scales, int base) {
+                return scaling && base >= 0 ? __ldcg(scales + (base >> 4)) : 1.f;
+            };
+            const auto load = [&](uint4(&to)[kLoads], int base, int j) {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int r = r0 + i * step;
+                    const int from = __shfl_sync(kFullMask, base, (r >> 4) & 7);
+                    to[i] = r < kTileKeys && from >= 0 && j * kTileKeys + r < it.vis
+                                ? __ldcg(reinterpret_cast<const uint4 *>(cache + (static_cast<int64_t>(from) + (r & 15)) * D) + chunk)
+                                : make_uint4(0, 0, 0, 0);
+                }
+            };
+            int base_next = base_at(page_at(run.off), run.off);
+            float ks = scale_at(a.k_scales, base_next), vs = scale_at(a.v_scales, base_next);
+            uint4 code[kLoads];
+            load(code, base_next, run.off);
+            base_next = base_at(page_at(run.off + 1), run.off + 1);
+            int page_later = page_at(run.off + 2);
+            for (int j = run.off; j < run.t1; ++j, ++tile) {
+                const uint32_t buf = tile & 1;
+                const float ks_next = scale_at(a.k_scales, base_next), vs_next = scale_at(a.v_scales, base_next);
+                if (tile >= 2) wait(&freed[buf], ((tile >> 1) - 1) & 1);
+                if (wait.dead) break;
+                if (scaling) {
+                    const float v = vs < kAttnLeastScale ? kAttnLeastScale : vs, l = attn_log2(v);
+                    ctl->scale[tile & 3][lane] = make_float4(ks, l, __frcp_rn(v), fmaxf(l, kAttnLeastLog));
+                }
+                // 16 codes fill two pieces of a swizzled row; half of the lanes store them in the other order, off the
+                // banks of the others
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int r = r0 + i * step;
+                    uint8_t *half = to_smem + buf * Shape::kKv + (chunk >> 2) * 16384;
+                    uint4 x, y;
+                    e4m3x4_to_f16x2x2(code[i].x, x.x, x.y);
+                    e4m3x4_to_f16x2x2(code[i].y, x.z, x.w);
+                    e4m3x4_to_f16x2x2(code[i].z, y.x, y.y);
+                    e4m3x4_to_f16x2x2(code[i].w, y.z, y.w);
+                    const int p = (chunk & 3) * 2, swap = kChunks == 8 ? chunk >> 2 : r & 1;
+                    if (r < kTileKeys) {
                         *reinterpret_cast<uint4 *>(half + piece_at(r, p + swap)) = swap ? y : x;
                         *reinterpret_cast<uint4 *>(half + piece_at(r, p + 1 - swap)) = swap ? x : y;
                     }
-                };
-                long long base = base_at(off), base_next = base_at(off + 1);
-                uint4 kc[kLoads], vc[kLoads];
-                load(kc, a.k_cache, base, off);
-                load(vc, a.v_cache, base, off);
-                for (int j = off; j < t1; ++j, ++tile) {
-                    const uint32_t buf = tile & 1, use = tile >> 1;
-                    float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
-                    if (warp == kWidenWarp && lane < 8 && base >= 0) {
-                        sc.x = __ldcg(a.k_scales + (base >> 4));
-                        float v = __ldcg(a.v_scales + (base >> 4));
-                        if (v < kAttnLeastScale) v = kAttnLeastScale;
-                        sc.y = attn_log2(v);
-                        sc.z = __frcp_rn(v);
-                        sc.w = fmaxf(sc.y, kAttnLeastLog);
-                    }
-                    if (tile >= 2) wait(&ctl->k_free[buf], (use - 1) & 1);
-                    if (wait.dead) break;
-                    if (warp == kWidenWarp && lane < 8) ctl->scale[tile & 3][lane] = sc;
-                    widen(k_smem + buf * Shape::kKv, kc);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->k_full[buf]);
-                    base = base_next;
-                    load(kc, a.k_cache, base, j + 1);
-                    if (tile >= 2) wait(&ctl->v_free[buf], (use - 1) & 1);
-                    if (wait.dead) break;
-                    widen(v_smem + buf * Shape::kKv, vc);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->v_full[buf]);
-                    load(vc, a.v_cache, base, j + 1);
-                    base_next = base_at(j + 2);
                 }
-            } else if (warp == kIssueWarp && n > 0) {
-                // -------------------------------------------------------- products
-                constexpr uint32_t kQk = f16_idesc(kTileKeys, false), kPv = f16_idesc(D, true);
-                const uint32_t q_at = smem_u32(q_smem), k_at = smem_u32(k_smem), v_at = smem_u32(v_smem);
-                const auto scores = [&](int b, uint32_t buf) {
-                    if (elect_one()) {
-#pragma unroll
-                        for (int term = 0; term < (Q2 ? 2 : 1); ++term)
-#pragma unroll
-                            for (int i = 0; i < D / 16; ++i) {
-                                const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
-                                mma_f16_ss(s_col[b], smem_desc(q_at + (Q2 ? term : b) * (128 * D * 2) + at, 128),
-                                           smem_desc(k_at + buf * Shape::kKv + at, 128), kQk, term > 0 || i > 0);
-                            }
-                        tc_commit(&ctl->scores[b]);
-                    }
-                    __syncwarp();
-                };
-                const auto outputs = [&](int b, uint32_t buf, bool acc) {
-                    if (elect_one()) {
-#pragma unroll
-                        for (int term = 0; term < (P2 ? 2 : 1); ++term)
-#pragma unroll
-                            for (int i = 0; i < kTileKeys / 16; ++i)
-                                mma_f16_ts(o_col[b], s_col[b] + term * 64 + i * 8,
-                                           values_desc(v_at + buf * Shape::kKv + i * 2048, 16384), kPv,
-                                           acc || term > 0 || i > 0);
-                    }
-                    __syncwarp();
-                };
-                const auto commit = [&](uint64_t *bar) {
-                    if (elect_one()) tc_commit(bar);
-                    __syncwarp();
-                };
-                wait(&ctl->q_ready, all_items & 1);
-                wait(&ctl->k_full[tile & 1], (tile >> 1) & 1);
-                tc_fence_after();
-                if (!wait.dead) {
-                    for (int b = 0; b < live_blocks; ++b) scores(b, tile & 1);
-                    commit(&ctl->k_free[tile & 1]);
-                }
-                for (int j = 0; j < n && !wait.dead; ++j, ++tile) {
-                    const uint32_t buf = tile & 1, next = tile + 1;
-                    wait(&ctl->v_full[buf], (tile >> 1) & 1);
-                    for (int b = 0; b < live_blocks; ++b) {
-                        wait(&ctl->weights[b], turns[b] & 1);
-                        ++turns[b];
-                        if (b == 0 && j + 1 < n) wait(&ctl->k_full[next & 1], (next >> 1) & 1);
-                        if (wait.dead) break;
-                        tc_fence_after();
-                        outputs(b, buf, j > 0);
-                        if (j + 1 < n)
-                            scores(b, next & 1);
-                        else
-                            commit(&ctl->out_done[b]);
-                    }
-                    if (wait.dead) break;
-                    commit(&ctl->v_free[buf]);
-                    if (j + 1 < n) commit(&ctl->k_free[next & 1]);
-                }
-            } else if (warp < kBlocks * 4) {
-                // -------------------------------------------------------- weights and the way out
-                const int b = warp >> 2, wq = warp & 3, r = b * 128 + wq * 32 + lane;
-                const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-                const uint32_t at_s = s_col[b] + lanes, at_o = o_col[b] + lanes;
-                float ref = kAttnUnset, total_w = 0.f;
-                const bool mine = b < live_blocks;
-                if (n > 0) {
-                    if (mine) stage_queries<D, Q2>(a, it, q_smem, ctl->factor, b, wq, lane);
-                    fence_async_smem();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->q_ready);
-                    if (!mine) wait(&ctl->q_ready, all_items & 1);  // never two arrivals in one phase
-                }
-                if (mine && n > 0) {
-                    const float factor = ctl->factor[r];
-                    const int see0 = it.s.kv - it.s.t + 1;
-                    const int lim = min(it.vis, max(0, see0 + (it.row0 + r) / a.group));
-                    const int all_see = max(0, see0 + (it.row0 + b * 128) / a.group);
-                    for (int j = off; j < t1; ++j) {
-                        const float4 *scale = ctl->scale[(tile + (j - off)) & 3];
-                        wait(&ctl->scores[b], turns[b] & 1);
-                        if (wait.dead) break;
-                        tc_fence_after();
-                        const int left = lim - j * kTileKeys;  // keys of the tile that the row sees
-                        const bool masked = (j + 1) * kTileKeys > all_see;
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            float s[32];
-                            tmem_ld32(at_s + c * 32, s);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float4 sc = scale[2 * c + h];
-                                float m = -INFINITY;
-                                if (masked) {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        if (c * 32 + h * 16 + i < left) m = fmaxf(m, s[h * 16 + i]);
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) m = fmaxf(m, s[h * 16 + i]);
-                                }
-                                // (a block of which nothing is seen has -inf, times a scale of 0 a NaN, which is passed over)
-                                top = fmaxf(top, fmaf(m, factor * sc.x, sc.w));
-                            }
-                        }
-                        if (__any_sync(kFullMask, top > ref + kAttnSlack)) {
-                            const float to = fmaxf(ref, top), by = ex2(ref - to);
-                            ref = to;
-                            total_w *= by;
-                            if (j > off) {  // the products so far are done: the scores came behind them
-#pragma unroll 1
-                                for (int c = 0; c < D / 32; ++c) {
-                                    float o[32];
-                                    tmem_ld32(at_o + c * 32, o);
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] *= by;
-                                    tmem_st32(at_o + c * 32, o);
-                                }
-                            }
-                        }
-                        uint32_t rest[P2 ? 64 : 1];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            float s[32];
-                            uint32_t w[16];
-                            tmem_ld32(at_s + c * 32, s);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float4 sc = scale[2 * c + h];
-                                const float f = factor * sc.x, shift = sc.y - ref + kAttnTop;
-                                float sum = 0.f;
-#pragma unroll
-                                for (int i = 0; i < 16; i += 2) {
-                                    float p0 = ex2(fmaf(s[h * 16 + i], f, shift)), p1 = ex2(fmaf(s[h * 16 + i + 1], f, shift));
-                                    if (masked) {
-                                        if (c * 32 + h * 16 + i >= left) p0 = 0.f;
-                                        if (c * 32 + h * 16 + i + 1 >= left) p1 = 0.f;
-                                    }
-                                    sum += p0 + p1;
-                                    w[h * 8 + i / 2] = f32x2_to_f16x2(p0, p1);
-                                    if (P2) rest[P2 ? c * 16 + h * 8 + i / 2 : 0] = attn_rest(p0, p1, w[h * 8 + i / 2]);
-                                }
-                                total_w = fmaf(sum, sc.z, total_w);
-                            }
-                            tmem_st16(at_s + c * 16, w);
-                        }
-                        if (P2) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t w[16];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) w[i] = rest[P2 ? c * 16 + i : 0];
-                                tmem_st16(at_s + 64 + c * 16, w);
-                            }
-                        }
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl->weights[b]);
-                        ++turns[b];
-                    }
-                    wait(&ctl->out_done[b], items[b] & 1);
-                    ++items[b];
-                    tc_fence_after();
-                }
-                if (mine && !wait.dead) {
-                    const bool whole = off == 0 && end == it.tiles;
-                    const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (off == 0 ? 1 : 0);
-                    const bool live = r < it.n_rows;
-                    const int64_t to = whole ? attn_out_at(a, it.s.start, it.head, it.row0 + (live ? r : 0), D)
-                                             : (piece * kRowsPer + r) * D;
-                    const float norm = !whole ? 1.f : total_w == 0.f ? 0.f : __fdiv_rn(1.f, total_w);
-                    if (!whole && live) a.stats[piece * kRowsPer + r] = make_float2(ref, total_w);
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        if (n > 0) {
-                            tmem_ld32(at_o + c * 32, o);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-                        }
-                        if (!live) continue;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= norm;
-                        if (whole && a.out_bf16) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to + c * 32);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                __nv_bfloat162 v[4];
-#pragma unroll
-                                for (int m = 0; m < 4; ++m) v[m] = __floats2bfloat162_rn(o[8 * i + 2 * m], o[8 * i + 2 * m + 1]);
-                                dst[i] = *reinterpret_cast<uint4 *>(v);
-                            }
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>((whole ? static_cast<float *>(a.out) : a.part) + to + c * 32);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                        }
-                    }
-                    if (!whole && off == 0 && warp == 0 && lane == 0) {
-                        AttnOwner owner;
-                        owner.start = it.s.start;
-                        owner.row0 = it.row0;
-                        owner.last = static_cast<int>((pos + it.tiles + kTileStart - 1) / per);
-                        owner.head = static_cast<short>(it.head);
-                        owner.rows = static_cast<short>(it.n_rows);
-                        a.owner[blockIdx.x] = owner;
-                    }
-                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[buf]);
+                load(code, base_next, j + 1);
+                base_next = base_at(page_later, j + 2);
+                page_later = page_at(j + 3);
+                ks = ks_next;
+                vs = vs_next;
             }
-            // every warp counts alike
-            if (!(warp >= kWidenWarp)) tile += n;
-            if (n > 0) ++all_items;
-            pos += it.tiles + kTileStart;
-            off = 0;
-            if (pos + kTileStart < run_hi) next_tile_item(a, kRowsPer, it);
         }
-        if (warp == kIssueWarp && wait.dead) {  // products in flight end before TMEM is given up, the wait bounded
-            if (elect_one()) tc_commit(&ctl->drain);
+    } else {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t kQk = f16_idesc(kTileKeys, false), kPv = f16_idesc(D, true);
+        const uint32_t q_at = smem_u32(q_smem), k_at = smem_u32(k_smem), v_at = smem_u32(v_smem);
+        const auto scores = [&](int b, uint32_t buf) {
+            if (elect_one()) {
+#pragma unroll
+                for (int term = 0; term < (Q2 ? 2 : 1); ++term)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
+                        mma_f16_ss(s_col[b], smem_desc(q_at + (Q2 ? term : b) * (128 * D * 2) + at, 128),
+                                   smem_desc(k_at + buf * Shape::kKv + at, 128), kQk, term > 0 || i > 0);
+                    }
+                tc_commit(&ctl->scores[b]);
+            }
             __syncwarp();
+        };
+        const auto outputs = [&](int b, uint32_t buf, bool acc) {
+            if (elect_one()) {
+#pragma unroll
+                for (int term = 0; term < (P2 ? 2 : 1); ++term)
+#pragma unroll
+                    for (int i = 0; i < kTileKeys / 16; ++i)
+                        mma_f16_ts(o_col[b], s_col[b] + term * 64 + i * 8,
+                                   values_desc(v_at + buf * Shape::kKv + i * 2048, 16384), kPv, acc || term > 0 || i > 0);
+            }
+            __syncwarp();
+        };
+        const auto commit = [&](uint64_t *bar) {
+            if (elect_one()) tc_commit(bar);
+            __syncwarp();
+        };
+        uint32_t tile = 0, turns[2] = {0, 0}, all_items = 0;
+        for (; run.more() && !wait.dead; run.next()) {
+            const int n = run.n, live_blocks = run.it.n_rows > 128 ? 2 : 1;
+            if (n == 0) continue;
+            wait(&ctl->q_ready, all_items & 1);
+            ++all_items;
+            wait(&ctl->k_full[tile & 1], (tile >> 1) & 1);
+            if (wait.dead) break;
+            tc_fence_after();
+            for (int b = 0; b < live_blocks; ++b) scores(b, tile & 1);
+            commit(&ctl->k_free[tile & 1]);
+            for (int j = 0; j < n && !wait.dead; ++j, ++tile) {
+                const uint32_t buf = tile & 1, next = tile + 1;
+                wait(&ctl->v_full[buf], (tile >> 1) & 1);
+                for (int b = 0; b < live_blocks; ++b) {
+                    if (b == 0 && j + 1 < n) wait(&ctl->k_full[next & 1], (next >> 1) & 1);
+                    wait(&ctl->weights[b], turns[b] & 1);
+                    ++turns[b];
+                    if (wait.dead) break;
+                    tc_fence_after();
+                    outputs(b, buf, j > 0);
+                    if (j + 1 < n)
+                        scores(b, next & 1);
+                    else
+                        commit(&ctl->out_done[b]);
+                }
+                if (wait.dead) break;
+                commit(&ctl->v_free[buf]);
+                if (j + 1 < n) commit(&ctl->k_free[next & 1]);
+            }
+        }
+        if (wait.dead) {  // products in flight end before TMEM is given up, the wait bounded
+            commit(&ctl->drain);
             (void)warp_wait_bounded(&ctl->drain, 0);
         }
     }

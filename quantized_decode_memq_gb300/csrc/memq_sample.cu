@@ -46,6 +46,32 @@ constexpr int kUnitLog = 44;  // weights are integers in units of 2^-44
 constexpr uint32_t kLeastKey = 0x007fffffu;  // of -infinity; NaN has key 0
 constexpr int64_t kMaxVocab = 360000;
 
+// 2^(-j / 512) in units of 2^-62, formed by the compiler: the 512th root of 1/2 by nine square roots, then its powers.
+struct Powers {
+    unsigned long long at[kTable];
+};
+constexpr unsigned long long root_of(unsigned __int128 x) {  // floor of the square root
+    unsigned __int128 r = 0;
+    for (int b = 63; b >= 0; --b) {
+        const unsigned __int128 t = r | (static_cast<unsigned __int128>(1) << b);
+        if (t * t <= x) r = t;
+    }
+    return static_cast<unsigned long long>(r);
+}
+constexpr Powers make_powers() {
+    Powers p{};
+    unsigned long long step = 1ull << 62;  // 2^-1 in units of 2^-63
+    for (int i = 0; i < 9; ++i) step = root_of(static_cast<unsigned __int128>(step) << 63);
+    unsigned long long run = 1ull << 63;
+    for (int j = 0; j < kTable; ++j) {
+        p.at[j] = (run >> 1) + (run & 1);
+        const unsigned __int128 next = static_cast<unsigned __int128>(run) * step;
+        run = static_cast<unsigned long long>((next + (static_cast<unsigned __int128>(1) << 62)) >> 63);
+    }
+    return p;
+}
+__device__ const Powers g_powers = make_powers();
+
 struct SampleArgs {
     const void *logits;
     int64_t stride;
@@ -105,6 +131,12 @@ struct Scale {
 // x = (top - l) log2(e) / T, rounded to f32: monotone in l, so its steps are ranges of the order.
 __device__ __forceinline__ float coarse(const Scale &s, float l) { return l == s.top ? 0.f : (s.top - l) * s.hi; }
 
+// 2^-x of x >= kCareful: x is off by 2^-24 of it and exp2 by 2^-22 of it, below 2^-42 together.
+constexpr float kCareful = 24.f;
+__device__ __forceinline__ unsigned long long small_weight(float x) {
+    return x < 60.f ? static_cast<unsigned long long>(__float2uint_rn(ex2(static_cast<float>(kUnitLog) - x))) : 0ull;
+}
+
 // 2^-x in units of 2^-kUnitLog.
 __device__ __forceinline__ unsigned long long weight_of(const Scale &s, const unsigned long long *table, float l) {
     if (l == s.top) return 1ull << kUnitLog;
@@ -112,10 +144,7 @@ __device__ __forceinline__ unsigned long long weight_of(const Scale &s, const un
     const float dh = __fsub_rn(s.top, l), bb = __fsub_rn(dh, s.top);
     const float dl = __fsub_rn(__fsub_rn(s.top, __fsub_rn(dh, bb)), __fadd_rn(l, bb));
     const float yh = __fmul_rn(dh, s.hi);
-    if (!(yh < 24.f)) {
-        const float w = ex2(static_cast<float>(kUnitLog) - yh);
-        return yh < 60.f ? static_cast<unsigned long long>(__float2uint_rn(w)) : 0ull;
-    }
+    if (!(yh < kCareful)) return small_weight(yh);
     const float yl = __fmaf_rn(dh, s.hi, -yh) + __fmaf_rn(dh, s.lo, dl * s.hi);
     // the nearest multiple n of 2^-9
     const float big = 0x1.8p23f / kTable;
@@ -150,6 +179,55 @@ template <bool BF16>
 struct Row {
     const uint8_t *data;  // this CTA's tokens
     int len, first;       // their number, the first one's index
+    int head;             // tokens ahead of the first 16-byte boundary
+    static constexpr int kVec = BF16 ? 8 : 4;
+    // f(i, value) of every token, in no order.
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+        const int body = (len - head) / kVec, tail = head + body * kVec, tid = threadIdx.x;
+        if (tid < head) f(tid, at(tid));
+        if (tail + tid < len && tid < kVec) f(tail + tid, at(tail + tid));
+        const uint4 *from = reinterpret_cast<const uint4 *>(data + head * (BF16 ? 2 : 4));
+        for (int i = tid; i < body; i += kThreads) {
+            float v[kVec];
+            vec(from[i], v);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) f(head + i * kVec + j, v[j]);
+        }
+    }
+    // f(i, values, n) of groups of n <= kVec tokens next to one another.
+    template <typename F>
+    __device__ __forceinline__ void each_group(F f) const {
+        const int body = (len - head) / kVec, tail = head + body * kVec, tid = threadIdx.x;
+        float v[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] = 0.f;
+        if (tid < head) {
+            v[0] = at(tid);
+            f(tid, v, 1);
+        }
+        if (tail + tid < len && tid < kVec) {
+            v[0] = at(tail + tid);
+            f(tail + tid, v, 1);
+        }
+        const uint4 *from = reinterpret_cast<const uint4 *>(data + head * (BF16 ? 2 : 4));
+        for (int i = tid; i < body; i += kThreads) {
+            vec(from[i], v);
+            f(head + i * kVec, v, kVec);
+        }
+    }
+    __device__ __forceinline__ static void vec(uint4 u, float (&v)[kVec]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (BF16) {
+                v[(2 * j) % kVec] = __uint_as_float(w[j] << 16) + 0.f;
+                v[(2 * j + 1) % kVec] = __uint_as_float(w[j] & 0xffff0000u) + 0.f;
+            } else {
+                v[j % kVec] = __uint_as_float(w[j]) + 0.f;
+            }
+        }
+    }
     __device__ __forceinline__ float at(int i) const {
         float v;
         if (BF16)
@@ -251,13 +329,34 @@ __device__ __forceinline__ int gather_lists(Shared &sh, uint32_t ctas) {
 __device__ __forceinline__ float value_of(unsigned long long place) { return unorder_bits(static_cast<uint32_t>(place >> 32)); }
 __device__ __forceinline__ int index_of(unsigned long long place) { return static_cast<int>(~static_cast<uint32_t>(place)); }
 
-// The least sum that reaches p of `total`, and u of `total` to be passed.
-__device__ __forceinline__ unsigned long long reach(double p, unsigned long long total) {
-    return static_cast<unsigned long long>(ceil(p * static_cast<double>(total)));
+// f * total for f in [0, 1], rounded down, and whether something was dropped.
+__device__ __forceinline__ unsigned long long part_of(float f, unsigned long long total, bool &rest) {
+    const uint32_t bits = __float_as_uint(f);
+    const int e = max(static_cast<int>(bits >> 23), 1);
+    const unsigned long long m = (bits & 0x7fffffu) | (bits >= 0x800000u ? 0x800000u : 0u);  // f = m 2^(e - 150)
+    const unsigned long long lo = m * total, hi = __umul64hi(m, total);
+    const int shift = 150 - e;  // 23 to 149
+    rest = false;
+    if (shift >= 128) {
+        rest = (hi | lo) != 0;
+        return 0;
+    }
+    if (shift >= 64) {
+        rest = lo != 0 || (shift > 64 && (hi << (128 - shift)) != 0);
+        return hi >> (shift - 64);
+    }
+    rest = (lo << (64 - shift)) != 0;
+    return hi << (64 - shift) | lo >> shift;
 }
-__device__ __forceinline__ unsigned long long below(double u, unsigned long long total) {
-    const unsigned long long t = static_cast<unsigned long long>(u * static_cast<double>(total));
-    return min(t, total - 1);
+// The least sum that reaches p of `total`; u of `total`, which the drawn token's sum is above.
+__device__ __forceinline__ unsigned long long reach(float p, unsigned long long total) {
+    bool rest;
+    const unsigned long long n = part_of(p, total, rest);
+    return n + rest;
+}
+__device__ __forceinline__ unsigned long long below(float u, unsigned long long total) {
+    bool rest;
+    return min(part_of(u, total, rest), total - 1);
 }
 
 // Of the sorted list's first n tokens: how many hold `need` of weight, at least one.  sh.weight has their sums.
@@ -290,6 +389,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
     uint8_t *dst = smem + sizeof(Shared) + skew;
     row.data = dst;
+    row.head = min(row.len, ((16 - skew) & 15) / kSize);
     float top = -INFINITY;  // of this thread's tokens
     bool any = false;       // one is a number
     {
@@ -332,8 +432,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
             }
         }
     }
-    for (int j = tid; j < kTable; j += kThreads)
-        sh.table[j] = static_cast<unsigned long long>(rint(exp2(-j / static_cast<double>(kTable)) * 0x1p62));
+    static_assert(kTable == kThreads, "a thread copies one power");
+    sh.table[tid] = __ldg(&g_powers.at[tid]);
     if (tid == 0) sh.count = 0;
     cluster_wait_entry();
     const uint32_t my_top = any ? key_of(top + 0.f) : 0u;
@@ -353,25 +453,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     const float temperature = a.temperature ? __ldcg(a.temperature + row_i) : 1.f;
     int k = a.top_k ? __ldcg(a.top_k + row_i) : 0;
     if (k <= 0 || k > a.vocab) k = a.vocab;
-    double p = a.top_p ? static_cast<double>(__ldcg(a.top_p + row_i)) : 1.0;
-    if (!(p < 1.0)) p = 1.0;
-    if (p <= 0.0) {
-        p = 1.0;
+    float p = a.top_p ? __ldcg(a.top_p + row_i) : 1.f;
+    if (!(p < 1.f)) p = 1.f;
+    if (p <= 0.f) {
+        p = 1.f;
         k = 1;
     }
     const float floor_p = a.min_p ? fminf(fmaxf(__ldcg(a.min_p + row_i), 0.f), 1.f) : 0.f;
-    const unsigned long long least = max(1ull, static_cast<unsigned long long>(ceil(static_cast<double>(floor_p) * (1ull << kUnitLog))));
+    const unsigned long long least = max(1ull, __float2ull_ru(floor_p * 0x1p44f));
     const float u_in = __ldcg(a.u + row_i);
-    const double u = u_in > 0.f ? static_cast<double>(fminf(u_in, 1.f)) : 0.0;
+    const float u = u_in > 0.f ? fminf(u_in, 1.f) : 0.f;
 
     // ------------------------------------------------------------------ greedy
     if (!(temperature > 0.f) || k == 1 || top_key <= kLeastKey) {
         uint32_t best = 0xffffffffu;
-        for (int i = tid; i < row.len; i += kThreads)
-            if (key_of(row.at(i)) == top_key) {
-                best = static_cast<uint32_t>(row.first + i);
-                break;
-            }
+        if (my_top == top_key)
+            row.each([&](int i, float v) {
+                if (key_of(v) == top_key) best = min(best, static_cast<uint32_t>(row.first + i));
+            });
         best = __reduce_min_sync(kFullMask, best);
         cluster_sync();  // the tops have been read
         if (lane == 0) sh.warp32[warp] = best;
@@ -390,9 +489,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     Scale s;
     s.top = unorder_bits(top_key);
     {
-        const double c = 1.4426950408889634074 / static_cast<double>(fmaxf(temperature, 1e-30f));
-        s.hi = static_cast<float>(c);
-        s.lo = static_cast<float>(c - static_cast<double>(s.hi));
+        const float t = fmaxf(temperature, 1e-30f), kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;
+        s.hi = __fdiv_rn(kLog2e, t);
+        s.lo = __fdiv_rn(__fmaf_rn(-s.hi, t, kLog2e) + kLog2eLo, t);
     }
 
     // ------------------------------------------------------------------ top-k: few tokens, sorted
@@ -413,13 +512,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         cluster_sync();
         uint32_t bound = 0xffffffffu;
         for (uint32_t r = 0; r < ctas; ++r) bound = min(bound, sh.from_cta[r]);
-        for (int i = tid; i < row.len; i += kThreads) {
-            const uint32_t key = key_of(row.at(i));
-            if (key >= bound) {
-                const uint32_t at = atomicAdd(&sh.count, 1u);
-                if (at < kCap) sh.list[at] = place_of(key, row.first + i);
-            }
-        }
+        if (my_top >= bound)
+            row.each([&](int i, float v) {
+                const uint32_t key = key_of(v);
+                if (key >= bound) {
+                    const uint32_t at = atomicAdd(&sh.count, 1u);
+                    if (at < kCap) sh.list[at] = place_of(key, row.first + i);
+                }
+            });
         __syncthreads();
         if (tid < static_cast<int>(ctas)) *in_cta(&sh.pair[rank][0], tid) = sh.count;
         cluster_sync();
@@ -434,7 +534,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
                 __syncthreads();
                 scan_weights(sh, m);
                 int kept = m;
-                if (p < 1.0) kept = first_reaching(sh, m, reach(p, sh.weight[m - 1]));
+                if (p < 1.f) kept = first_reaching(sh, m, reach(p, sh.weight[m - 1]));
                 __syncthreads();
                 // min-p, and the order of indices: a token's place there is its rank among the kept
                 int mine = 0;
@@ -476,19 +576,19 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         while (lo < hi) {
             const uint32_t mid = lo + (hi - lo) / 2 + 1;
             unsigned long long n = 0, none = 0;
-            for (int i = tid; i < row.len; i += kThreads) n += key_of(row.at(i)) >= mid;
+            row.each([&](int, float v) { n += key_of(v) >= mid; });
             cluster_sum(sh, rank, ctas, n, none);
             if (n >= static_cast<unsigned long long>(k)) lo = mid; else hi = mid - 1;
         }
         unsigned long long above = 0, none = 0;
-        for (int i = tid; i < row.len; i += kThreads) above += key_of(row.at(i)) > lo;
+        row.each([&](int, float v) { above += key_of(v) > lo; });
         cluster_sum(sh, rank, ctas, above, none);
         int from = 0, to = a.vocab - 1;  // the least index up to which enough equal ones lie
         while (from < to) {
             const int mid = (from + to) >> 1;
             unsigned long long n = 0;
             none = 0;
-            for (int i = tid; i < row.len; i += kThreads) n += key_of(row.at(i)) == lo && row.first + i <= mid;
+            row.each([&](int i, float v) { n += key_of(v) == lo && row.first + i <= mid; });
             cluster_sum(sh, rank, ctas, n, none);
             if (above + n >= static_cast<unsigned long long>(k)) to = mid; else from = mid + 1;
         }
@@ -497,7 +597,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
 
     // ------------------------------------------------------------------ top-p
     unsigned long long cut = cut_k;
-    if (p < 1.0) {
+    if (p < 1.f) {
         // steps of x = coarse(): [x0 + b / per, x0 + (b + 1) / per), the last open; below x0 all are kept
         float x0 = 0.f, per = 64.f;
         float x_from = 0.f, x_to = INFINITY;  // the cut lies at from <= x < to
@@ -506,14 +606,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         for (int level = 0; level < 3 && !sorted; ++level) {
             for (int b = tid; b < kBins; b += kThreads) sh.hist[b] = 0;
             __syncthreads();
-            for (int i = tid; i < row.len; i += kThreads) {
-                const float v = row.at(i);
+            row.each([&](int i, float v) {
                 const uint32_t key = key_of(v);
-                if (key <= kLeastKey || !in_k(key, row.first + i)) continue;
                 const float x = coarse(s, v);
-                if (x < x_from || x >= x_to) continue;
-                atomicAdd(&sh.hist[min(kBins - 1, static_cast<int>(fminf((x - x0) * per, 1e6f)))], 1u);
-            }
+                // (not of NaN and of -infinity, whose x is none or infinite)
+                if (x >= x_from && x < x_to && in_k(key, row.first + i))
+                    atomicAdd(&sh.hist[min(kBins - 1, static_cast<int>(fminf((x - x0) * per, 1e6f)))], 1u);
+            });
             cluster_sync();
             // Bounds of the weight up to each step; all CTAs form them alike.
             const int b0 = tid * (kBins / kThreads);
@@ -575,8 +674,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
             }
             // on the first level the total is bounded too; later it is known
             // (sums of f32 in another order differ by far less than 1e-5)
-            const float want_lo = static_cast<float>(p) * (level ? static_cast<float>(total) * 0x1p-44f : lo_all) * 0.99999f;
-            const float want_hi = static_cast<float>(p) * (level ? static_cast<float>(total) * 0x1p-44f : hi_all) * 1.00001f;
+            const float want_lo = p * (level ? static_cast<float>(total) * 0x1p-44f : lo_all) * 0.99999f;
+            const float want_hi = p * (level ? static_cast<float>(total) * 0x1p-44f : hi_all) * 1.00001f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 hi_run += highs[j];
@@ -589,21 +688,38 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
             const float w_to = sh.window[1] == kBins - 1 ? x_to : x0 + (sh.window[1] + 1) / per;
             // Exact weights of what lies above the window, and of everything; the window's tokens.
             unsigned long long above = 0, all = 0;
-            for (int i = tid; i < row.len; i += kThreads) {
-                const float v = row.at(i);
-                const uint32_t key = key_of(v);
-                if (key <= kLeastKey || !in_k(key, row.first + i)) continue;
-                const float x = coarse(s, v);
-                if (level == 0 || x < w_to) {
-                    const unsigned long long w = weight_of(s, sh.table, v);
+            // Small weights at once; those that need care are marked and taken one a thread at a time, for a
+            // warp waits for its slowest lane.
+            row.each_group([&](int i0, const float(&v)[Row<BF16>::kVec], int n) {
+                uint32_t careful = 0;
+#pragma unroll
+                for (int j = 0; j < Row<BF16>::kVec; ++j) {
+                    if (j >= n) break;
+                    const float x = coarse(s, v[j]);
+                    if (!(x < (level ? w_to : 60.f))) continue;  // NaN, -infinity, nothing
+                    const uint32_t key = key_of(v[j]);
+                    if (cut_k != 0 && !in_k(key, row.first + i0 + j)) continue;
+                    if (x < kCareful) {
+                        careful |= 1u << j;
+                    } else {
+                        const unsigned long long w = small_weight(x);
+                        all += w;
+                        if (x < w_from) above += w;
+                    }
+                    if (x >= w_from && x < w_to) {
+                        const uint32_t at = atomicAdd(&sh.count, 1u);
+                        if (at < kCap) sh.list[at] = place_of(key, row.first + i0 + j);
+                    }
+                }
+                while (careful) {
+                    const int j = __ffs(careful) - 1;
+                    careful &= careful - 1;
+                    const float l = row.at(i0 + j);
+                    const unsigned long long w = weight_of(s, sh.table, l);
                     all += w;
-                    if (x < w_from) above += w;
+                    if (coarse(s, l) < w_from) above += w;
                 }
-                if (x >= w_from && x < w_to) {
-                    const uint32_t at = atomicAdd(&sh.count, 1u);
-                    if (at < kCap) sh.list[at] = place_of(key, row.first + i);
-                }
-            }
+            });
             cluster_sum(sh, rank, ctas, above, all);
             if (level == 0) total = all;
             sure = above;
@@ -645,20 +761,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
             while (lo < hi) {
                 const uint32_t mid = lo + (hi - lo) / 2 + 1;
                 unsigned long long w = 0, none = 0;
-                for (int i = tid; i < row.len; i += kThreads) {
-                    const float v = row.at(i);
+                row.each([&](int i, float v) {
                     const uint32_t key = key_of(v);
                     if (key >= mid && in_k(key, row.first + i)) w += weight_of(s, sh.table, v);
-                }
+                });
                 cluster_sum(sh, rank, ctas, w, none);
                 if (w >= need) lo = mid; else hi = mid - 1;
             }
             unsigned long long above = 0, none = 0;
-            for (int i = tid; i < row.len; i += kThreads) {
-                const float v = row.at(i);
+            row.each([&](int i, float v) {
                 const uint32_t key = key_of(v);
                 if (key > lo && in_k(key, row.first + i)) above += weight_of(s, sh.table, v);
-            }
+            });
             cluster_sum(sh, rank, ctas, above, none);
             const unsigned long long one = max(1ull, weight_of(s, sh.table, unorder_bits(lo)));
             const unsigned long long ties = need > above ? (need - above + one - 1) / one : 1ull;
@@ -667,8 +781,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
                 const int mid = (from + to) >> 1;
                 unsigned long long n = 0;
                 none = 0;
-                for (int i = tid; i < row.len; i += kThreads)
-                    n += key_of(row.at(i)) == lo && row.first + i <= mid && in_k(lo, row.first + i);
+                row.each([&](int i, float v) {
+                    n += key_of(v) == lo && row.first + i <= mid && in_k(lo, row.first + i);
+                });
                 cluster_sum(sh, rank, ctas, n, none);
                 if (n >= ties) to = mid; else from = mid + 1;
             }
