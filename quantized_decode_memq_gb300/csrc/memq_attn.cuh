@@ -34,10 +34,11 @@ constexpr float kAttnLeastLog = -60.f;  // smaller value scales (log2) count as 
 struct __align__(16) AttnOwner {
     int start;        // the sequence's first token
     int row0;         // the item's first row among the t * group rows of (sequence, kv head)
-    int last;
-    short head, rows;
+    int first, last;  // runs
+    int head, rows;
+    int unused[2];
 };
-static_assert(sizeof(AttnOwner) == 16, "one load");
+static_assert(sizeof(AttnOwner) == 32, "two loads");
 
 struct AttnArgs {
     const void *q;
@@ -52,6 +53,7 @@ struct AttnArgs {
     int n_tok, n_seq, nh, n_kv, group, n_pages, page_shift, max_pages;
     int rows_from, rows_to;  // sequences with t * group in this range are served
     int out_bf16;
+    int by_item;  // owners are noted by item, not by run
     float scale_log2;
 };
 

@@ -47,19 +47,63 @@ struct Ring {
     static constexpr int kBytes = kWarps * kWarpBytes;
 };
 
-struct Run {
-    int seq, head, tile_row, tile;  // where it begins
-    int valid;
-};
-
 struct Control {
     uint64_t full[kWarps][6];
     long long warp_sum[kWarps];
+    int warp_items[kWarps];
 };
 
 __host__ __device__ constexpr int smem_bytes(int ring) { return ring + 1024 + static_cast<int>(sizeof(Control)); }
 
 __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
+
+// 16 query rows of a (sequence, kv head) and their part of a run.
+struct RowItem {
+    int seq, head, row_tile, index;  // index: among all items
+    AttnSeq s;
+    int rows, row_tiles, units;  // of the sequence and head; tiles of an item and its start
+    long long pos;               // of the item's first unit
+    int off;                     // the first tile that the run serves
+    bool live;
+    int row0, n_rows, vis, end, t1;  // end: of the run's part; t1: of what is seen
+    __device__ __forceinline__ void of_seq(const AttnArgs &a) {
+        rows = s.t * a.group;
+        row_tiles = (rows + kRows - 1) / kRows;
+        units = tiles_of(s.kv) + kStart;
+    }
+    __device__ __forceinline__ void sizes(const AttnArgs &a, long long run_hi) {
+        live = pos + kStart + off < run_hi;
+        row0 = row_tile * kRows;
+        n_rows = min(kRows, rows - row0);
+        vis = max(0, s.kv - s.t + (row0 + n_rows - 1) / a.group + 1);
+        end = static_cast<int>(min(static_cast<long long>(units - kStart), run_hi - pos - kStart));
+        t1 = min(end, (vis + kKeys - 1) / kKeys);
+    }
+    __device__ __forceinline__ bool whole() const { return off == 0 && end == units - kStart; }
+    __device__ __forceinline__ void advance(const AttnArgs &a, long long run_hi) {
+        pos += units;
+        off = 0;
+        ++index;
+        live = pos + kStart < run_hi;
+        if (!live) return;
+        if (++row_tile == row_tiles) {
+            row_tile = 0;
+            if (++head == a.n_kv) {
+                head = 0;
+                do {
+                    if (++seq >= a.n_seq) {  // not with lengths that stand still
+                        live = false;
+                        return;
+                    }
+                    s = attn_seq(a, __ldcg(a.cu_q + seq), __ldcg(a.cu_q + seq + 1), __ldcg(a.kv_len + seq));
+                    rows = s.t * a.group;
+                } while (rows == 0 || rows < a.rows_from || rows > a.rows_to);
+                of_seq(a);
+            }
+        }
+        sizes(a, run_hi);
+    }
+};
 
 template <int D, bool Q2, bool P2>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -85,10 +129,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
 
     // ------------------------------------------------------------------ the runs
-    long long *first = reinterpret_cast<long long *>(smem);  // units before each sequence
+    int4 *seqs = reinterpret_cast<int4 *>(smem);                            // (start, t, kv, items before)
+    long long *first = reinterpret_cast<long long *>(smem + a.n_seq * 16);  // units before each sequence
     const int per_seq = (a.n_seq + kThreads - 1) / kThreads;
     bool descends = false;
     long long sum = 0;
+    int items = 0;  // (at most 2^31: rows of q are)
     for (int i = 0; i < per_seq; ++i) {
         const int b = tid * per_seq + i;
         if (b >= a.n_seq) break;
@@ -99,108 +145,129 @@ __global__ void __launch_bounds__(kThreads, 1)
         const AttnSeq s = attn_seq(a, c0, c1, kv);
         const int rows = s.t * a.group;
         first[b] = sum;
-        if (rows >= a.rows_from && rows <= a.rows_to)
-            sum += static_cast<long long>(a.n_kv) * ((rows + kRows - 1) / kRows) * (tiles_of(s.kv) + kStart);
+        seqs[b] = make_int4(s.start, s.t, s.kv, items);
+        if (rows >= a.rows_from && rows <= a.rows_to) {
+            const int n = a.n_kv * ((rows + kRows - 1) / kRows);
+            items += n;
+            sum += static_cast<long long>(n) * (tiles_of(s.kv) + kStart);
+        }
     }
     long long incl = sum;
+    int items_incl = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long up = __shfl_up_sync(kFullMask, incl, o);
-        if (lane >= o) incl += up;
+        const int up_items = __shfl_up_sync(kFullMask, items_incl, o);
+        if (lane >= o) {
+            incl += up;
+            items_incl += up_items;
+        }
     }
-    if (lane == 31) ctl->warp_sum[warp] = incl;
+    if (lane == 31) {
+        ctl->warp_sum[warp] = incl;
+        ctl->warp_items[warp] = items_incl;
+    }
     const bool nothing = __syncthreads_or(descends);
     long long before = incl - sum, total = 0;
+    int items_before = items_incl - items, all_items = 0;
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += ctl->warp_sum[w];
+        if (w < warp) {
+            before += ctl->warp_sum[w];
+            items_before += ctl->warp_items[w];
+        }
         total += ctl->warp_sum[w];
+        all_items += ctl->warp_items[w];
     }
     for (int i = 0; i < per_seq; ++i) {
         const int b = tid * per_seq + i;
         if (b >= a.n_seq) break;
         first[b] += before;
+        seqs[b].w += items_before;
     }
     __syncthreads();
     const int run = blockIdx.x * kWarps + warp, runs = gridDim.x * kWarps;
     const long long per = max(static_cast<long long>(kStart + 1), (total + runs - 1) / runs);
-    long long pos = nothing ? total : run * per;
-    const long long run_hi = min(total, pos + per);
-    int seq = 0;
-    if (pos < run_hi) {
-        int hi = a.n_seq;  // first[seq] <= pos < first[hi]
+    const long long run_lo = nothing ? total : run * per, run_hi = min(total, run_lo + per);
+    RowItem it{};
+    if (run_lo < run_hi) {
+        int seq = 0, hi = a.n_seq;  // first[seq] <= run_lo < first[hi]
         while (hi - seq > 1) {
             const int mid = (seq + hi) >> 1;
-            if (first[mid] <= pos) seq = mid; else hi = mid;
+            if (first[mid] <= run_lo) seq = mid; else hi = mid;
         }
+        const int4 v = seqs[seq];
+        it.seq = seq;
+        it.s = AttnSeq{v.x, v.y, v.z};
+        it.of_seq(a);
+        const long long at = run_lo - first[seq];
+        const int n = static_cast<int>(at / it.units), in_item = static_cast<int>(at - static_cast<long long>(n) * it.units);
+        it.head = n / it.row_tiles;
+        it.row_tile = n - it.head * it.row_tiles;
+        it.index = v.w + n;
+        it.off = max(0, in_item - kStart);
+        it.pos = run_lo - in_item;
+        it.sizes(a, run_hi);
     }
-    long long seq_pos = pos < run_hi ? first[seq] : 0;
     fence_async_smem();
-    __syncthreads();  // copies may go where the sums lie
-    if (lane == 0) a.owner[run].rows = 0;
-    if (pos >= run_hi) return;
+    __syncthreads();  // copies may go where the lengths lie
+    // Owners are noted by run, or, where there are no more items than runs, by item: every item has one run that
+    // serves its first tile.
+    if (lane == 0 && (!a.by_item || nothing || run >= all_items)) a.owner[run].rows = 0;
+    if (!it.live) return;
 
-    AttnSeq s = attn_seq(a, __ldcg(a.cu_q + seq), __ldcg(a.cu_q + seq + 1), __ldcg(a.kv_len + seq));
-    int rows = s.t * a.group, row_tiles = (rows + kRows - 1) / kRows, units = tiles_of(s.kv) + kStart;
-    long long at = pos - seq_pos;
-    int head = static_cast<int>(at / (static_cast<long long>(row_tiles) * units));
-    at -= static_cast<long long>(head) * row_tiles * units;
-    int row_tile = static_cast<int>(at / units);
-    int off = max(0, static_cast<int>(at - static_cast<long long>(row_tile) * units) - kStart);
-    long long item_pos = pos - (at - static_cast<long long>(row_tile) * units);  // of the item's first unit
     uint32_t sent = 0, taken = 0;  // tiles of the ring
-
     bool dead = false;
-    while (item_pos + kStart + off < run_hi && !dead) {
-        const int n_all = units - kStart;
-        const int end = static_cast<int>(min(static_cast<long long>(n_all), run_hi - item_pos - kStart));
-        // keys that the tile's last row sees; tiles behind them are passed over
-        const int row0 = row_tile * kRows, n_rows = min(kRows, rows - row0);
-        const int tok_lo = row0 / a.group, tok_hi = (row0 + n_rows - 1) / a.group;
-        const int vis = max(0, s.kv - s.t + tok_hi + 1), all_see = max(0, s.kv - s.t + tok_lo + 1);
-        const int t1 = min(end, (vis + kKeys - 1) / kKeys);
-        const int32_t *table = a.table + static_cast<int64_t>(seq) * a.max_pages;
-
-        // ---- pages and scales: lane l serves block l of a window of 32 blocks
-        const auto page_at = [&](int tile) {
-            const int key = tile * kKeys + lane * kAttnBlock;
-            return key < vis && tile < t1 ? attn_page(a, table, key, &g_attn_fault) : -1;
-        };
-        const auto row_at = [&](int page, int tile) {
-            const int key = tile * kKeys + lane * kAttnBlock;
-            return page < 0 ? -1
-                            : static_cast<int>(((static_cast<int64_t>(page) * a.n_kv + head) << a.page_shift) +
-                                               (key & ((1 << a.page_shift) - 1)));
-        };
-        const auto scale_at = [&](const float *scales, int row) { return row < 0 ? 1.f : __ldcg(scales + (row >> 4)); };
-        int win = off;
-        int row_now = row_at(page_at(win), win);
-        float ks_now = scale_at(a.k_scales, row_now), vs_now = scale_at(a.v_scales, row_now);
-        int row_next = row_at(page_at(win + kWindow), win + kWindow);
-        float ks_next = scale_at(a.k_scales, row_next), vs_next = scale_at(a.v_scales, row_next);
-        int page_later = page_at(win + 2 * kWindow);
-
-        const auto send = [&](int tile) {  // the copies of a tile; all lanes
-            const int i = 2 * (tile - win);
-            const int r0 = __shfl_sync(kFullMask, i < 32 ? row_now : row_next, i & 31);
-            const int r1 = __shfl_sync(kFullMask, i < 32 ? row_now : row_next, (i + 1) & 31);
-            if (lane == 0) {
-                const uint32_t slot = sent % kStages;
-                uint64_t *bar = &ctl->full[warp][slot];
-                uint8_t *dst = ring + slot * Ring<D>::kTile;
-                const bool two = box < kKeys;
-                const int boxes = two ? (r1 >= 0 ? 2 : 1) : 1;
-                mbar_arrive_expect_tx(bar, 2 * boxes * box * D);
-                tma_load_2d_plain(dst, &k_map, 0, r0, bar);
-                tma_load_2d_plain(dst + kKeys * D, &v_map, 0, r0, bar);
-                if (boxes == 2) {
-                    tma_load_2d_plain(dst + kAttnBlock * D, &k_map, 0, r1, bar);
-                    tma_load_2d_plain(dst + (kKeys + kAttnBlock) * D, &v_map, 0, r1, bar);
-                }
+    // ---- pages and scales: lane l serves block l of a window of 32 blocks
+    const auto page_of = [&](const RowItem &i, int tile) {  // -1: none; not checked yet
+        const int key = tile * kKeys + lane * kAttnBlock;
+        return tile < i.t1 && key < i.vis
+                   ? __ldcg(a.table + static_cast<int64_t>(i.seq) * a.max_pages + (key >> a.page_shift))
+                   : -1;
+    };
+    const auto row_of = [&](const RowItem &i, int page, int tile) {
+        const int key = tile * kKeys + lane * kAttnBlock;
+        if (tile >= i.t1 || key >= i.vis) return -1;
+        if (page < 0 || page >= a.n_pages) {
+            atomicOr(&g_attn_fault, kAttnFaultInput);
+            page = 0;
+        }
+        return ((page * a.n_kv + i.head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+    };
+    const auto scale_at = [&](const float *scales, int row) { return row < 0 ? 1.f : __ldcg(scales + (row >> 4)); };
+    const auto send = [&](int r0, int r1) {  // the copies of a tile's blocks
+        if (lane == 0) {
+            const uint32_t slot = sent % kStages;
+            uint64_t *bar = &ctl->full[warp][slot];
+            uint8_t *dst = ring + slot * Ring<D>::kTile;
+            const int boxes = box < kKeys && r1 >= 0 ? 2 : 1;
+            mbar_arrive_expect_tx(bar, 2 * boxes * box * D);
+            tma_load_2d_plain(dst, &k_map, 0, r0, bar);
+            tma_load_2d_plain(dst + kKeys * D, &v_map, 0, r0, bar);
+            if (boxes == 2) {
+                tma_load_2d_plain(dst + kAttnBlock * D, &k_map, 0, r1, bar);
+                tma_load_2d_plain(dst + (kKeys + kAttnBlock) * D, &v_map, 0, r1, bar);
             }
-            ++sent;
-        };
-        int next_send = off;
-        for (; next_send < min(t1, off + kStages); ++next_send) send(next_send);
+        }
+        ++sent;
+    };
+    int row_now = row_of(it, page_of(it, it.off), it.off);
+    int early = 0;  // tiles of the item that were sent ahead of it
+    while (it.live && !dead) {
+        const int off = it.off, t1 = it.t1, vis = it.vis, row0 = it.row0, n_rows = it.n_rows;
+        const int all_see = max(0, it.s.kv - it.s.t + row0 / a.group + 1);
+        int win = off;
+        int page_next = page_of(it, win + kWindow), page_later = page_of(it, win + 2 * kWindow);
+        float ks_now = scale_at(a.k_scales, row_now), vs_now = scale_at(a.v_scales, row_now);
+        int next_send = off + early;
+        for (; next_send < t1 && sent - taken < kStages; ++next_send) {
+            const int i = 2 * (next_send - win);
+            send(__shfl_sync(kFullMask, row_now, i), __shfl_sync(kFullMask, row_now, i + 1));
+        }
+        // The item behind this one: its first tiles are sent as soon as this one's are.
+        RowItem next = it;
+        next.advance(a, run_hi);
+        int row_then = -1, page_then = -1, sent_then = 0;
+        if (next.live) page_then = page_of(next, 0);
 
         // ---- the query rows
         uint32_t q_hi[kSteps][4], q_lo[Q2 ? kSteps : 1][4];
@@ -211,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float x[D / 4];
             const bool live = r < n_rows;
             const int rr = row0 + (live ? r : 0), tok = rr / a.group;
-            const int64_t from = (static_cast<int64_t>(s.start) + tok) * a.q_stride +
-                                 (head * a.group + rr - tok * a.group) * D + c * (D / 4);
+            const int64_t from = (static_cast<int64_t>(it.s.start) + tok) * a.q_stride +
+                                 (it.head * a.group + rr - tok * a.group) * D + c * (D / 4);
             if (Q2) {
                 const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + from);
 #pragma unroll
@@ -266,7 +333,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lv_now = 0.f, inv_now = 1.f;
         int lim[2];  // keys that a row sees
 #pragma unroll
-        for (int k = 0; k < 2; ++k) lim[k] = min(vis, max(0, s.kv - s.t + (row0 + g + 8 * k) / a.group + 1));
+        for (int k = 0; k < 2; ++k) lim[k] = min(vis, max(0, it.s.kv - it.s.t + (row0 + g + 8 * k) / a.group + 1));
+        int row_next = row_of(it, page_next, win + kWindow);
+        float ks_next = scale_at(a.k_scales, row_next), vs_next = scale_at(a.v_scales, row_next);
+        if (next.live) row_then = row_of(next, page_then, 0);
+        const auto send_then = [&]() {
+            const int i = 2 * sent_then++;
+            send(__shfl_sync(kFullMask, row_then, i), __shfl_sync(kFullMask, row_then, i + 1));
+        };
+        const int most_then = next.live ? min(next.t1, kWindow) : 0;
+        while (next_send >= t1 && sent_then < most_then && sent - taken < kStages) send_then();
 
         for (int tile = off; tile < t1; ++tile) {
             if (tile - win == kWindow) {
@@ -274,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 row_now = row_next;
                 ks_now = ks_next;
                 vs_now = vs_next;
-                row_next = row_at(page_later, win + kWindow);
+                row_next = row_of(it, page_later, win + kWindow);
                 ks_next = scale_at(a.k_scales, row_next);
                 vs_next = scale_at(a.v_scales, row_next);
-                page_later = page_at(win + 2 * kWindow);
+                page_later = page_of(it, win + 2 * kWindow);
             }
             const uint32_t slot = taken % kStages;
             if (!warp_wait_bounded(&ctl->full[warp][slot], (taken / kStages) & 1)) {
@@ -413,7 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();  // all lanes have read the slot
-            if (next_send < t1) send(next_send++);
+            if (next_send < t1) {
+                const int i = 2 * (next_send++ - win);
+                const int from = i < 32 ? row_now : row_next;
+                send(__shfl_sync(kFullMask, from, i & 31), __shfl_sync(kFullMask, from, (i + 1) & 31));
+            } else if (sent_then < most_then) {
+                send_then();
+            }
         }
         if (dead) break;
 
@@ -423,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             total_w[k] += __shfl_xor_sync(kFullMask, total_w[k], 1);
             total_w[k] += __shfl_xor_sync(kFullMask, total_w[k], 2);
         }
-        const bool whole = off == 0 && end == n_all;
+        const bool whole = it.whole();
         const int piece = 2 * run + (off == 0 ? 1 : 0);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -432,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kCols = D / 8;  // columns of one n8 index
             if (whole) {
                 const float n = total_w[k] == 0.f ? 0.f : __fdiv_rn(1.f, total_w[k]);
-                const int64_t to = attn_out_at(a, s.start, head, row0 + r, D) + c * 2 * kCols;
+                const int64_t to = attn_out_at(a, it.s.start, it.head, row0 + r, D) + c * 2 * kCols;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (a.out_bf16) {
@@ -465,34 +547,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         o[4 * j + 3][2 * k + i]);
             }
         }
-        if (!whole && off == 0 && lane == 0) {
+        if (off == 0 && lane == 0 && (!whole || a.by_item)) {
             AttnOwner own;
-            own.start = s.start;
+            own.start = it.s.start;
             own.row0 = row0;
-            own.last = static_cast<int>((item_pos + units - 1) / per);
-            own.head = static_cast<short>(head);
-            own.rows = static_cast<short>(n_rows);
-            a.owner[run] = own;
+            own.first = run;
+            own.last = static_cast<int>((it.pos + it.units - 1) / per);
+            own.head = it.head;
+            own.rows = whole ? 0 : n_rows;
+            a.owner[a.by_item ? it.index : run] = own;
         }
-
-        // ---- the next item
-        item_pos += units;
-        off = 0;
-        if (item_pos + kStart >= run_hi) break;
-        if (++row_tile == row_tiles) {
-            row_tile = 0;
-            if (++head == a.n_kv) {
-                head = 0;
-                do {
-                    if (++seq >= a.n_seq) return;  // not with lengths that stand still
-                    s = attn_seq(a, __ldcg(a.cu_q + seq), __ldcg(a.cu_q + seq + 1), __ldcg(a.kv_len + seq));
-                    rows = s.t * a.group;
-                } while (rows == 0 || rows < a.rows_from || rows > a.rows_to);
-                row_tiles = (rows + kRows - 1) / kRows;
-                units = tiles_of(s.kv) + kStart;
-            }
-        }
+        it = next;
+        row_now = row_then;
+        early = sent_then;
     }
+    // (no owner's note stays what it was before the call)
+    for (; dead && a.by_item && it.live; it.advance(a, run_hi))
+        if (it.off == 0 && lane == 0) a.owner[it.index].rows = 0;
     if (dead) {  // copies in flight land before shared memory is given up, each wait bounded
         for (uint32_t i = taken; i != sent; ++i)
             (void)warp_wait_bounded(&ctl->full[warp][i % kStages], (i / kStages) & 1);
@@ -508,43 +579,16 @@ constexpr int kFewParts = 24;
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, int runs, int stride) {
     constexpr int E = D / 32;
-    __shared__ int counts[kWarps], found;
-    __shared__ AttnOwner owner;
     __shared__ float red[2][kWarps];
     __shared__ float sums[kWarps][D];
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) found = -1;
-    // the x-th owner: a thread looks at a few runs next to one another
-    const int per = (runs + kThreads - 1) / kThreads, i0 = tid * per, i1 = min(runs, i0 + per);
-    unsigned mine = 0;  // bit i: run i0 + i is one
-    for (int i = i0; i < i1; ++i) {
-        const uint4 raw = __ldcg(reinterpret_cast<const uint4 *>(a.owner + i));
-        mine |= static_cast<unsigned>(reinterpret_cast<const AttnOwner *>(&raw)->rows != 0) << (i - i0);
-    }
-    const int n_mine = __popc(mine);
-    int incl = n_mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(kFullMask, incl, o);
-        if (lane >= o) incl += up;
-    }
-    if (lane == 31) counts[warp] = incl;
-    __syncthreads();
-    int before = incl - n_mine;
-    for (int w = 0; w < warp; ++w) before += counts[w];
-    const int x = static_cast<int>(blockIdx.x);
-    if (x >= before && x < before + n_mine) {
-        unsigned m = mine;
-        for (int i = before; i < x; ++i) m &= m - 1;
-        found = i0 + __ffs(m) - 1;
-        const uint4 raw = __ldcg(reinterpret_cast<const uint4 *>(a.owner + found));
-        owner = *reinterpret_cast<const AttnOwner *>(&raw);
-    }
-    __syncthreads();
-    if (found < 0) return;
-    const int run = found, parts = min(owner.last, runs - 1) - run + 1;
+    const int4 *at = reinterpret_cast<const int4 *>(a.owner + blockIdx.x);
+    const int4 raw[2] = {__ldcg(at), __ldcg(at + 1)};
+    const AttnOwner owner = *reinterpret_cast<const AttnOwner *>(raw);
+    if (owner.rows == 0) return;
+    const int run = owner.first, parts = min(owner.last, runs - 1) - run + 1;
     const auto put = [&](int r, const float(&v)[E], float total) {
         const float n = total == 0.f ? 0.f : __fdiv_rn(1.f, total);
         const int64_t to = attn_out_at(a, owner.start, owner.head, owner.row0 + r, D) + lane * E;
@@ -779,6 +823,9 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     a.max_pages = max_pages;
     a.rows_from = 1;
     a.rows_to = 0x7fffffff;
+    // at least as many items as there are; the workspace notes them by item where they are no more than the runs
+    const auto items_of = [&](int rows) { return n_kv * (n_tok * a.group / rows + std::min<int64_t>(n_seq, n_tok)); };
+    a.by_item = items_of(kRows) <= runs;
     a.out_bf16 = out_dtype == MEMQ_BF16;
     a.scale_log2 = scale * kAttnLog2e;
     const int box = std::min(page_size, kKeys);
@@ -796,10 +843,8 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     const bool q2 = q_dtype == MEMQ_F32, p2 = out_dtype == MEMQ_F32;
     const Workspace of_rows(runs, kRows, d), of_tiles(grid, q2 ? 128 : 256, d);
     const auto join = [&](const AttnArgs &args, const Workspace &w) {
-        // at least as many as items, of which a run begins one at most; about eight CTAs an SM over all
-        const int64_t items = n_kv * (n_tok * a.group / w.rows + std::min<int64_t>(n_seq, n_tok));
-        const unsigned x = static_cast<unsigned>(std::min<int64_t>(items, w.runs));
-        cfg.gridDim = dim3(x, std::max(1u, std::min(w.rows / 8u * 2u, 8u * static_cast<unsigned>(grid) / x)));
+        const unsigned x = static_cast<unsigned>(args.by_item ? items_of(w.rows) : w.runs);
+        cfg.gridDim = dim3(x, std::max(1u, std::min(static_cast<unsigned>(w.rows), 8u * static_cast<unsigned>(grid) / x)));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, args, w.runs, w.rows) ==
@@ -811,6 +856,7 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     if (!rows_only) {
         AttnArgs t = a;
         t.rows_from = kRowsKernelMost + 1;
+        t.by_item = false;
         of_tiles.place(t, static_cast<uint8_t *>(workspace) + of_rows.bytes());
         a.rows_to = kRowsKernelMost;
         unsigned int *fault = nullptr;

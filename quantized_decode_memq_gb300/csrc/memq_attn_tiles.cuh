@@ -543,9 +543,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                     AttnOwner owner;
                     owner.start = it.s.start;
                     owner.row0 = it.row0;
+                    owner.first = blockIdx.x;
                     owner.last = static_cast<int>((run.pos + it.tiles + kTileStart - 1) / per);
-                    owner.head = static_cast<short>(it.head);
-                    owner.rows = static_cast<short>(it.n_rows);
+                    owner.head = it.head;
+                    owner.rows = it.n_rows;
                     a.owner[blockIdx.x] = owner;
                 }
             }
