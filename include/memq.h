@@ -506,7 +506,7 @@ int memq_kv_cache_read(int dtype, const uint8_t *cache, const float *scales, con
  * expires sets bit 6.
  * Numerics: codes are used exactly, sums, maxima and normalisation are f32.  A query element is rounded to
  * eleven bits (exact for bf16) down to 2^-29 of its row's largest, an f32 one to 22; a weight times its
- * values' scale, for bf16 outputs, to eleven bits, in steps of 2^-38 of the largest such product of the row where
+ * values' scale, for bf16 outputs, to eleven bits, in steps of 2^-33 of the largest such product of the row where
  * those are coarser; to 22 bits for f32 outputs.  A scale of values below 2^-100 counts as 2^-100.  A
  * query row that is not finite gives NaN.
  * Results do not depend on timing; they depend on how the keys are split, so the same row may differ in

@@ -23,9 +23,10 @@ constexpr int kAttnMaxGrid = 256;
 constexpr float kAttnUnset = -1e30f;  // a reference before the first visible key
 constexpr float kAttnLog2e = 1.4426950408889634f;
 // Weights are 2^kAttnTop at the reference: f16 keeps eleven bits of them down to 2^-14 and steps of 2^-24
-// below.  The reference moves when a score exceeds it by kAttnSlack (65504 is the largest f16).
-constexpr float kAttnTop = 13.f;
-constexpr float kAttnSlack = 2.f;
+// below.  The reference moves when a score exceeds it by kAttnSlack (65504 is the largest f16), which costs a pass
+// over the accumulators: with a slack of 2 most tiles of a short run had one.
+constexpr float kAttnTop = 9.f;
+constexpr float kAttnSlack = 6.f;
 constexpr float kAttnLeastScale = 0x1p-100f;  // a smaller scale of values counts as this
 constexpr float kAttnLeastLog = -60.f;  // smaller value scales (log2) count as this in the reference
 
@@ -71,14 +72,13 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int c0, int c1, i
     return s;
 }
 
-// The page that holds key `key` of a sequence.
-__device__ __forceinline__ int attn_page(const AttnArgs &a, const int32_t *table, int key, unsigned int *fault) {
-    int page = __ldcg(table + (key >> a.page_shift));
+// The pool's row, among all pages and heads, of key `key` of a sequence whose page it lies in.
+__device__ __forceinline__ int attn_row(const AttnArgs &a, int page, int head, int key, unsigned int *fault) {
     if (page < 0 || page >= a.n_pages) {
         atomicOr(fault, kAttnFaultInput);
         page = 0;
     }
-    return page;
+    return ((page * a.n_kv + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
 }
 
 // log2 of a scale, exact for powers of two; not a number or infinite as it is.

@@ -7,9 +7,9 @@
 // Codes are exact in f16 (cvt.rn.f16x2.e4m3x2), so both products are f16 products with f32 sums.  What is not
 // a code is rounded to f16: a query row after a power of two that brings its largest element below 2^15 (of an
 // f32 query the remainder, too, in a second product), and a weight, scaled by its values' scale,
-//   p_j = 2^13 exp2(s_j + log2 vs_j - R)
-// under a running reference R of the row that is never more than 2 (log2) behind the largest so far: eleven bits
-// down to 2^-27 of the largest, steps of 2^-38 of it below; for f32 outputs the remainder is a second product.  The
+//   p_j = 2^9 exp2(s_j + log2 vs_j - R)
+// under a running reference R of the row that is never more than 6 (log2) behind the largest so far: eleven bits
+// down to 2^-23 of the largest, steps of 2^-33 of it below; for f32 outputs the remainder is a second product.  The
 // sum of weights is kept apart in f32, from p_j / vs_j.
 //
 // The single-token kernel: its time is the cache's bytes, so it is built around a stream.  A warp holds 16
@@ -226,12 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const auto row_of = [&](const RowItem &i, int page, int tile) {
         const int key = tile * kKeys + lane * kAttnBlock;
-        if (tile >= i.t1 || key >= i.vis) return -1;
-        if (page < 0 || page >= a.n_pages) {
-            atomicOr(&g_attn_fault, kAttnFaultInput);
-            page = 0;
-        }
-        return ((page * a.n_kv + i.head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+        return tile < i.t1 && key < i.vis ? attn_row(a, page, i.head, key, &g_attn_fault) : -1;
     };
     const auto scale_at = [&](const float *scales, int row) { return row < 0 ? 1.f : __ldcg(scales + (row >> 4)); };
     const auto send = [&](int r0, int r1) {  // the copies of a tile's blocks

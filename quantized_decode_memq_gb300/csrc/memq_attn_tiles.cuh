@@ -16,10 +16,10 @@
 
 namespace memq {
 
-constexpr int kTileKeys = 128;
+constexpr int kTileKeys = 128, kHalfKeys = 64;
 constexpr int kTileThreads = 16 * 32;
 // Registers a thread: 128 at launch; the two warpgroups that hold scores take 168, the others give theirs.
-constexpr int kRegsWeights = 168, kRegsOthers = 88;
+constexpr int kRegsWeights = 152, kRegsOthers = 104;
 static_assert(2 * kRegsWeights + 2 * kRegsOthers <= 4 * 128, "a split beyond the launch's registers never comes");
 constexpr int kWidenWarp = 8, kIssueWarp = 12;
 constexpr int kTileStart = 3;  // tiles that starting an item counts as
@@ -34,7 +34,7 @@ struct TileItem {
 
 struct TileControl {
     uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
-    uint64_t scores[2], weights[2], out_done[2];  // by block of rows
+    uint64_t scores[2][2], weights[2][2];  // by block of rows and half of the keys
     uint64_t q_ready, drain;
     uint32_t tmem;
     int first_off;
@@ -98,13 +98,13 @@ __device__ __forceinline__ void next_tile_item(const AttnArgs &a, int rows_per, 
 struct TileRun {
     const AttnArgs &a;
     int rows_per;
-    long long lo, hi;
+    long long hi;
     TileItem it;
     int off, end, t1, n;  // first tile, where the run's part ends, where what is seen ends, tiles to do
     long long pos;        // of the item's first unit
     bool live;
-    __device__ __forceinline__ TileRun(const AttnArgs &args, int rows, long long run_lo, long long run_hi)
-        : a(args), rows_per(rows), lo(run_lo), hi(run_hi), live(false) {}
+    __device__ __forceinline__ TileRun(const AttnArgs &args, int rows, long long run_hi)
+        : a(args), rows_per(rows), hi(run_hi), live(false) {}
     __device__ __forceinline__ void start(const TileItem &first, int first_off, long long first_pos) {
         it = first;
         off = first_off;
@@ -160,6 +160,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+    return max3(__uint_as_float(a), __uint_as_float(b), __uint_as_float(c));
 }
 
 // Eight columns of a warp's lanes times a number of each lane's.
@@ -278,9 +287,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
             mbar_init(&ctl->k_free[i], 1);
             mbar_init(&ctl->v_full[i], 3);
             mbar_init(&ctl->v_free[i], 1);
-            mbar_init(&ctl->scores[i], 1);
-            mbar_init(&ctl->weights[i], 4);
-            mbar_init(&ctl->out_done[i], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&ctl->scores[i][h], 1);
+                mbar_init(&ctl->weights[i][h], 4);
+            }
         }
         mbar_init(&ctl->q_ready, kBlocks * 4);
         mbar_init(&ctl->drain, 1);
@@ -388,19 +398,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
     const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 384};
 
     AttnWaiter wait{fault};
-    TileRun run{a, kRowsPer, run_lo, run_hi};
-    if (run_lo < run_hi) run.start(ctl->first, ctl->first_off, ctl->first_pos);
-    __syncwarp();
+    const auto my_run = [&]() {
+        TileRun run{a, kRowsPer, run_hi};
+        if (run_lo < run_hi) run.start(ctl->first, ctl->first_off, ctl->first_pos);
+        return run;
+    };
     if (warp < 8)  // whole warpgroups, one instruction each
         set_registers_up<kRegsWeights>();
     else
         set_registers_down<kRegsOthers>();
     if (warp < 8) {
         // ------------------------------------------------------------ weights and the way out
+        TileRun run = my_run();
         const int b = warp >> 2, wq = warp & 3, r = b * 128 + wq * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t at_s = s_col[b] + lanes, at_o = o_col[b] + lanes;
-        uint32_t tile = 0, turns = 0, items = 0, all_items = 0;
+        uint32_t tile = 0, turns = 0, all_items = 0;
         for (; b < kBlocks && run.more() && !wait.dead; run.next()) {
             const TileItem &it = run.it;
             const int n = run.n;
@@ -420,52 +433,60 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                 const int see0 = it.s.kv - it.s.t + 1;
                 const int lim = min(it.vis, max(0, see0 + (it.row0 + r) / a.group));
                 const int all_see = max(0, see0 + (it.row0 + b * 128) / a.group);
-                for (int j = 0; j < n; ++j) {
-                    const float4 *scale = ctl->scale[(tile + j) & 3];
-                    const int key0 = (run.off + j) * kTileKeys;
-                    wait(&ctl->scores[b], turns & 1);
+                // Half a tile a time: a half's scores have their own columns, so that the products of the next half
+                // run meanwhile.
+                for (int u = 0; u < 2 * n; ++u) {
+                    const int half = u & 1, key0 = (run.off + (u >> 1)) * kTileKeys + half * kHalfKeys;
+                    const float4 *scale = ctl->scale[(tile + (u >> 1)) & 3] + half * 4;
+                    const uint32_t at = at_s + half * kHalfKeys;
+                    wait(&ctl->scores[b][half], (turns + (u >> 1)) & 1);
                     if (wait.dead) break;
                     tc_fence_after();
-                    const bool masked = key0 + kTileKeys > all_see;
-                    const int left = masked ? lim - key0 : kTileKeys;  // keys of the tile that the row sees
-                    uint32_t raw[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32_nowait(at_s + c * 32, raw[c]);
+                    const bool masked = key0 + kHalfKeys > all_see;
+                    const int left = masked ? lim - key0 : kHalfKeys;  // keys of the half that the row sees
+                    uint32_t raw[2][32];
+                    tmem_ld32_nowait(at, raw[0]);
+                    tmem_ld32_nowait(at + 32, raw[1]);
                     tc_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32_done(raw[c]);
+                    tmem_ld32_done(raw[0]);
+                    tmem_ld32_done(raw[1]);
                     if (masked) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (c * 32 + i >= left) raw[c][i] = 0xff800000u;
                     }
                     float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float m[8];
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)  // 0 to 3: the chunk's first block of keys
-                            m[i] = fmaxf(fmaxf(__uint_as_float(raw[c][4 * i]), __uint_as_float(raw[c][4 * i + 1])),
-                                         fmaxf(__uint_as_float(raw[c][4 * i + 2]), __uint_as_float(raw[c][4 * i + 3])));
-                        const float4 s0 = scale[2 * c], s1 = scale[2 * c + 1];
-                        // (a block of which nothing is seen has -inf, times a scale of 0 a NaN, which is passed over)
-                        top = fmaxf(top, fmaxf(fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), factor * s0.x, s0.w),
-                                               fmaf(fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7])), factor * s1.x, s1.w)));
-                    }
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 sc = scale[2 * c + h];
+                            const uint32_t(&x)[32] = raw[c];
+                            const int k = 16 * h;
+                            const float m0 = max3(max3(x[k], x[k + 1], x[k + 2]), max3(x[k + 3], x[k + 4], x[k + 5]),
+                                                  max3(x[k + 6], x[k + 7], x[k + 8]));
+                            const float m1 = max3(max3(x[k + 9], x[k + 10], x[k + 11]), max3(x[k + 12], x[k + 13], x[k + 14]),
+                                                  __uint_as_float(x[k + 15]));
+                            // (a block of which nothing is seen has -inf, times a scale of 0 a NaN, which is passed over)
+                            top = fmaxf(top, fmaf(fmaxf(m0, m1), factor * sc.x, sc.w));
+                        }
                     if (__any_sync(kFullMask, top > ref + kAttnSlack)) {
                         const float to = fmaxf(ref, top), by = ex2(ref - to);
                         ref = to;
                         total_w *= by;
-                        if (j > 0) {  // the products so far are done: the scores came behind them
+                        if (u > 0) {  // behind the last half's products: the scores after these come behind them
+                            wait(&ctl->scores[b][half ^ 1], (turns + ((u + 1) >> 1)) & 1);
+                            if (wait.dead) break;
+                            tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D / 8; ++c) tmem_scale8(at_o + c * 8, by);
                         }
                     }
-                    float sums[8];
+                    float sums[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t w[16], rest[P2 ? 16 : 1];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -489,18 +510,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                             const float2 t = unpack2(add2(sum[0], sum[1]));
                             sums[2 * c + h] = (t.x + t.y) * sc.z;
                         }
-                        tmem_st16(at_s + c * 16, w);
-                        if (P2) tmem_st16(at_s + 64 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(rest));
+                        tmem_st16(at + c * 16, w);
+                        if (P2) tmem_st16(at + 32 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(rest));
                     }
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->weights[b]);
-                    total_w += ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
-                    ++turns;
+                    if (lane == 0) mbar_arrive(&ctl->weights[b][half]);
+                    total_w += (sums[0] + sums[1]) + (sums[2] + sums[3]);
                 }
-                wait(&ctl->out_done[b], items & 1);
-                ++items;
+                // the last products: the turns behind the last scores
+                wait(&ctl->scores[b][0], (turns + n) & 1);
+                wait(&ctl->scores[b][1], (turns + n) & 1);
+                turns += n + 1;
                 tc_fence_after();
             }
             tile += n;
@@ -555,6 +577,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         // ------------------------------------------------------------ codes -> f16
         // The lower four warps widen keys, three of the upper values.  16 codes are a thread's load.
         constexpr int kChunks = D / 16;
+        TileRun run = my_run();
         const bool keys = warp < kIssueWarp;
         const int ct = keys ? tid - kWidenWarp * 32 : tid - (kIssueWarp + 1) * 32;
         const int chunk = ct % kChunks, r0 = ct / kChunks, step = (keys ? 128 : 96) / kChunks;
@@ -570,13 +593,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
             const int32_t *table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
             // Lane l (of 8) serves the tile's block l: its page, three tiles ahead of the codes' use; its first row in
             // the pool, two; its scales, one.
-            const auto page_at = [&](int j) {
+            const auto page_at = [&](int j) {  // not checked yet
                 const int key = j * kTileKeys + (lane & 7) * kAttnBlock;
-                return j < run.t1 && key < it.vis ? attn_page(a, table, key, fault) : -1;
+                return j < run.t1 && key < it.vis ? __ldcg(table + (key >> a.page_shift)) : -1;
             };
             const auto base_at = [&](int page, int j) -> int {
                 const int key = j * kTileKeys + (lane & 7) * kAttnBlock;
-                return page < 0 ? -1 : ((page * a.n_kv + it.head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+                return j < run.t1 && key < it.vis ? attn_row(a, page, it.head, key, fault) : -1;
             };
             const auto scale_at = [&](const float *scales, int base) {
                 return scaling && base >= 0 ? __ldcg(scales + (base >> 4)) : 1.f;
@@ -635,37 +658,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         }
     } else {
         // ------------------------------------------------------------ products
-        constexpr uint32_t kQk = f16_idesc(kTileKeys, false), kPv = f16_idesc(D, true);
+        constexpr uint32_t kQk = f16_idesc(kHalfKeys, false), kPv = f16_idesc(D, true);
         const uint32_t q_at = smem_u32(q_smem), k_at = smem_u32(k_smem), v_at = smem_u32(v_smem);
-        const auto scores = [&](int b, uint32_t buf) {
-            if (elect_one()) {
+        const auto scores = [&](int b, int half, uint32_t buf) {
 #pragma unroll
-                for (int term = 0; term < (Q2 ? 2 : 1); ++term)
+            for (int term = 0; term < (Q2 ? 2 : 1); ++term)
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
-                        mma_f16_ss(s_col[b], smem_desc(q_at + (Q2 ? term : b) * (128 * D * 2) + at, 128),
-                                   smem_desc(k_at + buf * Shape::kKv + at, 128), kQk, term > 0 || i > 0);
-                    }
-                tc_commit(&ctl->scores[b]);
-            }
-            __syncwarp();
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
+                    mma_f16_ss(s_col[b] + half * kHalfKeys, smem_desc(q_at + (Q2 ? term : b) * (128 * D * 2) + at, 128),
+                               smem_desc(k_at + buf * Shape::kKv + half * (kHalfKeys * 128) + at, 128), kQk, term > 0 || i > 0);
+                }
         };
-        const auto outputs = [&](int b, uint32_t buf, bool acc) {
-            if (elect_one()) {
+        const auto outputs = [&](int b, int half, uint32_t buf, bool acc) {
 #pragma unroll
-                for (int term = 0; term < (P2 ? 2 : 1); ++term)
+            for (int term = 0; term < (P2 ? 2 : 1); ++term)
 #pragma unroll
-                    for (int i = 0; i < kTileKeys / 16; ++i)
-                        mma_f16_ts(o_col[b], s_col[b] + term * 64 + i * 8,
-                                   values_desc(v_at + buf * Shape::kKv + i * 2048, 16384), kPv, acc || term > 0 || i > 0);
-            }
-            __syncwarp();
+                for (int i = 0; i < kHalfKeys / 16; ++i)
+                    mma_f16_ts(o_col[b], s_col[b] + half * kHalfKeys + term * 32 + i * 8,
+                               values_desc(v_at + buf * Shape::kKv + half * (kHalfKeys * 128) + i * 2048, 16384), kPv,
+                               acc || term > 0 || i > 0);
         };
         const auto commit = [&](uint64_t *bar) {
             if (elect_one()) tc_commit(bar);
             __syncwarp();
         };
+        TileRun run = my_run();
         uint32_t tile = 0, turns[2] = {0, 0}, all_items = 0;
         for (; run.more() && !wait.dead; run.next()) {
             const int n = run.n, live_blocks = run.it.n_rows > 128 ? 2 : 1;
@@ -675,27 +693,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
             wait(&ctl->k_full[tile & 1], (tile >> 1) & 1);
             if (wait.dead) break;
             tc_fence_after();
-            for (int b = 0; b < live_blocks; ++b) scores(b, tile & 1);
-            commit(&ctl->k_free[tile & 1]);
-            for (int j = 0; j < n && !wait.dead; ++j, ++tile) {
-                const uint32_t buf = tile & 1, next = tile + 1;
-                wait(&ctl->v_full[buf], (tile >> 1) & 1);
+            if (elect_one()) {
+                for (int half = 0; half < 2; ++half)
+                    for (int b = 0; b < live_blocks; ++b) {
+                        scores(b, half, tile & 1);
+                        tc_commit(&ctl->scores[b][half]);
+                    }
+                tc_commit(&ctl->k_free[tile & 1]);
+            }
+            __syncwarp();
+            for (int u = 0; u < 2 * n; ++u) {
+                const int half = u & 1, j = u >> 1;
+                const uint32_t buf = (tile + j) & 1, next = tile + j + 1;
+                const bool more = j + 1 < n;
+                if (half == 0) wait(&ctl->v_full[buf], ((tile + j) >> 1) & 1);
+                if (half == 0 && more) wait(&ctl->k_full[next & 1], (next >> 1) & 1);
                 for (int b = 0; b < live_blocks; ++b) {
-                    if (b == 0 && j + 1 < n) wait(&ctl->k_full[next & 1], (next >> 1) & 1);
-                    wait(&ctl->weights[b], turns[b] & 1);
-                    ++turns[b];
+                    wait(&ctl->weights[b][half], (turns[b] + j) & 1);
                     if (wait.dead) break;
                     tc_fence_after();
-                    outputs(b, buf, j > 0);
-                    if (j + 1 < n)
-                        scores(b, next & 1);
-                    else
-                        commit(&ctl->out_done[b]);
+                    if (elect_one()) {
+                        outputs(b, half, buf, u > 0);
+                        if (more) scores(b, half, next & 1);
+                        tc_commit(&ctl->scores[b][half]);  // behind the last scores: of the products alone
+                    }
+                    __syncwarp();
                 }
                 if (wait.dead) break;
-                commit(&ctl->v_free[buf]);
-                if (j + 1 < n) commit(&ctl->k_free[next & 1]);
+                if (half == 1 && elect_one()) {
+                    tc_commit(&ctl->v_free[buf]);
+                    if (more) tc_commit(&ctl->k_free[next & 1]);
+                }
+                __syncwarp();
             }
+            tile += n;
+            for (int b = 0; b < live_blocks; ++b) turns[b] += n;
         }
         if (wait.dead) {  // products in flight end before TMEM is given up, the wait bounded
             commit(&ctl->drain);

@@ -74,8 +74,8 @@ def attend(q, k, v, t, scale, p_terms, out_eps, vs):
       scores    sums of d products on the tensor cores, 2^-17 of the sum of |products|; then three products
                 and the argument of exp2, of |s log2 e| + |reference| + 15 at most, 4 x 2^-24 of that;
                 exp2 itself 2^-22
-      weights   u = exp(s) vs: 2^-11 u (two terms 2^-22 u), and 2^-25 against 2^13 at a reference that is
-                at most 2 (log2) below the largest u: 2^-38 max u; |codes| <= 448 multiply it
+      weights   u = exp(s) vs: 2^-11 u (two terms 2^-22 u), and 2^-25 against 2^9 at a reference that is
+                at most the largest u: 2^-34 max u; |codes| <= 448 multiply it
       sums      a term of n is rounded n times at most: (kv / 16 + 64) 2^-23 of the sum of |terms|, for the
                 weights and the outputs
       output    one rounding to its type
@@ -104,7 +104,7 @@ def attend(q, k, v, t, scale, p_terms, out_eps, vs):
             total = p.sum(1, keepdims=True)
             o = p @ vi / total
             u = p * si
-            du = p_eps * u + 2.0 ** -38 * u.max(1, keepdims=True)
+            du = p_eps * u + 2.0 ** -34 * u.max(1, keepdims=True)
             a = np.abs(vi)
             codes = a / np.maximum(si, 2.0 ** -200)[:, None]
             grow = np.expm1(np.minimum(ds, 50.0))
