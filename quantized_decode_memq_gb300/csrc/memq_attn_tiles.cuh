@@ -193,9 +193,27 @@ struct AttnWaiter {
     unsigned int *fault;
     bool dead = false;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
-        if (!dead && !warp_wait_bounded(bar, parity)) {
+        if (dead || __all_sync(kFullMask, mbar_test(bar, parity))) return;
+        if (!warp_wait_bounded(bar, parity)) {
             dead = true;
             if ((threadIdx.x & 31) == 0) atomicOr(fault, kAttnFaultWait);
+        }
+    }
+};
+
+// The same for a single thread.
+struct AttnThreadWaiter {
+    unsigned int *fault;
+    bool dead = false;
+    __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
+        if (dead || mbar_test(bar, parity)) return;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, parity)) {
+            if (clock64() - t0 > kWaitCycles) {
+                dead = true;
+                atomicOr(fault, kAttnFaultWait);
+                return;
+            }
         }
     }
 };
@@ -679,60 +697,57 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                                values_desc(v_at + buf * Shape::kKv + half * (kHalfKeys * 128) + i * 2048, 16384), kPv,
                                acc || term > 0 || i > 0);
         };
-        const auto commit = [&](uint64_t *bar) {
-            if (elect_one()) tc_commit(bar);
-            __syncwarp();
-        };
-        TileRun run = my_run();
-        uint32_t tile = 0, turns[2] = {0, 0}, all_items = 0;
-        for (; run.more() && !wait.dead; run.next()) {
-            const int n = run.n, live_blocks = run.it.n_rows > 128 ? 2 : 1;
-            if (n == 0) continue;
-            wait(&ctl->q_ready, all_items & 1);
-            ++all_items;
-            wait(&ctl->k_full[tile & 1], (tile >> 1) & 1);
-            if (wait.dead) break;
-            tc_fence_after();
-            if (elect_one()) {
+        if (elect_one()) {
+            // One thread from here on: a branch that ptxas knows to have one keeps descriptors in uniform registers, and its
+            // waits need no votes.
+            AttnThreadWaiter ready{fault};
+            TileRun run = my_run();
+            uint32_t tile = 0, turns[2] = {0, 0}, all_items = 0;
+            for (; run.more() && !ready.dead; run.next()) {
+                const int n = run.n, live_blocks = run.it.n_rows > 128 ? 2 : 1;
+                if (n == 0) continue;
+                ready(&ctl->q_ready, all_items & 1);
+                ++all_items;
+                ready(&ctl->k_full[tile & 1], (tile >> 1) & 1);
+                if (ready.dead) break;
+                tc_fence_after();
                 for (int half = 0; half < 2; ++half)
                     for (int b = 0; b < live_blocks; ++b) {
                         scores(b, half, tile & 1);
                         tc_commit(&ctl->scores[b][half]);
                     }
                 tc_commit(&ctl->k_free[tile & 1]);
-            }
-            __syncwarp();
-            for (int u = 0; u < 2 * n; ++u) {
-                const int half = u & 1, j = u >> 1;
-                const uint32_t buf = (tile + j) & 1, next = tile + j + 1;
-                const bool more = j + 1 < n;
-                if (half == 0) wait(&ctl->v_full[buf], ((tile + j) >> 1) & 1);
-                if (half == 0 && more) wait(&ctl->k_full[next & 1], (next >> 1) & 1);
-                for (int b = 0; b < live_blocks; ++b) {
-                    wait(&ctl->weights[b][half], (turns[b] + j) & 1);
-                    if (wait.dead) break;
-                    tc_fence_after();
-                    if (elect_one()) {
+                for (int u = 0; u < 2 * n && !ready.dead; ++u) {
+                    const int half = u & 1, j = u >> 1;
+                    const uint32_t buf = (tile + j) & 1, next = tile + j + 1;
+                    const bool more = j + 1 < n;
+                    if (half == 0) {
+                        ready(&ctl->v_full[buf], ((tile + j) >> 1) & 1);
+                        if (more) ready(&ctl->k_full[next & 1], (next >> 1) & 1);
+                    }
+                    for (int b = 0; b < live_blocks; ++b) {
+                        ready(&ctl->weights[b][half], (turns[b] + j) & 1);
+                        if (ready.dead) break;
+                        tc_fence_after();
                         outputs(b, half, buf, u > 0);
                         if (more) scores(b, half, next & 1);
                         tc_commit(&ctl->scores[b][half]);  // behind the last scores: of the products alone
                     }
-                    __syncwarp();
+                    if (half == 1 && !ready.dead) {
+                        tc_commit(&ctl->v_free[buf]);
+                        if (more) tc_commit(&ctl->k_free[next & 1]);
+                    }
                 }
-                if (wait.dead) break;
-                if (half == 1 && elect_one()) {
-                    tc_commit(&ctl->v_free[buf]);
-                    if (more) tc_commit(&ctl->k_free[next & 1]);
-                }
-                __syncwarp();
+                tile += n;
+                for (int b = 0; b < live_blocks; ++b) turns[b] += n;
             }
-            tile += n;
-            for (int b = 0; b < live_blocks; ++b) turns[b] += n;
+            if (ready.dead) {  // products in flight end before TMEM is given up, the wait bounded
+                tc_commit(&ctl->drain);
+                ready.dead = false;
+                ready(&ctl->drain, 0);
+            }
         }
-        if (wait.dead) {  // products in flight end before TMEM is given up, the wait bounded
-            commit(&ctl->drain);
-            (void)warp_wait_bounded(&ctl->drain, 0);
-        }
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
