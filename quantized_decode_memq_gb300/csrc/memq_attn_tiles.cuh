@@ -461,34 +461,37 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                     if (wait.dead) break;
                     tc_fence_after();
                     const bool masked = key0 + kHalfKeys > all_see;
-                    const int left = masked ? lim - key0 : kHalfKeys;  // keys of the half that the row sees
                     uint32_t raw[2][32];
                     tmem_ld32_nowait(at, raw[0]);
                     tmem_ld32_nowait(at + 32, raw[1]);
                     tc_wait_ld();
                     tmem_ld32_done(raw[0]);
                     tmem_ld32_done(raw[1]);
-                    if (masked) {
+                    if (masked) {  // -infinity is a weight of 0 under any factor but 0, which there is none of
+                        const int left = lim - key0;  // keys of the half that the row sees
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (c * 32 + i >= left) raw[c][i] = 0xff800000u;
                     }
-                    float top = -INFINITY;
+                    float f[4], top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[i] = factor * scale[i].x;
+                        if (f[i] == 0.f) f[i] = 0x1p-120f;
+                    }
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float4 sc = scale[2 * c + h];
                             const uint32_t(&x)[32] = raw[c];
                             const int k = 16 * h;
                             const float m0 = max3(max3(x[k], x[k + 1], x[k + 2]), max3(x[k + 3], x[k + 4], x[k + 5]),
                                                   max3(x[k + 6], x[k + 7], x[k + 8]));
                             const float m1 = max3(max3(x[k + 9], x[k + 10], x[k + 11]), max3(x[k + 12], x[k + 13], x[k + 14]),
                                                   __uint_as_float(x[k + 15]));
-                            // (a block of which nothing is seen has -inf, times a scale of 0 a NaN, which is passed over)
-                            top = fmaxf(top, fmaf(fmaxf(m0, m1), factor * sc.x, sc.w));
+                            top = fmaxf(top, fmaf(fmaxf(m0, m1), f[2 * c + h], scale[2 * c + h].w));
                         }
                     if (__any_sync(kFullMask, top > ref + kAttnSlack)) {
                         const float to = fmaxf(ref, top), by = ex2(ref - to);
@@ -509,18 +512,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float4 sc = scale[2 * c + h];
-                            const float f = factor * sc.x, shift = sc.y - ref + kAttnTop;
-                            const uint64_t f2 = pack2(f, f), shift2 = pack2(shift, shift);
+                            const float shift = sc.y - ref + kAttnTop;
+                            const uint64_t f2 = pack2(f[2 * c + h], f[2 * c + h]), shift2 = pack2(shift, shift);
                             uint64_t sum[2] = {0, 0};
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int k = h * 16 + 2 * i;
                                 const float2 x = unpack2(fma2(bits2(raw[c][k], raw[c][k + 1]), f2, shift2));
-                                float p0 = ex2(x.x), p1 = ex2(x.y);
-                                if (masked) {  // (a scale of 0 makes a NaN of -inf)
-                                    if (c * 32 + k >= left) p0 = 0.f;
-                                    if (c * 32 + k + 1 >= left) p1 = 0.f;
-                                }
+                                const float p0 = ex2(x.x), p1 = ex2(x.y);
                                 sum[i & 1] = add2(sum[i & 1], pack2(p0, p1));
                                 w[h * 8 + i] = f32x2_to_f16x2(p0, p1);
                                 if (P2) rest[P2 ? h * 8 + i : 0] = attn_rest(p0, p1, w[h * 8 + i]);
