@@ -568,18 +568,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Adds the pieces of the items that several runs shared, in the runs' order.  CTAs (x, 0 .. gridDim.y - 1) serve the
 // x-th such item.  Up to kFewParts pieces a warp adds a row's alone, eight rows under way; above, the CTA's warps add
 // every eighth and the eight sums are added in turn (one token over 131071 keys: 152 pieces an item; a warp alone
-// took 55 us).  `stride` rows a piece.
+// took 55 us). 
 constexpr int kFewParts = 24;
 
+struct JoinPart {
+    const AttnOwner *owner;
+    const float2 *stats;
+    const float *part;
+    int x, runs, stride;  // owners to look at, runs, rows of a piece
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, int runs, int stride) {
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, const JoinPart tiles, const JoinPart rows) {
     constexpr int E = D / 32;
     __shared__ float red[2][kWarps];
     __shared__ float sums[kWarps][D];
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int4 *at = reinterpret_cast<const int4 *>(a.owner + blockIdx.x);
+    const bool of_tiles = static_cast<int>(blockIdx.x) < tiles.x;
+    const JoinPart &p = of_tiles ? tiles : rows;
+    const int runs = p.runs, stride = p.stride;
+    const int4 *at = reinterpret_cast<const int4 *>(p.owner + blockIdx.x - (of_tiles ? 0 : tiles.x));
     const int4 raw[2] = {__ldcg(at), __ldcg(at + 1)};
     const AttnOwner owner = *reinterpret_cast<const AttnOwner *>(raw);
     if (owner.rows == 0) return;
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, i
     };
     const auto slot_of = [&](int k, int r) { return static_cast<int64_t>(k == 0 ? 2 * run + 1 : 2 * (run + k)) * stride + r; };
     const auto add = [&](float(&acc)[E], int64_t slot, float by) {
-        const float *src = a.part + slot * D + lane * E;
+        const float *src = p.part + slot * D + lane * E;
         if (E == 4) {
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
             acc[0] = fmaf(v.x, by, acc[0]);
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, i
     if (parts <= kFewParts) {
         for (int r = blockIdx.y * kWarps + warp; r < owner.rows; r += gridDim.y * kWarps) {
             float2 st = make_float2(kAttnUnset, 0.f);
-            if (lane < parts) st = __ldcg(a.stats + slot_of(lane, r));
+            if (lane < parts) st = __ldcg(p.stats + slot_of(lane, r));
             const float w = ex2(st.x - warp_max(st.x)), total = warp_sum(st.y * w);
             float acc[E];
 #pragma unroll
@@ -632,7 +642,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, i
     }
     for (int r = blockIdx.y; r < owner.rows; r += gridDim.y) {
         float top = kAttnUnset;
-        for (int k = tid; k < parts; k += kThreads) top = fmaxf(top, __ldcg(a.stats + slot_of(k, r)).x);
+        for (int k = tid; k < parts; k += kThreads) top = fmaxf(top, __ldcg(p.stats + slot_of(k, r)).x);
         top = warp_max(top);
         if (lane == 0) red[0][warp] = top;
         __syncthreads();
@@ -645,7 +655,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, i
             const int k = k0 + lane * kWarps;
             float w = 0.f;
             if (k < parts) {
-                const float2 st = __ldcg(a.stats + slot_of(k, r));
+                const float2 st = __ldcg(p.stats + slot_of(k, r));
                 w = ex2(st.x - top);
                 total += st.y * w;
             }
@@ -747,8 +757,10 @@ struct Workspace {
     }
 };
 int64_t workspace_need(int grid, int d) { return Workspace(grid * kWarps, kRows, d).bytes() + Workspace(grid, 256, d).bytes(); }
-// Sequences of more query rows than this take the tensor-core kernel.
-constexpr int kRowsKernelMost = 16;
+// Sequences of more query rows (heads of a group, times tokens) than this take the tensor-core kernel.  us with 16 /
+// 32 / 64, 64 query and 8 kv heads of 128: 4 tokens (32 rows) over 32768 rows 42.4 / 35.9 / 35.9, 48 sequences of 4 over
+// 4096 171 / 147 / 146; 8 tokens (64 rows) over 32768 48.0 / 48.0 / 51.3, 48 sequences of 8 177 / 177 / 269.
+constexpr int kRowsKernelMost = 32;
 
 }  // namespace
 }  // namespace memq
@@ -837,17 +849,10 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     cfg.numAttrs = 1;
     const bool q2 = q_dtype == MEMQ_F32, p2 = out_dtype == MEMQ_F32;
     const Workspace of_rows(runs, kRows, d), of_tiles(grid, q2 ? 128 : 256, d);
-    const auto join = [&](const AttnArgs &args, const Workspace &w) {
-        const unsigned x = static_cast<unsigned>(args.by_item ? items_of(w.rows) : w.runs);
-        cfg.gridDim = dim3(x, std::max(1u, std::min(static_cast<unsigned>(w.rows), 8u * static_cast<unsigned>(grid) / x)));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = 0;
-        return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, args, w.runs, w.rows) ==
-               cudaSuccess;
-    };
     // One token a sequence, or rows that no sequence can have more of than a warp holds: the stream of keys is
     // all.  (More tokens than sequences may still lie in short ones: each kernel takes its own.)
     const bool rows_only = n_tok <= n_seq || n_tok * a.group <= kRowsKernelMost;
+    JoinPart tiles{};
     if (!rows_only) {
         AttnArgs t = a;
         t.rows_from = kRowsKernelMost + 1;
@@ -866,8 +871,8 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
         cfg.blockDim = dim3(kTileThreads);
         cfg.dynamicSmemBytes = static_cast<size_t>(d == 128 ? (q2 ? TileShape<128, true>::kBytes : TileShape<128, false>::kBytes)
                                                             : (q2 ? TileShape<64, true>::kBytes : TileShape<64, false>::kBytes));
-        if (cudaLaunchKernelEx(&cfg, kTiles[d == 128][q2][p2], t, fault) != cudaSuccess || !join(t, of_tiles))
-            return MEMQ_ERR_LAUNCH;
+        if (cudaLaunchKernelEx(&cfg, kTiles[d == 128][q2][p2], t, fault) != cudaSuccess) return MEMQ_ERR_LAUNCH;
+        tiles = JoinPart{t.owner, t.stats, t.part, of_tiles.runs, of_tiles.runs, of_tiles.rows};
     }
     of_rows.place(a, static_cast<uint8_t *>(workspace));
     using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const AttnArgs, const int);
@@ -880,5 +885,13 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(d == 128 ? Ring<128>::kBytes : Ring<64>::kBytes));
     if (cudaLaunchKernelEx(&cfg, kKernels[d == 128][q2][p2], k_map, v_map, a, box) != cudaSuccess) return MEMQ_ERR_LAUNCH;
-    return join(a, of_rows) ? MEMQ_OK : MEMQ_ERR_LAUNCH;
+    const JoinPart rows{a.owner, a.stats, a.part, a.by_item ? static_cast<int>(items_of(kRows)) : runs, runs, kRows};
+    // about eight CTAs an SM over all
+    const unsigned x = static_cast<unsigned>(tiles.x + rows.x);
+    cfg.gridDim = dim3(x, std::max(tiles.x ? 4u : 1u, std::min(16u, 8u * static_cast<unsigned>(grid) / x)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, a, tiles, rows) == cudaSuccess
+               ? MEMQ_OK
+               : MEMQ_ERR_LAUNCH;
 }

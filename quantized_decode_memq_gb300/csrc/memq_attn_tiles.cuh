@@ -12,6 +12,8 @@
 // of warp 12 issues the products.  An f32 query has two terms, two products, and its 128 rows the shared memory of 256.
 #pragma once
 
+#include <type_traits>
+
 #include "memq_attn.cuh"
 
 namespace memq {
@@ -226,64 +228,86 @@ __device__ __forceinline__ int piece_at(int r, int p) { return r * 128 + ((p ^ (
 template <int D, bool Q2>
 __device__ __forceinline__ void stage_queries(const AttnArgs &a, const TileItem &it, uint8_t *q, float *factors, int block,
                                               int warp, int lane) {
-    constexpr int E = D / 16;
+    constexpr int E = D / 16, kBatch = Q2 ? 4 : 8;  // rows whose loads are out at once
+    using Load = typename std::conditional<Q2, float4[E / 4], typename std::conditional<E == 8, uint4[1], uint2[1]>::type>::type;
     const int part = lane & 15;
     const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-        const int r = warp * 32 + i * 2 + (lane >> 4), rr = it.row0 + block * 128 + r;
-        const bool live = block * 128 + r < it.n_rows;
-        const int tok = live ? rr / a.group : 0;
-        const int64_t from = (static_cast<int64_t>(it.s.start) + tok) * a.q_stride +
-                             (live ? it.head * a.group + rr - tok * a.group : 0) * D + part * E;
-        float x[E];
-        if (Q2) {
-            const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + from);
+    // (token, head) of this lane's first row; the next is two rows on
+    const int first = warp * 32 + (lane >> 4);
+    int tok = (it.row0 + block * 128 + first) / a.group, head = it.row0 + block * 128 + first - tok * a.group;
+    const int tok_step = 2 / a.group, head_step = 2 - tok_step * a.group;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 16; i0 += kBatch) {
+        Load raw[kBatch];
 #pragma unroll
-            for (int j = 0; j < E / 4; ++j) {
-                const float4 v = live ? __ldcg(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-                x[4 * j] = v.x;
-                x[4 * j + 1] = v.y;
-                x[4 * j + 2] = v.z;
-                x[4 * j + 3] = v.w;
+        for (int i = 0; i < kBatch; ++i) {
+            const bool live = block * 128 + first + (i0 + i) * 2 < it.n_rows;
+            const int64_t from = (static_cast<int64_t>(it.s.start) + tok) * a.q_stride + (it.head * a.group + head) * D + part * E;
+            if constexpr (Q2) {
+#pragma unroll
+                for (int j = 0; j < E / 4; ++j) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (live) v = __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + from) + j);
+                    raw[i][j] = v;
+                }
+            } else if constexpr (E == 8) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (live) v = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + from));
+                raw[i][0] = v;
+            } else {
+                uint2 v = make_uint2(0, 0);
+                if (live) v = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + from));
+                raw[i][0] = v;
             }
-        } else {
-            const uint2 *src = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + from);
-#pragma unroll
-            for (int j = 0; j < E / 4; ++j) {
-                const uint2 v = live ? __ldcg(src + j) : make_uint2(0, 0);
-                x[4 * j] = __uint_as_float(v.x << 16);
-                x[4 * j + 1] = __uint_as_float(v.x & 0xffff0000u);
-                x[4 * j + 2] = __uint_as_float(v.y << 16);
-                x[4 * j + 3] = __uint_as_float(v.y & 0xffff0000u);
+            tok += tok_step;
+            head += head_step;
+            if (head >= a.group) {
+                head -= a.group;
+                ++tok;
             }
         }
-        uint32_t top = 0;  // as bits, infinities and NaN lie above all numbers
 #pragma unroll
-        for (int j = 0; j < E; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = first + (i0 + i) * 2;
+            float x[E];
+            const uint32_t *words = reinterpret_cast<const uint32_t *>(&raw[i]);
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
-        const int e = max(static_cast<int>(top >> 23), 32);
-        const float inv = sign * __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
-        const float back = __uint_as_float(static_cast<uint32_t>(max(1, e - 14)) << 23);
-        if (part == 0) factors[block * 128 + r] = top < 0x7f800000u ? back * fabsf(a.scale_log2) : NAN;
-        uint32_t hi[E / 2], lo[E / 2];
+            for (int j = 0; j < E / 2; ++j) {
+                if constexpr (Q2) {
+                    x[2 * j] = __uint_as_float(words[2 * j]);
+                    x[2 * j + 1] = __uint_as_float(words[2 * j + 1]);
+                } else {
+                    x[2 * j] = __uint_as_float(words[j] << 16);
+                    x[2 * j + 1] = __uint_as_float(words[j] & 0xffff0000u);
+                }
+            }
+            uint32_t top = 0;  // as bits, infinities and NaN lie above all numbers
 #pragma unroll
-        for (int j = 0; j < E / 2; ++j) {
-            const float u = x[2 * j] * inv, v = x[2 * j + 1] * inv;
-            hi[j] = f32x2_to_f16x2(u, v);
-            if (Q2) lo[j] = attn_rest(u, v, hi[j]);
-        }
-        uint8_t *base = q + (Q2 ? 0 : block) * (128 * D * 2);
-        const int byte = part * E * 2, half = byte >> 7, p = (byte & 127) >> 4;
-        uint8_t *at = base + half * 16384 + piece_at(r, p) + (byte & 15);
-        if (E == 8) {
-            *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[E / 2 - 2], hi[E / 2 - 1]);
-            if (Q2)
-                *reinterpret_cast<uint4 *>(at + 128 * D * 2) = make_uint4(lo[0], lo[1], lo[E / 2 - 2], lo[E / 2 - 1]);
-        } else {
-            *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
-            if (Q2) *reinterpret_cast<uint2 *>(at + 128 * D * 2) = make_uint2(lo[0], lo[1]);
+            for (int j = 0; j < E; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
+            const int e = max(static_cast<int>(top >> 23), 32);
+            const float inv = sign * __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
+            const float back = __uint_as_float(static_cast<uint32_t>(max(1, e - 14)) << 23);
+            if (part == 0) factors[block * 128 + r] = top < 0x7f800000u ? back * fabsf(a.scale_log2) : NAN;
+            uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) {
+                const float u = x[2 * j] * inv, v = x[2 * j + 1] * inv;
+                hi[j] = f32x2_to_f16x2(u, v);
+                if (Q2) lo[j] = attn_rest(u, v, hi[j]);
+            }
+            uint8_t *base = q + (Q2 ? 0 : block) * (128 * D * 2);
+            const int byte = part * E * 2, half = byte >> 7, p = (byte & 127) >> 4;
+            uint8_t *at = base + half * 16384 + piece_at(r, p) + (byte & 15);
+            if (E == 8) {
+                *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[E / 2 - 2], hi[E / 2 - 1]);
+                if (Q2)
+                    *reinterpret_cast<uint4 *>(at + 128 * D * 2) = make_uint4(lo[0], lo[1], lo[E / 2 - 2], lo[E / 2 - 1]);
+            } else {
+                *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
+                if (Q2) *reinterpret_cast<uint2 *>(at + 128 * D * 2) = make_uint2(lo[0], lo[1]);
+            }
         }
     }
 }
