@@ -14,14 +14,13 @@
 // times a polynomial, both in integers; below 2^-24 of the largest the hardware's exp2 is exact enough.
 //
 // A cluster of CTAs keeps a row in shared memory, so it is read once; the number of CTAs is chosen to fill
-// the GPU with few rows and to let a row fit with many.  Then, by what the row asks for:
+// the GPU with few rows and to let two CTAs share an SM with many.  Then, by what the row asks for:
 //   greedy          the first of the largest
 //   top-k           The k-th largest of all is not below t if every one of the C CTAs has ceil(k / C) threads whose
 //                   largest is t or more; what is t or more (usually little over k) is gathered and sorted by one CTA.
-//   top-p           A histogram of x over 2048 steps of 2^-6 bounds the weight above every step; only the
-//                   steps between which the cut must lie (1 or 2% of the weight) are gathered and sorted; finer
-//                   steps when they hold too much.
-//   neither         One pass of weights, the draw from the warps' sums.
+//   top-p           The weights go into 1536 steps of 2^-6 of x = log2 of the largest's ratio, exactly, so the step
+//                   that holds the cut is known; its tokens are gathered and sorted (finer steps when they are many).
+//   then            One pass of weights over what is kept, the draw from the warps' sums.
 // Rows that defeat this (thousands of equal logits at the cut) are cut by bisection over keys, then over indices.
 #include <algorithm>
 #include <atomic>
@@ -40,8 +39,9 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
 constexpr int kCap = 2048;   // tokens that are sorted
-constexpr int kBins = 2048;
+constexpr int kBins = 1536, kPerOctave = 64;  // steps of x, up to kCareful
 constexpr int kTable = 512;
+constexpr int kMine = kBins / kThreads;  // steps a thread adds up, where a row has one CTA
 constexpr int kUnitLog = 44;  // weights are integers in units of 2^-44
 constexpr uint32_t kLeastKey = 0x007fffffu;  // of -infinity; NaN has key 0
 constexpr int64_t kMaxVocab = 360000;
@@ -82,19 +82,24 @@ struct SampleArgs {
 };
 
 struct __align__(16) Shared {
-    unsigned long long table[kTable];    // 2^(-j / 512) in units of 2^-62
-    unsigned long long list[kCap];       // sorted tokens: key << 32 | ~index, largest first
-    unsigned long long weight[kCap];
+    unsigned long long table[kTable];           // g_powers
+    unsigned long long list[kCap];              // tokens: key << 32 | ~index; sorted, largest first
+    union {
+        unsigned long long weight[kCap];        // of the list
+        struct {
+            uint32_t lo[kBins], hi[kBins];      // weight of the steps of x
+        } steps;
+    };
     unsigned long long sums[kMaxCtas][kWarps];  // of every CTA's warps
     unsigned long long pair[kMaxCtas][2];
     unsigned long long warp64[2][kWarps];
-    uint32_t hist[kBins];
-    uint32_t from_cta[kMaxCtas];
+    unsigned long long cut;      // place of the last token that is kept
+    unsigned long long before;   // weight ahead of the step that holds the cut
+    uint32_t from_cta[kMaxCtas], bounds[kMaxCtas];
     uint32_t warp32[kWarps];
-    unsigned long long cut;      // key << 32 | ~index of the last token that is kept
-    uint32_t count;              // tokens in this CTA's list
-    int window[2];
+    uint32_t count;              // tokens in the first CTA's list
     uint32_t found;
+    int step;
 };
 
 // ------------------------------------------------------------------------------ clusters
@@ -114,6 +119,8 @@ __device__ __forceinline__ void cluster_wait_entry() { asm volatile("barrier.clu
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address of `p` in CTA `rank`'s shared memory.
 template <typename T>
 __device__ __forceinline__ T *in_cta(T *p, uint32_t rank) {
@@ -271,8 +278,22 @@ __device__ __forceinline__ void cluster_sum(Shared &sh, uint32_t rank, uint32_t 
     cluster_sync();  // the pairs may be written again
 }
 
-// Sorts n places (padded with zeros to a power of two), largest first.
-__device__ __forceinline__ int sort_list(Shared &sh, int n) {
+// Sorts n places, largest first: few by counting the larger ones, many (padded with zeros to a power of two) in
+// bitonic turns.
+__device__ __forceinline__ void sort_list(Shared &sh, int n) {
+    if (n <= kThreads) {
+        unsigned long long mine = 0;
+        int at = 0;
+        if (static_cast<int>(threadIdx.x) < n) {
+            mine = sh.list[threadIdx.x];
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) at += sh.list[j] > mine;
+        }
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < n) sh.list[at] = mine;
+        __syncthreads();
+        return;
+    }
     int size = 32;
     while (size < n) size <<= 1;
     for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
@@ -289,7 +310,6 @@ __device__ __forceinline__ int sort_list(Shared &sh, int n) {
             }
             __syncthreads();
         }
-    return size;
 }
 
 // Inclusive prefix sums of sh.weight[0 .. n), by the whole CTA.
@@ -312,18 +332,11 @@ __device__ __forceinline__ void scan_weights(Shared &sh, int n) {
     __syncthreads();
 }
 
-// Gathers the CTAs' lists in the first one's, after a cluster barrier; the number of them.  Its lists lie
-// from its own on; the others' are read from their shared memory.
-__device__ __forceinline__ int gather_lists(Shared &sh, uint32_t ctas) {
-    int n = static_cast<int>(sh.count);
-    for (uint32_t r = 1; r < ctas; ++r) {
-        const Shared *other = in_cta(&sh, r);
-        const int m = static_cast<int>(other->count);
-        for (int i = threadIdx.x; i < m; i += kThreads) sh.list[n + i] = other->list[i];
-        n += m;
-    }
-    __syncthreads();
-    return n;
+// Appends a token to the first CTA's list, which may be full.
+__device__ __forceinline__ void append(Shared &sh, unsigned long long place) {
+    Shared *first = in_cta(&sh, 0);
+    const uint32_t at = atomicAdd(&first->count, 1u);
+    if (at < kCap) first->list[at] = place;
 }
 
 __device__ __forceinline__ float value_of(unsigned long long place) { return unorder_bits(static_cast<uint32_t>(place >> 32)); }
@@ -432,8 +445,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
             }
         }
     }
-    static_assert(kTable == kThreads, "a thread copies one power");
-    sh.table[tid] = __ldg(&g_powers.at[tid]);
+    for (int j = tid; j < kTable; j += kThreads) sh.table[j] = __ldg(&g_powers.at[j]);
     if (tid == 0) sh.count = 0;
     cluster_wait_entry();
     const uint32_t my_top = any ? key_of(top + 0.f) : 0u;
@@ -498,75 +510,93 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     const int each = (k + static_cast<int>(ctas) - 1) / static_cast<int>(ctas);
     unsigned long long cut_k = 0;  // what is kept has this place or a higher one; 0: everything
     if (k < a.vocab && each <= kThreads / 2 && k <= kCap / 2) {
-        // a key that `each` threads' largest reach, near the highest such
+        // a key that `each` threads' largest reach, near the highest such: of the warps' largest where they are enough
         uint32_t lo = 0, hi = 0xffffffffu;
-        for (int bit = 0; bit < 32; ++bit) {
-            const uint32_t mid = lo + (hi - lo) / 2 + 1;
-            const int n = __syncthreads_count(my_top >= mid);
-            if (n >= each) lo = mid; else hi = mid - 1;
-            if (n >= each && n <= each + each / 8) break;
-            if (lo == hi) break;
+        if (each <= kWarps - 2) {
+            __syncthreads();
+            const uint32_t w = lane < kWarps ? sh.warp32[lane] : 0u;
+            int above = 0;
+#pragma unroll
+            for (int j = 0; j < kWarps; ++j) {
+                const uint32_t o = __shfl_sync(kFullMask, w, j);
+                above += o > w || (o == w && j < lane);
+            }
+            lo = __shfl_sync(kFullMask, w, __ffs(__ballot_sync(kFullMask, lane < kWarps && above == each - 1)) - 1);
+        } else {
+            for (int bit = 0; bit < 32; ++bit) {
+                const uint32_t mid = lo + (hi - lo) / 2 + 1;
+                const int n = __syncthreads_count(my_top >= mid);
+                if (n >= each) lo = mid; else hi = mid - 1;
+                if (n >= each && n <= each + each / 8) break;
+                if (lo == hi) break;
+            }
         }
-        cluster_sync();  // the tops have been read
-        if (tid < static_cast<int>(ctas)) *in_cta(&sh.from_cta[rank], tid) = lo;
+        if (tid < static_cast<int>(ctas)) *in_cta(&sh.bounds[rank], tid) = lo;
         cluster_sync();
         uint32_t bound = 0xffffffffu;
-        for (uint32_t r = 0; r < ctas; ++r) bound = min(bound, sh.from_cta[r]);
+        for (uint32_t r = 0; r < ctas; ++r) bound = min(bound, sh.bounds[r]);
+        bound = max(bound, kLeastKey + 1);  // masked tokens are never drawn, however few are left
         if (my_top >= bound)
             row.each([&](int i, float v) {
                 const uint32_t key = key_of(v);
-                if (key >= bound) {
-                    const uint32_t at = atomicAdd(&sh.count, 1u);
-                    if (at < kCap) sh.list[at] = place_of(key, row.first + i);
-                }
+                if (key >= bound) append(sh, place_of(key, row.first + i));
             });
-        __syncthreads();
-        if (tid < static_cast<int>(ctas)) *in_cta(&sh.pair[rank][0], tid) = sh.count;
         cluster_sync();
-        unsigned long long n_all = 0;
-        for (uint32_t r = 0; r < ctas; ++r) n_all += sh.pair[r][0];
+        const int n_all = static_cast<int>(in_cta(&sh, 0)->count);
+        cluster_arrive();  // the count has been read
         if (n_all <= kCap) {
             if (rank == 0) {
-                const int n = gather_lists(sh, ctas);
+                const int n = n_all;
                 sort_list(sh, n);
                 const int m = min(n, k);
-                for (int i = tid; i < m; i += kThreads) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
-                __syncthreads();
-                scan_weights(sh, m);
-                int kept = m;
-                if (p < 1.f) kept = first_reaching(sh, m, reach(p, sh.weight[m - 1]));
-                __syncthreads();
-                // min-p, and the order of indices: a token's place there is its rank among the kept
-                int mine = 0;
-                for (int i = tid; i < kept; i += kThreads) {
-                    const unsigned long long w = sh.weight[i] - (i ? sh.weight[i - 1] : 0ull);
-                    mine += i == 0 || w >= least;
+                unsigned long long w[kCap / kThreads];  // of this thread's places
+                for (int c = 0; c * kThreads < m; ++c) {
+                    const int i = c * kThreads + tid;
+                    if (i < m) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
                 }
-                // weights fall along the list, so those that pass are its first ones
-                mine = __reduce_add_sync(kFullMask, mine);
-                if (lane == 0) sh.warp32[warp] = mine;
+                __syncthreads();
+                int kept = m;
+                if (p < 1.f) {
+#pragma unroll
+                    for (int c = 0; c < kCap / kThreads; ++c) w[c] = c * kThreads + tid < m ? sh.weight[c * kThreads + tid] : 0ull;
+                    __syncthreads();
+                    scan_weights(sh, m);
+                    kept = first_reaching(sh, m, reach(p, sh.weight[m - 1]));
+                    __syncthreads();
+#pragma unroll
+                    for (int c = 0; c < kCap / kThreads; ++c)
+                        if (c * kThreads + tid < m) sh.weight[c * kThreads + tid] = w[c];
+                    __syncthreads();
+                }
+                // min-p: weights fall along the list, so those that pass are its first ones
+                int pass = 0;
+                for (int i = tid; i < kept; i += kThreads) pass += i == 0 || sh.weight[i] >= least;
+                pass = __reduce_add_sync(kFullMask, pass);
+                unsigned long long sum = 0;
+                if (lane == 0) sh.warp32[warp] = pass;
                 __syncthreads();
                 kept = 0;
-                for (int w = 0; w < kWarps; ++w) kept += static_cast<int>(sh.warp32[w]);
-                const unsigned long long goal = below(u, sh.weight[kept - 1]);
-                // sums by index, in turn of the sorted list: the first with sum > goal
+                for (int j = 0; j < kWarps; ++j) kept += static_cast<int>(sh.warp32[j]);
+                for (int i = tid; i < kept; i += kThreads) sum += sh.weight[i];
+                sum = warp_sum64(sum);
+                if (lane == 0) sh.warp64[0][warp] = sum;
+                __syncthreads();
+                sum = 0;
+                for (int j = 0; j < kWarps; ++j) sum += sh.warp64[0][j];
+                const unsigned long long goal = below(u, sum);
+                // a token's sum by index: of the kept ones with lower indices (which have the larger low words)
                 for (int i = tid; i < kept; i += kThreads) {
-                    const uint32_t mine_i = static_cast<uint32_t>(index_of(sh.list[i]));
+                    const uint32_t mine = static_cast<uint32_t>(sh.list[i]);
                     unsigned long long before = 0;
-                    for (int j = 0; j < kept; ++j) {
-                        const unsigned long long w = sh.weight[j] - (j ? sh.weight[j - 1] : 0ull);
-                        before += static_cast<uint32_t>(index_of(sh.list[j])) < mine_i ? w : 0ull;
-                    }
-                    const unsigned long long w = sh.weight[i] - (i ? sh.weight[i - 1] : 0ull);
-                    if (before <= goal && goal < before + w) a.out[row_i] = static_cast<int>(mine_i);
+#pragma unroll 4
+                    for (int j = 0; j < kept; ++j) before += static_cast<uint32_t>(sh.list[j]) > mine ? sh.weight[j] : 0ull;
+                    if (before <= goal && goal < before + sh.weight[i]) a.out[row_i] = static_cast<int>(~mine);
                 }
             }
-            cluster_sync();  // the lists have been read
+            cluster_wait();
             return;
         }
-        __syncthreads();
-        if (tid == 0) sh.count = 0;
-        cluster_sync();
+        cluster_wait();
     }
     const auto in_k = [&](uint32_t key, int index) { return place_of(key, index) >= cut_k; };
 
@@ -598,162 +628,123 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     // ------------------------------------------------------------------ top-p
     unsigned long long cut = cut_k;
     if (p < 1.f) {
-        // steps of x = coarse(): [x0 + b / per, x0 + (b + 1) / per), the last open; below x0 all are kept
-        float x0 = 0.f, per = 64.f;
-        float x_from = 0.f, x_to = INFINITY;  // the cut lies at from <= x < to
         unsigned long long total = 0, sure = 0;  // weight of all, and of what is surely kept
         bool sorted = false;
-        for (int level = 0; level < 3 && !sorted; ++level) {
-            for (int b = tid; b < kBins; b += kThreads) sh.hist[b] = 0;
+        int step0 = -1;  // the step that holds the cut, on the second level
+        for (int level = 0; level < 2 && !sorted; ++level) {
+            // A token's step: of 1 / 64, and within the one that holds the cut of 1 / (64 * 1536).  Both are monotone in
+            // l, whatever f32 rounds.
+            const auto step_of = [&](float x) {
+                const int b = static_cast<int>(x * kPerOctave);
+                if (level == 0) return b;
+                if (b != step0) return b < step0 ? -1 : kBins;
+                return min(kBins - 1, max(0, static_cast<int>((x - step0 * (1.f / kPerOctave)) * (kPerOctave * kBins))));
+            };
+            for (int b = tid; b < 2 * kBins; b += kThreads) sh.steps.lo[b] = 0;
+            if (tid == 0) sh.count = 0;
             __syncthreads();
-            row.each([&](int i, float v) {
-                const uint32_t key = key_of(v);
-                const float x = coarse(s, v);
-                // (not of NaN and of -infinity, whose x is none or infinite)
-                if (x >= x_from && x < x_to && in_k(key, row.first + i))
-                    atomicAdd(&sh.hist[min(kBins - 1, static_cast<int>(fminf((x - x0) * per, 1e6f)))], 1u);
-            });
-            cluster_sync();
-            // Bounds of the weight up to each step; all CTAs form them alike.
-            const int b0 = tid * (kBins / kThreads);
-            float lo_sum = 0.f, hi_sum = 0.f;
-            uint32_t cnt[kBins / kThreads];
-#pragma unroll
-            for (int j = 0; j < kBins / kThreads; ++j) cnt[j] = 0;
-            for (uint32_t r = 0; r < ctas; ++r) {
-                const uint4 h = *reinterpret_cast<const uint4 *>(&in_cta(&sh, r)->hist[b0]);
-                cnt[0] += h.x;
-                cnt[1] += h.y;
-                cnt[2] += h.z;
-                cnt[3] += h.w;
-            }
-            static_assert(kBins / kThreads == 4, "one load");
-            float lows[4], highs[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int b = b0 + j;
-                const float x = x0 + b / per;
-                highs[j] = cnt[j] * ex2(-x) * 1.00001f;
-                lows[j] = b == kBins - 1 ? 0.f : cnt[j] * ex2(-(x0 + (b + 1) / per)) * 0.99999f;
-                hi_sum += highs[j];
-                lo_sum += lows[j];
-            }
-            // what is surely kept already counts as it is
-            const float base = static_cast<float>(sure) * 0x1p-44f;
-            float hi_run = hi_sum, lo_run = lo_sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float x = __shfl_up_sync(kFullMask, hi_run, o), y = __shfl_up_sync(kFullMask, lo_run, o);
-                if (lane >= o) {
-                    hi_run += x;
-                    lo_run += y;
-                }
-            }
-            if (lane == 31) {
-                sh.warp64[0][warp] = __float_as_uint(hi_run);
-                sh.warp64[1][warp] = __float_as_uint(lo_run);
-            }
-            if (tid == 0) {
-                sh.window[0] = kBins - 1;
-                sh.window[1] = kBins - 1;
-                sh.count = 0;
-            }
-            __syncthreads();
-            float hi_all = 0.f, lo_all = 0.f;
-            hi_run -= hi_sum;
-            lo_run -= lo_sum;
-            for (int w = 0; w < kWarps; ++w) {
-                const float x = __uint_as_float(static_cast<uint32_t>(sh.warp64[0][w]));
-                const float y = __uint_as_float(static_cast<uint32_t>(sh.warp64[1][w]));
-                if (w < warp) {
-                    hi_run += x;
-                    lo_run += y;
-                }
-                hi_all += x;
-                lo_all += y;
-            }
-            // on the first level the total is bounded too; later it is known
-            // (sums of f32 in another order differ by far less than 1e-5)
-            const float want_lo = p * (level ? static_cast<float>(total) * 0x1p-44f : lo_all) * 0.99999f;
-            const float want_hi = p * (level ? static_cast<float>(total) * 0x1p-44f : hi_all) * 1.00001f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                hi_run += highs[j];
-                lo_run += lows[j];
-                if (base + hi_run >= want_lo) atomicMin(&sh.window[0], b0 + j);
-                if (base + lo_run >= want_hi) atomicMin(&sh.window[1], b0 + j);
-            }
-            __syncthreads();
-            const float w_from = x0 + sh.window[0] / per;
-            const float w_to = sh.window[1] == kBins - 1 ? x_to : x0 + (sh.window[1] + 1) / per;
-            // Exact weights of what lies above the window, and of everything; the window's tokens.
-            unsigned long long above = 0, all = 0;
-            // Small weights at once; those that need care are marked and taken one a thread at a time, for a
-            // warp waits for its slowest lane.
+            // Small weights at once, into one sum: no cut lies there but in the flattest of rows.  Those that need care
+            // are marked and taken one a thread at a time, for a warp waits for its slowest lane.
+            unsigned long long tail = 0, none = 0;
             row.each_group([&](int i0, const float(&v)[Row<BF16>::kVec], int n) {
                 uint32_t careful = 0;
 #pragma unroll
                 for (int j = 0; j < Row<BF16>::kVec; ++j) {
-                    if (j >= n) break;
                     const float x = coarse(s, v[j]);
-                    if (!(x < (level ? w_to : 60.f))) continue;  // NaN, -infinity, nothing
-                    const uint32_t key = key_of(v[j]);
-                    if (cut_k != 0 && !in_k(key, row.first + i0 + j)) continue;
-                    if (x < kCareful) {
+                    if (j >= n || !(x < 60.f)) continue;  // NaN, -infinity, nothing
+                    if (x < kCareful)
                         careful |= 1u << j;
-                    } else {
-                        const unsigned long long w = small_weight(x);
-                        all += w;
-                        if (x < w_from) above += w;
-                    }
-                    if (x >= w_from && x < w_to) {
-                        const uint32_t at = atomicAdd(&sh.count, 1u);
-                        if (at < kCap) sh.list[at] = place_of(key, row.first + i0 + j);
-                    }
+                    else if (level == 0 && (cut_k == 0 || in_k(key_of(v[j]), row.first + i0 + j)))
+                        tail += small_weight(x);
                 }
                 while (careful) {
                     const int j = __ffs(careful) - 1;
                     careful &= careful - 1;
                     const float l = row.at(i0 + j);
+                    if (cut_k != 0 && !in_k(key_of(l), row.first + i0 + j)) continue;
+                    const int b = step_of(coarse(s, l));
+                    if (b < 0 || b >= kBins) continue;
                     const unsigned long long w = weight_of(s, sh.table, l);
-                    all += w;
-                    if (coarse(s, l) < w_from) above += w;
+                    const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.steps.lo[b], lo);
+                    const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old);
+                    if (hi) atomicAdd(&sh.steps.hi[b], hi);
                 }
             });
-            cluster_sum(sh, rank, ctas, above, all);
-            if (level == 0) total = all;
-            sure = above;
-            if (tid < static_cast<int>(ctas)) *in_cta(&sh.pair[rank][0], tid) = sh.count;
-            cluster_sync();
-            unsigned long long n_all = 0;
-            for (uint32_t r = 0; r < ctas; ++r) n_all += sh.pair[r][0];
-            if (n_all <= kCap) {
-                if (rank == 0) {
-                    const int n = gather_lists(sh, ctas);
-                    sort_list(sh, n);
-                    for (int i = tid; i < n; i += kThreads) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
-                    __syncthreads();
-                    scan_weights(sh, n);
-                    const unsigned long long need = reach(p, total);
-                    if (tid < static_cast<int>(ctas)) {
-                        // the steps are f32: that the cut lies between them is seen here
-                        const bool in = n > 0 && need > sure && need <= sure + sh.weight[n - 1];
-                        *in_cta(&sh.found, tid) = in;
-                        *in_cta(&sh.cut, tid) = in ? sh.list[first_reaching(sh, n, need - sure) - 1] : 0ull;
+            cluster_sum(sh, rank, ctas, tail, none);
+            // Every CTA adds all CTAs' weights of its share of the steps (all of them by every one would be 12 KB from
+            // each of the others: 13 us with 8); their sums tell in whose share the cut lies.
+            const int share = kBins / static_cast<int>(ctas), b0 = static_cast<int>(rank) * share + tid * kMine;
+            unsigned long long mass[kMine], own = 0;
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                mass[j] = 0;
+                if (tid * kMine + j < share)
+                    for (uint32_t r = 0; r < ctas; ++r) {
+                        const Shared *other = in_cta(&sh, r);
+                        mass[j] += static_cast<unsigned long long>(other->steps.hi[b0 + j]) << 32 | other->steps.lo[b0 + j];
                     }
-                }
-                cluster_sync();
-                sorted = sh.found != 0;
-                cut = max(cut, sh.cut);
-                if (!sorted) break;
-            } else {
-                x_from = w_from;
-                x_to = w_to;
-                x0 = w_from;
-                const float wide = (w_to < 48.f ? w_to : fmaxf(48.f, w_from + 1.f)) - w_from;
-                per = fminf(kBins / fmaxf(wide, 0x1p-20f), 0x1p28f);
-                cluster_sync();
+                own += mass[j];
             }
+            unsigned long long incl = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long up = __shfl_up_sync(kFullMask, incl, o);
+                if (lane >= o) incl += up;
+            }
+            if (lane == 31) sh.warp64[0][warp] = incl;
+            __syncthreads();
+            unsigned long long run = incl - own, share_sum = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                const unsigned long long x = sh.warp64[0][w];
+                if (w < warp) run += x;
+                share_sum += x;
+            }
+            if (tid < static_cast<int>(ctas)) *in_cta(&sh.pair[rank][0], tid) = share_sum;
+            cluster_sync();  // and all steps have been read
+            unsigned long long all = 0;
+            for (uint32_t r = 0; r < ctas; ++r) {
+                if (r == rank) run += all;
+                all += sh.pair[r][0];
+            }
+            if (level == 0) total = all + tail;
+            const unsigned long long need = reach(p, total) - sure;  // at least 1: the cut lies behind what is sure
+            if (need > all) break;                                   // in the tail
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                if (run < need && need <= run + mass[j])
+                    for (uint32_t r = 0; r < ctas; ++r) {
+                        Shared *other = in_cta(&sh, r);
+                        other->step = b0 + j;
+                        other->before = run;
+                    }
+                run += mass[j];
+            }
+            cluster_sync();
+            const int step = sh.step;
+            sure += sh.before;
+            row.each([&](int i, float v) {
+                const float x = coarse(s, v);
+                if (x < kCareful && step_of(x) == step) {
+                    const uint32_t key = key_of(v);
+                    if (cut_k == 0 || in_k(key, row.first + i)) append(sh, place_of(key, row.first + i));
+                }
+            });
+            cluster_sync();
+            const int n_all = static_cast<int>(in_cta(&sh, 0)->count);
+            if (n_all <= kCap) {
+                sorted = true;
+                if (rank == 0) {
+                    sort_list(sh, n_all);
+                    for (int i = tid; i < n_all; i += kThreads) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
+                    __syncthreads();
+                    scan_weights(sh, n_all);
+                    if (tid < static_cast<int>(ctas))
+                        *in_cta(&sh.cut, tid) = sh.list[first_reaching(sh, n_all, reach(p, total) - sure) - 1];
+                }
+            }
+            cluster_sync();
+            if (sorted) cut = max(cut, sh.cut);
+            step0 = step;
         }
         if (!sorted) {  // thousands of equal tokens: bisection over keys, by weight
             const unsigned long long need = reach(p, total);
@@ -792,17 +783,52 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
 
     // ------------------------------------------------------------------ the draw
-    // A warp's tokens are consecutive, so its sum's place among the others is its place by index.
-    const int seg = (row.len + kWarps - 1) / kWarps, seg0 = min(row.len, warp * seg), seg1 = min(row.len, seg0 + seg);
+    // A warp's tokens are consecutive (the first warp has those ahead of the 16-byte groups too, the last those behind
+    // them), so its sum's place among the others is its place by index.
+    const float cut_v = cut ? value_of(cut) : -INFINITY;
+    const int cut_i = cut ? index_of(cut) : 0x7fffffff;
+    constexpr int kVec = Row<BF16>::kVec;
+    const int body = (row.len - row.head) / kVec, per = (body + kWarps - 1) / kWarps;
+    const int g0 = min(body, warp * per), g1 = min(body, g0 + per);
+    const uint4 *groups = reinterpret_cast<const uint4 *>(row.data + row.head * kSize);
+    const auto keep = [&](float v, int i) { return v > cut_v || (v == cut_v && row.first + i <= cut_i); };
     const auto kept_weight = [&](int i) -> unsigned long long {
         const float v = row.at(i);
-        const uint32_t key = key_of(v);
-        if (key <= kLeastKey || place_of(key, row.first + i) < cut) return 0ull;
+        if (!keep(v, i)) return 0ull;
         const unsigned long long w = weight_of(s, sh.table, v);
-        return w >= least || key == top_key ? w : 0ull;
+        return w >= least ? w : 0ull;
     };
-    unsigned long long mine = 0;
-    for (int i = seg0 + lane; i < seg1; i += 32) mine += kept_weight(i);
+    const auto group_weight = [&](int g) {
+        float v[kVec];
+        Row<BF16>::vec(groups[g], v);
+        const int i0 = row.head + g * kVec;
+        unsigned long long sum = 0;
+        uint32_t careful = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const float x = coarse(s, v[j]);
+            if (!(x < 60.f) || !keep(v[j], i0 + j)) continue;
+            if (x < kCareful) {
+                careful |= 1u << j;
+            } else {
+                const unsigned long long w = small_weight(x);
+                if (w >= least) sum += w;
+            }
+        }
+        while (careful) {
+            const int j = __ffs(careful) - 1;
+            careful &= careful - 1;
+            const unsigned long long w = weight_of(s, sh.table, row.at(i0 + j));
+            if (w >= least) sum += w;
+        }
+        return sum;
+    };
+    // the tokens ahead of the groups and behind them: a lane each
+    const int tail0 = row.head + body * kVec;
+    const unsigned long long ahead = warp == 0 && lane < row.head ? kept_weight(lane) : 0ull;
+    const unsigned long long behind = warp == kWarps - 1 && tail0 + lane < row.len ? kept_weight(tail0 + lane) : 0ull;
+    unsigned long long mine = ahead + behind;
+    for (int g = g0 + lane; g < g1; g += 32) mine += group_weight(g);
     mine = warp_sum64(mine);
     if (lane < static_cast<int>(ctas)) *in_cta(&sh.sums[rank][warp], lane) = mine;
     cluster_sync();
@@ -813,23 +839,34 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
             all += sh.sums[r][w];
         }
     const unsigned long long goal = below(u, all);
-    if (before <= goal && goal < before + mine) {
-        for (int i0 = seg0; i0 < seg1; i0 += 32) {
-            const unsigned long long w = i0 + lane < seg1 ? kept_weight(i0 + lane) : 0ull;
-            unsigned long long incl = w;
+    if (goal < before || goal >= before + mine) return;
+    // This warp's: 32 sums a turn, by index; the lane whose sum passes the goal looks into its tokens.
+    const auto turn = [&](unsigned long long w, int i, int n) {
+        unsigned long long incl = w;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long up = __shfl_up_sync(kFullMask, incl, o);
-                if (lane >= o) incl += up;
-            }
-            const unsigned over = __ballot_sync(kFullMask, before + incl > goal);
-            if (over) {
-                if (lane == 0) a.out[row_i] = row.first + i0 + __ffs(over) - 1;
-                break;
-            }
-            before += __shfl_sync(kFullMask, incl, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long up = __shfl_up_sync(kFullMask, incl, o);
+            if (lane >= o) incl += up;
         }
-    }
+        const unsigned over = __ballot_sync(kFullMask, before + incl > goal);
+        if (over) {
+            if (lane == __ffs(over) - 1) {
+                unsigned long long run = before + incl - w;
+                for (; n > 1; ++i, --n) {
+                    run += kept_weight(i);
+                    if (run > goal) break;
+                }
+                a.out[row_i] = row.first + i;
+            }
+            return true;
+        }
+        before += __shfl_sync(kFullMask, incl, 31);
+        return false;
+    };
+    if (warp == 0 && turn(ahead, lane, 1)) return;
+    for (int i = g0; i < g1; i += 32)
+        if (turn(i + lane < g1 ? group_weight(i + lane) : 0ull, row.head + (i + lane) * kVec, kVec)) return;
+    if (warp == kWarps - 1) turn(behind, tail0 + lane, 1);
 }
 
 bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -876,11 +913,11 @@ extern "C" int memq_sample(int dtype, const void *logits, int64_t stride, const 
     int sms = 0, smem = 0;
     if (!device_info(sms, smem)) return MEMQ_ERR_LAUNCH;
     SampleArgs a{logits, stride, temperature, top_p, min_p, u, top_k, out, static_cast<int>(vocab), 0};
-    // As many CTAs a row as fill the GPU, no fewer than hold it.
+    // As many CTAs a row as fill the GPU, and so many that two of them fit on an SM, if a cluster has as many.
     const auto slice_of = [&](int ctas) { return static_cast<int>(((vocab + ctas - 1) / ctas + 15) / 16 * 16); };
     const auto bytes_of = [&](int ctas) { return static_cast<int>(sizeof(Shared)) + slice_of(ctas) * size + 16; };
     int ctas = 1;
-    while (ctas < kMaxCtas && (bytes_of(ctas) > smem || (rows * ctas * 2 <= sms && slice_of(ctas) > 2048))) ctas *= 2;
+    while (ctas < kMaxCtas && (bytes_of(ctas) > smem / 2 || (rows * ctas * 2 <= sms && slice_of(ctas) > 2048))) ctas *= 2;
     if (bytes_of(ctas) > smem) return MEMQ_ERR_SHAPE;
     a.slice = slice_of(ctas);
     cudaLaunchConfig_t cfg = {};
