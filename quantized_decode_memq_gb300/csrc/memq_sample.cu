@@ -140,18 +140,16 @@ __device__ __forceinline__ float coarse(const Scale &s, float l) { return l == s
 
 // 2^-x of x >= kCareful: x is off by 2^-24 of it and exp2 by 2^-22 of it, below 2^-42 together.
 constexpr float kCareful = 24.f;
-__device__ __forceinline__ unsigned long long small_weight(float x) {
+__device__ __forceinline__ unsigned long long small_weight(float x) {  // 0 of 60 and more
     return x < 60.f ? static_cast<unsigned long long>(__float2uint_rn(ex2(static_cast<float>(kUnitLog) - x))) : 0ull;
 }
 
 // 2^-x in units of 2^-kUnitLog.
-__device__ __forceinline__ unsigned long long weight_of(const Scale &s, const unsigned long long *table, float l) {
-    if (l == s.top) return 1ull << kUnitLog;
+__device__ __forceinline__ unsigned long long careful_weight(const Scale &s, const unsigned long long *table, float l) {
     // the difference, exactly: dh + dl
     const float dh = __fsub_rn(s.top, l), bb = __fsub_rn(dh, s.top);
     const float dl = __fsub_rn(__fsub_rn(s.top, __fsub_rn(dh, bb)), __fadd_rn(l, bb));
-    const float yh = __fmul_rn(dh, s.hi);
-    if (!(yh < kCareful)) return small_weight(yh);
+    const float yh = fminf(__fmul_rn(dh, s.hi), kCareful);  // (of a larger one the result is not used)
     const float yl = __fmaf_rn(dh, s.hi, -yh) + __fmaf_rn(dh, s.lo, dl * s.hi);
     // the nearest multiple n of 2^-9
     const float big = 0x1.8p23f / kTable;
@@ -166,13 +164,35 @@ __device__ __forceinline__ unsigned long long weight_of(const Scale &s, const un
     const float zh = __fmul_rn(r, kLn2);
     const float zl = __fmaf_rn(r, kLn2, -zh) + __fmaf_rn(r, kLn2Lo, rl * kLn2);
     const float q = zh * zh * __fmaf_rn(zh, __fmaf_rn(zh, 1.f / 24.f, -1.f / 6.f), 0.5f);
-    const long long a = static_cast<long long>(__float2int_rn(zh * 0x1p41f)) + __float2int_rn((zl - q) * 0x1p41f);
+    const int a = __float2int_rn(zh * 0x1p41f) + __float2int_rn((zl - q) * 0x1p41f);  // below 2^30.6
     const int j = n & (kTable - 1), e = n >> 9;
     const unsigned long long p = table[j];
-    const long long down = (static_cast<long long>(static_cast<uint32_t>((p + 0x40000000ull) >> 31)) * a) >> 10;
+    const long long down = static_cast<long long>(static_cast<int>((p + 0x80000000ull) >> 32)) * a >> 9;
     const unsigned long long w = p - static_cast<unsigned long long>(down);
     const int shift = 62 - kUnitLog + e;
-    return (w + (1ull << (shift - 1))) >> shift;
+    return l == s.top ? 1ull << kUnitLog : (w + (1ull << (shift - 1))) >> shift;  // (infinity less itself is no number)
+}
+__device__ __forceinline__ unsigned long long weight_of(const Scale &s, const unsigned long long *table, float l) {
+    const float x = coarse(s, l);
+    return x < kCareful ? careful_weight(s, table, l) : small_weight(x);
+}
+// The weights of N tokens: a warp's lanes take the longer way together, all at once, if one of them has to.
+template <int N>
+__device__ __forceinline__ void weights_of(const Scale &s, const unsigned long long *table, const float (&l)[N],
+                                           const float (&x)[N], unsigned long long (&w)[N]) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        w[j] = small_weight(x[j]);
+        any = any || x[j] < kCareful;
+    }
+    if (__any_sync(kFullMask, any)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const unsigned long long c = careful_weight(s, table, l[j]);
+            if (x[j] < kCareful) w[j] = c;
+        }
+    }
 }
 
 // ------------------------------------------------------------------------------ reductions
@@ -202,25 +222,27 @@ struct Row {
             for (int j = 0; j < kVec; ++j) f(head + i * kVec + j, v[j]);
         }
     }
-    // f(i, values, n) of groups of n <= kVec tokens next to one another.
+    // f(i, values, n) of groups of n <= kVec tokens next to one another in [from, to), a whole warp together (n = 0 for
+    // lanes without any).
     template <typename F>
-    __device__ __forceinline__ void each_group(F f) const {
-        const int body = (len - head) / kVec, tail = head + body * kVec, tid = threadIdx.x;
+    __device__ __forceinline__ void walk(int from, int to, F f) const {
+        const int lane = threadIdx.x & 31;
+        // whole 16-byte groups, and a lane a token ahead of them and behind
+        const int g0 = min(to, from + (((head - from) % kVec) + kVec) % kVec), groups = (to - g0) / kVec, tail = g0 + groups * kVec;
         float v[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) v[j] = 0.f;
-        if (tid < head) {
-            v[0] = at(tid);
-            f(tid, v, 1);
+        if (from < g0 || tail < to) {
+            const int n0 = g0 - from, n1 = to - tail, i = lane < n0 ? from + lane : tail + lane - n0;
+            const bool live = lane < n0 + n1;
+            if (live) v[0] = at(i);
+            f(i, v, live ? 1 : 0);
         }
-        if (tail + tid < len && tid < kVec) {
-            v[0] = at(tail + tid);
-            f(tail + tid, v, 1);
-        }
-        const uint4 *from = reinterpret_cast<const uint4 *>(data + head * (BF16 ? 2 : 4));
-        for (int i = tid; i < body; i += kThreads) {
-            vec(from[i], v);
-            f(head + i * kVec, v, kVec);
+        const uint4 *src = reinterpret_cast<const uint4 *>(data + g0 * (BF16 ? 2 : 4));
+        for (int g = 0; g < groups; g += 32) {
+            const bool live = g + lane < groups;
+            vec(live ? src[g + lane] : make_uint4(0, 0, 0, 0), v);
+            f(g0 + (g + lane) * kVec, v, live ? kVec : 0);
         }
     }
     __device__ __forceinline__ static void vec(uint4 u, float (&v)[kVec]) {
@@ -383,7 +405,7 @@ __device__ __forceinline__ int first_reaching(const Shared &sh, int n, unsigned 
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -599,6 +621,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         cluster_wait();
     }
     const auto in_k = [&](uint32_t key, int index) { return place_of(key, index) >= cut_k; };
+    // a warp's tokens
+    const int seg = (row.len + kWarps - 1) / kWarps, seg0 = min(row.len, warp * seg), seg1 = min(row.len, seg0 + seg);
 
     // ------------------------------------------------------------------ top-k by bisection
     if (k < a.vocab) {
@@ -643,30 +667,28 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
             for (int b = tid; b < 2 * kBins; b += kThreads) sh.steps.lo[b] = 0;
             if (tid == 0) sh.count = 0;
             __syncthreads();
-            // Small weights at once, into one sum: no cut lies there but in the flattest of rows.  Those that need care
-            // are marked and taken one a thread at a time, for a warp waits for its slowest lane.
+            // Small weights at once, into one sum: no cut lies there but in the flattest of rows.
             unsigned long long tail = 0, none = 0;
-            row.each_group([&](int i0, const float(&v)[Row<BF16>::kVec], int n) {
-                uint32_t careful = 0;
+            row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16>::kVec], int n) {
+                float x[Row<BF16>::kVec];
+                unsigned long long w[Row<BF16>::kVec];
 #pragma unroll
                 for (int j = 0; j < Row<BF16>::kVec; ++j) {
-                    const float x = coarse(s, v[j]);
-                    if (j >= n || !(x < 60.f)) continue;  // NaN, -infinity, nothing
-                    if (x < kCareful)
-                        careful |= 1u << j;
-                    else if (level == 0 && (cut_k == 0 || in_k(key_of(v[j]), row.first + i0 + j)))
-                        tail += small_weight(x);
+                    x[j] = coarse(s, v[j]);
+                    // (NaN, -infinity: nothing)
+                    if (j >= n || !(x[j] < 60.f) || (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j))) x[j] = 100.f;
+                    if (level > 0 && (x[j] >= kCareful || step_of(x[j]) < 0 || step_of(x[j]) >= kBins)) x[j] = 100.f;
                 }
-                while (careful) {
-                    const int j = __ffs(careful) - 1;
-                    careful &= careful - 1;
-                    const float l = row.at(i0 + j);
-                    if (cut_k != 0 && !in_k(key_of(l), row.first + i0 + j)) continue;
-                    const int b = step_of(coarse(s, l));
-                    if (b < 0 || b >= kBins) continue;
-                    const unsigned long long w = weight_of(s, sh.table, l);
-                    const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.steps.lo[b], lo);
-                    const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old);
+                weights_of(s, sh.table, v, x, w);
+#pragma unroll
+                for (int j = 0; j < Row<BF16>::kVec; ++j) {
+                    if (x[j] >= kCareful) {
+                        tail += w[j];
+                        continue;
+                    }
+                    const int b = step_of(x[j]);
+                    const uint32_t lo = static_cast<uint32_t>(w[j]), old = atomicAdd(&sh.steps.lo[b], lo);
+                    const uint32_t hi = static_cast<uint32_t>(w[j] >> 32) + (old + lo < old);
                     if (hi) atomicAdd(&sh.steps.hi[b], hi);
                 }
             });
@@ -783,14 +805,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
 
     // ------------------------------------------------------------------ the draw
-    // A warp's tokens are consecutive (the first warp has those ahead of the 16-byte groups too, the last those behind
-    // them), so its sum's place among the others is its place by index.
+    // A warp's tokens are consecutive, so its sum's place among the others is its place by index.
     const float cut_v = cut ? value_of(cut) : -INFINITY;
     const int cut_i = cut ? index_of(cut) : 0x7fffffff;
-    constexpr int kVec = Row<BF16>::kVec;
-    const int body = (row.len - row.head) / kVec, per = (body + kWarps - 1) / kWarps;
-    const int g0 = min(body, warp * per), g1 = min(body, g0 + per);
-    const uint4 *groups = reinterpret_cast<const uint4 *>(row.data + row.head * kSize);
     const auto keep = [&](float v, int i) { return v > cut_v || (v == cut_v && row.first + i <= cut_i); };
     const auto kept_weight = [&](int i) -> unsigned long long {
         const float v = row.at(i);
@@ -798,51 +815,65 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         const unsigned long long w = weight_of(s, sh.table, v);
         return w >= least ? w : 0ull;
     };
-    const auto group_weight = [&](int g) {
-        float v[kVec];
-        Row<BF16>::vec(groups[g], v);
-        const int i0 = row.head + g * kVec;
-        unsigned long long sum = 0;
-        uint32_t careful = 0;
+    unsigned long long mine = 0;
+    row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16>::kVec], int n) {
+        float x[Row<BF16>::kVec];
+        unsigned long long w[Row<BF16>::kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const float x = coarse(s, v[j]);
-            if (!(x < 60.f) || !keep(v[j], i0 + j)) continue;
-            if (x < kCareful) {
-                careful |= 1u << j;
-            } else {
-                const unsigned long long w = small_weight(x);
-                if (w >= least) sum += w;
-            }
+        for (int j = 0; j < Row<BF16>::kVec; ++j) {
+            x[j] = coarse(s, v[j]);
+            if (j >= n || !(x[j] < 60.f) || !keep(v[j], i0 + j)) x[j] = 100.f;
         }
-        while (careful) {
-            const int j = __ffs(careful) - 1;
-            careful &= careful - 1;
-            const unsigned long long w = weight_of(s, sh.table, row.at(i0 + j));
-            if (w >= least) sum += w;
-        }
-        return sum;
-    };
-    // the tokens ahead of the groups and behind them: a lane each
-    const int tail0 = row.head + body * kVec;
-    const unsigned long long ahead = warp == 0 && lane < row.head ? kept_weight(lane) : 0ull;
-    const unsigned long long behind = warp == kWarps - 1 && tail0 + lane < row.len ? kept_weight(tail0 + lane) : 0ull;
-    unsigned long long mine = ahead + behind;
-    for (int g = g0 + lane; g < g1; g += 32) mine += group_weight(g);
+        weights_of(s, sh.table, v, x, w);
+#pragma unroll
+        for (int j = 0; j < Row<BF16>::kVec; ++j)
+            if (w[j] >= least) mine += w[j];
+    });
     mine = warp_sum64(mine);
     if (lane < static_cast<int>(ctas)) *in_cta(&sh.sums[rank][warp], lane) = mine;
     cluster_sync();
-    unsigned long long before = 0, all = 0;
-    for (uint32_t r = 0; r < ctas; ++r)
-        for (int w = 0; w < kWarps; ++w) {
-            if (r < rank || (r == rank && w < warp)) before += sh.sums[r][w];
-            all += sh.sums[r][w];
-        }
-    const unsigned long long goal = below(u, all);
+    // The warp whose sum passes the goal: its CTA's warps share its tokens, then one goes through what is left.  A lane
+    // holds four of the cluster's sums.
+    constexpr int kEach = kMaxCtas * kWarps / 32;
+    unsigned long long some[kEach], incl = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int k = lane * kEach + j;
+        some[j] = k < static_cast<int>(ctas) * kWarps ? sh.sums[k / kWarps][k % kWarps] : 0ull;
+        incl += some[j];
+    }
+    const unsigned long long own = incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long up = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += up;
+    }
+    const unsigned long long goal = below(u, __shfl_sync(kFullMask, incl, 31));
+    const int at = __ffs(__ballot_sync(kFullMask, incl > goal)) - 1;
+    unsigned long long before = incl - own;
+    int place = lane * kEach;
+#pragma unroll
+    for (int j = 0; j < kEach - 1; ++j) {
+        if (before + some[j] > goal) break;
+        before += some[j];
+        ++place;
+    }
+    before = __shfl_sync(kFullMask, before, at);
+    place = __shfl_sync(kFullMask, place, at);
+    const uint32_t r = static_cast<uint32_t>(place / kWarps);
+    const int w = place % kWarps;
+    if (r != rank) return;
+    const int from = min(row.len, w * seg), to = min(row.len, from + seg), part = (to - from + kWarps - 1) / kWarps;
+    const int part0 = min(to, from + warp * part), part1 = min(to, part0 + part);
+    mine = 0;
+    for (int i = part0 + lane; i < part1; i += 32) mine += kept_weight(i);
+    mine = warp_sum64(mine);
+    if (lane == 0) sh.warp64[0][warp] = mine;
+    __syncthreads();
+    for (int j = 0; j < warp; ++j) before += sh.warp64[0][j];
     if (goal < before || goal >= before + mine) return;
-    // This warp's: 32 sums a turn, by index; the lane whose sum passes the goal looks into its tokens.
-    const auto turn = [&](unsigned long long w, int i, int n) {
-        unsigned long long incl = w;
+    for (int i0 = part0; i0 < part1; i0 += 32) {
+        incl = i0 + lane < part1 ? kept_weight(i0 + lane) : 0ull;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned long long up = __shfl_up_sync(kFullMask, incl, o);
@@ -850,23 +881,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         }
         const unsigned over = __ballot_sync(kFullMask, before + incl > goal);
         if (over) {
-            if (lane == __ffs(over) - 1) {
-                unsigned long long run = before + incl - w;
-                for (; n > 1; ++i, --n) {
-                    run += kept_weight(i);
-                    if (run > goal) break;
-                }
-                a.out[row_i] = row.first + i;
-            }
-            return true;
+            if (lane == 0) a.out[row_i] = row.first + i0 + __ffs(over) - 1;
+            return;
         }
         before += __shfl_sync(kFullMask, incl, 31);
-        return false;
-    };
-    if (warp == 0 && turn(ahead, lane, 1)) return;
-    for (int i = g0; i < g1; i += 32)
-        if (turn(i + lane < g1 ? group_weight(i + lane) : 0ull, row.head + (i + lane) * kVec, kVec)) return;
-    if (warp == kWarps - 1) turn(behind, tail0 + lane, 1);
+    }
 }
 
 bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
