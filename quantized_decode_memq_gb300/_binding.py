@@ -758,6 +758,12 @@ def memq_mla_attn_paged(q_lat: torch.Tensor, q_pe, cache: torch.Tensor, scales: 
     return out
 
 
+# The calls below pass through one test of all their arguments when everything is as it should be; the single checks,
+# which name what is wrong, run when that test fails (of a step of serving's small calls the checks took half the time).
+def _here_index():
+    return _cur_device() if _cur_device is not None else torch.cuda.current_device()
+
+
 def _i32(name: str, t, shape, device):
     """An int32 CUDA tensor of the shape, a new one for None."""
     if t is None:
@@ -777,6 +783,35 @@ def memq_page_plan(cached: torch.Tensor, new_tok: torch.Tensor, block_table: tor
     Returns (slots [n_tok], positions [n_tok], cu_q [n_seq + 1], kv_len [n_seq], granted [n_seq],
     n_free_out [1]), all int32.  kv_len may be cached itself and n_free_out n_free (both in place)."""
     fn = "memq_page_plan"
+    i32 = torch.int32
+    try:
+        n_seq, max_pages = block_table.shape
+        row, toks, one = (n_seq,), (n_tok,), (1,)
+        fits = (cached.dtype is new_tok.dtype is block_table.dtype is free_pages.dtype is n_free.dtype is kv_len.dtype
+                is n_free_out.dtype is cu_q.dtype is slots.dtype is positions.dtype is granted.dtype is i32
+                and (keep is None or (keep.dtype is i32 and keep.shape == row and keep.is_contiguous()
+                                      and keep.get_device() == cached.get_device()))
+                and cached.shape == new_tok.shape == kv_len.shape == granted.shape == row
+                and slots.shape == positions.shape == toks and cu_q.shape == (n_seq + 1,)
+                and n_free.shape == n_free_out.shape == one and free_pages.dim() == 1
+                and _here_index() == cached.get_device() == new_tok.get_device() == block_table.get_device()
+                == free_pages.get_device() == n_free.get_device() == kv_len.get_device() == n_free_out.get_device()
+                == cu_q.get_device() == slots.get_device() == positions.get_device() == granted.get_device()
+                and cached.is_contiguous() and new_tok.is_contiguous() and block_table.is_contiguous()
+                and free_pages.is_contiguous() and n_free.is_contiguous() and kv_len.is_contiguous()
+                and n_free_out.is_contiguous() and cu_q.is_contiguous() and slots.is_contiguous()
+                and positions.is_contiguous() and granted.is_contiguous())
+    except (AttributeError, TypeError, ValueError):  # an output left out, an argument of another kind
+        fits = False
+    if fits:
+        rc = lib().memq_page_plan(cached.data_ptr(), None if keep is None else keep.data_ptr(), new_tok.data_ptr(),
+                                  block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), kv_len.data_ptr(),
+                                  n_free_out.data_ptr(), cu_q.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                                  granted.data_ptr(), n_seq, n_tok, max_pages, page_size, free_pages.shape[0],
+                                  _stream(stream))
+        if rc != 0:
+            _check(fn, rc)
+        return slots, positions, cu_q, kv_len, granted, n_free_out
     _cuda("cached", cached, torch.int32)
     if cached.dim() != 1:
         raise ValueError(f"{fn}: cached must be [n_seq]")
@@ -850,6 +885,29 @@ def memq_kv_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, 
     k_cache, v_cache uint8 (E4M3 codes) [n_pages, n_kv, page_size, d] and k_scales, v_scales f32 [n_pages, n_kv,
     page_size / 16] are written in place."""
     fn = "memq_kv_cache_append"
+    try:
+        n, n_kv, d = k.shape
+        pages, _, page_size, _ = k_cache.shape
+        ks, vs, plane = k.stride(), v.stride(), (pages, n_kv, page_size // 16)
+        kind = _DTYPES.get(k.dtype)
+        fits = (kind is not None and v.dtype is k.dtype and v.shape == k.shape and n > 1 and n_kv > 0 and d > 1
+                and ks[2] == vs[2] == 1 and ks[1] == vs[1] == d and slots.dtype is torch.int32 and slots.shape == (n,)
+                and k_cache.dtype is v_cache.dtype is torch.uint8
+                and k_cache.shape == v_cache.shape == (pages, n_kv, page_size, d)
+                and k_scales.dtype is v_scales.dtype is torch.float32 and k_scales.shape == v_scales.shape == plane
+                and _here_index() == k.get_device() == v.get_device() == slots.get_device() == k_cache.get_device()
+                == v_cache.get_device() == k_scales.get_device() == v_scales.get_device()
+                and slots.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and k_scales.is_contiguous() and v_scales.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if fits:
+        rc = lib().memq_kv_cache_append(kind, k.data_ptr(), ks[0], v.data_ptr(), vs[0], slots.data_ptr(),
+                                        k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
+                                        v_scales.data_ptr(), n, n_kv, d, pages, page_size, _stream(stream))
+        if rc != 0:
+            _check(fn, rc)
+        return
     kind, k_stride = _rows("k", k)
     n, n_kv, d = k.shape
     _, v_stride = _rows("v", v, k.dtype, k.shape)
@@ -870,6 +928,23 @@ def memq_kv_cache_read(cache: torch.Tensor, scales: torch.Tensor, slots: torch.T
     """The values of the pool rows named by slots (int32 [n], repeats allowed, negative = zeros), of keys or
     of values: f32 or bf16 [n, n_kv, d], in `out` or a new tensor of `dtype`."""
     fn = "memq_kv_cache_read"
+    try:
+        pages, n_kv, page_size, d = cache.shape
+        n, = slots.shape
+        kind = _DTYPES.get(out.dtype)
+        fits = (kind is not None and cache.dtype is torch.uint8 and scales.dtype is torch.float32
+                and scales.shape == (pages, n_kv, page_size // 16) and slots.dtype is torch.int32
+                and out.shape == (n, n_kv, d) and _here_index() == cache.get_device() == scales.get_device()
+                == slots.get_device() == out.get_device() and cache.is_contiguous() and scales.is_contiguous()
+                and slots.is_contiguous() and out.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if fits:
+        rc = lib().memq_kv_cache_read(kind, cache.data_ptr(), scales.data_ptr(), slots.data_ptr(), out.data_ptr(), n,
+                                      n_kv, d, pages, page_size, _stream(stream))
+        if rc != 0:
+            _check(fn, rc)
+        return out
     pages, n_kv, page_size, d = _kv_pool(fn, "kv", cache, scales)
     _cuda("slots", slots, torch.int32)
     if slots.dim() != 1:
@@ -912,22 +987,47 @@ def memq_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     bf16 is faster.  workspace: uint8 scratch of at least memq_attn_paged_workspace(d) bytes, one per call
     that may run at the same time; a new one is taken when it is None."""
     fn = "memq_attn_paged"
-    q_kind, q_stride = _rows("q", q)
-    n_tok, nh, d = q.shape
-    pages, n_kv, page_size, width = _kv_pool(fn, "k", k_cache, k_scales)
-    if width != d:
-        raise ValueError(f"{fn}: the cache's heads have {width} elements, q's {d}")
-    _kv_pool(fn, "v", v_cache, v_scales, k_cache.shape)
-    _cuda("block_table", block_table, torch.int32)
-    if block_table.dim() != 2:
-        raise ValueError(f"{fn}: block_table must be [n_seq, max_pages]")
-    n_seq, max_pages = block_table.shape
-    _cuda("kv_len", kv_len, torch.int32, (n_seq,))
-    _cuda("cu_q", cu_q, torch.int32, (n_seq + 1,))
-    if out is None:
-        out = torch.empty((n_tok, nh, d), dtype=q.dtype, device=q.device)
-    o_kind = _float("out", out, None, (n_tok, nh, d))
-    _here(fn, q, k_cache, v_cache, k_scales, v_scales, block_table, kv_len, cu_q, out, workspace)
+    i32, f32 = torch.int32, torch.float32
+    try:
+        n_tok, nh, d = q.shape
+        pages, n_kv, page_size, _ = k_cache.shape
+        n_seq, max_pages = block_table.shape
+        stride, plane = q.stride(), (pages, n_kv, page_size // 16)
+        q_kind, o_kind = _DTYPES.get(q.dtype), _DTYPES.get(out.dtype)
+        dev = _here_index()
+        fits = (q_kind is not None and o_kind is not None and nh > 0 and d > 1 and stride[2] == 1 and stride[1] == d
+                and out.shape == q.shape and k_cache.dtype is v_cache.dtype is torch.uint8
+                and k_cache.shape == v_cache.shape == (pages, n_kv, page_size, d)
+                and k_scales.dtype is v_scales.dtype is f32 and k_scales.shape == v_scales.shape == plane
+                and block_table.dtype is kv_len.dtype is cu_q.dtype is i32 and kv_len.shape == (n_seq,)
+                and cu_q.shape == (n_seq + 1,) and dev == q.get_device() == k_cache.get_device()
+                == v_cache.get_device() == k_scales.get_device() == v_scales.get_device() == block_table.get_device()
+                == kv_len.get_device() == cu_q.get_device() == out.get_device()
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scales.is_contiguous()
+                and v_scales.is_contiguous() and block_table.is_contiguous() and kv_len.is_contiguous()
+                and cu_q.is_contiguous() and out.is_contiguous()
+                and (workspace is None or workspace.get_device() == dev))
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if fits:
+        q_stride = stride[0] if n_tok > 1 else nh * d
+    else:
+        q_kind, q_stride = _rows("q", q)
+        n_tok, nh, d = q.shape
+        pages, n_kv, page_size, width = _kv_pool(fn, "k", k_cache, k_scales)
+        if width != d:
+            raise ValueError(f"{fn}: the cache's heads have {width} elements, q's {d}")
+        _kv_pool(fn, "v", v_cache, v_scales, k_cache.shape)
+        _cuda("block_table", block_table, i32)
+        if block_table.dim() != 2:
+            raise ValueError(f"{fn}: block_table must be [n_seq, max_pages]")
+        n_seq, max_pages = block_table.shape
+        _cuda("kv_len", kv_len, i32, (n_seq,))
+        _cuda("cu_q", cu_q, i32, (n_seq + 1,))
+        if out is None:
+            out = torch.empty((n_tok, nh, d), dtype=q.dtype, device=q.device)
+        o_kind = _float("out", out, None, (n_tok, nh, d))
+        _here(fn, q, k_cache, v_cache, k_scales, v_scales, block_table, kv_len, cu_q, out, workspace)
     st = _stream(stream)
     if workspace is None:
         need = memq_attn_paged_workspace(d)
@@ -939,10 +1039,10 @@ def memq_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     else:
         _cuda("workspace", workspace, torch.uint8)
         need = workspace.numel()
-    rc = lib().memq_attn_paged(q_kind, _ptr(q), q_stride, _ptr(k_cache), _ptr(k_scales), _ptr(v_cache),
-                               _ptr(v_scales), _ptr(block_table), _ptr(kv_len), _ptr(cu_q), o_kind, _ptr(out),
-                               _ptr(workspace), need, n_tok, n_seq, nh, n_kv, d, pages, page_size, max_pages,
-                               scale, st)
+    rc = lib().memq_attn_paged(q_kind, q.data_ptr(), q_stride, k_cache.data_ptr(), k_scales.data_ptr(),
+                               v_cache.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(), kv_len.data_ptr(),
+                               cu_q.data_ptr(), o_kind, out.data_ptr(), workspace.data_ptr(), need, n_tok, n_seq, nh,
+                               n_kv, d, pages, page_size, max_pages, scale, st)
     _check(fn, rc)
     return out
 

@@ -26,8 +26,8 @@ __device__ unsigned int g_kv_fault = 0;
 constexpr unsigned int kFaultInput = 32;  // a slot was outside the pool
 
 constexpr int kBlock = 16;  // tokens that share a scale
-constexpr int kKvThreads = 256;
-constexpr int kKvWarps = kKvThreads / 32;
+constexpr int kAppendThreads = 128, kAppendWarps = kAppendThreads / 32;
+constexpr int kReadThreads = 256;
 constexpr int kLeast = -100;  // exponent of the least scale
 
 struct AppendArgs {
@@ -40,51 +40,48 @@ struct AppendArgs {
     int n_kv, page_shift, window;
 };
 
-// E elements of a row.
+// E elements of a row, as they come: 16 rows of bf16 take 64 registers a lane and leave room for four CTAs on an SM
+// (as f32 they took 128: one CTA, and loads, work and stores of a block did not overlap).
 template <int E, bool BF16>
 struct Elems {
-    float x[E];
+    static constexpr int kWords = BF16 ? E / 2 : E;
+    uint32_t w[kWords];
     __device__ __forceinline__ void load(const void *p, int64_t at) {
-        if (BF16) {
-            const uint2 *src = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + at);
-            uint2 u[E / 4];
-            if (E == 8) {
-                const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(src));
-                u[0] = make_uint2(w.x, w.y);
-                u[E / 4 - 1] = make_uint2(w.z, w.w);
-            } else {
-                u[0] = __ldcg(src);
-            }
-#pragma unroll
-            for (int i = 0; i < E / 4; ++i) {
-                x[4 * i] = __uint_as_float(u[i].x << 16);
-                x[4 * i + 1] = __uint_as_float(u[i].x & 0xffff0000u);
-                x[4 * i + 2] = __uint_as_float(u[i].y << 16);
-                x[4 * i + 3] = __uint_as_float(u[i].y & 0xffff0000u);
-            }
+        const uint8_t *src = static_cast<const uint8_t *>(p) + at * (BF16 ? 2 : 4);
+        if constexpr (kWords == 2) {
+            const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(src));
+            w[0] = u.x;
+            w[1] = u.y;
         } else {
-            const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
 #pragma unroll
-            for (int i = 0; i < E / 4; ++i) {
-                const float4 w = __ldcg(src + i);
-                x[4 * i] = w.x;
-                x[4 * i + 1] = w.y;
-                x[4 * i + 2] = w.z;
-                x[4 * i + 3] = w.w;
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(src) + i);
+                w[4 * i] = u.x;
+                w[4 * i + 1] = u.y;
+                w[4 * i + 2] = u.z;
+                w[4 * i + 3] = u.w;
             }
         }
     }
-    __device__ __forceinline__ bool finite() const {
-        bool f = true;
-#pragma unroll
-        for (int i = 0; i < E; ++i) f = f && isfinite(x[i]);
-        return f;
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (BF16)
+            return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        else
+            return __uint_as_float(w[i]);
     }
-    __device__ __forceinline__ float largest() const {
-        float m = 0.f;
+    // max |x| as bits: infinities and NaN lie above all numbers.
+    __device__ __forceinline__ uint32_t largest() const {
+        if constexpr (BF16) {
+            uint32_t m = 0;  // two 16-bit maxima
 #pragma unroll
-        for (int i = 0; i < E; ++i) m = fmaxf(m, fabsf(x[i]));
-        return m;
+            for (int i = 0; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            return max(m << 16, m & 0xffff0000u);
+        } else {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        }
     }
 };
 
@@ -102,16 +99,15 @@ __device__ __forceinline__ void store_row(uint8_t *at, const Elems<E, BF16> &r, 
     uint32_t c[E / 4];
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
-        c[i] = f32x2_to_e4m3x2(r.x[4 * i] * inv, r.x[4 * i + 1] * inv) |
-               f32x2_to_e4m3x2(r.x[4 * i + 2] * inv, r.x[4 * i + 3] * inv) << 16;
+        c[i] = f32x2_to_e4m3x2(r.at(4 * i) * inv, r.at(4 * i + 1) * inv) |
+               f32x2_to_e4m3x2(r.at(4 * i + 2) * inv, r.at(4 * i + 3) * inv) << 16;
         if (!fin) c[i] = keys ? 0x7f7f7f7fu : 0u;
     }
     store_codes<E>(at, c);
 }
 
 // e of the least power of two with top <= 448 * 2^e = 1.75 * 2^(e + 8).
-__device__ __forceinline__ int scale_exponent(float top) {
-    const uint32_t b = __float_as_uint(top);
+__device__ __forceinline__ int scale_exponent(uint32_t b) {  // of the bits of `top`
     const int k = static_cast<int>(b >> 23) - 127;
     return max(kLeast, (b & 0x7fffffu) <= 0x600000u ? k - 8 : k - 7);
 }
@@ -120,12 +116,12 @@ __device__ __forceinline__ float power_of_two(int e) {  // -149 <= e <= 127
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, BF16 || D == 64 ? 4 : 2) kv_append_kernel(const AppendArgs a) {
     constexpr int E = D / 16;
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, half = lane >> 4, part = lane & 15;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kKvWarps + (threadIdx.x >> 5);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
     const int64_t r0 = unit / a.n_kv * a.window;
     const int h = static_cast<int>(unit % a.n_kv);
     if (r0 >= a.n) return;
@@ -171,13 +167,14 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendArgs 
 #pragma unroll
         for (int i = 0; i < kBlock; ++i)
             if (i < n0) x[i].load(src, at0 + i * stride);
-        float top = 0.f;
+        uint32_t top = 0;
         unsigned fin = 0, written = 0;
 #pragma unroll
         for (int i = 0; i < kBlock; ++i) {
             if (i < n0) {
-                const bool f = __all_sync(kFullMask, x[i].finite());
-                if (f) top = fmaxf(top, x[i].largest());
+                const uint32_t m = x[i].largest();
+                const bool f = __all_sync(kFullMask, m < 0x7f800000u);
+                if (f) top = max(top, m);
                 fin |= static_cast<unsigned>(f) << i;
                 written |= 1u << __shfl_sync(kFullMask, slot, i);
             }
@@ -185,11 +182,12 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendArgs 
         for (int64_t i = kBlock; i < count; ++i) {  // more rows than places: some are named twice
             Elems<E, BF16> y;
             y.load(src, at0 + i * stride);
-            if (__all_sync(kFullMask, y.finite())) top = fmaxf(top, y.largest());
+            const uint32_t m = y.largest();
+            if (__all_sync(kFullMask, m < 0x7f800000u)) top = max(top, m);
             written |= 1u << (__ldcg(a.slots + r + i) & (kBlock - 1));
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
         int e = scale_exponent(top);
         // Rows that are there keep their values; offset 0 starts a block afresh.  A scale that no call
         // of this kind left there (not a power of two) is rounded up to one.
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendArgs 
         for (int64_t i = kBlock; i < count; ++i) {
             Elems<E, BF16> y;
             y.load(src, at0 + i * stride);
-            const bool f = __all_sync(kFullMask, y.finite());
+            const bool f = __all_sync(kFullMask, y.largest() < 0x7f800000u);
             store_row(rows + (__ldcg(a.slots + r + i) & (kBlock - 1)) * D, y, inv, f, half == 0);
         }
         if (part == 0) *scale_at = scale;
@@ -241,51 +239,74 @@ struct ReadArgs {
     int n_kv, page_shift;
 };
 
-// A thread returns eight values: 64 bits of codes.
+// A thread returns 16 values of each of kTurns rows' parts, whose loads are out together: a part's slot, then its codes
+// and scale.
+constexpr int kTurns = 2;
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const ReadArgs a) {
-    constexpr int P = D / 8;
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
+    constexpr int P = D / 16;
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x;
-    const int64_t row = i / (a.n_kv * P);
-    if (row >= a.n) return;
-    const int rest = static_cast<int>(i - row * (a.n_kv * P)), h = rest / P, p = rest % P;
-    int64_t slot = __ldcg(a.slots + row);
-    if (slot >= a.pool) {
-        if (rest == 0) atomicOr(&g_kv_fault, kFaultInput);
-        slot = -1;
-    }
-    uint2 code = make_uint2(0, 0);
-    float scale = 0.f;
-    if (slot >= 0) {
-        const int page = 1 << a.page_shift, in_page = static_cast<int>(slot & (page - 1));
-        const int64_t plane = (slot >> a.page_shift) * a.n_kv + h;
-        code = __ldcg(reinterpret_cast<const uint2 *>(a.cache + (plane * page + in_page) * D) + p);
-        scale = __ldcg(a.scales + plane * (page / kBlock) + in_page / kBlock);
-    }
-    float o[8];
-    const uint32_t w[2] = {code.x, code.y};
+    const int64_t parts = a.n * a.n_kv * P;
+    const int page = 1 << a.page_shift;
+    int64_t at[kTurns], slot[kTurns];
+    int head[kTurns];
+    uint4 code[kTurns];
+    float scale[kTurns];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        uint32_t lo, hi;
-        e4m3x4_to_f16x2x2(w[j], lo, hi);
-        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        o[4 * j] = x.x * scale;
-        o[4 * j + 1] = x.y * scale;
-        o[4 * j + 2] = y.x * scale;
-        o[4 * j + 3] = y.y * scale;
+    for (int t = 0; t < kTurns; ++t) {
+        at[t] = (static_cast<int64_t>(blockIdx.x) * kTurns + t) * kReadThreads + threadIdx.x;
+        const int64_t row = parts >> 32 ? at[t] / (a.n_kv * P) : static_cast<uint32_t>(at[t]) / static_cast<uint32_t>(a.n_kv * P);
+        const int rest = static_cast<int>(at[t] - row * (a.n_kv * P));
+        head[t] = rest / P;
+        slot[t] = at[t] < parts ? __ldcg(a.slots + row) : -1;
+        if (slot[t] >= a.pool) {
+            if (rest == 0) atomicOr(&g_kv_fault, kFaultInput);
+            slot[t] = -1;
+        }
     }
-    if (BF16) {
-        __nv_bfloat162 b[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(o[2 * j], o[2 * j + 1]);
-        reinterpret_cast<uint4 *>(a.out)[i] = *reinterpret_cast<uint4 *>(b);
-    } else {
-        float4 *dst = reinterpret_cast<float4 *>(a.out) + 2 * i;
-        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+    for (int t = 0; t < kTurns; ++t) {
+        code[t] = make_uint4(0, 0, 0, 0);
+        scale[t] = 0.f;
+        if (slot[t] >= 0) {
+            const int in_page = static_cast<int>(slot[t] & (page - 1));
+            const int64_t plane = (slot[t] >> a.page_shift) * a.n_kv + head[t];
+            code[t] = __ldcg(reinterpret_cast<const uint4 *>(a.cache + (plane * page + in_page) * D) + at[t] % P);
+            scale[t] = __ldcg(a.scales + plane * (page / kBlock) + in_page / kBlock);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+        if (at[t] >= parts) continue;
+        const uint32_t w[4] = {code[t].x, code[t].y, code[t].z, code[t].w};
+        float o[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t lo, hi;
+            e4m3x4_to_f16x2x2(w[j], lo, hi);
+            const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+            const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+            o[4 * j] = x.x * scale[t];
+            o[4 * j + 1] = x.y * scale[t];
+            o[4 * j + 2] = y.x * scale[t];
+            o[4 * j + 3] = y.y * scale[t];
+        }
+        if (BF16) {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out) + 2 * at[t];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                __nv_bfloat162 b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(o[8 * i + 2 * j], o[8 * i + 2 * j + 1]);
+                dst[i] = *reinterpret_cast<uint4 *>(b);
+            }
+        } else {
+            float4 *dst = reinterpret_cast<float4 *>(a.out) + 4 * at[t];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
     }
 }
 
@@ -298,10 +319,10 @@ bool sizes_ok(int dtype, int64_t n, int n_kv, int d, int64_t n_pages, int page_s
 }
 
 template <typename Args>
-int launch(void (*kern)(const Args), int64_t ctas, void *stream, const Args &a) {
+int launch(void (*kern)(const Args), int64_t ctas, int threads, void *stream, const Args &a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kKvThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -341,11 +362,11 @@ extern "C" int memq_kv_cache_append(int dtype, const void *k, int64_t k_stride, 
     const int window = n * n_kv <= 16384 ? 1 : kBlock;
     AppendArgs a{k, v, k_stride, v_stride, slots, k_cache, v_cache, k_scales, v_scales, n, n_pages * page_size, n_kv,
                  __builtin_ctz(static_cast<unsigned>(page_size)), window};
-    const int64_t units = (n + window - 1) / window * n_kv, ctas = (units + kKvWarps - 1) / kKvWarps;
+    const int64_t units = (n + window - 1) / window * n_kv, ctas = (units + kAppendWarps - 1) / kAppendWarps;
     const bool b = dtype == MEMQ_BF16;
     return launch<AppendArgs>(d == 128 ? (b ? kv_append_kernel<128, true> : kv_append_kernel<128, false>)
                                        : (b ? kv_append_kernel<64, true> : kv_append_kernel<64, false>),
-                              ctas, stream, a);
+                              ctas, kAppendThreads, stream, a);
 }
 
 extern "C" int memq_kv_cache_read(int dtype, const uint8_t *cache, const float *scales, const int32_t *slots, void *out,
@@ -357,10 +378,10 @@ extern "C" int memq_kv_cache_read(int dtype, const uint8_t *cache, const float *
     if (misaligned(cache, 16) || misaligned(scales, 4) || misaligned(slots, 4) || misaligned(out, 16))
         return MEMQ_ERR_ALIGN;
     ReadArgs a{cache, scales, slots, out, n, n_pages * page_size, n_kv, __builtin_ctz(static_cast<unsigned>(page_size))};
-    const int64_t threads = n * n_kv * (d / 8), ctas = (threads + kKvThreads - 1) / kKvThreads;
+    const int64_t parts = n * n_kv * (d / 16), ctas = (parts + kTurns * kReadThreads - 1) / (kTurns * kReadThreads);
     if (ctas > 0x7fffffffLL) return MEMQ_ERR_SHAPE;
     const bool b = dtype == MEMQ_BF16;
     return launch<ReadArgs>(d == 128 ? (b ? kv_read_kernel<128, true> : kv_read_kernel<128, false>)
                                      : (b ? kv_read_kernel<64, true> : kv_read_kernel<64, false>),
-                            ctas, stream, a);
+                            ctas, kReadThreads, stream, a);
 }

@@ -39,6 +39,7 @@ struct PlanArgs {
     const int32_t *n_free;
     int32_t *kv_len, *n_free_out, *cu_q, *slots, *positions, *granted;
     int n_seq, n_tok, max_pages, page_shift, n_pages;
+    int wide;  // slots and positions are 16-byte aligned
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -221,24 +222,41 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PlanAr
         const int b = owner_of(pop0, a.n_seq, k);
         a.table[static_cast<int64_t>(b) * a.max_pages + have_of[b] + (k - pop0[b])] = __ldcg(a.free_pages + top - k);
     }
+    // Four tokens next to one another a thread: one bisection, and a store of 16 bytes where the outputs lie so.
     const int live = tok0[a.n_seq];
-    for (int t = first; t < a.n_tok; t += stride) {
-        int slot = -1, pos = -1;
-        if (t < live) {
-            const int b = owner_of(tok0, a.n_seq, t);
-            pos = keep_of[b] + (t - tok0[b]);
-            if (need_of[b] >= 0) {
-                const int col = pos >> a.page_shift;
-                const int p = col < have_of[b] ? __ldcg(a.table + static_cast<int64_t>(b) * a.max_pages + col)
-                                               : __ldcg(a.free_pages + top - (pop0[b] + col - have_of[b]));
-                if (p >= 0 && p < a.n_pages)
-                    slot = (p << a.page_shift) + (pos & (page - 1));
-                else
-                    atomicOr(&g_plan_fault, kFaultInput);
+    for (int t0 = 4 * first; t0 < a.n_tok; t0 += 4 * stride) {
+        int slot[4], pos[4], col_then = -1, page_then = -1, b = t0 < live ? owner_of(tok0, a.n_seq, t0) : 0, b_then = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + i;
+            slot[i] = pos[i] = -1;
+            if (t >= live) continue;
+            while (tok0[b + 1] <= t) ++b;  // (t < live = tok0[n_seq])
+            pos[i] = keep_of[b] + (t - tok0[b]);
+            if (need_of[b] < 0) continue;
+            const int col = pos[i] >> a.page_shift;
+            if (col != col_then || b != b_then) {
+                page_then = col < have_of[b] ? __ldcg(a.table + static_cast<int64_t>(b) * a.max_pages + col)
+                                             : __ldcg(a.free_pages + top - (pop0[b] + col - have_of[b]));
+                col_then = col;
+                b_then = b;
             }
+            if (page_then >= 0 && page_then < a.n_pages)
+                slot[i] = (page_then << a.page_shift) + (pos[i] & (page - 1));
+            else
+                atomicOr(&g_plan_fault, kFaultInput);
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
+        if (a.wide && t0 + 4 <= a.n_tok) {
+            *reinterpret_cast<int4 *>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t0 + i < a.n_tok) {
+                    a.slots[t0 + i] = slot[i];
+                    a.positions[t0 + i] = pos[i];
+                }
+        }
     }
 }
 
@@ -278,9 +296,10 @@ extern "C" int memq_page_plan(const int32_t *cached, const int32_t *keep, const 
         if (misaligned4(p)) return MEMQ_ERR_ALIGN;
     PlanArgs a{cached, keep, new_tok, block_table, free_pages, n_free, kv_len, n_free_out, cu_q, slots, positions,
                granted, n_seq, static_cast<int>(n_tok), max_pages, __builtin_ctz(static_cast<unsigned>(page_size)),
-               static_cast<int>(n_pages)};
+               static_cast<int>(n_pages),
+               ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(positions)) & 15) == 0};
     // One CTA serves what its threads hold in one round; more of it is shared by a cluster.
-    const bool small = n_seq <= kPlanThreads && n_tok <= kPlanThreads;
+    const bool small = n_seq <= kPlanThreads && n_tok <= 4 * kPlanThreads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(small ? 1 : kClusterCtas);
     cfg.blockDim = dim3(kPlanThreads);
