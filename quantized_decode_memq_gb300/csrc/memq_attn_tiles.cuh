@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
 
     // ------------------------------------------------------------------ this CTA's run of tiles
     // Blocks of rows before each sequence; then a thread counts the tiles of a slice of the blocks.
-    int *first = reinterpret_cast<int *>(smem);  // [n_seq + 1], of at most 2^27 blocks
+    int4 *seqs = reinterpret_cast<int4 *>(smem);  // (start, t, kv, blocks before), of at most 2^27 blocks
     const auto prefix = [&](long long v, long long &total) {  // exclusive, over the CTA
         long long incl = v;
 #pragma unroll
@@ -354,13 +354,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         __syncthreads();
         if (lane == 31) ctl->warp_sum[warp] = incl;
         __syncthreads();
-        long long before = incl - v;
-        total = 0;
-        for (int w = 0; w < kTileThreads / 32; ++w) {
-            if (w < warp) before += ctl->warp_sum[w];
-            total += ctl->warp_sum[w];
+        const long long s = lane < kTileThreads / 32 ? ctl->warp_sum[lane] : 0;
+        long long run = s;
+#pragma unroll
+        for (int o = 1; o < kTileThreads / 32; o <<= 1) {
+            const long long up = __shfl_up_sync(kFullMask, run, o);
+            if (lane >= o) run += up;
         }
-        return before;
+        total = __shfl_sync(kFullMask, run, kTileThreads / 32 - 1);
+        return __shfl_sync(kFullMask, run - s, warp) + incl - v;
     };
     const int per_seq = (a.n_seq + kTileThreads - 1) / kTileThreads;
     bool descends = false;
@@ -372,15 +374,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         if (c0 < 0 || c0 > c1 || c1 > a.n_tok || kv < 0 || kv > (static_cast<long long>(a.max_pages) << a.page_shift))
             atomicOr(fault, kAttnFaultInput);
         descends = descends || c0 > c1;
-        const int rows = attn_seq(a, c0, c1, kv).t * a.group;
-        first[b] = static_cast<int>(blocks);
+        const AttnSeq s = attn_seq(a, c0, c1, kv);
+        const int rows = s.t * a.group;
+        seqs[b] = make_int4(s.start, s.t, s.kv, static_cast<int>(blocks));
         if (tile_served(a, rows)) blocks += (rows + kRowsPer - 1) / kRowsPer;
     }
     const bool nothing = __syncthreads_or(descends);
     long long before = prefix(blocks, total_blocks);
     for (int i = 0; i < per_seq; ++i) {
         const int b = tid * per_seq + i;
-        if (b < a.n_seq) first[b] += static_cast<int>(before);
+        if (b < a.n_seq) seqs[b].w += static_cast<int>(before);
     }
     if (nothing) total_blocks = 0;
     __syncthreads();
@@ -398,12 +401,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
             int lo = 0, hi = a.n_seq;  // the last sequence whose first block is at or before lo_block
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (first[mid] <= lo_block) lo = mid; else hi = mid;
+                if (seqs[mid].w <= lo_block) lo = mid; else hi = mid;
             }
+            const int4 v = seqs[lo];
             it.seq = lo;
-            it.s = attn_seq(a, __ldcg(a.cu_q + lo), __ldcg(a.cu_q + lo + 1), __ldcg(a.kv_len + lo));
+            it.s = AttnSeq{v.x, v.y, v.z};
             it.rows = it.s.t * a.group;
-            it.row_tile = lo_block - first[lo];
+            it.row_tile = lo_block - v.w;
             tile_sizes(a, kRowsPer, it);
         }
         for (int b = lo_block; b < hi_block; ++b) {
@@ -437,7 +441,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFullMask, ctl->tmem, 0);
-    const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 384};
+    // columns of a block's scores and outputs
+    const auto s_col = [&](int b) { return tmem + static_cast<uint32_t>(b) * 128; };
+    const auto o_col = [&](int b) { return tmem + 256 + static_cast<uint32_t>(b) * 128; };
 
     AttnWaiter wait{fault};
     const auto my_run = [&]() {
@@ -454,7 +460,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         TileRun run = my_run();
         const int b = warp >> 2, wq = warp & 3, r = b * 128 + wq * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t at_s = s_col[b] + lanes, at_o = o_col[b] + lanes;
+        const uint32_t at_s = s_col(b) + lanes, at_o = o_col(b) + lanes;
         uint32_t tile = 0, turns = 0, all_items = 0;
         for (; b < kBlocks && run.more() && !wait.dead; run.next()) {
             const TileItem &it = run.it;
@@ -707,7 +713,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
-                    mma_f16_ss(s_col[b] + half * kHalfKeys, smem_desc(q_at + (Q2 ? term : b) * (128 * D * 2) + at, 128),
+                    mma_f16_ss(s_col(b) + half * kHalfKeys, smem_desc(q_at + (Q2 ? term : b) * (128 * D * 2) + at, 128),
                                smem_desc(k_at + buf * Shape::kKv + half * (kHalfKeys * 128) + at, 128), kQk, term > 0 || i > 0);
                 }
         };
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
             for (int term = 0; term < (P2 ? 2 : 1); ++term)
 #pragma unroll
                 for (int i = 0; i < kHalfKeys / 16; ++i)
-                    mma_f16_ts(o_col[b], s_col[b] + half * kHalfKeys + term * 32 + i * 8,
+                    mma_f16_ts(o_col(b), s_col(b) + half * kHalfKeys + term * 32 + i * 8,
                                values_desc(v_at + buf * Shape::kKv + half * (kHalfKeys * 128) + i * 2048, 16384), kPv,
                                acc || term > 0 || i > 0);
         };
