@@ -794,7 +794,7 @@ def memq_page_plan(cached: torch.Tensor, new_tok: torch.Tensor, block_table: tor
                 and cached.shape == new_tok.shape == kv_len.shape == granted.shape == row
                 and slots.shape == positions.shape == toks and cu_q.shape == (n_seq + 1,)
                 and n_free.shape == n_free_out.shape == one and free_pages.dim() == 1
-                and _here_index() == cached.get_device() == new_tok.get_device() == block_table.get_device()
+                and cached.is_cuda and _here_index() == cached.get_device() == new_tok.get_device() == block_table.get_device()
                 == free_pages.get_device() == n_free.get_device() == kv_len.get_device() == n_free_out.get_device()
                 == cu_q.get_device() == slots.get_device() == positions.get_device() == granted.get_device()
                 and cached.is_contiguous() and new_tok.is_contiguous() and block_table.is_contiguous()
@@ -895,7 +895,7 @@ def memq_kv_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, 
                 and k_cache.dtype is v_cache.dtype is torch.uint8
                 and k_cache.shape == v_cache.shape == (pages, n_kv, page_size, d)
                 and k_scales.dtype is v_scales.dtype is torch.float32 and k_scales.shape == v_scales.shape == plane
-                and _here_index() == k.get_device() == v.get_device() == slots.get_device() == k_cache.get_device()
+                and k.is_cuda and _here_index() == k.get_device() == v.get_device() == slots.get_device() == k_cache.get_device()
                 == v_cache.get_device() == k_scales.get_device() == v_scales.get_device()
                 and slots.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
                 and k_scales.is_contiguous() and v_scales.is_contiguous())
@@ -934,7 +934,7 @@ def memq_kv_cache_read(cache: torch.Tensor, scales: torch.Tensor, slots: torch.T
         kind = _DTYPES.get(out.dtype)
         fits = (kind is not None and cache.dtype is torch.uint8 and scales.dtype is torch.float32
                 and scales.shape == (pages, n_kv, page_size // 16) and slots.dtype is torch.int32
-                and out.shape == (n, n_kv, d) and _here_index() == cache.get_device() == scales.get_device()
+                and out.shape == (n, n_kv, d) and cache.is_cuda and _here_index() == cache.get_device() == scales.get_device()
                 == slots.get_device() == out.get_device() and cache.is_contiguous() and scales.is_contiguous()
                 and slots.is_contiguous() and out.is_contiguous())
     except (AttributeError, TypeError, ValueError):
@@ -994,8 +994,8 @@ def memq_attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         n_seq, max_pages = block_table.shape
         stride, plane = q.stride(), (pages, n_kv, page_size // 16)
         q_kind, o_kind = _DTYPES.get(q.dtype), _DTYPES.get(out.dtype)
-        dev = _here_index()
-        fits = (q_kind is not None and o_kind is not None and nh > 0 and d > 1 and stride[2] == 1 and stride[1] == d
+        dev = _here_index() if q.is_cuda else -1
+        fits = (dev >= 0 and q_kind is not None and o_kind is not None and nh > 0 and d > 1 and stride[2] == 1 and stride[1] == d
                 and out.shape == q.shape and k_cache.dtype is v_cache.dtype is torch.uint8
                 and k_cache.shape == v_cache.shape == (pages, n_kv, page_size, d)
                 and k_scales.dtype is v_scales.dtype is f32 and k_scales.shape == v_scales.shape == plane

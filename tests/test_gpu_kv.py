@@ -634,3 +634,131 @@ def test_plan_refusals(memq):
         with pytest.raises(memq.MemqError):
             run(cached, new, table, free, n_free, page, 4)
     assert memq.memq_device_fault() == 0
+
+
+# ------------------------------------------------------------------------------- the calls together
+class Model:
+    """One attention layer between random projections: what a serving step computes around the calls."""
+
+    def __init__(self, rng, nh, n_kv, d, vocab):
+        self.nh, self.n_kv, self.d = nh, n_kv, d
+        self.emb = to_dev(rng.normal(0, 1, (vocab, 96)).astype(np.float32))
+        self.w = to_dev((rng.normal(0, 1, (96, (nh + 2 * n_kv) * d)) / 10).astype(np.float32))
+        self.head = to_dev((rng.normal(0, 1, (nh * d, vocab)) / np.sqrt(d)).astype(np.float32))
+
+    def qkv(self, tokens, positions):
+        x = self.emb[tokens.long()] + torch.sin(0.3 * positions.float())[:, None]
+        y = (x @ self.w).view(-1, self.nh + 2 * self.n_kv, self.d)
+        return y[:, :self.nh], y[:, self.nh:self.nh + self.n_kv], y[:, self.nh + self.n_kv:]
+
+
+def test_serving_steps(memq):
+    """Prompts, decodes, rejected drafts, a finished and a replaced request, over a pool that is nearly full:
+    plan, append, attention and sampling, each against its reference on the state as it was."""
+    rng = np.random.default_rng(30)
+    nh, n_kv, d, page, vocab, n = 6, 2, 64, 16, 500, 5
+    model, pages, max_pages = Model(rng, nh, n_kv, d, vocab), 40, 12
+    pool = Pool(rng, pages, n_kv, page, d)
+    kc, vc, ks, vs = pool.device()
+    table, free = np.full((n, max_pages), -1, np.int64), rng.permutation(pages).astype(np.int64)
+    state = [to_dev(x.astype(np.int32)) for x in (table, free)]
+    kv, n_free = torch.zeros(n, dtype=torch.int32, device="cuda"), to_dev(np.array([pages], np.int32))
+    steps = [([0] * n, [37, 0, 90, 5, 16]),                    # prompts
+             ([37, 0, 90, 5, 16], [1, 1, 4, 1, 1]),             # decodes, one with drafts
+             ([38, 1, 92, 6, 0], [1, 1, 4, 1, 0]),              # two drafts rejected, one finished
+             ([39, 2, 96, 0, 0], [1, 30, 1, 20, 150]),          # a prompt's chunk, one replaced, one new
+             ([40, 32, 97, 20, 150], [1, 1, 1, 1, 1])]
+    kv_host, left = np.zeros(n, np.int64), pages
+    for keep, new in steps:
+        n_tok = sum(new) + 3
+        args = [to_dev(np.array(x, np.int32)) for x in (new, keep)]
+        before = kv_host.copy()
+        slots, pos, cu, kv2, ok, _ = memq.memq_page_plan(kv, args[0], state[0], state[1], n_free, page, n_tok, keep=args[1],
+                                                         kv_len=kv, n_free_out=n_free)
+        s, p, c, kv_host, granted, left = ref.plan(before, np.array(keep), np.array(new), table, free, left, page, n_tok)
+        for got, want in ((slots, s), (pos, p), (cu, c), (kv, kv_host), (ok, granted), (state[0], table), (state[1], free),
+                          (n_free, [left])):
+            assert np.array_equal(got.cpu().numpy(), want)
+        assert granted.all()
+
+        tokens = to_dev(rng.integers(0, vocab, n_tok).astype(np.int32))
+        q, k, v = model.qkv(tokens, pos)
+        memq.memq_kv_cache_append(k, v, slots, kc, vc, ks, vs)
+        ref.append(k.cpu().numpy(), v.cpu().numpy(), s, pool.codes, pool.scales, page)
+        for got, want in zip((kc, vc, ks, vs), (*pool.codes, *pool.scales)):
+            assert np.array_equal(got.cpu().numpy(), want)
+
+        out = torch.zeros(n_tok, nh, d, device="cuda")
+        memq.memq_attn_paged(q, kc, vc, ks, vs, state[0], kv, cu, d ** -0.5, out=out)
+        qh, oh = q.cpu().numpy().astype(np.float64), out.double().cpu().numpy()
+        for b in range(n):
+            rows = np.arange(kv_host[b])
+            at = table[b, rows // page] * page + rows % page
+            kb, vb = (ref.values(pool.codes[i], pool.scales[i], at) for i in range(2))
+            scales = pool.scales[1][at // page, :, at % page // 16].astype(np.float64)
+            want, bound = ref.attend(qh[c[b]:c[b + 1]], kb, vb, new[b], d ** -0.5, 2, 2.0 ** -23, scales)
+            assert np.all(np.abs(oh[c[b]:c[b + 1]] - want) <= bound)
+        assert np.all(oh[c[-1]:] == 0)
+
+        live = [b for b in range(n) if new[b]]
+        logits = out.view(n_tok, -1)[cu[1:].long()[live] - 1] @ model.head
+        u = rng.uniform(0, 1, len(live)).astype(np.float32)
+        got = memq.memq_sample(logits, to_dev(u), temperature=torch.full((len(live),), 0.8, device="cuda"),
+                               top_k=torch.full((len(live),), 40, dtype=torch.int32, device="cuda"),
+                               top_p=torch.full((len(live),), 0.9, device="cuda"))
+        for i, t in enumerate(got.tolist()):
+            assert t in ref.sample(logits[i].cpu().numpy(), np.float32(0.8), 40, float(np.float32(0.9)), 0.0, float(u[i]))
+    assert memq.memq_device_fault() == 0
+
+
+def test_captured_decode_loop(memq):
+    """A decode step captured once: lengths, block tables, slots, tokens and the draw move on with every replay;
+    the same steps launched one by one give the same tokens and the same cache."""
+    rng = np.random.default_rng(31)
+    nh, n_kv, d, page, vocab, n, pages = 8, 2, 128, 16, 900, 7, 64
+    model = Model(rng, nh, n_kv, d, vocab)
+    us = to_dev(rng.uniform(0, 1, (40, n)).astype(np.float32))
+    ws = torch.empty(memq.memq_attn_paged_workspace(d), dtype=torch.uint8, device="cuda")
+    order = rng.permutation(pages).astype(np.int32)
+
+    def fresh():
+        kc, vc = (torch.zeros(pages, n_kv, page, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros(pages, n_kv, 1, device="cuda") for _ in range(2))
+        i = dict(dtype=torch.int32, device="cuda")
+        return dict(kc=kc, vc=vc, ks=ks, vs=vs, table=torch.full((n, 8), -1, **i), free=to_dev(order),
+                    n_free=torch.full((1,), pages, **i), kv=torch.zeros(n, **i), new=torch.ones(n, **i),
+                    slots=torch.empty(n, **i), pos=torch.empty(n, **i), cu=torch.empty(n + 1, **i),
+                    ok=torch.empty(n, **i), tok=torch.arange(n, **i), u=us[0].clone(), out=torch.empty(n, nh, d, device="cuda"),
+                    topp=torch.full((n,), 0.95, device="cuda"))
+
+    def step(s):
+        memq.memq_page_plan(s["kv"], s["new"], s["table"], s["free"], s["n_free"], page, n, kv_len=s["kv"],
+                            n_free_out=s["n_free"], cu_q=s["cu"], slots=s["slots"], positions=s["pos"], granted=s["ok"])
+        q, k, v = model.qkv(s["tok"], s["pos"])
+        memq.memq_kv_cache_append(k, v, s["slots"], s["kc"], s["vc"], s["ks"], s["vs"])
+        memq.memq_attn_paged(q, s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["kv"], s["cu"], d ** -0.5, out=s["out"],
+                             workspace=ws)
+        memq.memq_sample(s["out"].view(n, -1) @ model.head, s["u"], top_p=s["topp"], out=s["tok"])
+
+    a, b = fresh(), fresh()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        warm = fresh()
+        step(warm)
+    torch.cuda.current_stream().wait_stream(st)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(a)
+    tokens = []
+    for i in range(40):
+        a["u"].copy_(us[i])
+        g.replay()
+        b["u"].copy_(us[i])
+        step(b)
+        assert torch.equal(a["tok"], b["tok"]) and torch.equal(a["out"], b["out"])
+        tokens.append(a["tok"].tolist())
+    assert a["kv"].tolist() == [40] * n and a["n_free"].item() == pages - 3 * n
+    assert all(torch.equal(a[x], b[x]) for x in ("kc", "vc", "ks", "vs", "table", "free", "slots"))
+    assert len({tuple(t) for t in tokens}) > 20
+    assert memq.memq_device_fault() == 0
