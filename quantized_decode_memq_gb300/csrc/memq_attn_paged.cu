@@ -378,12 +378,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
+                // f32 queries: the tensor cores' sums lose a bit with each step, so the halves of the row and the remainders
+                // are summed apart.
+                float upper[4] = {0.f, 0.f, 0.f, 0.f}, rest[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < kSteps; ++j) {
                     uint32_t b0, b1;
                     e4m3x4_to_f16x2x2(w[j], b0, b1);
-                    mma_f16_16816(sc[n], q_hi[j][0], q_hi[j][1], q_hi[j][2], q_hi[j][3], b0, b1);
-                    if (Q2) mma_f16_16816(sc[n], q_lo[Q2 ? j : 0][0], q_lo[Q2 ? j : 0][1], q_lo[Q2 ? j : 0][2], q_lo[Q2 ? j : 0][3], b0, b1);
+                    if constexpr (Q2) {
+                        mma_f16_16816(j < kSteps / 2 ? sc[n] : upper, q_hi[j][0], q_hi[j][1], q_hi[j][2], q_hi[j][3], b0, b1);
+                        mma_f16_16816(rest, q_lo[j][0], q_lo[j][1], q_lo[j][2], q_lo[j][3], b0, b1);
+                    } else {
+                        mma_f16_16816(sc[n], q_hi[j][0], q_hi[j][1], q_hi[j][2], q_hi[j][3], b0, b1);
+                    }
+                }
+                if constexpr (Q2) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[n][i] += upper[i] + rest[i];
                 }
             }
             // ---- their maxima, with the values' scales
@@ -478,8 +489,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     e4m3x4_to_f16x2x2(__byte_perm(w[2][j], w[3][j], 0x7362), hi[2], hi[3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        mma_f16_16816(o[4 * j + i], p_hi[b][0], p_hi[b][1], p_hi[b][2], p_hi[b][3], lo[i], hi[i]);
-                        if (P2) mma_f16_16816(o[4 * j + i], p_lo[P2 ? b : 0][0], p_lo[P2 ? b : 0][1], p_lo[P2 ? b : 0][2], p_lo[P2 ? b : 0][3], lo[i], hi[i]);
+                        if constexpr (P2) {
+                            // f32 outputs: a block's products are summed apart, for the tensor cores truncate as they
+                            // add to a long sum (64 x 16384 keys: thousands of steps)
+                            float t[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_f16_16816(t, p_lo[b][0], p_lo[b][1], p_lo[b][2], p_lo[b][3], lo[i], hi[i]);
+                            mma_f16_16816(t, p_hi[b][0], p_hi[b][1], p_hi[b][2], p_hi[b][3], lo[i], hi[i]);
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) o[4 * j + i][m] += t[m];
+                        } else {
+                            mma_f16_16816(o[4 * j + i], p_hi[b][0], p_hi[b][1], p_hi[b][2], p_hi[b][3], lo[i], hi[i]);
+                        }
                     }
                 }
             }
@@ -722,7 +742,7 @@ bool allow() {
     return cudaFuncSetAttribute(attn_rows_kernel<D, Q2, P2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 smem_bytes(Ring<D>::kBytes)) == cudaSuccess &&
            cudaFuncSetAttribute(attn_tiles_kernel<D, Q2, P2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                TileShape<D, Q2>::kBytes) == cudaSuccess;
+                                TileShape<D, Q2, P2>::kBytes) == cudaSuccess;
 }
 
 // SM count of the current device, after allowing the kernels their shared memory (once per device).
@@ -848,7 +868,7 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const bool q2 = q_dtype == MEMQ_F32, p2 = out_dtype == MEMQ_F32;
-    const Workspace of_rows(runs, kRows, d), of_tiles(grid, q2 ? 128 : 256, d);
+    const Workspace of_rows(runs, kRows, d), of_tiles(grid, q2 || p2 ? 128 : 256, d);
     // One token a sequence, or rows that no sequence can have more of than a warp holds: the stream of keys is
     // all.  (More tokens than sequences may still lie in short ones: each kernel takes its own.)
     const bool rows_only = n_tok <= n_seq || n_tok * a.group <= kRowsKernelMost;
@@ -869,8 +889,12 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
              {attn_tiles_kernel<128, true, false>, attn_tiles_kernel<128, true, true>}}};
         cfg.gridDim = dim3(static_cast<unsigned>(grid));
         cfg.blockDim = dim3(kTileThreads);
-        cfg.dynamicSmemBytes = static_cast<size_t>(d == 128 ? (q2 ? TileShape<128, true>::kBytes : TileShape<128, false>::kBytes)
-                                                            : (q2 ? TileShape<64, true>::kBytes : TileShape<64, false>::kBytes));
+        static constexpr int kTileBytes[2][2][2] = {
+            {{TileShape<64, false, false>::kBytes, TileShape<64, false, true>::kBytes},
+             {TileShape<64, true, false>::kBytes, TileShape<64, true, true>::kBytes}},
+            {{TileShape<128, false, false>::kBytes, TileShape<128, false, true>::kBytes},
+             {TileShape<128, true, false>::kBytes, TileShape<128, true, true>::kBytes}}};
+        cfg.dynamicSmemBytes = static_cast<size_t>(kTileBytes[d == 128][q2][p2]);
         if (cudaLaunchKernelEx(&cfg, kTiles[d == 128][q2][p2], t, fault) != cudaSuccess) return MEMQ_ERR_LAUNCH;
         tiles = JoinPart{t.owner, t.stats, t.part, of_tiles.runs, of_tiles.runs, of_tiles.rows};
     }

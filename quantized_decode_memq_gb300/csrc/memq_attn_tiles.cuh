@@ -56,14 +56,16 @@ __device__ __forceinline__ void set_registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-template <int D, bool Q2>
+template <int D, bool Q2, bool P2>
 struct TileShape {
-    static constexpr int kBlocks = Q2 ? 1 : 2;                  // of 128 rows
+    // Blocks of 128 rows.  f32 queries need the second one's shared memory, f32 outputs its columns: the tensor cores
+    // truncate as they add to a long sum, so the weights' remainders and every other tile have sums of their own
+    // (error of 300 rows over 4000 keys against 64 bits 6.3e-6 with one sum, 1.4e-6 that of f32 arithmetic).
+    static constexpr int kBlocks = Q2 || P2 ? 1 : 2;
     static constexpr int kRows = kBlocks * 128;
     static constexpr int kQ = 2 * 128 * D * 2;                  // two blocks, or two terms of one
     static constexpr int kKv = kTileKeys * D * 2;
     static constexpr int kBytes = kQ + 4 * kKv + static_cast<int>(sizeof(TileControl));
-    static constexpr int kHalves = D / 64;                      // of 64 elements, a swizzled 128-byte row each
 };
 
 __device__ __forceinline__ void tile_sizes(const AttnArgs &a, int rows_per, TileItem &it) {
@@ -314,7 +316,7 @@ __device__ __forceinline__ void stage_queries(const AttnArgs &a, const TileItem 
 
 template <int D, bool Q2, bool P2>
 __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnArgs a, unsigned int *fault) {
-    using Shape = TileShape<D, Q2>;
+    using Shape = TileShape<D, Q2, P2>;
     constexpr int kBlocks = Shape::kBlocks, kRowsPer = Shape::kRows;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31;
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         TileRun run = my_run();
         const int b = warp >> 2, wq = warp & 3, r = b * 128 + wq * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t at_s = s_col(b) + lanes, at_o = o_col(b) + lanes;
+        const uint32_t at_s = s_col(b) + lanes, at_o = o_col(b) + lanes, at_odd = o_col(1) + lanes, at_rest = s_col(1) + lanes;
         uint32_t tile = 0, turns = 0, all_items = 0;
         for (; b < kBlocks && run.more() && !wait.dead; run.next()) {
             const TileItem &it = run.it;
@@ -533,6 +535,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D / 8; ++c) tmem_scale8(at_o + c * 8, by);
+                            if (P2) {
+#pragma unroll 1
+                                for (int c = 0; c < D / 8; ++c) {
+                                    tmem_scale8(at_rest + c * 8, by);
+                                    if (u >= 3) tmem_scale8(at_odd + c * 8, by);  // (its first products are of the third half)
+                                }
+                            }
                         }
                     }
                     float sums[4];
@@ -586,6 +595,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                     float o[32];
                     if (n > 0) {
                         tmem_ld32(at_o + c * 32, o);
+                        if (P2) {
+                            float more[32];
+                            tmem_ld32(at_rest + c * 32, more);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] += more[i];
+                            if (n > 1) {
+                                tmem_ld32(at_odd + c * 32, more);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] += more[i];
+                            }
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0.f;
@@ -709,22 +729,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         const uint32_t q_at = smem_u32(q_smem), k_at = smem_u32(k_smem), v_at = smem_u32(v_smem);
         const auto scores = [&](int b, int half, uint32_t buf) {
 #pragma unroll
-            for (int term = 0; term < (Q2 ? 2 : 1); ++term)
+            for (int term = Q2 ? 1 : 0; term >= 0; --term)  // the remainders first, while the sums are small
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
                     mma_f16_ss(s_col(b) + half * kHalfKeys, smem_desc(q_at + (Q2 ? term : b) * (128 * D * 2) + at, 128),
-                               smem_desc(k_at + buf * Shape::kKv + half * (kHalfKeys * 128) + at, 128), kQk, term > 0 || i > 0);
+                               smem_desc(k_at + buf * Shape::kKv + half * (kHalfKeys * 128) + at, 128), kQk,
+                               (Q2 && term == 0) || i > 0);
                 }
         };
-        const auto outputs = [&](int b, int half, uint32_t buf, bool acc) {
+        const auto outputs = [&](int b, int u, uint32_t buf) {
+            const int half = u & 1;
+            const uint32_t to = P2 ? o_col((u >> 1) & 1) : o_col(b);
+            const bool acc = P2 ? u >= 4 || half : u > 0;
 #pragma unroll
-            for (int term = 0; term < (P2 ? 2 : 1); ++term)
-#pragma unroll
-                for (int i = 0; i < kHalfKeys / 16; ++i)
-                    mma_f16_ts(o_col(b), s_col(b) + half * kHalfKeys + term * 32 + i * 8,
-                               values_desc(v_at + buf * Shape::kKv + half * (kHalfKeys * 128) + i * 2048, 16384), kPv,
-                               acc || term > 0 || i > 0);
+            for (int i = 0; i < kHalfKeys / 16; ++i) {
+                const uint64_t v = values_desc(v_at + buf * Shape::kKv + half * (kHalfKeys * 128) + i * 2048, 16384);
+                const uint32_t p = s_col(b) + half * kHalfKeys + i * 8;
+                mma_f16_ts(to, p, v, kPv, acc || i > 0);
+                if (P2) mma_f16_ts(s_col(1), p + 32, v, kPv, u > 0 || i > 0);
+            }
         };
         if (elect_one()) {
             // One thread from here on: a branch that ptxas knows to have one keeps descriptors in uniform registers, and its
@@ -758,7 +782,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                         ready(&ctl->weights[b][half], (turns[b] + j) & 1);
                         if (ready.dead) break;
                         tc_fence_after();
-                        outputs(b, half, buf, u > 0);
+                        outputs(b, u, buf);
                         if (more) scores(b, half, next & 1);
                         tc_commit(&ctl->scores[b][half]);  // behind the last scores: of the products alone
                     }
