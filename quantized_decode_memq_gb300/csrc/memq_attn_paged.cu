@@ -47,14 +47,6 @@ struct Ring {
     static constexpr int kBytes = kWarps * kWarpBytes;
 };
 
-struct Control {
-    uint64_t full[kWarps][6];
-    long long warp_sum[kWarps];
-    int warp_items[kWarps];
-};
-
-__host__ __device__ constexpr int smem_bytes(int ring) { return ring + 1024 + static_cast<int>(sizeof(Control)); }
-
 __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
 
 // 16 query rows of a (sequence, kv head) and their part of a run.
@@ -104,6 +96,15 @@ struct RowItem {
         sizes(a, run_hi);
     }
 };
+
+struct Control {
+    uint64_t full[kWarps][6];
+    long long warp_sum[kWarps];
+    int warp_items[kWarps];
+    RowItem next[kWarps];  // of each warp
+};
+
+__host__ __device__ constexpr int smem_bytes(int ring) { return ring + 1024 + static_cast<int>(sizeof(Control)); }
 
 template <int D, bool Q2, bool P2>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -258,11 +259,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i = 2 * (next_send - win);
             send(__shfl_sync(kFullMask, row_now, i), __shfl_sync(kFullMask, row_now, i + 1));
         }
-        // The item behind this one: its first tiles are sent as soon as this one's are.
-        RowItem next = it;
-        next.advance(a, run_hi);
-        int row_then = -1, page_then = -1, sent_then = 0;
-        if (next.live) page_then = page_of(next, 0);
+        // The item behind this one: its first tiles are sent as soon as this one's are.  It waits in shared memory.
+        int row_then = -1, page_then = -1, sent_then = 0, most_then = 0;
+        {
+            RowItem next = it;
+            next.advance(a, run_hi);
+            if (next.live) {
+                page_then = page_of(next, 0);
+                most_then = min(next.t1, kWindow);
+            }
+            __syncwarp();
+            if (lane == 0) ctl->next[warp] = next;
+            __syncwarp();
+        }
 
         // ---- the query rows
         uint32_t q_hi[kSteps][4], q_lo[Q2 ? kSteps : 1][4];
@@ -331,12 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 2; ++k) lim[k] = min(vis, max(0, it.s.kv - it.s.t + (row0 + g + 8 * k) / a.group + 1));
         int row_next = row_of(it, page_next, win + kWindow);
         float ks_next = scale_at(a.k_scales, row_next), vs_next = scale_at(a.v_scales, row_next);
-        if (next.live) row_then = row_of(next, page_then, 0);
+        if (most_then) row_then = row_of(ctl->next[warp], page_then, 0);
         const auto send_then = [&]() {
             const int i = 2 * sent_then++;
             send(__shfl_sync(kFullMask, row_then, i), __shfl_sync(kFullMask, row_then, i + 1));
         };
-        const int most_then = next.live ? min(next.t1, kWindow) : 0;
         while (next_send >= t1 && sent_then < most_then && sent - taken < kStages) send_then();
 
         for (int tile = off; tile < t1; ++tile) {
@@ -378,23 +386,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
-                // f32 queries: the tensor cores' sums lose a bit with each step, so the halves of the row and the remainders
-                // are summed apart.
-                float upper[4] = {0.f, 0.f, 0.f, 0.f}, rest[4] = {0.f, 0.f, 0.f, 0.f};
+                // f32 queries: the tensor cores' sums lose a bit with each step, so the remainders come first, while the sum
+                // is small, and the row's halves are summed apart.
+                if constexpr (Q2) {
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) {
+                        uint32_t b0, b1;
+                        e4m3x4_to_f16x2x2(w[j], b0, b1);
+                        mma_f16_16816(sc[n], q_lo[j][0], q_lo[j][1], q_lo[j][2], q_lo[j][3], b0, b1);
+                    }
+                }
+                float upper[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < kSteps; ++j) {
                     uint32_t b0, b1;
                     e4m3x4_to_f16x2x2(w[j], b0, b1);
-                    if constexpr (Q2) {
-                        mma_f16_16816(j < kSteps / 2 ? sc[n] : upper, q_hi[j][0], q_hi[j][1], q_hi[j][2], q_hi[j][3], b0, b1);
-                        mma_f16_16816(rest, q_lo[j][0], q_lo[j][1], q_lo[j][2], q_lo[j][3], b0, b1);
-                    } else {
-                        mma_f16_16816(sc[n], q_hi[j][0], q_hi[j][1], q_hi[j][2], q_hi[j][3], b0, b1);
-                    }
+                    mma_f16_16816(Q2 && j >= kSteps / 2 ? upper : sc[n], q_hi[j][0], q_hi[j][1], q_hi[j][2], q_hi[j][3], b0, b1);
                 }
                 if constexpr (Q2) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[n][i] += upper[i] + rest[i];
+                    for (int i = 0; i < 4; ++i) sc[n][i] += upper[i];
                 }
             }
             // ---- their maxima, with the values' scales
@@ -572,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             own.rows = whole ? 0 : n_rows;
             a.owner[a.by_item ? it.index : run] = own;
         }
-        it = next;
+        it = ctl->next[warp];
         row_now = row_then;
         early = sent_then;
     }
