@@ -16,6 +16,10 @@ namespace memq {
 constexpr unsigned int kAttnFaultWait = 64;   // a bounded wait expired
 constexpr unsigned int kAttnFaultInput = 32;  // a length or page index was out of range
 
+namespace {
+__device__ unsigned int g_attn_fault = 0;  // (one translation unit includes this)
+}
+
 constexpr int kAttnBlock = 16;  // keys that share a scale
 constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxCached = 1 << 30;  // rows a sequence
@@ -73,9 +77,9 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int c0, int c1, i
 }
 
 // The pool's row, among all pages and heads, of key `key` of a sequence whose page it lies in.
-__device__ __forceinline__ int attn_row(const AttnArgs &a, int page, int head, int key, unsigned int *fault) {
+__device__ __forceinline__ int attn_row(const AttnArgs &a, int page, int head, int key) {
     if (page < 0 || page >= a.n_pages) {
-        atomicOr(fault, kAttnFaultInput);
+        atomicOr(&g_attn_fault, kAttnFaultInput);
         page = 0;
     }
     return ((page * a.n_kv + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));

@@ -3,13 +3,21 @@
 // A CTA serves 128 or 256 rows (heads of a group, times tokens) of one kv head, 128 keys a time:
 //   S [128 rows x 128 keys] = Q [128 x d] . K^T     kind::f16, both from shared memory
 //   O [128 rows x d]       += P [128 x 128] . V     P from TMEM, where it takes the place of its scores
-// Both products are f16: the codes are widened to f16 in shared memory (which they cost 64 KB of writes a
-// tile, against 2 x 192 KB that the products read), the query rows and the weights rounded to it.  Two blocks of 128
-// rows take turns: while the weights of one are formed, the tensor cores serve the other.
+// Both products are f16: the codes are widened to f16 in shared memory (64 KB of writes a tile, against 256 KB that the
+// products read), the query rows and the weights rounded to it.  Two blocks of 128 rows take turns, and a block's
+// scores are formed in halves of 64 keys with columns of their own: while the weights of one half are formed, the
+// tensor cores run the products of the others.  (With one set of columns a block: 1170 us where this takes 865.)
 //
 // Warps 0-3 and 4-7 form the weights of the two blocks, a thread a row, so that a row's maximum and sum need no
 // exchange; warps 8-11 and 13-15 load codes of keys and of values, a tile ahead in registers, and widen them; one thread
-// of warp 12 issues the products.  An f32 query has two terms, two products, and its 128 rows the shared memory of 256.
+// of warp 12 issues the products, and waits for itself (as a warp with votes: 1090).  An f32 query has two terms, two
+// products, and its 128 rows the shared memory of 256.
+//
+// What bounds it, of 2048 tokens over 16384 rows with 64 query and 8 kv heads of 128 (865 us, 1.19 PFLOP/s, 63% of the
+// measured bf16 peak): a half's weights take a warp some 1000 cycles besides 500 of waits and hand-over (two warps a
+// scheduler: 64 exp2 each are 512), the tensor cores 640 a block and half (QK^T as m128n64 is bound by shared memory, 48
+// cycles an instruction); no part alone explains the rest: without exp2, widening, loads and 7 of 8 products it still
+// takes 80% of the time.
 #pragma once
 
 #include <type_traits>
@@ -20,7 +28,8 @@ namespace memq {
 
 constexpr int kTileKeys = 128, kHalfKeys = 64;
 constexpr int kTileThreads = 16 * 32;
-// Registers a thread: 128 at launch; the two warpgroups that hold scores take 168, the others give theirs.
+// Registers a thread: 128 at launch; the two warpgroups that hold scores take 152, the others give theirs
+// (168 and 88 spill in the others: 192 bytes of stack).
 constexpr int kRegsWeights = 152, kRegsOthers = 104;
 static_assert(2 * kRegsWeights + 2 * kRegsOthers <= 4 * 128, "a split beyond the launch's registers never comes");
 constexpr int kWidenWarp = 8, kIssueWarp = 12;
@@ -194,20 +203,18 @@ __device__ __forceinline__ void tmem_scale8(uint32_t addr, float by) {
 
 // Waits for a barrier phase; after one wait expired, none is made any more, and the fault word says so.
 struct AttnWaiter {
-    unsigned int *fault;
     bool dead = false;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
         if (dead || __all_sync(kFullMask, mbar_test(bar, parity))) return;
         if (!warp_wait_bounded(bar, parity)) {
             dead = true;
-            if ((threadIdx.x & 31) == 0) atomicOr(fault, kAttnFaultWait);
+            if ((threadIdx.x & 31) == 0) atomicOr(&g_attn_fault, kAttnFaultWait);
         }
     }
 };
 
 // The same for a single thread.
 struct AttnThreadWaiter {
-    unsigned int *fault;
     bool dead = false;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
         if (dead || mbar_test(bar, parity)) return;
@@ -215,7 +222,7 @@ struct AttnThreadWaiter {
         while (!mbar_try_wait(bar, parity)) {
             if (clock64() - t0 > kWaitCycles) {
                 dead = true;
-                atomicOr(fault, kAttnFaultWait);
+                atomicOr(&g_attn_fault, kAttnFaultWait);
                 return;
             }
         }
@@ -315,7 +322,7 @@ __device__ __forceinline__ void stage_queries(const AttnArgs &a, const TileItem 
 }
 
 template <int D, bool Q2, bool P2>
-__global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnArgs a, unsigned int *fault) {
+__global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnArgs a) {
     using Shape = TileShape<D, Q2, P2>;
     constexpr int kBlocks = Shape::kBlocks, kRowsPer = Shape::kRows;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         if (b >= a.n_seq) break;
         const int c0 = __ldcg(a.cu_q + b), c1 = __ldcg(a.cu_q + b + 1), kv = __ldcg(a.kv_len + b);
         if (c0 < 0 || c0 > c1 || c1 > a.n_tok || kv < 0 || kv > (static_cast<long long>(a.max_pages) << a.page_shift))
-            atomicOr(fault, kAttnFaultInput);
+            atomicOr(&g_attn_fault, kAttnFaultInput);
         descends = descends || c0 > c1;
         const AttnSeq s = attn_seq(a, c0, c1, kv);
         const int rows = s.t * a.group;
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
     const auto s_col = [&](int b) { return tmem + static_cast<uint32_t>(b) * 128; };
     const auto o_col = [&](int b) { return tmem + 256 + static_cast<uint32_t>(b) * 128; };
 
-    AttnWaiter wait{fault};
+    AttnWaiter wait;
     const auto my_run = [&]() {
         TileRun run{a, kRowsPer, run_hi};
         if (run_lo < run_hi) run.start(ctl->first, ctl->first_off, ctl->first_pos);
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
             };
             const auto base_at = [&](int page, int j) -> int {
                 const int key = j * kTileKeys + (lane & 7) * kAttnBlock;
-                return j < run.t1 && key < it.vis ? attn_row(a, page, it.head, key, fault) : -1;
+                return j < run.t1 && key < it.vis ? attn_row(a, page, it.head, key) : -1;
             };
             const auto scale_at = [&](const float *scales, int base) {
                 return scaling && base >= 0 ? __ldcg(scales + (base >> 4)) : 1.f;
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         if (elect_one()) {
             // One thread from here on: a branch that ptxas knows to have one keeps descriptors in uniform registers, and its
             // waits need no votes.
-            AttnThreadWaiter ready{fault};
+            AttnThreadWaiter ready;
             TileRun run = my_run();
             uint32_t tile = 0, turns[2] = {0, 0}, all_items = 0;
             for (; run.more() && !ready.dead; run.next()) {

@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     Scale s;
     s.top = unorder_bits(top_key);
     {
-        const float t = fmaxf(temperature, 1e-30f), kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;
+        const float t = fminf(fmaxf(temperature, 1e-30f), 1e30f), kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;
         s.hi = __fdiv_rn(kLog2e, t);
         s.lo = __fdiv_rn(__fmaf_rn(-s.hi, t, kLog2e) + kLog2eLo, t);
     }

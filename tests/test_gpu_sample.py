@@ -114,6 +114,7 @@ def test_borders_of_the_settings(memq):
         assert int(got[r]) in ref.sample(x[r], 1.0, 0, 1.0, 0.0, float(n(u)[r]))
     base = rng.uniform(0, 1, 8)
     for name, odd, plain in (("temperature", [nan, -1, 0, -inf], 0.0), ("top_p", [nan, 1, 7, inf], 1.0),
+                             ("temperature", [inf, 1e30, 3e38, inf], 1e30), ("temperature", [1e-30, 1e-45, 1e-38, 1e-31], 1e-30),
                              ("min_p", [nan, -1, 0, -inf], 0.0), ("min_p", [1, 2, inf, 1.0000001], 1.0),
                              ("top_p", [0, -1, -inf, -0.0], 0.0), ("top_k", [0, -5, 700, 10 ** 9], 0)):
         t = np.int32 if name == "top_k" else np.float32
