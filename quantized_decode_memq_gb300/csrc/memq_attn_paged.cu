@@ -608,7 +608,8 @@ struct JoinPart {
     const AttnOwner *owner;
     const float2 *stats;
     const float *part;
-    int x, runs, stride;  // owners to look at, runs, rows of a piece
+    int x, share;      // owners to look at, CTAs for each
+    int runs, stride;  // runs, rows of a piece
 };
 
 template <int D>
@@ -619,10 +620,11 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, c
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool of_tiles = static_cast<int>(blockIdx.x) < tiles.x;
-    const JoinPart &p = of_tiles ? tiles : rows;
-    const int runs = p.runs, stride = p.stride;
-    const int4 *at = reinterpret_cast<const int4 *>(p.owner + blockIdx.x - (of_tiles ? 0 : tiles.x));
+    const int of_tiles = tiles.x * tiles.share, cta = static_cast<int>(blockIdx.x);
+    const JoinPart &p = cta < of_tiles ? tiles : rows;
+    const int runs = p.runs, stride = p.stride, in_part = cta < of_tiles ? cta : cta - of_tiles;
+    const int y = in_part % p.share;  // of the item's CTAs
+    const int4 *at = reinterpret_cast<const int4 *>(p.owner + in_part / p.share);
     const int4 raw[2] = {__ldcg(at), __ldcg(at + 1)};
     const AttnOwner owner = *reinterpret_cast<const AttnOwner *>(raw);
     if (owner.rows == 0) return;
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, c
         }
     };
     if (parts <= kFewParts) {
-        for (int r = blockIdx.y * kWarps + warp; r < owner.rows; r += gridDim.y * kWarps) {
+        for (int r = y * kWarps + warp; r < owner.rows; r += p.share * kWarps) {
             float2 st = make_float2(kAttnUnset, 0.f);
             if (lane < parts) st = __ldcg(p.stats + slot_of(lane, r));
             const float w = ex2(st.x - warp_max(st.x)), total = warp_sum(st.y * w);
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, c
         }
         return;
     }
-    for (int r = blockIdx.y; r < owner.rows; r += gridDim.y) {
+    for (int r = y; r < owner.rows; r += p.share) {
         float top = kAttnUnset;
         for (int k = tid; k < parts; k += kThreads) top = fmaxf(top, __ldcg(p.stats + slot_of(k, r)).x);
         top = warp_max(top);
@@ -907,7 +909,7 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
              {TileShape<128, true, false>::kBytes, TileShape<128, true, true>::kBytes}}};
         cfg.dynamicSmemBytes = static_cast<size_t>(kTileBytes[d == 128][q2][p2]);
         if (cudaLaunchKernelEx(&cfg, kTiles[d == 128][q2][p2], t) != cudaSuccess) return MEMQ_ERR_LAUNCH;
-        tiles = JoinPart{t.owner, t.stats, t.part, of_tiles.runs, of_tiles.runs, of_tiles.rows};
+        tiles = JoinPart{t.owner, t.stats, t.part, of_tiles.runs, 16, of_tiles.runs, of_tiles.rows};
     }
     of_rows.place(a, static_cast<uint8_t *>(workspace));
     using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const AttnArgs, const int);
@@ -920,10 +922,10 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(d == 128 ? Ring<128>::kBytes : Ring<64>::kBytes));
     if (cudaLaunchKernelEx(&cfg, kKernels[d == 128][q2][p2], k_map, v_map, a, box) != cudaSuccess) return MEMQ_ERR_LAUNCH;
-    const JoinPart rows{a.owner, a.stats, a.part, a.by_item ? static_cast<int>(items_of(kRows)) : runs, runs, kRows};
-    // about eight CTAs an SM over all
-    const unsigned x = static_cast<unsigned>(tiles.x + rows.x);
-    cfg.gridDim = dim3(x, std::max(tiles.x ? 4u : 1u, std::min(16u, 8u * static_cast<unsigned>(grid) / x)));
+    // about eight CTAs an SM over the row kernel's items, 16 rows or fewer a CTA of the other's
+    const int x = a.by_item ? static_cast<int>(items_of(kRows)) : runs;
+    const JoinPart rows{a.owner, a.stats, a.part, x, std::max(1, std::min(kRows, 8 * grid / x)), runs, kRows};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles.x * tiles.share + rows.x * rows.share));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, a, tiles, rows) == cudaSuccess
