@@ -486,9 +486,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
                 ++all_items;
             }
             if (mine && n > 0) {
-                const float factor = ctl->factor[r];
                 const int see0 = it.s.kv - it.s.t + 1;
                 const int lim = min(it.vis, max(0, see0 + (it.row0 + r) / a.group));
+                const float factor = lim > 0 ? ctl->factor[r] : 1.f;  // of no keys there is no NaN, whatever the query is
                 const int all_see = max(0, see0 + (it.row0 + b * 128) / a.group);
                 // Half a tile a time: a half's scores have their own columns, so that the products of the next half
                 // run meanwhile.

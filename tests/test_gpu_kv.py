@@ -335,6 +335,19 @@ def test_not_finite_rows_reach_only_who_sees_them(memq, t):
     assert np.all(np.abs(got - want)[1, 3] <= bound[1, 3]) and np.all(np.abs(got - want)[1, :2] <= bound[1, :2])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t", [7, 60])
+def test_not_finite_queries_without_keys(memq, t, dtype):
+    """Tokens that see no row give zeros, whatever their queries hold."""
+    b = Batch([(t, t - 5), (t, 0)], 8, 2, 64, 16, dtype, seed=23)
+    want, bound = b.reference()
+    b.q[:5], b.q[1, ::2], b.q[t:] = np.nan, np.inf, -np.inf
+    got = b.run(memq).double().cpu().numpy()
+    assert np.all(got[:5] == 0) and np.all(got[t:] == 0)
+    assert np.all(np.abs(got - want)[5:t] <= bound[5:t])
+    assert memq.memq_device_fault() == 0
+
+
 def test_queries_that_are_parts_of_a_projection(memq):
     for dtype in (torch.float32, torch.bfloat16):
         b = Batch([(3, 40), (50, 80)], 8, 2, 128, 16, dtype, seed=17)
