@@ -59,6 +59,7 @@ struct AttnArgs {
     int rows_from, rows_to;  // sequences with t * group in this range are served
     int out_bf16;
     int by_item;  // owners are noted by item, not by run
+    int behind_tiles;  // the launch before this one is the other kernel's, of the same call
     float scale_log2;
 };
 

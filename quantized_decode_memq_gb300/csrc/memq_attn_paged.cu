@@ -129,7 +129,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kStages; ++i) mbar_init(&ctl->full[w][i], 1);
         mbar_init_fence();
     }
-    griddep_wait();
+    // The tensor-core kernel lets this one start when all of its CTAs are past their own wait, so what came before is
+    // there; nothing is taken from it or written where it writes.  This kernel's end still waits for it: the join
+    // waits for this one alone.
+    if (!a.behind_tiles) griddep_wait();
 
     // ------------------------------------------------------------------ the runs
     int4 *seqs = reinterpret_cast<int4 *>(smem);                            // (start, t, kv, items before)
@@ -216,7 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Owners are noted by run, or, where there are no more items than runs, by item: every item has one run that
     // serves its first tile.
     if (lane == 0 && (!a.by_item || nothing || run >= all_items)) a.owner[run].rows = 0;
-    if (!it.live) return;
+    if (!it.live) {
+        griddep_wait();
+        return;
+    }
 
     uint32_t sent = 0, taken = 0;  // tiles of the ring
     bool dead = false;
@@ -596,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = taken; i != sent; ++i)
             (void)warp_wait_bounded(&ctl->full[warp][i % kStages], (i / kStages) & 1);
     }
+    griddep_wait();
 }
 
 // Adds the pieces of the items that several runs shared, in the runs' order.  CTAs (x, 0 .. gridDim.y - 1) serve the
@@ -894,6 +901,7 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
         t.by_item = false;
         of_tiles.place(t, static_cast<uint8_t *>(workspace) + of_rows.bytes());
         a.rows_to = kRowsKernelMost;
+        a.behind_tiles = true;
         using Tiles = void (*)(const AttnArgs);
         static constexpr Tiles kTiles[2][2][2] = {
             {{attn_tiles_kernel<64, false, false>, attn_tiles_kernel<64, false, true>},

@@ -331,7 +331,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
     uint8_t *q_smem = smem, *k_smem = smem + Shape::kQ, *v_smem = k_smem + 2 * Shape::kKv;
     TileControl *ctl = reinterpret_cast<TileControl *>(v_smem + 2 * Shape::kKv);
 
-    griddep_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->k_full[i], 4);
@@ -349,6 +348,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
     }
     if (warp == kIssueWarp) tmem_alloc(&ctl->tmem, 512);
     griddep_wait();
+    griddep_launch_dependents();  // behind the wait: the row kernel may start on what this one may
 
     // ------------------------------------------------------------------ this CTA's run of tiles
     // Blocks of rows before each sequence; then a thread counts the tiles of a slice of the blocks.
