@@ -35,16 +35,18 @@
 namespace memq {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 32;  // of a CTA: 512 threads, or 1024
 constexpr int kMaxCtas = 8;
 constexpr int kCap = 2048;   // tokens that are sorted
 constexpr int kBins = 1536, kPerOctave = 64;  // steps of x, up to kCareful
 constexpr int kTable = 512;
-constexpr int kMine = kBins / kThreads;  // steps a thread adds up, where a row has one CTA
 constexpr int kUnitLog = 44;  // weights are integers in units of 2^-44
 constexpr uint32_t kLeastKey = 0x007fffffu;  // of -infinity; NaN has key 0
 constexpr int64_t kMaxVocab = 360000;
+// bf16 logits: a table of the weights of ten binades of values, of either sign.
+constexpr uint32_t kHalf = 10 * 128, kValues = 2 * kHalf;
+constexpr int kTabled = 8192;   // tokens of a CTA from which it pays
+constexpr int kNoStep = 0x7ff;  // in an entry: x is kCareful or more
 
 // 2^(-j / 512) in units of 2^-62, formed by the compiler: the 512th root of 1/2 by nine square roots, then its powers.
 struct Powers {
@@ -83,20 +85,24 @@ struct SampleArgs {
 
 struct __align__(16) Shared {
     unsigned long long table[kTable];           // g_powers
-    unsigned long long list[kCap];              // tokens: key << 32 | ~index; sorted, largest first
     union {
-        unsigned long long weight[kCap];        // of the list
         struct {
+            unsigned long long list[kCap];      // tokens: key << 32 | ~index; sorted, largest first
+            unsigned long long weight[kCap];    // of the list
+        };
+        struct {
+            unsigned long long value[kValues];  // step << 48 | weight
             uint32_t lo[kBins], hi[kBins];      // weight of the steps of x
         } steps;
     };
-    unsigned long long sums[kMaxCtas][kWarps];  // of every CTA's warps
+    unsigned long long sums[kMaxCtas][kMaxWarps];  // of every CTA's warps
     unsigned long long pair[kMaxCtas][2];
-    unsigned long long warp64[2][kWarps];
+    unsigned long long partial[kMaxCtas];       // weight of what every CTA keeps of the step that holds the cut
+    unsigned long long warp64[2][kMaxWarps];
     unsigned long long cut;      // place of the last token that is kept
     unsigned long long before;   // weight ahead of the step that holds the cut
     uint32_t from_cta[kMaxCtas], bounds[kMaxCtas];
-    uint32_t warp32[kWarps];
+    uint32_t warp32[kMaxWarps];
     uint32_t count;              // tokens in the first CTA's list
     uint32_t found;
     int step;
@@ -195,6 +201,68 @@ __device__ __forceinline__ void weights_of(const Scale &s, const unsigned long l
     }
 }
 
+__device__ __forceinline__ int step_of(float x) { return static_cast<int>(x * kPerOctave); }
+
+// Few bf16 numbers lie between the largest logit and 24 octaves of weight below it: their weights and steps are formed
+// once a row and looked up (60 instructions a token and pass otherwise).
+struct Values {
+    uint32_t base;  // the least magnitude's bits
+    bool on;
+};
+__device__ __forceinline__ unsigned long long entry_of(const Scale &s, const unsigned long long *table, float l) {
+    const float x = coarse(s, l);
+    if (!(x < 60.f)) return static_cast<unsigned long long>(kNoStep) << 48;  // NaN, too
+    return static_cast<unsigned long long>(x < kCareful ? step_of(x) : kNoStep) << 48 | weight_of(s, table, l);
+}
+template <int T>
+__device__ __forceinline__ Values make_values(const Scale &s, Shared &sh, bool on) {
+    Values v;
+    const float far = fmaxf(fabsf(s.top), fabsf(s.top - __fdiv_rn(kCareful, s.hi)));
+    v.on = on && far < 0x1p100f;
+    v.base = static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(far) >> 23) - 9, 0)) << 7;
+    if (v.on)
+        for (uint32_t i = threadIdx.x; i < kValues; i += T) {
+            const uint32_t sign = i >= kHalf, bits = sign << 31 | (v.base + i - sign * kHalf) << 16;
+            const float l = __uint_as_float(bits) + 0.f;
+            sh.steps.value[i] = l <= s.top ? entry_of(s, sh.table, l) : 0ull;  // (none is above the largest)
+        }
+    __syncthreads();
+    return v;
+}
+// The entries of a group of tokens, of which the first n are there; what the table does not have is formed.
+template <int N>
+__device__ __forceinline__ void entries_of(const Scale &s, const Shared &sh, const Values &t, const float (&l)[N], int n,
+                                           unsigned long long (&e)[N]) {
+    uint32_t miss = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const uint32_t bits = __float_as_uint(l[j]), at = (bits >> 16 & 0x7fffu) - t.base;
+        e[j] = static_cast<unsigned long long>(kNoStep) << 48;
+        if (j < n) {
+            if (at < kHalf) {
+                e[j] = sh.steps.value[at + (bits >> 31) * kHalf];
+            } else {
+                const float x = coarse(s, l[j]);
+                if (x < kCareful) miss |= 1u << j;
+                else e[j] |= small_weight(x);
+            }
+        }
+    }
+    while (__any_sync(kFullMask, miss != 0)) {
+        const int now = __ffs(miss) - 1;
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j == now) v = l[j];
+        const unsigned long long x = entry_of(s, sh.table, v);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j == now) e[j] = x;
+        miss &= miss - 1;
+    }
+}
+constexpr unsigned long long kWeightMask = (1ull << 48) - 1;
+
 // ------------------------------------------------------------------------------ reductions
 __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
 #pragma unroll
@@ -202,7 +270,7 @@ __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
     return v;
 }
 
-template <bool BF16>
+template <bool BF16, int T>
 struct Row {
     const uint8_t *data;  // this CTA's tokens
     int len, first;       // their number, the first one's index
@@ -215,7 +283,7 @@ struct Row {
         if (tid < head) f(tid, at(tid));
         if (tail + tid < len && tid < kVec) f(tail + tid, at(tail + tid));
         const uint4 *from = reinterpret_cast<const uint4 *>(data + head * (BF16 ? 2 : 4));
-        for (int i = tid; i < body; i += kThreads) {
+        for (int i = tid; i < body; i += T) {
             float v[kVec];
             vec(from[i], v);
 #pragma unroll
@@ -272,6 +340,7 @@ __device__ __forceinline__ unsigned long long place_of(uint32_t key, int index) 
 }
 
 // Sum over the cluster of two 64-bit numbers a thread; all threads get the totals.
+template <int T>
 __device__ __forceinline__ void cluster_sum(Shared &sh, uint32_t rank, uint32_t ctas, unsigned long long &a,
                                             unsigned long long &b) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -283,8 +352,8 @@ __device__ __forceinline__ void cluster_sum(Shared &sh, uint32_t rank, uint32_t 
     }
     __syncthreads();
     if (warp == 0) {
-        a = warp_sum64(lane < kWarps ? sh.warp64[0][lane] : 0);
-        b = warp_sum64(lane < kWarps ? sh.warp64[1][lane] : 0);
+        a = warp_sum64(lane < T / 32 ? sh.warp64[0][lane] : 0);
+        b = warp_sum64(lane < T / 32 ? sh.warp64[1][lane] : 0);
         if (lane < static_cast<int>(ctas)) {
             unsigned long long *to = in_cta(&sh.pair[rank][0], lane);
             to[0] = a;
@@ -302,8 +371,9 @@ __device__ __forceinline__ void cluster_sum(Shared &sh, uint32_t rank, uint32_t 
 
 // Sorts n places, largest first: few by counting the larger ones, many (padded with zeros to a power of two) in
 // bitonic turns.
+template <int T>
 __device__ __forceinline__ void sort_list(Shared &sh, int n) {
-    if (n <= kThreads) {
+    if (n <= 512) {
         unsigned long long mine = 0;
         int at = 0;
         if (static_cast<int>(threadIdx.x) < n) {
@@ -318,11 +388,11 @@ __device__ __forceinline__ void sort_list(Shared &sh, int n) {
     }
     int size = 32;
     while (size < n) size <<= 1;
-    for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
+    for (int i = n + threadIdx.x; i < size; i += T) sh.list[i] = 0;
     __syncthreads();
     for (int k = 2; k <= size; k <<= 1)
         for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+            for (int t = threadIdx.x; t < size / 2; t += T) {
                 const int i = (t / j) * 2 * j + (t & (j - 1)), o = i + j;
                 const unsigned long long a = sh.list[i], b = sh.list[o];
                 if ((a < b) == ((i & k) == 0)) {
@@ -335,8 +405,9 @@ __device__ __forceinline__ void sort_list(Shared &sh, int n) {
 }
 
 // Inclusive prefix sums of sh.weight[0 .. n), by the whole CTA.
+template <int T>
 __device__ __forceinline__ void scan_weights(Shared &sh, int n) {
-    const int per = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * per;
+    const int per = (n + T - 1) / T, i0 = threadIdx.x * per;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned long long s = 0;
     for (int i = i0; i < min(n, i0 + per); ++i) s += sh.weight[i];
@@ -404,8 +475,9 @@ __device__ __forceinline__ int first_reaching(const Shared &sh, int n, unsigned 
     return lo + 1;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+template <bool BF16, int T>
+__global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a) {
+    constexpr int kWarps = T / 32;
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -415,9 +487,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     cluster_arrive_entry();
     griddep_launch_dependents();
     griddep_wait();
+    const float temperature = a.temperature ? __ldcg(a.temperature + row_i) : 1.f;
+    const int k_in = a.top_k ? __ldcg(a.top_k + row_i) : 0;
+    const float p_in = a.top_p ? __ldcg(a.top_p + row_i) : 1.f, min_in = a.min_p ? __ldcg(a.min_p + row_i) : 0.f,
+                u_in = __ldcg(a.u + row_i);
 
     // ------------------------------------------------------------------ the row into shared memory
-    Row<BF16> row;
+    Row<BF16, T> row;
     row.first = min(a.vocab, static_cast<int>(rank) * a.slice);
     row.len = min(a.vocab, row.first + a.slice) - row.first;
     const uint8_t *src = static_cast<const uint8_t *>(a.logits) + (row_i * a.stride + row.first) * kSize;
@@ -452,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const uint4 *from = reinterpret_cast<const uint4 *>(src + head);
         uint4 *to = reinterpret_cast<uint4 *>(dst + head);
 #pragma unroll 8
-        for (int i = tid; i < body; i += kThreads) {
+        for (int i = tid; i < body; i += T) {
             const uint4 v = __ldcg(from + i);
             to[i] = v;
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -467,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             }
         }
     }
-    for (int j = tid; j < kTable; j += kThreads) sh.table[j] = __ldg(&g_powers.at[j]);
+    for (int j = tid; j < kTable; j += T) sh.table[j] = __ldg(&g_powers.at[j]);
     if (tid == 0) sh.count = 0;
     cluster_wait_entry();
     const uint32_t my_top = any ? key_of(top + 0.f) : 0u;
@@ -484,18 +560,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     uint32_t top_key = 0;
     for (uint32_t r = 0; r < ctas; ++r) top_key = max(top_key, sh.from_cta[r]);
 
-    const float temperature = a.temperature ? __ldcg(a.temperature + row_i) : 1.f;
-    int k = a.top_k ? __ldcg(a.top_k + row_i) : 0;
+    int k = k_in;
     if (k <= 0 || k > a.vocab) k = a.vocab;
-    float p = a.top_p ? __ldcg(a.top_p + row_i) : 1.f;
+    float p = p_in;
     if (!(p < 1.f)) p = 1.f;
     if (p <= 0.f) {
         p = 1.f;
         k = 1;
     }
-    const float floor_p = a.min_p ? fminf(fmaxf(__ldcg(a.min_p + row_i), 0.f), 1.f) : 0.f;
+    const float floor_p = fminf(fmaxf(min_in, 0.f), 1.f);
     const unsigned long long least = max(1ull, __float2ull_ru(floor_p * 0x1p44f));
-    const float u_in = __ldcg(a.u + row_i);
     const float u = u_in > 0.f ? fminf(u_in, 1.f) : 0.f;
 
     // ------------------------------------------------------------------ greedy
@@ -531,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // ------------------------------------------------------------------ top-k: few tokens, sorted
     const int each = (k + static_cast<int>(ctas) - 1) / static_cast<int>(ctas);
     unsigned long long cut_k = 0;  // what is kept has this place or a higher one; 0: everything
-    if (k < a.vocab && each <= kThreads / 2 && k <= kCap / 2) {
+    if (k < a.vocab && each <= T / 2 && k <= kCap / 2) {
         // a key that `each` threads' largest reach, near the highest such: of the warps' largest where they are enough
         uint32_t lo = 0, hi = 0xffffffffu;
         if (each <= kWarps - 2) {
@@ -569,37 +643,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (n_all <= kCap) {
             if (rank == 0) {
                 const int n = n_all;
-                sort_list(sh, n);
+                sort_list<T>(sh, n);
                 const int m = min(n, k);
-                unsigned long long w[kCap / kThreads];  // of this thread's places
-                for (int c = 0; c * kThreads < m; ++c) {
-                    const int i = c * kThreads + tid;
+                unsigned long long w[kCap / T];  // of this thread's places
+                for (int c = 0; c * T < m; ++c) {
+                    const int i = c * T + tid;
                     if (i < m) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
                 }
                 __syncthreads();
                 int kept = m;
                 if (p < 1.f) {
 #pragma unroll
-                    for (int c = 0; c < kCap / kThreads; ++c) w[c] = c * kThreads + tid < m ? sh.weight[c * kThreads + tid] : 0ull;
+                    for (int c = 0; c < kCap / T; ++c) w[c] = c * T + tid < m ? sh.weight[c * T + tid] : 0ull;
                     __syncthreads();
-                    scan_weights(sh, m);
+                    scan_weights<T>(sh, m);
                     kept = first_reaching(sh, m, reach(p, sh.weight[m - 1]));
                     __syncthreads();
 #pragma unroll
-                    for (int c = 0; c < kCap / kThreads; ++c)
-                        if (c * kThreads + tid < m) sh.weight[c * kThreads + tid] = w[c];
+                    for (int c = 0; c < kCap / T; ++c)
+                        if (c * T + tid < m) sh.weight[c * T + tid] = w[c];
                     __syncthreads();
                 }
                 // min-p: weights fall along the list, so those that pass are its first ones
                 int pass = 0;
-                for (int i = tid; i < kept; i += kThreads) pass += i == 0 || sh.weight[i] >= least;
+                for (int i = tid; i < kept; i += T) pass += i == 0 || sh.weight[i] >= least;
                 pass = __reduce_add_sync(kFullMask, pass);
                 unsigned long long sum = 0;
                 if (lane == 0) sh.warp32[warp] = pass;
                 __syncthreads();
                 kept = 0;
                 for (int j = 0; j < kWarps; ++j) kept += static_cast<int>(sh.warp32[j]);
-                for (int i = tid; i < kept; i += kThreads) sum += sh.weight[i];
+                for (int i = tid; i < kept; i += T) sum += sh.weight[i];
                 sum = warp_sum64(sum);
                 if (lane == 0) sh.warp64[0][warp] = sum;
                 __syncthreads();
@@ -607,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 for (int j = 0; j < kWarps; ++j) sum += sh.warp64[0][j];
                 const unsigned long long goal = below(u, sum);
                 // a token's sum by index: of the kept ones with lower indices (which have the larger low words)
-                for (int i = tid; i < kept; i += kThreads) {
+                for (int i = tid; i < kept; i += T) {
                     const uint32_t mine = static_cast<uint32_t>(sh.list[i]);
                     unsigned long long before = 0;
 #pragma unroll 4
@@ -631,19 +705,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             const uint32_t mid = lo + (hi - lo) / 2 + 1;
             unsigned long long n = 0, none = 0;
             row.each([&](int, float v) { n += key_of(v) >= mid; });
-            cluster_sum(sh, rank, ctas, n, none);
+            cluster_sum<T>(sh, rank, ctas, n, none);
             if (n >= static_cast<unsigned long long>(k)) lo = mid; else hi = mid - 1;
         }
         unsigned long long above = 0, none = 0;
         row.each([&](int, float v) { above += key_of(v) > lo; });
-        cluster_sum(sh, rank, ctas, above, none);
+        cluster_sum<T>(sh, rank, ctas, above, none);
         int from = 0, to = a.vocab - 1;  // the least index up to which enough equal ones lie
         while (from < to) {
             const int mid = (from + to) >> 1;
             unsigned long long n = 0;
             none = 0;
             row.each([&](int i, float v) { n += key_of(v) == lo && row.first + i <= mid; });
-            cluster_sum(sh, rank, ctas, n, none);
+            cluster_sum<T>(sh, rank, ctas, n, none);
             if (above + n >= static_cast<unsigned long long>(k)) to = mid; else from = mid + 1;
         }
         cut_k = place_of(lo, from);
@@ -651,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
     // ------------------------------------------------------------------ top-p
     unsigned long long cut = cut_k;
+    bool by_cta = false;  // what every CTA keeps is known
     if (p < 1.f) {
         unsigned long long total = 0, sure = 0;  // weight of all, and of what is surely kept
         bool sorted = false;
@@ -658,53 +733,81 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         for (int level = 0; level < 2 && !sorted; ++level) {
             // A token's step: of 1 / 64, and within the one that holds the cut of 1 / (64 * 1536).  Both are monotone in
             // l, whatever f32 rounds.
-            const auto step_of = [&](float x) {
-                const int b = static_cast<int>(x * kPerOctave);
+            const auto step_in = [&](float x) {
+                const int b = step_of(x);
                 if (level == 0) return b;
                 if (b != step0) return b < step0 ? -1 : kBins;
                 return min(kBins - 1, max(0, static_cast<int>((x - step0 * (1.f / kPerOctave)) * (kPerOctave * kBins))));
             };
-            for (int b = tid; b < 2 * kBins; b += kThreads) sh.steps.lo[b] = 0;
+            for (int b = tid; b < 2 * kBins; b += T) sh.steps.lo[b] = 0;
+            if (tid < kMaxCtas) sh.partial[tid] = 0;
             if (tid == 0) sh.count = 0;
-            __syncthreads();
+            const Values values = make_values<T>(s, sh, BF16 && level == 0 && row.len >= kTabled);
             // Small weights at once, into one sum: no cut lies there but in the flattest of rows.
             unsigned long long tail = 0, none = 0;
-            row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16>::kVec], int n) {
-                float x[Row<BF16>::kVec];
-                unsigned long long w[Row<BF16>::kVec];
+            const auto count = [&](int b, unsigned long long w) {
+                const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.steps.lo[b], lo);
+                const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old);
+                if (hi) atomicAdd(&sh.steps.hi[b], hi);
+            };
+            row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
+                float x[Row<BF16, T>::kVec];
+                unsigned long long w[Row<BF16, T>::kVec];
+                if (BF16 && values.on) {
+                    entries_of(s, sh, values, v, n, w);
 #pragma unroll
-                for (int j = 0; j < Row<BF16>::kVec; ++j) {
+                    for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
+                        const int b = static_cast<int>(w[j] >> 48);
+                        if (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j)) continue;
+                        if (b == kNoStep)
+                            tail += w[j] & kWeightMask;
+                        else
+                            count(b, w[j] & kWeightMask);
+                    }
+                    return;
+                }
+#pragma unroll
+                for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
                     x[j] = coarse(s, v[j]);
                     // (NaN, -infinity: nothing)
                     if (j >= n || !(x[j] < 60.f) || (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j))) x[j] = 100.f;
-                    if (level > 0 && (x[j] >= kCareful || step_of(x[j]) < 0 || step_of(x[j]) >= kBins)) x[j] = 100.f;
+                    if (level > 0 && (x[j] >= kCareful || step_in(x[j]) < 0 || step_in(x[j]) >= kBins)) x[j] = 100.f;
                 }
                 weights_of(s, sh.table, v, x, w);
 #pragma unroll
-                for (int j = 0; j < Row<BF16>::kVec; ++j) {
+                for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
                     if (x[j] >= kCareful) {
                         tail += w[j];
                         continue;
                     }
-                    const int b = step_of(x[j]);
-                    const uint32_t lo = static_cast<uint32_t>(w[j]), old = atomicAdd(&sh.steps.lo[b], lo);
-                    const uint32_t hi = static_cast<uint32_t>(w[j] >> 32) + (old + lo < old);
-                    if (hi) atomicAdd(&sh.steps.hi[b], hi);
+                    count(step_in(x[j]), w[j]);
                 }
             });
-            cluster_sum(sh, rank, ctas, tail, none);
+            cluster_sum<T>(sh, rank, ctas, tail, none);
             // Every CTA adds all CTAs' weights of its share of the steps (all of them by every one would be 12 KB from
-            // each of the others: 13 us with 8); their sums tell in whose share the cut lies.
-            const int share = kBins / static_cast<int>(ctas), b0 = static_cast<int>(rank) * share + tid * kMine;
-            unsigned long long mass[kMine], own = 0;
+            // each of the others: 13 us with 8); their sums tell in whose share the cut lies.  All loads are out at once.
+            constexpr int kFetch = (kBins + T - 1) / T;
+            const int share = kBins / static_cast<int>(ctas), per = (share + T - 1) / T;
+            const int mine0 = tid * per, b0 = static_cast<int>(rank) * share + mine0;
+            unsigned long long mass[kFetch], own = 0;
 #pragma unroll
-            for (int j = 0; j < kMine; ++j) {
+            for (int j = 0; j < kFetch; ++j) {
+                const int i = j * T + tid, r = i / share;
+                if (i < kBins) {
+                    const Shared *other = in_cta(&sh, r);
+                    const int b = static_cast<int>(rank) * share + i - r * share;
+                    mass[j] = static_cast<unsigned long long>(other->steps.hi[b]) << 32 | other->steps.lo[b];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kFetch; ++j)
+                if (j * T + tid < kBins) sh.list[j * T + tid] = mass[j];
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kFetch; ++j) {
                 mass[j] = 0;
-                if (tid * kMine + j < share)
-                    for (uint32_t r = 0; r < ctas; ++r) {
-                        const Shared *other = in_cta(&sh, r);
-                        mass[j] += static_cast<unsigned long long>(other->steps.hi[b0 + j]) << 32 | other->steps.lo[b0 + j];
-                    }
+                if (j < per && mine0 + j < share)
+                    for (uint32_t r = 0; r < ctas; ++r) mass[j] += sh.list[static_cast<int>(r) * share + mine0 + j];
                 own += mass[j];
             }
             unsigned long long incl = own;
@@ -732,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             const unsigned long long need = reach(p, total) - sure;  // at least 1: the cut lies behind what is sure
             if (need > all) break;                                   // in the tail
 #pragma unroll
-            for (int j = 0; j < kMine; ++j) {
+            for (int j = 0; j < kFetch; ++j) {
                 if (run < need && need <= run + mass[j])
                     for (uint32_t r = 0; r < ctas; ++r) {
                         Shared *other = in_cta(&sh, r);
@@ -744,24 +847,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             cluster_sync();
             const int step = sh.step;
             sure += sh.before;
+            unsigned long long ahead = 0;  // what this CTA keeps of the steps ahead
+            for (int b = tid; b < step; b += T) ahead += static_cast<unsigned long long>(sh.steps.hi[b]) << 32 | sh.steps.lo[b];
+            ahead = warp_sum64(ahead);
+            if (lane == 0) sh.warp64[1][warp] = ahead;
             row.each([&](int i, float v) {
                 const float x = coarse(s, v);
-                if (x < kCareful && step_of(x) == step) {
+                if (x < kCareful && step_in(x) == step) {
                     const uint32_t key = key_of(v);
                     if (cut_k == 0 || in_k(key, row.first + i)) append(sh, place_of(key, row.first + i));
                 }
             });
             cluster_sync();
+            if (tid < static_cast<int>(ctas)) {
+                ahead = 0;
+                for (int w = 0; w < kWarps; ++w) ahead += sh.warp64[1][w];
+                in_cta(&sh, tid)->pair[rank][1] = ahead;
+            }
             const int n_all = static_cast<int>(in_cta(&sh, 0)->count);
             if (n_all <= kCap) {
                 sorted = true;
+                by_cta = level == 0 && least == 1;
                 if (rank == 0) {
-                    sort_list(sh, n_all);
-                    for (int i = tid; i < n_all; i += kThreads) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
+                    sort_list<T>(sh, n_all);
+                    for (int i = tid; i < n_all; i += T) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
                     __syncthreads();
-                    scan_weights(sh, n_all);
-                    if (tid < static_cast<int>(ctas))
-                        *in_cta(&sh.cut, tid) = sh.list[first_reaching(sh, n_all, reach(p, total) - sure) - 1];
+                    scan_weights<T>(sh, n_all);
+                    const int kept = first_reaching(sh, n_all, reach(p, total) - sure);
+                    if (tid < static_cast<int>(ctas)) *in_cta(&sh.cut, tid) = sh.list[kept - 1];
+                    for (int i = tid; i < kept; i += T)
+                        atomicAdd(&sh.partial[index_of(sh.list[i]) / a.slice], sh.weight[i] - (i ? sh.weight[i - 1] : 0ull));
+                    __syncthreads();
+                    for (int i = tid; i < static_cast<int>(ctas * ctas); i += T)
+                        if (i / static_cast<int>(ctas) != 0)
+                            in_cta(&sh, i / ctas)->partial[i % ctas] = sh.partial[i % ctas];
                 }
             }
             cluster_sync();
@@ -778,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                     const uint32_t key = key_of(v);
                     if (key >= mid && in_k(key, row.first + i)) w += weight_of(s, sh.table, v);
                 });
-                cluster_sum(sh, rank, ctas, w, none);
+                cluster_sum<T>(sh, rank, ctas, w, none);
                 if (w >= need) lo = mid; else hi = mid - 1;
             }
             unsigned long long above = 0, none = 0;
@@ -786,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 const uint32_t key = key_of(v);
                 if (key > lo && in_k(key, row.first + i)) above += weight_of(s, sh.table, v);
             });
-            cluster_sum(sh, rank, ctas, above, none);
+            cluster_sum<T>(sh, rank, ctas, above, none);
             const unsigned long long one = max(1ull, weight_of(s, sh.table, unorder_bits(lo)));
             const unsigned long long ties = need > above ? (need - above + one - 1) / one : 1ull;
             int from = 0, to = a.vocab - 1;
@@ -797,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 row.each([&](int i, float v) {
                     n += key_of(v) == lo && row.first + i <= mid && in_k(lo, row.first + i);
                 });
-                cluster_sum(sh, rank, ctas, n, none);
+                cluster_sum<T>(sh, rank, ctas, n, none);
                 if (n >= ties) to = mid; else from = mid + 1;
             }
             cut = max(cut, place_of(lo, from));
@@ -815,23 +934,50 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const unsigned long long w = weight_of(s, sh.table, v);
         return w >= least ? w : 0ull;
     };
-    unsigned long long mine = 0;
-    row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16>::kVec], int n) {
-        float x[Row<BF16>::kVec];
-        unsigned long long w[Row<BF16>::kVec];
+    unsigned long long mine = 0, goal = 0;
+    if (by_cta) {  // the steps' weights tell whose token it is: the others are done
+        unsigned long long total = 0, first = 0, mine_all = 0;
+        for (uint32_t r = 0; r < ctas; ++r) total += sh.pair[r][1] + sh.partial[r];
+        goal = below(u, total);
+        for (uint32_t r = 0; r < ctas; ++r) {
+            const unsigned long long w = sh.pair[r][1] + sh.partial[r];
+            if (r < rank) first += w;
+            if (r == rank) mine_all = w;
+        }
+        if (goal < first || goal >= first + mine_all) return;
+        goal -= first;
+    }
+    const Values values = make_values<T>(s, sh, BF16 && row.len >= kTabled);
+    row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
+        float x[Row<BF16, T>::kVec];
+        unsigned long long w[Row<BF16, T>::kVec];
+        if (BF16 && values.on) {
+            entries_of(s, sh, values, v, n, w);
 #pragma unroll
-        for (int j = 0; j < Row<BF16>::kVec; ++j) {
+            for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
+                w[j] &= kWeightMask;
+                if (w[j] >= least && keep(v[j], i0 + j)) mine += w[j];
+            }
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
             x[j] = coarse(s, v[j]);
             if (j >= n || !(x[j] < 60.f) || !keep(v[j], i0 + j)) x[j] = 100.f;
         }
         weights_of(s, sh.table, v, x, w);
 #pragma unroll
-        for (int j = 0; j < Row<BF16>::kVec; ++j)
+        for (int j = 0; j < Row<BF16, T>::kVec; ++j)
             if (w[j] >= least) mine += w[j];
     });
     mine = warp_sum64(mine);
-    if (lane < static_cast<int>(ctas)) *in_cta(&sh.sums[rank][warp], lane) = mine;
-    cluster_sync();
+    if (by_cta) {
+        if (lane == 0) sh.sums[rank][warp] = mine;
+        __syncthreads();
+    } else {
+        if (lane < static_cast<int>(ctas)) *in_cta(&sh.sums[rank][warp], lane) = mine;
+        cluster_sync();
+    }
     // The warp whose sum passes the goal: its CTA's warps share its tokens, then one goes through what is left.  A lane
     // holds four of the cluster's sums.
     constexpr int kEach = kMaxCtas * kWarps / 32;
@@ -839,7 +985,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int k = lane * kEach + j;
-        some[j] = k < static_cast<int>(ctas) * kWarps ? sh.sums[k / kWarps][k % kWarps] : 0ull;
+        const bool there = by_cta ? k / kWarps == static_cast<int>(rank) : k < static_cast<int>(ctas) * kWarps;
+        some[j] = there ? sh.sums[k / kWarps][k % kWarps] : 0ull;
         incl += some[j];
     }
     const unsigned long long own = incl;
@@ -848,7 +995,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const unsigned long long up = __shfl_up_sync(kFullMask, incl, o);
         if (lane >= o) incl += up;
     }
-    const unsigned long long goal = below(u, __shfl_sync(kFullMask, incl, 31));
+    const unsigned long long of_all = __shfl_sync(kFullMask, incl, 31);
+    if (!by_cta) goal = below(u, of_all);
     const int at = __ffs(__ballot_sync(kFullMask, incl > goal)) - 1;
     unsigned long long before = incl - own;
     int place = lane * kEach;
@@ -892,6 +1040,10 @@ bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t
 
 constexpr int kMaxDevices = 64;
 
+bool allow(void (*kern)(const SampleArgs), int smem) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+}
+
 // SM count and opt-in shared memory of the current device, after allowing the kernels all of it.
 bool device_info(int &sms, int &smem) {
     static std::atomic<int> sm_cache[kMaxDevices], smem_cache[kMaxDevices];
@@ -903,8 +1055,8 @@ bool device_info(int &sms, int &smem) {
     }
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(sample_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(sample_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        !allow(sample_kernel<false, 512>, smem) || !allow(sample_kernel<true, 512>, smem) ||
+        !allow(sample_kernel<false, 1024>, smem) || !allow(sample_kernel<true, 1024>, smem))
         return false;
     if (dev < kMaxDevices) {
         smem_cache[dev].store(smem, std::memory_order_relaxed);
@@ -939,9 +1091,11 @@ extern "C" int memq_sample(int dtype, const void *logits, int64_t stride, const 
     while (ctas < kMaxCtas && (bytes_of(ctas) > smem / 2 || (rows * ctas * 2 <= sms && slice_of(ctas) > 2048))) ctas *= 2;
     if (bytes_of(ctas) > smem) return MEMQ_ERR_SHAPE;
     a.slice = slice_of(ctas);
+    // A CTA that has its SM to itself takes all the threads that two would.
+    const bool wide = rows * ctas <= sms && a.slice > 8192;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(wide ? 1024 : 512);
     cfg.dynamicSmemBytes = static_cast<size_t>(bytes_of(ctas));
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
@@ -952,7 +1106,10 @@ extern "C" int memq_sample(int dtype, const void *logits, int64_t stride, const 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, dtype == MEMQ_BF16 ? sample_kernel<true> : sample_kernel<false>, a) == cudaSuccess
+    using Kernel = void (*)(const SampleArgs);
+    static constexpr Kernel kKernels[2][2] = {{sample_kernel<false, 512>, sample_kernel<false, 1024>},
+                                              {sample_kernel<true, 512>, sample_kernel<true, 1024>}};
+    return cudaLaunchKernelEx(&cfg, kKernels[dtype == MEMQ_BF16][wide], a) == cudaSuccess
                ? MEMQ_OK
                : MEMQ_ERR_LAUNCH;
 }
