@@ -91,7 +91,10 @@ struct __align__(16) Shared {
             unsigned long long weight[kCap];    // of the list
         };
         struct {
-            unsigned long long value[kValues];  // step << 48 | weight
+            union {
+                unsigned long long value[kValues];  // bf16 values' weights
+                uint32_t times[2 * kValues];        // and how often they are there
+            };
             uint32_t lo[kBins], hi[kBins];      // weight of the steps of x
         } steps;
     };
@@ -203,48 +206,50 @@ __device__ __forceinline__ void weights_of(const Scale &s, const unsigned long l
 
 __device__ __forceinline__ int step_of(float x) { return static_cast<int>(x * kPerOctave); }
 
+constexpr unsigned long long kWeightMask = (1ull << 48) - 1;
+
 // Few bf16 numbers lie between the largest logit and 24 octaves of weight below it: their weights and steps are formed
 // once a row and looked up (60 instructions a token and pass otherwise).
-struct Values {
-    uint32_t base;  // the least magnitude's bits
-    bool on;
-};
+// The least magnitude, as bits, of `binades` up to the largest of any logit there.
+__device__ __forceinline__ uint32_t table_base(const Scale &s, int binades) {
+    const float far = fmaxf(fabsf(s.top), fabsf(s.top - __fdiv_rn(kCareful, s.hi)));
+    return static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(far) >> 23) - (binades - 1), 0)) << 7;
+}
 __device__ __forceinline__ unsigned long long entry_of(const Scale &s, const unsigned long long *table, float l) {
     const float x = coarse(s, l);
     if (!(x < 60.f)) return static_cast<unsigned long long>(kNoStep) << 48;  // NaN, too
     return static_cast<unsigned long long>(x < kCareful ? step_of(x) : kNoStep) << 48 | weight_of(s, table, l);
 }
+// Of logits up to `after` and weights below `least` the entries are without weight.
 template <int T>
-__device__ __forceinline__ Values make_values(const Scale &s, Shared &sh, bool on) {
-    Values v;
-    const float far = fmaxf(fabsf(s.top), fabsf(s.top - __fdiv_rn(kCareful, s.hi)));
-    v.on = on && far < 0x1p100f;
-    v.base = static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(far) >> 23) - 9, 0)) << 7;
-    if (v.on)
-        for (uint32_t i = threadIdx.x; i < kValues; i += T) {
-            const uint32_t sign = i >= kHalf, bits = sign << 31 | (v.base + i - sign * kHalf) << 16;
-            const float l = __uint_as_float(bits) + 0.f;
-            sh.steps.value[i] = l <= s.top ? entry_of(s, sh.table, l) : 0ull;  // (none is above the largest)
-        }
+__device__ __forceinline__ void make_values(const Scale &s, Shared &sh, uint32_t base, float after, unsigned long long least) {
+    for (uint32_t i = threadIdx.x; i < kValues; i += T) {
+        const uint32_t sign = i >= kHalf, bits = sign << 31 | (base + i - sign * kHalf) << 16;
+        const float l = __uint_as_float(bits) + 0.f;
+        unsigned long long e = l > s.top || l <= after ? 0ull : entry_of(s, sh.table, l) & kWeightMask;  // (none is above)
+        sh.steps.value[i] = e < least ? 0ull : e;
+    }
     __syncthreads();
-    return v;
 }
-// The entries of a group of tokens, of which the first n are there; what the table does not have is formed.
+// The sum of the weights of a group of tokens, of which the first n are there; what the table does not have is formed.
 template <int N>
-__device__ __forceinline__ void entries_of(const Scale &s, const Shared &sh, const Values &t, const float (&l)[N], int n,
-                                           unsigned long long (&e)[N]) {
+__device__ __forceinline__ unsigned long long sum_values(const Scale &s, const Shared &sh, uint32_t base, const float (&l)[N],
+                                                         int n, float after, unsigned long long least) {
     uint32_t miss = 0;
+    unsigned long long sum = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const uint32_t bits = __float_as_uint(l[j]), at = (bits >> 16 & 0x7fffu) - t.base;
-        e[j] = static_cast<unsigned long long>(kNoStep) << 48;
-        if (j < n) {
-            if (at < kHalf) {
-                e[j] = sh.steps.value[at + (bits >> 31) * kHalf];
+        const uint32_t bits = __float_as_uint(l[j]), at = (bits >> 16 & 0x7fffu) - base;
+        if (j >= n) continue;
+        if (at < kHalf) {
+            sum += sh.steps.value[at + (bits >> 31) * kHalf];
+        } else if (l[j] > after) {
+            const float x = coarse(s, l[j]);
+            if (x < kCareful) {
+                miss |= 1u << j;
             } else {
-                const float x = coarse(s, l[j]);
-                if (x < kCareful) miss |= 1u << j;
-                else e[j] |= small_weight(x);
+                const unsigned long long w = small_weight(x);
+                sum += w >= least ? w : 0ull;
             }
         }
     }
@@ -254,14 +259,12 @@ __device__ __forceinline__ void entries_of(const Scale &s, const Shared &sh, con
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if (j == now) v = l[j];
-        const unsigned long long x = entry_of(s, sh.table, v);
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j == now) e[j] = x;
+        const unsigned long long w = weight_of(s, sh.table, v);
+        if (miss && w >= least) sum += w;
         miss &= miss - 1;
     }
+    return sum;
 }
-constexpr unsigned long long kWeightMask = (1ull << 48) - 1;
 
 // ------------------------------------------------------------------------------ reductions
 __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
@@ -369,6 +372,22 @@ __device__ __forceinline__ void cluster_sum(Shared &sh, uint32_t rank, uint32_t 
     cluster_sync();  // the pairs may be written again
 }
 
+// The least key in (lo, hi] for which f holds, which it does for hi and what lies between; by half a warp, whose lanes
+// differ from the other half's in what they ask for.
+template <typename F>
+__device__ __forceinline__ uint32_t first_key(uint32_t lo, uint32_t hi, F f) {
+    const int lane = threadIdx.x & 15, half = threadIdx.x & 16;
+#pragma unroll 1
+    for (int round = 0; round < 8; ++round) {  // 16^8 keys
+        const uint32_t step = (hi - lo - 1) / 16 + 1;
+        const unsigned long long at = lo + static_cast<unsigned long long>(lane + 1) * step;
+        const unsigned no = __ballot_sync(kFullMask, !f(at < hi ? static_cast<uint32_t>(at) : hi));
+        lo += __popc(no >> half & 0xffffu) * step;
+        hi = static_cast<uint32_t>(min(static_cast<unsigned long long>(hi), static_cast<unsigned long long>(lo) + step));
+    }
+    return hi;
+}
+
 // Sorts n places, largest first: few by counting the larger ones, many (padded with zeros to a power of two) in
 // bitonic turns.
 template <int T>
@@ -425,11 +444,26 @@ __device__ __forceinline__ void scan_weights(Shared &sh, int n) {
     __syncthreads();
 }
 
-// Appends a token to the first CTA's list, which may be full.
+// Appends a token to this CTA's list, which may be full.
 __device__ __forceinline__ void append(Shared &sh, unsigned long long place) {
-    Shared *first = in_cta(&sh, 0);
-    const uint32_t at = atomicAdd(&first->count, 1u);
-    if (at < kCap) first->list[at] = place;
+    const uint32_t at = atomicAdd(&sh.count, 1u);
+    if (at < kCap) sh.list[at] = place;
+}
+// All CTAs' lists join the first one's, whose count is then of all.  (Appended there one by one a token waits for its
+// place 1500 cycles.)
+template <int T>
+__device__ __forceinline__ void join_lists(Shared &sh, uint32_t rank) {
+    __syncthreads();
+    if (rank != 0) {
+        Shared *first = in_cta(&sh, 0);
+        const uint32_t n = sh.count;
+        if (threadIdx.x == 0 && n > 0) sh.found = atomicAdd(&first->count, n);
+        __syncthreads();
+        const uint32_t at = sh.found;
+        for (uint32_t i = threadIdx.x; i < min(n, static_cast<uint32_t>(kCap)) && at + i < kCap; i += T)
+            first->list[at + i] = sh.list[i];
+    }
+    cluster_sync();
 }
 
 __device__ __forceinline__ float value_of(unsigned long long place) { return unorder_bits(static_cast<uint32_t>(place >> 32)); }
@@ -637,7 +671,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                 const uint32_t key = key_of(v);
                 if (key >= bound) append(sh, place_of(key, row.first + i));
             });
-        cluster_sync();
+        join_lists<T>(sh, rank);
         const int n_all = static_cast<int>(in_cta(&sh, 0)->count);
         cluster_arrive();  // the count has been read
         if (n_all <= kCap) {
@@ -680,6 +714,23 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                 sum = 0;
                 for (int j = 0; j < kWarps; ++j) sum += sh.warp64[0][j];
                 const unsigned long long goal = below(u, sum);
+                if (kept > 128) {  // the least index up to which the sum passes the goal: every warp tries one
+                    int from = 0, to = a.vocab - 1;
+                    while (from < to) {
+                        const int step = (to - from) / kWarps + 1, mid = min(to, from + (warp + 1) * step - 1);
+                        unsigned long long part = 0;
+                        for (int i = lane; i < kept; i += 32) part += index_of(sh.list[i]) <= mid ? sh.weight[i] : 0ull;
+                        part = warp_sum64(part);
+                        if (lane == 0) sh.warp32[warp] = part > goal;
+                        __syncthreads();
+                        const unsigned yes = __ballot_sync(kFullMask, lane < kWarps && sh.warp32[lane % kWarps] != 0);
+                        from += (kWarps - __popc(yes)) * step;
+                        to = min(to, from + step - 1);
+                        __syncthreads();
+                    }
+                    if (tid == 0) a.out[row_i] = from;
+                    kept = 0;
+                }
                 // a token's sum by index: of the kept ones with lower indices (which have the larger low words)
                 for (int i = tid; i < kept; i += T) {
                     const uint32_t mine = static_cast<uint32_t>(sh.list[i]);
@@ -723,6 +774,30 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
         cut_k = place_of(lo, from);
     }
 
+    // f(entry, times) of this CTA's bf16 values, counted: twenty binades of either sign, the others one by one.
+    const bool tabled = BF16 && a.slice >= kTabled && fabsf(s.top) < 0x1p100f && 1.f / s.hi < 0x1p90f;
+    const auto each_value = [&](auto f) {
+        const uint32_t base = table_base(s, 20);
+        for (int i = tid; i < static_cast<int>(2 * kValues); i += T) sh.steps.times[i] = 0;
+        __syncthreads();
+        row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
+#pragma unroll
+            for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
+                if (j >= n || (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j))) continue;
+                const uint32_t bits = __float_as_uint(v[j]), at = (bits >> 16 & 0x7fffu) - base;
+                if (at < kValues)
+                    atomicAdd(&sh.steps.times[at + (bits >> 31) * kValues], 1u);
+                else
+                    f(entry_of(s, sh.table, v[j]), 1u);
+            }
+        });
+        __syncthreads();
+        for (uint32_t i = tid; i < 2 * kValues; i += T) {
+            const uint32_t times = sh.steps.times[i], sign = i >= kValues;
+            if (times) f(entry_of(s, sh.table, __uint_as_float(sign << 31 | (base + i - sign * kValues) << 16)), times);
+        }
+    };
+
     // ------------------------------------------------------------------ top-p
     unsigned long long cut = cut_k;
     bool by_cta = false;  // what every CTA keeps is known
@@ -740,9 +815,8 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                 return min(kBins - 1, max(0, static_cast<int>((x - step0 * (1.f / kPerOctave)) * (kPerOctave * kBins))));
             };
             for (int b = tid; b < 2 * kBins; b += T) sh.steps.lo[b] = 0;
-            if (tid < kMaxCtas) sh.partial[tid] = 0;
             if (tid == 0) sh.count = 0;
-            const Values values = make_values<T>(s, sh, BF16 && level == 0 && row.len >= kTabled);
+            __syncthreads();
             // Small weights at once, into one sum: no cut lies there but in the flattest of rows.
             unsigned long long tail = 0, none = 0;
             const auto count = [&](int b, unsigned long long w) {
@@ -750,39 +824,36 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                 const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old);
                 if (hi) atomicAdd(&sh.steps.hi[b], hi);
             };
-            row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
-                float x[Row<BF16, T>::kVec];
-                unsigned long long w[Row<BF16, T>::kVec];
-                if (BF16 && values.on) {
-                    entries_of(s, sh, values, v, n, w);
+            if (BF16 && level == 0 && tabled)
+                each_value([&](unsigned long long e, uint32_t times) {
+                    const int b = static_cast<int>(e >> 48);
+                    const unsigned long long w = (e & kWeightMask) * times;
+                    if (b == kNoStep)
+                        tail += w;
+                    else
+                        count(b, w);
+                });
+            else
+                row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
+                    float x[Row<BF16, T>::kVec];
+                    unsigned long long w[Row<BF16, T>::kVec];
 #pragma unroll
                     for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
-                        const int b = static_cast<int>(w[j] >> 48);
-                        if (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j)) continue;
-                        if (b == kNoStep)
-                            tail += w[j] & kWeightMask;
-                        else
-                            count(b, w[j] & kWeightMask);
+                        x[j] = coarse(s, v[j]);
+                        // (NaN, -infinity: nothing)
+                        if (j >= n || !(x[j] < 60.f) || (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j))) x[j] = 100.f;
+                        if (level > 0 && (x[j] >= kCareful || step_in(x[j]) < 0 || step_in(x[j]) >= kBins)) x[j] = 100.f;
                     }
-                    return;
-                }
+                    weights_of(s, sh.table, v, x, w);
 #pragma unroll
-                for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
-                    x[j] = coarse(s, v[j]);
-                    // (NaN, -infinity: nothing)
-                    if (j >= n || !(x[j] < 60.f) || (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j))) x[j] = 100.f;
-                    if (level > 0 && (x[j] >= kCareful || step_in(x[j]) < 0 || step_in(x[j]) >= kBins)) x[j] = 100.f;
-                }
-                weights_of(s, sh.table, v, x, w);
-#pragma unroll
-                for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
-                    if (x[j] >= kCareful) {
-                        tail += w[j];
-                        continue;
+                    for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
+                        if (x[j] >= kCareful) {
+                            tail += w[j];
+                            continue;
+                        }
+                        count(step_in(x[j]), w[j]);
                     }
-                    count(step_in(x[j]), w[j]);
-                }
-            });
+                });
             cluster_sum<T>(sh, rank, ctas, tail, none);
             // Every CTA adds all CTAs' weights of its share of the steps (all of them by every one would be 12 KB from
             // each of the others: 13 us with 8); their sums tell in whose share the cut lies.  All loads are out at once.
@@ -851,14 +922,23 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
             for (int b = tid; b < step; b += T) ahead += static_cast<unsigned long long>(sh.steps.hi[b]) << 32 | sh.steps.lo[b];
             ahead = warp_sum64(ahead);
             if (lane == 0) sh.warp64[1][warp] = ahead;
+            // the step's logits are a range: its least, and the least behind it (if it is not the first)
+            if (warp == 0) {
+                const uint32_t key = first_key(kLeastKey, top_key, [&](uint32_t key) {
+                    return step_in(coarse(s, unorder_bits(key))) <= step - (lane >> 4);
+                });
+                if ((lane & 15) == 0) sh.bounds[lane >> 4] = key;
+            }
+            __syncthreads();
+            const float least_v = unorder_bits(sh.bounds[0]);
+            const float most_v = step_in(0.f) < step ? unorder_bits(sh.bounds[1] - 1) : s.top;
             row.each([&](int i, float v) {
-                const float x = coarse(s, v);
-                if (x < kCareful && step_in(x) == step) {
+                if (v >= least_v && v <= most_v) {
                     const uint32_t key = key_of(v);
                     if (cut_k == 0 || in_k(key, row.first + i)) append(sh, place_of(key, row.first + i));
                 }
             });
-            cluster_sync();
+            join_lists<T>(sh, rank);
             if (tid < static_cast<int>(ctas)) {
                 ahead = 0;
                 for (int w = 0; w < kWarps; ++w) ahead += sh.warp64[1][w];
@@ -875,12 +955,13 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                     scan_weights<T>(sh, n_all);
                     const int kept = first_reaching(sh, n_all, reach(p, total) - sure);
                     if (tid < static_cast<int>(ctas)) *in_cta(&sh.cut, tid) = sh.list[kept - 1];
-                    for (int i = tid; i < kept; i += T)
-                        atomicAdd(&sh.partial[index_of(sh.list[i]) / a.slice], sh.weight[i] - (i ? sh.weight[i - 1] : 0ull));
-                    __syncthreads();
-                    for (int i = tid; i < static_cast<int>(ctas * ctas); i += T)
-                        if (i / static_cast<int>(ctas) != 0)
-                            in_cta(&sh, i / ctas)->partial[i % ctas] = sh.partial[i % ctas];
+                    if (warp < static_cast<int>(ctas)) {  // a warp adds up what a CTA keeps of the step
+                        unsigned long long of_cta = 0;
+                        for (int i = lane; i < kept; i += 32)
+                            if (index_of(sh.list[i]) / a.slice == warp) of_cta += sh.weight[i] - (i ? sh.weight[i - 1] : 0ull);
+                        of_cta = warp_sum64(of_cta);
+                        if (lane < static_cast<int>(ctas)) *in_cta(&sh.partial[warp], lane) = of_cta;
+                    }
                 }
             }
             cluster_sync();
@@ -947,17 +1028,18 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
         if (goal < first || goal >= first + mine_all) return;
         goal -= first;
     }
-    const Values values = make_values<T>(s, sh, BF16 && row.len >= kTabled);
+    const float after = cut ? cut_v : -INFINITY;
+    const uint32_t base = table_base(s, 10);
+    if (tabled) make_values<T>(s, sh, base, after, least);
+    const unsigned long long cut_w = cut ? weight_of(s, sh.table, cut_v) : 0ull;
     row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
         float x[Row<BF16, T>::kVec];
         unsigned long long w[Row<BF16, T>::kVec];
-        if (BF16 && values.on) {
-            entries_of(s, sh, values, v, n, w);
+        if (tabled) {
+            mine += sum_values(s, sh, base, v, n, after, least);
 #pragma unroll
-            for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
-                w[j] &= kWeightMask;
-                if (w[j] >= least && keep(v[j], i0 + j)) mine += w[j];
-            }
+            for (int j = 0; j < Row<BF16, T>::kVec; ++j)
+                if (v[j] == cut_v && row.first + i0 + j <= cut_i && j < n && cut_w >= least) mine += cut_w;
             return;
         }
 #pragma unroll
