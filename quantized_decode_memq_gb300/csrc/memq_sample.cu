@@ -38,7 +38,8 @@ namespace {
 constexpr int kMaxWarps = 32;  // of a CTA: 512 threads, or 1024
 constexpr int kMaxCtas = 8;
 constexpr int kCap = 2048;   // tokens that are sorted
-constexpr int kBins = 1536, kPerOctave = 64;  // steps of x, up to kCareful
+constexpr int kBins = 1536, kPerOctave = 64;  // steps of x, up to kCareful for weights
+constexpr int kCountOctave = 25;              // and up to 60 for numbers of tokens
 constexpr int kTable = 512;
 constexpr int kUnitLog = 44;  // weights are integers in units of 2^-44
 constexpr uint32_t kLeastKey = 0x007fffffu;  // of -infinity; NaN has key 0
@@ -46,7 +47,6 @@ constexpr int64_t kMaxVocab = 360000;
 // bf16 logits: a table of the weights of ten binades of values, of either sign.
 constexpr uint32_t kHalf = 10 * 128, kValues = 2 * kHalf;
 constexpr int kTabled = 8192;   // tokens of a CTA from which it pays
-constexpr int kNoStep = 0x7ff;  // in an entry: x is kCareful or more
 
 // 2^(-j / 512) in units of 2^-62, formed by the compiler: the 512th root of 1/2 by nine square roots, then its powers.
 struct Powers {
@@ -204,10 +204,6 @@ __device__ __forceinline__ void weights_of(const Scale &s, const unsigned long l
     }
 }
 
-__device__ __forceinline__ int step_of(float x) { return static_cast<int>(x * kPerOctave); }
-
-constexpr unsigned long long kWeightMask = (1ull << 48) - 1;
-
 // Few bf16 numbers lie between the largest logit and 24 octaves of weight below it: their weights and steps are formed
 // once a row and looked up (60 instructions a token and pass otherwise).
 // The least magnitude, as bits, of `binades` up to the largest of any logit there.
@@ -215,18 +211,13 @@ __device__ __forceinline__ uint32_t table_base(const Scale &s, int binades) {
     const float far = fmaxf(fabsf(s.top), fabsf(s.top - __fdiv_rn(kCareful, s.hi)));
     return static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(far) >> 23) - (binades - 1), 0)) << 7;
 }
-__device__ __forceinline__ unsigned long long entry_of(const Scale &s, const unsigned long long *table, float l) {
-    const float x = coarse(s, l);
-    if (!(x < 60.f)) return static_cast<unsigned long long>(kNoStep) << 48;  // NaN, too
-    return static_cast<unsigned long long>(x < kCareful ? step_of(x) : kNoStep) << 48 | weight_of(s, table, l);
-}
 // Of logits up to `after` and weights below `least` the entries are without weight.
 template <int T>
 __device__ __forceinline__ void make_values(const Scale &s, Shared &sh, uint32_t base, float after, unsigned long long least) {
     for (uint32_t i = threadIdx.x; i < kValues; i += T) {
         const uint32_t sign = i >= kHalf, bits = sign << 31 | (base + i - sign * kHalf) << 16;
         const float l = __uint_as_float(bits) + 0.f;
-        unsigned long long e = l > s.top || l <= after ? 0ull : entry_of(s, sh.table, l) & kWeightMask;  // (none is above)
+        unsigned long long e = l > s.top || l <= after ? 0ull : weight_of(s, sh.table, l);  // (none is above)
         sh.steps.value[i] = e < least ? 0ull : e;
     }
     __syncthreads();
@@ -749,8 +740,36 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
     // a warp's tokens
     const int seg = (row.len + kWarps - 1) / kWarps, seg0 = min(row.len, warp * seg), seg1 = min(row.len, seg0 + seg);
 
-    // ------------------------------------------------------------------ top-k by bisection
-    if (k < a.vocab) {
+    // f(value, times) of this CTA's bf16 tokens, counted: twenty binades of either sign, the others one by one.
+    const bool tabled = BF16 && a.slice >= kTabled && fabsf(s.top) < 0x1p100f && 1.f / s.hi < 0x1p90f;
+    const auto each_value = [&](auto f) {
+        const uint32_t base = table_base(s, 20);
+        for (int i = tid; i < static_cast<int>(2 * kValues); i += T) sh.steps.times[i] = 0;
+        __syncthreads();
+        row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
+#pragma unroll
+            for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
+                if (j >= n || (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j))) continue;
+                const uint32_t bits = __float_as_uint(v[j]), at = (bits >> 16 & 0x7fffu) - base;
+                if (at < kValues)
+                    atomicAdd(&sh.steps.times[at + (bits >> 31) * kValues], 1u);
+                else
+                    f(v[j], 1u);
+            }
+        });
+        __syncthreads();
+        for (uint32_t i = tid; i < 2 * kValues; i += T) {
+            const uint32_t times = sh.steps.times[i], sign = i >= kValues;
+            if (times) f(__uint_as_float(sign << 31 | (base + i - sign * kValues) << 16), times);
+        }
+    };
+
+    // ------------------------------------------------------------------ top-k, then top-p
+    // The same by numbers of tokens and by their weights.
+    unsigned long long cut = 0;
+    bool by_cta = false;  // what every CTA keeps is known
+    // top-k by bisection over keys, then over indices
+    const auto bisect_k = [&]() {
         uint32_t lo = 0, hi = top_key;  // the largest key that k tokens reach
         while (lo < hi) {
             const uint32_t mid = lo + (hi - lo) / 2 + 1;
@@ -771,48 +790,23 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
             cluster_sum<T>(sh, rank, ctas, n, none);
             if (above + n >= static_cast<unsigned long long>(k)) to = mid; else from = mid + 1;
         }
-        cut_k = place_of(lo, from);
-    }
-
-    // f(entry, times) of this CTA's bf16 values, counted: twenty binades of either sign, the others one by one.
-    const bool tabled = BF16 && a.slice >= kTabled && fabsf(s.top) < 0x1p100f && 1.f / s.hi < 0x1p90f;
-    const auto each_value = [&](auto f) {
-        const uint32_t base = table_base(s, 20);
-        for (int i = tid; i < static_cast<int>(2 * kValues); i += T) sh.steps.times[i] = 0;
-        __syncthreads();
-        row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
-#pragma unroll
-            for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
-                if (j >= n || (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j))) continue;
-                const uint32_t bits = __float_as_uint(v[j]), at = (bits >> 16 & 0x7fffu) - base;
-                if (at < kValues)
-                    atomicAdd(&sh.steps.times[at + (bits >> 31) * kValues], 1u);
-                else
-                    f(entry_of(s, sh.table, v[j]), 1u);
-            }
-        });
-        __syncthreads();
-        for (uint32_t i = tid; i < 2 * kValues; i += T) {
-            const uint32_t times = sh.steps.times[i], sign = i >= kValues;
-            if (times) f(entry_of(s, sh.table, __uint_as_float(sign << 31 | (base + i - sign * kValues) << 16)), times);
-        }
+        cut = place_of(lo, from);
     };
-
-    // ------------------------------------------------------------------ top-p
-    unsigned long long cut = cut_k;
-    bool by_cta = false;  // what every CTA keeps is known
-    if (p < 1.f) {
+    for (int turn = k < a.vocab ? 0 : 1; turn < (p < 1.f ? 2 : 1); ++turn) {
+        const bool counting = turn == 0;
+        const float octave = counting ? kCountOctave : kPerOctave;
+        const float limit = counting ? 60.f : kCareful;
         unsigned long long total = 0, sure = 0;  // weight of all, and of what is surely kept
-        bool sorted = false;
+        bool sorted = false, beyond = false;
         int step0 = -1;  // the step that holds the cut, on the second level
         for (int level = 0; level < 2 && !sorted; ++level) {
-            // A token's step: of 1 / 64, and within the one that holds the cut of 1 / (64 * 1536).  Both are monotone in
+            // A token's step: of 1 / octave, and within the one that holds the cut of 1 / (1536 octave).  Both are monotone in
             // l, whatever f32 rounds.
             const auto step_in = [&](float x) {
-                const int b = step_of(x);
+                const int b = static_cast<int>(x * octave);
                 if (level == 0) return b;
                 if (b != step0) return b < step0 ? -1 : kBins;
-                return min(kBins - 1, max(0, static_cast<int>((x - step0 * (1.f / kPerOctave)) * (kPerOctave * kBins))));
+                return min(kBins - 1, max(0, static_cast<int>((x - step0 * __frcp_rn(octave)) * (octave * kBins))));
             };
             for (int b = tid; b < 2 * kBins; b += T) sh.steps.lo[b] = 0;
             if (tid == 0) sh.count = 0;
@@ -825,13 +819,14 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                 if (hi) atomicAdd(&sh.steps.hi[b], hi);
             };
             if (BF16 && level == 0 && tabled)
-                each_value([&](unsigned long long e, uint32_t times) {
-                    const int b = static_cast<int>(e >> 48);
-                    const unsigned long long w = (e & kWeightMask) * times;
-                    if (b == kNoStep)
+                each_value([&](float l, uint32_t times) {
+                    const float x = coarse(s, l);
+                    if (!(x < 60.f)) return;
+                    const unsigned long long w = (counting ? 1ull : weight_of(s, sh.table, l)) * times;
+                    if (x >= limit)
                         tail += w;
                     else
-                        count(b, w);
+                        count(step_in(x), w);
                 });
             else
                 row.walk(seg0, seg1, [&](int i0, const float(&v)[Row<BF16, T>::kVec], int n) {
@@ -842,16 +837,16 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                         x[j] = coarse(s, v[j]);
                         // (NaN, -infinity: nothing)
                         if (j >= n || !(x[j] < 60.f) || (cut_k != 0 && !in_k(key_of(v[j]), row.first + i0 + j))) x[j] = 100.f;
-                        if (level > 0 && (x[j] >= kCareful || step_in(x[j]) < 0 || step_in(x[j]) >= kBins)) x[j] = 100.f;
+                        if (level > 0 && (x[j] >= limit || step_in(x[j]) < 0 || step_in(x[j]) >= kBins)) x[j] = 100.f;
                     }
-                    weights_of(s, sh.table, v, x, w);
+                    if (!counting) weights_of(s, sh.table, v, x, w);
 #pragma unroll
                     for (int j = 0; j < Row<BF16, T>::kVec; ++j) {
-                        if (x[j] >= kCareful) {
+                        if (counting) w[j] = x[j] < 60.f;
+                        if (x[j] >= limit)
                             tail += w[j];
-                            continue;
-                        }
-                        count(step_in(x[j]), w[j]);
+                        else
+                            count(step_in(x[j]), w[j]);
                     }
                 });
             cluster_sum<T>(sh, rank, ctas, tail, none);
@@ -903,8 +898,10 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                 all += sh.pair[r][0];
             }
             if (level == 0) total = all + tail;
-            const unsigned long long need = reach(p, total) - sure;  // at least 1: the cut lies behind what is sure
-            if (need > all) break;                                   // in the tail
+            const unsigned long long goal = counting ? static_cast<unsigned long long>(k) : reach(p, total);
+            const unsigned long long need = goal - sure;  // at least 1: the cut lies behind what is sure
+            beyond = need > all;                          // in the tail
+            if (beyond) break;
 #pragma unroll
             for (int j = 0; j < kFetch; ++j) {
                 if (run < need && need <= run + mass[j])
@@ -947,13 +944,14 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
             const int n_all = static_cast<int>(in_cta(&sh, 0)->count);
             if (n_all <= kCap) {
                 sorted = true;
-                by_cta = level == 0 && least == 1;
+                by_cta = !counting && level == 0 && least == 1;
                 if (rank == 0) {
                     sort_list<T>(sh, n_all);
-                    for (int i = tid; i < n_all; i += T) sh.weight[i] = weight_of(s, sh.table, value_of(sh.list[i]));
+                    for (int i = tid; i < n_all; i += T)
+                        sh.weight[i] = counting ? 1ull : weight_of(s, sh.table, value_of(sh.list[i]));
                     __syncthreads();
                     scan_weights<T>(sh, n_all);
-                    const int kept = first_reaching(sh, n_all, reach(p, total) - sure);
+                    const int kept = first_reaching(sh, n_all, goal - sure);
                     if (tid < static_cast<int>(ctas)) *in_cta(&sh.cut, tid) = sh.list[kept - 1];
                     if (warp < static_cast<int>(ctas)) {  // a warp adds up what a CTA keeps of the step
                         unsigned long long of_cta = 0;
@@ -967,6 +965,12 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
             cluster_sync();
             if (sorted) cut = max(cut, sh.cut);
             step0 = step;
+        }
+        if (counting) {
+            // (behind 60 octaves no token has a weight, so nothing is cut)
+            if (!sorted && !beyond) bisect_k();
+            cut_k = cut;
+            continue;
         }
         if (!sorted) {  // thousands of equal tokens: bisection over keys, by weight
             const unsigned long long need = reach(p, total);

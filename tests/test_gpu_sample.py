@@ -69,6 +69,36 @@ def test_flat_and_steep_rows(memq, spread):
     check(memq, to_dev(x).bfloat16(), 1.0, 0, np.linspace(0.01, 0.9999, n), 0.0, u)
 
 
+@pytest.mark.parametrize("n", [24, 200])
+def test_long_bfloat16_rows(memq, n):
+    """Few values many times, of every magnitude: about zero, far below the largest, masked, all negative."""
+    rng = np.random.default_rng(10)
+    v = 40003
+    x = peaked(rng, n, v) * rng.choice([1e-3, 0.1, 1.0, 1.0, 30.0], (n, 1)).astype(np.float32)
+    x[0::6] -= 25
+    x[1::6, rng.random(v) < 0.5] = -np.inf
+    x[2::6] *= np.exp2(-rng.integers(0, 30, v)).astype(np.float32)
+    x[3::6, 1000:] = np.where(rng.random(v - 1000) < 0.5, 0.0, -0.0)
+    x[4::6, rng.random(v) < 0.3] = 1e-38
+    x[5::12, rng.random(v) < 0.01] = np.nan
+    t, k, p, m, u = settings(rng, n)
+    x = to_dev(x).bfloat16()
+    with np.errstate(invalid="ignore"):
+        check(memq, x, np.where(t == 0, 1, t), k, p, m, u)
+        check(memq, x, rng.choice([0.05, 1, 20, 1e4, 1e29], n), 0, rng.choice([0.3, 0.9, 1.0], n), 0.0, u)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,v", [(200, 16384), (4, 50000)])
+def test_many_of_the_largest(memq, n, v, dtype):
+    """top_k of hundreds to nearly all, in rows of one CTA and of several, near and far from the largest."""
+    rng = np.random.default_rng(11)
+    x = to_dev((rng.choice([0.1, 2.0, 8.0], (n, 1)) * rng.normal(0, 1, (n, v))).astype(np.float32)).to(dtype)
+    k = rng.choice([257, 500, 1000, 1025, 3000, 12000, v - 1], n)
+    for t in (rng.choice([0.05, 0.3, 1.0, 4.0], n), np.full(n, 100.0)):
+        check(memq, x, t, k, rng.choice([1.0, 1.0, 0.9], n), rng.choice([0, 0, 1e-3], n), rng.choice([0.999999, 0.5, 0.99], n))
+
+
 def test_equal_logits(memq):
     """Ties at every cut: all tokens alike, or one of a few values; the lowest indices are kept."""
     v = 20000
