@@ -26,6 +26,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 
 #include "memq.h"
@@ -792,10 +793,9 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
         }
         cut = place_of(lo, from);
     };
-    for (int turn = k < a.vocab ? 0 : 1; turn < (p < 1.f ? 2 : 1); ++turn) {
-        const bool counting = turn == 0;
-        const float octave = counting ? kCountOctave : kPerOctave;
-        const float limit = counting ? 60.f : kCareful;
+    const auto find_cut = [&](auto what) {
+        constexpr bool counting = decltype(what)::value;
+        constexpr float octave = counting ? kCountOctave : kPerOctave, limit = counting ? 60.f : kCareful;
         unsigned long long total = 0, sure = 0;  // weight of all, and of what is surely kept
         bool sorted = false, beyond = false;
         int step0 = -1;  // the step that holds the cut, on the second level
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
                 const int b = static_cast<int>(x * octave);
                 if (level == 0) return b;
                 if (b != step0) return b < step0 ? -1 : kBins;
-                return min(kBins - 1, max(0, static_cast<int>((x - step0 * __frcp_rn(octave)) * (octave * kBins))));
+                return min(kBins - 1, max(0, static_cast<int>((x - step0 * (1.f / octave)) * (octave * kBins))));
             };
             for (int b = tid; b < 2 * kBins; b += T) sh.steps.lo[b] = 0;
             if (tid == 0) sh.count = 0;
@@ -970,7 +970,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
             // (behind 60 octaves no token has a weight, so nothing is cut)
             if (!sorted && !beyond) bisect_k();
             cut_k = cut;
-            continue;
+            return;
         }
         if (!sorted) {  // thousands of equal tokens: bisection over keys, by weight
             const unsigned long long need = reach(p, total);
@@ -1006,7 +1006,9 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
             }
             cut = max(cut, place_of(lo, from));
         }
-    }
+    };
+    if (k < a.vocab) find_cut(std::true_type{});
+    if (p < 1.f) find_cut(std::false_type{});
 
     // ------------------------------------------------------------------ the draw
     // A warp's tokens are consecutive, so its sum's place among the others is its place by index.
