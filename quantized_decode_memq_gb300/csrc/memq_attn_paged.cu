@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Adds the pieces of the items that several runs shared, in the runs' order.  CTAs (x, 0 .. gridDim.y - 1) serve the
 // x-th such item.  Up to kFewParts pieces a warp adds a row's alone, eight rows under way; above, the CTA's warps add
 // every eighth and the eight sums are added in turn (one token over 131071 keys: 152 pieces an item; a warp alone
-// took 55 us). 
+// took 55 us).
 constexpr int kFewParts = 24;
 
 struct JoinPart {

@@ -6,14 +6,14 @@
 // Both products are f16: the codes are widened to f16 in shared memory (64 KB of writes a tile, against 256 KB that the
 // products read), the query rows and the weights rounded to it.  Two blocks of 128 rows take turns, and a block's
 // scores are formed in halves of 64 keys with columns of their own: while the weights of one half are formed, the
-// tensor cores run the products of the others.  (With one set of columns a block: 1170 us where this takes 865.)
+// tensor cores run the products of the others.  (With one set of columns a block: 1170 us where this took 865.)
 //
 // Warps 0-3 and 4-7 form the weights of the two blocks, a thread a row, so that a row's maximum and sum need no
 // exchange; warps 8-11 and 13-15 load codes of keys and of values, a tile ahead in registers, and widen them; one thread
 // of warp 12 issues the products, and waits for itself (as a warp with votes: 1090).  An f32 query has two terms, two
 // products, and its 128 rows the shared memory of 256.
 //
-// What bounds it, of 2048 tokens over 16384 rows with 64 query and 8 kv heads of 128 (865 us, 1.19 PFLOP/s, 63% of the
+// What bounds it, of 2048 tokens over 16384 rows with 64 query and 8 kv heads of 128 (841 us, 1.23 PFLOP/s, 65% of the
 // measured bf16 peak): a half's weights take a warp some 1000 cycles besides 500 of waits and hand-over (two warps a
 // scheduler: 64 exp2 each are 512), the tensor cores 640 a block and half (QK^T as m128n64 is bound by shared memory, 48
 // cycles an instruction); no part alone explains the rest: without exp2, widening, loads and 7 of 8 products it still

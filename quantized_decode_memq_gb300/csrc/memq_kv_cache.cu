@@ -9,7 +9,11 @@
 //
 // A warp serves the rows of one block and head, keys in its lower half and values in its upper: a lane
 // holds D / 16 elements of each row, so inputs are read once, a row's codes leave as 16 lanes x 8 bytes and
-// the maximum is one reduction a block.
+// the maximum is one reduction a block.  16381 rows of bf16, 8 kv heads of 128: 26 us, 3.9 TB/s of what is read and
+// written (67 + 34 MB), bound by a block's work behind its loads (issue 42%, DRAM 33%); 256 single rows of f32 6.5 us.
+//
+// A read is latency: slot, then codes and scale, of rows that lie anywhere (16381 rows of 8 x 128 11 us each pool, 4.6
+// TB/s of codes and bf16).
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>

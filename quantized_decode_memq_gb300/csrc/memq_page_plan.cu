@@ -13,7 +13,8 @@
 // bisection in the sums.  Pops may take what was pushed by the same call: a cluster of CTAs, with one
 // barrier between the two, rather than a grid, which would need two launches.
 //
-// A step is bound by latency.  1 request: one CTA; 1024 requests with 27,000 new tokens: a cluster of 8.
+// A step is bound by latency.  1 request: one CTA, 4.5 us; 1024 requests with 27,000 new tokens: a cluster of 8, 9.6 us,
+// of three prefix sums behind one another, the barrier and a bisection a thread.
 #include <cstdint>
 #include <cuda_runtime.h>
 

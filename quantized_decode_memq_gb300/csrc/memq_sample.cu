@@ -16,12 +16,22 @@
 // A cluster of CTAs keeps a row in shared memory, so it is read once; the number of CTAs is chosen to fill
 // the GPU with few rows and to let two CTAs share an SM with many.  Then, by what the row asks for:
 //   greedy          the first of the largest
-//   top-k           The k-th largest of all is not below t if every one of the C CTAs has ceil(k / C) threads whose
+//   small top-k     The k-th largest of all is not below t if every one of the C CTAs has ceil(k / C) threads whose
 //                   largest is t or more; what is t or more (usually little over k) is gathered and sorted by one CTA.
-//   top-p           The weights go into 1536 steps of 2^-6 of x = log2 of the largest's ratio, exactly, so the step
-//                   that holds the cut is known; its tokens are gathered and sorted (finer steps when they are many).
-//   then            One pass of weights over what is kept, the draw from the warps' sums.
+//   other top-k     The tokens are counted by steps of 1 / 25 of x = log2 of the largest's ratio, so the step that
+//                   holds the cut is known; its tokens are gathered and sorted (finer steps when they are many).
+//   top-p           The same with weights, added exactly, in 1536 steps of 1 / 64.
+//   then            One pass of weights over what is kept, the draw from the warps' sums; behind top-p, by the one CTA
+//                   whose steps' sum holds the drawn place.
+// bf16 logits have few values: top-p counts them and weighs each once, the draw looks them up (256 rows of 131072 169 us
+// -> 111, f32 as before; from 8192 tokens a CTA, 256 rows of 16384 with top-p 55 -> 37, 4000 tokens a CTA gain nothing).
 // Rows that defeat this (thousands of equal logits at the cut) are cut by bisection over keys, then over indices.
+//
+// us by what all rows ask for, greedy / top-k 50 / no cut / top-p 0.9:  1 x 32000 f32 3.5 / 8.7 / 7.4 / 23;  8 x 128259 f32
+// 5.0 / 12 / 17 / 42;  256 x 131072 bf16 28 / 59 / 99 / 187, f32 49 / 89 / 156 / 343;  256 x 16384 bf16 with top-k 500 31.
+// What bounds it: the load alone is 0.8 (256 x 131072 bf16, greedy: 2.4 TB/s, a CTA loads and then works), the exact weights 60
+// instructions a token and pass (f32), counting 11 cycles a warp and token (shared atomics); of few rows, latency: eight
+// cluster barriers of 1200 cycles, the sort by one CTA 7000 (8 x 128259: 80000 cycles, 37000 of them in the two passes).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -47,7 +57,7 @@ constexpr uint32_t kLeastKey = 0x007fffffu;  // of -infinity; NaN has key 0
 constexpr int64_t kMaxVocab = 360000;
 // bf16 logits: a table of the weights of ten binades of values, of either sign.
 constexpr uint32_t kHalf = 10 * 128, kValues = 2 * kHalf;
-constexpr int kTabled = 8192;   // tokens of a CTA from which it pays
+constexpr int kTabled = 8192;  // tokens of a CTA from which it pays
 
 // 2^(-j / 512) in units of 2^-62, formed by the compiler: the 512th root of 1/2 by nine square roots, then its powers.
 struct Powers {
@@ -205,9 +215,8 @@ __device__ __forceinline__ void weights_of(const Scale &s, const unsigned long l
     }
 }
 
-// Few bf16 numbers lie between the largest logit and 24 octaves of weight below it: their weights and steps are formed
-// once a row and looked up (60 instructions a token and pass otherwise).
-// The least magnitude, as bits, of `binades` up to the largest of any logit there.
+// Few bf16 numbers lie between the largest logit and 24 octaves of weight below it: a table of them starts at
+// the least magnitude, as bits, of `binades` up to the largest of any logit there.
 __device__ __forceinline__ uint32_t table_base(const Scale &s, int binades) {
     const float far = fmaxf(fabsf(s.top), fabsf(s.top - __fdiv_rn(kCareful, s.hi)));
     return static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(far) >> 23) - (binades - 1), 0)) << 7;
@@ -247,7 +256,7 @@ __device__ __forceinline__ unsigned long long sum_values(const Scale &s, const S
     }
     while (__any_sync(kFullMask, miss != 0)) {
         const int now = __ffs(miss) - 1;
-        float v = 0.f;
+        float v = s.top;
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if (j == now) v = l[j];
@@ -1179,7 +1188,9 @@ extern "C" int memq_sample(int dtype, const void *logits, int64_t stride, const 
     while (ctas < kMaxCtas && (bytes_of(ctas) > smem / 2 || (rows * ctas * 2 <= sms && slice_of(ctas) > 2048))) ctas *= 2;
     if (bytes_of(ctas) > smem) return MEMQ_ERR_SHAPE;
     a.slice = slice_of(ctas);
-    // A CTA that has its SM to itself takes all the threads that two would.
+    // A CTA that has its SM to itself takes all the threads that two would (us with 512 / 1024: 32 x 128259 bf16 top-p
+    // 52 / 43, no cut 30 / 19; 64 x 32000 19 / 15; 8 x 128259 f32 42.5 / 42.0), unless its tokens are few (4000 of 1 x 32000:
+    // 23 / 26).
     const bool wide = rows * ctas <= sms && a.slice > 8192;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
