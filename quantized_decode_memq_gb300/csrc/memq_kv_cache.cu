@@ -9,8 +9,9 @@
 //
 // A warp serves the rows of one block and head, keys in its lower half and values in its upper: a lane
 // holds D / 16 elements of each row, so inputs are read once, a row's codes leave as 16 lanes x 8 bytes and
-// the maximum is one reduction a block.  16381 rows of bf16, 8 kv heads of 128: 26 us, 3.9 TB/s of what is read and
-// written (67 + 34 MB), bound by a block's work behind its loads (issue 42%, DRAM 33%); 256 single rows of f32 6.5 us.
+// the maximum is one reduction a block.  16381 rows of bf16, 8 kv heads of 128: 24.4 us (26 without the
+// prefetch), 4.1 TB/s of what is read and written (67 + 34 MB), bound by a block's work behind its loads (issue 42%,
+// DRAM 33%); 256 single rows of f32 6.6 us.
 //
 // A read is latency: slot, then codes and scale, of rows that lie anywhere (16381 rows of 8 x 128 11 us each pool, 4.6
 // TB/s of codes and bf16).
@@ -33,6 +34,8 @@ constexpr int kBlock = 16;  // tokens that share a scale
 constexpr int kAppendThreads = 128, kAppendWarps = kAppendThreads / 32;
 constexpr int kReadThreads = 256;
 constexpr int kLeast = -100;  // exponent of the least scale
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 struct AppendArgs {
     const void *k, *v;
@@ -135,6 +138,12 @@ __global__ void __launch_bounds__(kAppendThreads, BF16 || D == 64 ? 4 : 2) kv_ap
         const int64_t s = __ldcg(a.slots + r);
         return s < 0 || s >= a.pool ? -1 : s / kBlock;
     };
+    if (a.window > 1 && r0 + part < a.n) {  // the rows are on their way to L2 while the slots are looked up
+        const uint8_t *row = static_cast<const uint8_t *>(half ? a.v : a.k) +
+                             ((r0 + part) * (half ? a.v_stride : a.k_stride) + h * D) * (BF16 ? 2 : 4);
+#pragma unroll
+        for (int i = 0; i < D * (BF16 ? 2 : 4); i += 128) prefetch_l2(row + i);
+    }
     // rows of this window that begin a block
     const int64_t mine = r0 + lane < r_end ? r0 + lane : -1;
     if (h == 0 && mine >= 0 && __ldcg(a.slots + mine) >= a.pool) atomicOr(&g_kv_fault, kFaultInput);
