@@ -508,7 +508,7 @@ int memq_kv_cache_read(int dtype, const uint8_t *cache, const float *scales, con
  * eleven bits (exact for bf16) down to 2^-29 of its row's largest, an f32 one to 22; a weight times its
  * values' scale, for bf16 outputs, to eleven bits, in steps of 2^-33 of the largest such product of the row where
  * those are coarser; to 22 bits for f32 outputs.  A scale of values below 2^-100 counts as 2^-100.  A
- * query row that is not finite gives NaN.
+ * query row that is not finite gives NaN, or zeros if it sees no row.
  * Results do not depend on timing; they depend on how the keys are split, so the same row may differ in
  * the last bits between batches.
  * Errors: MEMQ_ERR_SHAPE (also a workspace too small), MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
