@@ -1,6 +1,8 @@
 """The K/V cache, the attention over it, the page plan and the sampler on the CPU: the f64 reference's own
 pins, and refusals before any CUDA call."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -8,6 +10,7 @@ import torch
 
 import kv_reference as ref
 from paged_reference import E4M3
+from quantized_decode_memq_gb300.build import CSRC
 
 
 @pytest.fixture(scope="module")
@@ -190,3 +193,15 @@ def test_binding_refuses_host_tensors_and_wrong_kinds(lib):
         m.memq_sample(torch.zeros(2, 5), torch.zeros(2))
     with pytest.raises(TypeError):
         m.memq_sample(torch.zeros(2, 5, dtype=torch.float16), torch.zeros(2))
+
+
+def test_the_sampler_reaches_into_other_ctas_between_cluster_barriers():
+    """Another CTA's shared memory is touched only behind the entry barrier's wait, and a wait stands behind the last time."""
+    with open(os.path.join(CSRC, "memq_sample.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    body = text[text.index("sample_kernel(const SampleArgs a) {"):text.index("bool misaligned(")]
+    remote = [m.start() for m in re.finditer(r"\b(?:in_cta|join_lists<T>|cluster_sum<T>)\(", body)]
+    waits = [m.start() for m in re.finditer(r"\b(?:cluster_sync|cluster_wait)\(\)", body)]
+    entry = [m.start() for m in re.finditer(r"\bcluster_wait_entry\(\)", body)]
+    assert len(entry) == 1 and body.index("cluster_arrive_entry()") < entry[0] < remote[0]
+    assert len(remote) > 10 and remote[-1] < waits[-1]
