@@ -22,8 +22,8 @@
 // memory 16 bytes at once, and no code is moved between lanes.  The first tiles of a warp's next item are sent behind
 // the last of this one, so the ring does not run dry between items.
 // 64 sequences of up to 16384 rows, 64 query and 8 kv heads of 128: 212 us, 6.36 TB/s, 94% of the measured copy rate;
-// one of 131071 rows: 47 us, 5.7 TB/s, and 11 for the pieces (8 items in 1216 runs).  A short call is latency: of 16 us at
-// 2048 rows the row kernel takes 10 (lengths, pages, scales and codes are read one behind another), the join 6.
+// one of 131071 rows: 47 us, 5.7 TB/s, and 7 for the pieces (8 items in 1216 runs).  A short call is latency: of 14 us at
+// 8192 rows the row kernel takes 10 (lengths, pages, scales and codes are read one behind another), the join 4.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -608,7 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Adds the pieces of the items that several runs shared, in the runs' order.  CTAs (x, 0 .. gridDim.y - 1) serve the
 // x-th such item.  Up to kFewParts pieces a warp adds a row's alone, eight rows under way; above, the CTA's warps add
 // every eighth and the eight sums are added in turn (one token over 131071 keys: 152 pieces an item; a warp alone
-// took 55 us).
+// took 55 us).  A join of few CTAs is latency, so its pieces are fetched EARLY, while their weights are formed, which takes
+// 180 registers: 1 x 131071 56.6 -> 53.7 us, 1 x 8192 15.4 -> 13.8; one of many keeps 48 (2048 tokens over 2048 rows 117,
+// early 142).
 constexpr int kFewParts = 24;
 
 struct JoinPart {
@@ -619,8 +621,8 @@ struct JoinPart {
     int runs, stride;  // runs, rows of a piece
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, const JoinPart tiles, const JoinPart rows) {
+template <int D, bool EARLY>
+__global__ void __launch_bounds__(kThreads, EARLY ? 1 : 5) attn_join_kernel(const AttnArgs a, const JoinPart tiles, const JoinPart rows) {
     constexpr int E = D / 32;
     __shared__ float red[2][kWarps];
     __shared__ float sums[kWarps][D];
@@ -649,33 +651,49 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, c
         }
     };
     const auto slot_of = [&](int k, int r) { return static_cast<int64_t>(k == 0 ? 2 * run + 1 : 2 * (run + k)) * stride + r; };
-    const auto add = [&](float(&acc)[E], int64_t slot, float by) {
+    const auto fetch = [&](float(&v)[E], int64_t slot) {
         const float *src = p.part + slot * D + lane * E;
         if (E == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-            acc[0] = fmaf(v.x, by, acc[0]);
-            acc[1] = fmaf(v.y, by, acc[1]);
-            acc[E - 2] = fmaf(v.z, by, acc[E - 2]);
-            acc[E - 1] = fmaf(v.w, by, acc[E - 1]);
+            const float4 u = __ldcg(reinterpret_cast<const float4 *>(src));
+            v[0] = u.x;
+            v[1] = u.y;
+            v[E - 2] = u.z;
+            v[E - 1] = u.w;
         } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-            acc[0] = fmaf(v.x, by, acc[0]);
-            acc[1] = fmaf(v.y, by, acc[1]);
+            const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
+            v[0] = u.x;
+            v[1] = u.y;
         }
+    };
+    const auto add = [&](float(&acc)[E], const float(&v)[E], float by) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = fmaf(v[i], by, acc[i]);
     };
     if (parts <= kFewParts) {
         for (int r = y * kWarps + warp; r < owner.rows; r += p.share * kWarps) {
             float2 st = make_float2(kAttnUnset, 0.f);
             if (lane < parts) st = __ldcg(p.stats + slot_of(lane, r));
+            float v[EARLY ? kFewParts : 1][E];  // past the last piece: the last again, with weight 0
+            if constexpr (EARLY) {
+#pragma unroll
+                for (int k0 = 0; k0 < kFewParts; k0 += 8)
+                    if (k0 < parts) {
+#pragma unroll
+                        for (int k = k0; k < k0 + 8; ++k) fetch(v[k], slot_of(min(k, parts - 1), r));
+                    }
+            }
             const float w = ex2(st.x - warp_max(st.x)), total = warp_sum(st.y * w);
             float acc[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] = 0.f;
-            for (int k0 = 0; k0 < parts; k0 += 8) {  // past the last piece: the last again, with weight 0
+#pragma unroll(EARLY ? kFewParts / 8 : 1)
+            for (int k0 = 0; k0 < kFewParts && (EARLY || k0 < parts); k0 += 8) {
+                if (EARLY && k0 >= parts) continue;
 #pragma unroll
-                for (int k = k0; k < k0 + 8; ++k) {
-                    const float by = __shfl_sync(kFullMask, w, k & 31);
-                    add(acc, slot_of(min(k, parts - 1), r), k < parts ? by : 0.f);
+                for (int i = 0; i < 8; ++i) {
+                    if (!EARLY) fetch(v[0], slot_of(min(k0 + i, parts - 1), r));
+                    const float by = __shfl_sync(kFullMask, w, (k0 + i) & 31);
+                    add(acc, v[EARLY ? k0 + i : 0], k0 + i < parts ? by : 0.f);
                 }
             }
             put(r, acc, total);
@@ -683,7 +701,12 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, c
         return;
     }
     for (int r = y; r < owner.rows; r += p.share) {
-        float top = kAttnUnset;
+        float v[EARLY ? 16 : 1][E], top = kAttnUnset;
+        const auto fetch16 = [&](int k0) {  // of this warp's: every eighth from k0 on
+#pragma unroll
+            for (int i = 0; i < 16; ++i) fetch(v[EARLY ? i : 0], slot_of(min(k0 + i * kWarps, parts - 1), r));
+        };
+        if (EARLY) fetch16(warp);
         for (int k = tid; k < parts; k += kThreads) top = fmaxf(top, __ldcg(p.stats + slot_of(k, r)).x);
         top = warp_max(top);
         if (lane == 0) red[0][warp] = top;
@@ -703,10 +726,12 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a, c
             }
             const int n = min(32, (parts - k0 + kWarps - 1) / kWarps);
             for (int i0 = 0; i0 < n; i0 += 16) {
+                if (EARLY && (k0 != warp || i0 != 0)) fetch16(k0 + i0 * kWarps);
 #pragma unroll
-                for (int i = i0; i < i0 + 16; ++i) {
-                    const float by = __shfl_sync(kFullMask, w, i & 31);
-                    add(acc, slot_of(min(k0 + i * kWarps, parts - 1), r), i < n ? by : 0.f);
+                for (int i = 0; i < 16; ++i) {
+                    if (!EARLY) fetch(v[0], slot_of(min(k0 + (i0 + i) * kWarps, parts - 1), r));
+                    const float by = __shfl_sync(kFullMask, w, (i0 + i) & 31);
+                    add(acc, v[EARLY ? i : 0], i0 + i < n ? by : 0.f);
                 }
             }
         }
@@ -936,7 +961,9 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     cfg.gridDim = dim3(static_cast<unsigned>(tiles.x * tiles.share + rows.x * rows.share));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, d == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, a, tiles, rows) == cudaSuccess
-               ? MEMQ_OK
-               : MEMQ_ERR_LAUNCH;
+    using Join = void (*)(const AttnArgs, const JoinPart, const JoinPart);
+    static constexpr Join kJoins[2][2] = {{attn_join_kernel<64, false>, attn_join_kernel<64, true>},
+                                          {attn_join_kernel<128, false>, attn_join_kernel<128, true>}};
+    const bool early = cfg.gridDim.x <= static_cast<unsigned>(2 * grid);
+    return cudaLaunchKernelEx(&cfg, kJoins[d == 128][early], a, tiles, rows) == cudaSuccess ? MEMQ_OK : MEMQ_ERR_LAUNCH;
 }
