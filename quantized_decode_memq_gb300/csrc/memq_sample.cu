@@ -910,7 +910,10 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
             const unsigned long long goal = counting ? static_cast<unsigned long long>(k) : reach(p, total);
             const unsigned long long need = goal - sure;  // at least 1: the cut lies behind what is sure
             beyond = need > all;                          // in the tail
-            if (beyond) break;
+            if (beyond) {
+                cluster_sync();  // the sums have been read: what comes next writes them again
+                break;
+            }
 #pragma unroll
             for (int j = 0; j < kFetch; ++j) {
                 if (run < need && need <= run + mass[j])
