@@ -15,6 +15,7 @@
 //
 // A step is bound by latency.  1 request: one CTA, 4.5 us; 1024 requests with 27,000 new tokens: a cluster of 8, 9.6 us,
 // of three prefix sums behind one another, the barrier and a bisection a thread.
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -261,6 +262,24 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PlanAr
     }
 }
 
+constexpr int kMaxDevices = 64;
+
+constexpr int smem_bytes(int n_seq) { return (n_seq * 6 + 1) * static_cast<int>(sizeof(int32_t)); }
+
+// Allows the kernel the shared memory of the most requests on the current device, once: the allowance is the
+// function's, for all host threads, and the default one holds for the warps' sums beside it too.
+bool allow() {
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxSeqs)) !=
+        cudaSuccess)
+        return false;
+    if (dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+    return true;
+}
+
 bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 
 }  // namespace
@@ -299,12 +318,13 @@ extern "C" int memq_page_plan(const int32_t *cached, const int32_t *keep, const 
                granted, n_seq, static_cast<int>(n_tok), max_pages, __builtin_ctz(static_cast<unsigned>(page_size)),
                static_cast<int>(n_pages),
                ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(positions)) & 15) == 0};
+    if (!allow()) return MEMQ_ERR_LAUNCH;
     // One CTA serves what its threads hold in one round; more of it is shared by a cluster.
     const bool small = n_seq <= kPlanThreads && n_tok <= 4 * kPlanThreads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(small ? 1 : kClusterCtas);
     cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = (static_cast<size_t>(n_seq) * 6 + 1) * sizeof(int32_t);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(n_seq));
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -314,9 +334,5 @@ extern "C" int memq_page_plan(const int32_t *cached, const int32_t *keep, const 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cfg.dynamicSmemBytes > 48 * 1024 &&
-        cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(cfg.dynamicSmemBytes)) != cudaSuccess)
-        return MEMQ_ERR_LAUNCH;
     return cudaLaunchKernelEx(&cfg, page_plan_kernel, a) == cudaSuccess ? MEMQ_OK : MEMQ_ERR_LAUNCH;
 }
