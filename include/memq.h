@@ -439,8 +439,8 @@ int64_t memq_mla_attn_paged_workspace(int kv_rank);
  *   1 <= n_seq <= 4096;  n_tok <= 2^24;  page_size a power of two, 16 to 1024;  n_pages * page_size < 2^31;
  *   max_pages * page_size <= 2^30.  n_seq == 0 with n_tok == 0 is a no-op that accepts NULL pointers.
  * Nothing outside the arrays is read or written whatever the lengths say: a cached, keep, new_tok or n_free out
- * of range is clamped, new tokens past n_tok are not served, a page index outside the pool gives slot
- * -1, and pages that would pass the stack's end are dropped; each sets bit 5 of the device fault word.
+ * of range is clamped, a request whose new tokens pass n_tok is not served (those behind it without new tokens are),
+ * a page index outside the pool gives slot -1, and pages that would pass the stack's end are dropped; each sets bit 5 of the device fault word.
  * Errors: MEMQ_ERR_SHAPE, MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
  */
 int memq_page_plan(const int32_t *cached, const int32_t *keep, const int32_t *new_tok,

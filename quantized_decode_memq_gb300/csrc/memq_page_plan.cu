@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PlanAr
         tok0[b] = static_cast<int>(min(tok, static_cast<long long>(a.n_tok)));
         tok += fresh[i];
         const long long want = static_cast<long long>(keep[i]) + fresh[i];
-        room[i] = want <= cap && tok <= a.n_tok;
+        room[i] = want <= cap && (fresh[i] == 0 || tok <= a.n_tok);  // (behind too many tokens, those without any)
         bad = bad || tok > a.n_tok;
         have[i] = static_cast<int>((static_cast<long long>(cached[i]) + page - 1) >> a.page_shift);
         need[i] = room[i] ? static_cast<int>((want + page - 1) >> a.page_shift) : have[i];
