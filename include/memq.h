@@ -440,7 +440,8 @@ int64_t memq_mla_attn_paged_workspace(int kv_rank);
  *   max_pages * page_size <= 2^30.  n_seq == 0 with n_tok == 0 is a no-op that accepts NULL pointers.
  * Nothing outside the arrays is read or written whatever the lengths say: a cached, keep, new_tok or n_free out
  * of range is clamped, a request whose new tokens pass n_tok is not served (those behind it without new tokens are),
- * a page index outside the pool gives slot -1, and pages that would pass the stack's end are dropped; each sets bit 5 of the device fault word.
+ * a page index outside the pool gives slot -1, and pages that would pass the stack's end are dropped; each sets
+ * bit 5 of the device fault word.
  * Errors: MEMQ_ERR_SHAPE, MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
  */
 int memq_page_plan(const int32_t *cached, const int32_t *keep, const int32_t *new_tok,
@@ -506,9 +507,9 @@ int memq_kv_cache_read(int dtype, const uint8_t *cache, const float *scales, con
  * expires sets bit 6.
  * Numerics: codes are used exactly, sums, maxima and normalisation are f32.  A query element is rounded to
  * eleven bits (exact for bf16) down to 2^-29 of its row's largest, an f32 one to 22; a weight times its
- * values' scale, for bf16 outputs, to eleven bits, in steps of 2^-33 of the largest such product of the row where
- * those are coarser; to 22 bits for f32 outputs.  A scale of values below 2^-100 counts as 2^-100.  A
- * query row that is not finite gives NaN, or zeros if it sees no row.
+ * values' scale, to eleven bits for bf16 outputs and to 22 for f32 ones, in steps of 2^-33 of the largest such product
+ * of the row where those are coarser (for that product a scale below 2^-80 counts as 2^-80).  A scale of values below
+ * 2^-100 counts as 2^-100.  A query row that is not finite gives NaN, or zeros if it sees no row.
  * Results do not depend on timing; they depend on how the keys are split, so the same row may differ in
  * the last bits between batches.
  * Errors: MEMQ_ERR_SHAPE (also a workspace too small), MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.

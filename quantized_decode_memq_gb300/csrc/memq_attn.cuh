@@ -32,7 +32,10 @@ constexpr float kAttnLog2e = 1.4426950408889634f;
 constexpr float kAttnTop = 9.f;
 constexpr float kAttnSlack = 6.f;
 constexpr float kAttnLeastScale = 0x1p-100f;  // a smaller scale of values counts as this
-constexpr float kAttnLeastLog = -60.f;  // smaller value scales (log2) count as this in the reference
+// Value scales below 2^kAttnLeastLog count as that in the reference.  The sum of weights is of p / vs, each at most
+// 2^(kAttnTop + kAttnSlack - kAttnLeastLog) = 2^95: 2^30 of them stay below 2^125, and the reciprocal is a normal number.
+// (At -60 weights of rows whose scales are all below 2^-70 lost bits, and from 2^-95 on all of them.)
+constexpr float kAttnLeastLog = -80.f;
 
 // A piece of an item's rows whose keys were shared among several runs, noted by the run that holds its
 // first key (`rows` is 0 otherwise): the other pieces are those of the runs up to `last`.
