@@ -532,8 +532,8 @@ int64_t memq_attn_paged_workspace(int d);
  *           first token)
  *   min_p   of those the ones with w_i >= min_p (<= 0 or NaN: all; 1 at most), and the first token in any case
  * and out = the first kept token in the order of indices whose cumulative weight is above u times the kept
- * tokens' weight (u < 0 or NaN counts as 0, u >= 1 gives the last kept token).  temperature <= 0 or NaN: the largest
- * logit, the first of equal ones.
+ * tokens' weight (u < 0 or NaN counts as 0, u >= 1 gives the last kept token that has a weight).  temperature <= 0
+ * or NaN: the largest logit, the first of equal ones.
  *   dtype    a memq_dtype: the type of the logits
  *   logits   device, [rows][vocab], rows `stride` elements apart (>= 0), aligned to an element
  *   temperature, top_p, min_p, u   device, f32 [rows];  top_k   device int32 [rows]; each but u may be NULL
@@ -542,9 +542,10 @@ int64_t memq_attn_paged_workspace(int d);
  *   0 <= rows <= 2^20 (0 = no-op);  1 <= vocab <= 360000
  * NaN logits and those of -infinity are never drawn; in a row without others the first of the largest is given
  * (NaN below -infinity).  Several of +infinity share the weight.  -0 equals 0.
- * Numerics: a weight is formed to within 2^-41 of the largest one's and sums are exact, so that a token's
- * cumulative weight is known to about vocab^(1/2) 2^-42; a weight below 2^-60 counts as 0.  Results do not depend
- * on timing or on the other rows.
+ * Numerics: a weight is a whole number of 2^-44 of the largest one's, formed to within 2^-41, and sums are exact, so
+ * that a token's cumulative weight is known to vocab 2^-41 (equal logits are off alike), to about vocab^(1/2) 2^-42
+ * where logits differ; a weight of 2^-45 or less counts as 0 and is not drawn.  Results do not depend on timing or on
+ * the other rows.
  * Errors: MEMQ_ERR_SHAPE, MEMQ_ERR_NULL, MEMQ_ERR_ALIGN, MEMQ_ERR_LAUNCH.
  */
 int memq_sample(int dtype, const void *logits, int64_t stride, const float *temperature,
