@@ -21,8 +21,10 @@
 // 16) consecutive bytes of key g, and of the values the 16 (8) columns from 16 g on: both are read from shared
 // memory 16 bytes at once, and no code is moved between lanes.  The first tiles of a warp's next item are sent behind
 // the last of this one, so the ring does not run dry between items.
-// 64 sequences of up to 16384 rows, 64 query and 8 kv heads of 128: 212 us, 6.36 TB/s, 94% of the measured copy rate;
-// one of 131071 rows: 47 us, 5.7 TB/s, and 7 for the pieces (8 items in 1216 runs).  A short call is latency: of 14 us at
+// 64 sequences of up to 16384 rows, 64 query and 8 kv heads of 128: 213 to 221 us from run to run, 6.1 to 6.3 TB/s, 90 to
+// 94% of the measured copy rate; one of 131071 rows: 47 us, 5.7 TB/s, and 7 for the pieces (8 items in 1216 runs).
+// More than 16 rows of a kv head are items of their own, each of which reads the keys again (through L2): 4 tokens of 8
+// heads over 32768 rows 35 us, where the cache's bytes take 9.9.  A short call is latency: of 14 us at
 // 8192 rows the row kernel takes 10 (lengths, pages, scales and codes are read one behind another), the join 4.
 #include <algorithm>
 #include <atomic>
@@ -825,8 +827,8 @@ struct Workspace {
 };
 int64_t workspace_need(int grid, int d) { return Workspace(grid * kWarps, kRows, d).bytes() + Workspace(grid, 256, d).bytes(); }
 // Sequences of more query rows (heads of a group, times tokens) than this take the tensor-core kernel.  us with 16 /
-// 32 / 64, 64 query and 8 kv heads of 128: 4 tokens (32 rows) over 32768 rows 42.4 / 35.9 / 35.9, 48 sequences of 4 over
-// 4096 171 / 147 / 146; 8 tokens (64 rows) over 32768 48.0 / 48.0 / 51.3, 48 sequences of 8 177 / 177 / 269.
+// 32 / 64, 64 query and 8 kv heads of 128: 4 tokens (32 rows) over 32768 rows 41.9 / 35.2 / 35.2, 48 sequences of 4 over
+// 4096 169 / 149 / 150; 8 tokens (64 rows) over 32768 43.1 / 42.8 / 50.9, 48 sequences of 8 172 / 172 / 271.
 constexpr int kRowsKernelMost = 32;
 
 }  // namespace
@@ -917,7 +919,9 @@ extern "C" int memq_attn_paged(int q_dtype, const void *q, int64_t q_stride, con
     const bool q2 = q_dtype == MEMQ_F32, p2 = out_dtype == MEMQ_F32;
     const Workspace of_rows(runs, kRows, d), of_tiles(grid, q2 || p2 ? 128 : 256, d);
     // One token a sequence, or rows that no sequence can have more of than a warp holds: the stream of keys is
-    // all.  (More tokens than sequences may still lie in short ones: each kernel takes its own.)
+    // all.  (More tokens than sequences may still lie in short ones: each kernel takes its own.  No more tokens than
+    // sequences may be one sequence's, which the lengths on the device tell too late: a chunk of 200 over 4096 rows takes
+    // 54 us alone and 129 in 256 slots of which the others are empty.)
     const bool rows_only = n_tok <= n_seq || n_tok * a.group <= kRowsKernelMost;
     JoinPart tiles{};
     if (!rows_only) {

@@ -10,11 +10,11 @@
 // A warp serves the rows of one block and head, keys in its lower half and values in its upper: a lane
 // holds D / 16 elements of each row, so inputs are read once, a row's codes leave as 16 lanes x 8 bytes and
 // the maximum is one reduction a block.  16381 rows of bf16, 8 kv heads of 128: 24.4 us (26 without the
-// prefetch), 4.1 TB/s of what is read and written (67 + 34 MB), bound by a block's work behind its loads (issue 42%,
-// DRAM 33%); 256 single rows of f32 6.6 us.
+// prefetch), 4.1 TB/s of what is read and written (67 + 34 MB), bound by a block's work behind its loads, with none of the
+// next one's in flight (issue 42%, DRAM 33%); of f32 42.6 us, 3.9 TB/s; 256 single rows of f32 6.6 us.
 //
-// A read is latency: slot, then codes and scale, of rows that lie anywhere (16381 rows of 8 x 128 11 us each pool, 4.6
-// TB/s of codes and bf16).
+// A read is latency: slot, then codes and scale, of rows that lie anywhere (16381 rows of 8 x 128 11.4 us each pool, 4.4
+// TB/s of codes and bf16; to f32 20.4 us).
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -371,7 +371,9 @@ extern "C" int memq_kv_cache_append(int dtype, const void *k, int64_t k_stride, 
         misaligned(v_scales, 4))
         return MEMQ_ERR_ALIGN;
     // A warp looks for its blocks among 16 rows (a prompt has one or two there), or serves the one row that it
-    // has when rows are few: a decode step's rows lie in different blocks, which would wait for one another.
+    // has when rows are few: a decode step's rows lie in different blocks, which would wait for one another.  us with one
+    // row / 16 rows a warp, 8 kv heads of 128: 256 rows of bf16 in as many blocks 4.5 / 32, of a prompt 4.5 / 4.3; 2048
+    // rows 22 / 36 and 10.6 / 6.3; 4096 rows 42 / 37 and 17.5 / 6.7; f32, 2048 rows 40 / 36 and 17.6 / 6.9.
     const int window = n * n_kv <= 16384 ? 1 : kBlock;
     AppendArgs a{k, v, k_stride, v_stride, slots, k_cache, v_cache, k_scales, v_scales, n, n_pages * page_size, n_kv,
                  __builtin_ctz(static_cast<unsigned>(page_size)), window};

@@ -20,15 +20,18 @@
 //                   largest is t or more; what is t or more (usually little over k) is gathered and sorted by one CTA.
 //   other top-k     The tokens are counted by steps of 1 / 25 of x = log2 of the largest's ratio, so the step that
 //                   holds the cut is known; its tokens are gathered and sorted (finer steps when they are many).
-//   top-p           The same with weights, added exactly, in 1536 steps of 1 / 64.
+//   top-p           The same with weights, added exactly, in 1536 steps of 1 / 64 (24 octaves).
 //   then            One pass of weights over what is kept, the draw from the warps' sums; behind top-p, by the one CTA
 //                   whose steps' sum holds the drawn place.
 // bf16 logits have few values: top-p counts them and weighs each once, the draw looks them up (256 rows of 131072 169 us
 // -> 111, f32 as before; from 8192 tokens a CTA, 256 rows of 16384 with top-p 55 -> 37, 4000 tokens a CTA gain nothing).
-// Rows that defeat this (thousands of equal logits at the cut) are cut by bisection over keys, then over indices.
+// Rows that defeat this are cut by bisection over keys, then over indices: thousands of equal logits at the cut, and a
+// top-p that ends among weights below 2^-24 (which have no steps), as near 1 it does in steep rows and flat ones.
 //
 // us by what all rows ask for, greedy / top-k 50 / no cut / top-p 0.9:  1 x 32000 f32 3.5 / 8.7 / 7.4 / 23;  8 x 128259 f32
 // 5.0 / 12 / 17 / 42;  256 x 131072 bf16 28 / 59 / 99 / 187, f32 49 / 89 / 156 / 343;  256 x 16384 bf16 with top-k 500 31.
+// Top-p 0.999 with the cut behind the steps in some rows: 8 x 128259 355, 256 x 131072 bf16 1120, f32 880; in all rows (one
+// token far above the others) 199, 1930 and 2370: bisection forms every weight up to 32 times.
 // What bounds it: the load alone is 0.8 (256 x 131072 bf16, greedy: 2.4 TB/s, a CTA loads and then works), the exact weights 60
 // instructions a token and pass (f32), counting 11 cycles a warp and token (shared atomics); of few rows, latency: eight
 // cluster barriers of 1200 cycles, the sort by one CTA 7000 (8 x 128259: 80000 cycles, 37000 of them in the two passes).
@@ -820,7 +823,8 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleArgs a)
             for (int b = tid; b < 2 * kBins; b += T) sh.steps.lo[b] = 0;
             if (tid == 0) sh.count = 0;
             __syncthreads();
-            // Small weights at once, into one sum: no cut lies there but in the flattest of rows.
+            // Small weights at once, into one sum: of 1e5 tokens up to 1e5 2^-24 of the largest, so that a cut lies there
+            // where top-p leaves less, in steep rows as in flat ones.
             unsigned long long tail = 0, none = 0;
             const auto count = [&](int b, unsigned long long w) {
                 const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.steps.lo[b], lo);
