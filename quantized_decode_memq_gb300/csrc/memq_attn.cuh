@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 
 #include "memq.h"
+#include "memq_attn_owner.cuh"
 #include "memq_dev.cuh"
 #include "memq_tc.cuh"
 
@@ -36,17 +37,6 @@ constexpr float kAttnLeastScale = 0x1p-100f;  // a smaller scale of values count
 // 2^(kAttnTop + kAttnSlack - kAttnLeastLog) = 2^95: 2^30 of them stay below 2^125, and the reciprocal is a normal number.
 // (At -60 weights of rows whose scales are all below 2^-70 lost bits, and from 2^-95 on all of them.)
 constexpr float kAttnLeastLog = -80.f;
-
-// A piece of an item's rows whose keys were shared among several runs, noted by the run that holds its
-// first key (`rows` is 0 otherwise): the other pieces are those of the runs up to `last`.
-struct __align__(16) AttnOwner {
-    int start;        // the sequence's first token
-    int row0;         // the item's first row among the t * group rows of (sequence, kv head)
-    int first, last;  // runs
-    int head, rows;
-    int unused[2];
-};
-static_assert(sizeof(AttnOwner) == 32, "two loads");
 
 struct AttnArgs {
     const void *q;

@@ -639,6 +639,10 @@ __global__ void __launch_bounds__(kThreads, EARLY ? 1 : 5) attn_join_kernel(cons
     const int4 raw[2] = {__ldcg(at), __ldcg(at + 1)};
     const AttnOwner owner = *reinterpret_cast<const AttnOwner *>(raw);
     if (owner.rows == 0) return;
+    if (!attn_owner_ok(owner, a.n_tok, a.n_kv, a.group, runs, stride)) {
+        if (tid == 0) atomicOr(&g_attn_fault, kAttnFaultInput);
+        return;
+    }
     const int run = owner.first, parts = min(owner.last, runs - 1) - run + 1;
     const auto put = [&](int r, const float(&v)[E], float total) {
         const float n = total == 0.f ? 0.f : __fdiv_rn(1.f, total);
