@@ -499,8 +499,8 @@ int memq_kv_cache_read(int dtype, const uint8_t *cache, const float *scales, con
  *   block_table, kv_len, cu_q   as memq_mla_attn_paged
  *   out_dtype    a memq_dtype: the type of out, [n_tok][nh][d] (device, 16-byte aligned)
  *   workspace    device, 16-byte aligned, at least memq_attn_paged_workspace(d) bytes; scratch of this
- *                call alone, neither initialised nor kept (what else writes there while the call runs spoils its
- *                outputs and may set bit 5, but nothing outside the arrays is touched)
+ *                call alone, neither initialised nor kept (what else writes there, or changes the lengths, while the
+ *                call runs spoils its outputs and may set bits 5 and 6, but nothing outside the arrays is touched)
  *   n_kv divides nh <= 1024;  n_tok <= 2^24;  n_tok * nh < 2^31;  n_seq <= 4096;  max_pages * page_size <= 2^30;
  *   scale * log2(e) finite.  n_tok == 0 or n_seq == 0 is a no-op that accepts NULL pointers.
  * Lengths are read on the device only, so a captured call serves other lengths of the same arrays; lengths,

@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             own.last = static_cast<int>((it.pos + it.units - 1) / per);
             own.head = it.head;
             own.rows = whole ? 0 : n_rows;
-            a.owner[a.by_item ? it.index : run] = own;
+            if (!a.by_item || it.index < runs) a.owner[a.by_item ? it.index : run] = own;
         }
         it = ctl->next[warp];
         row_now = row_then;
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // (no owner's note stays what it was before the call)
     for (; dead && a.by_item && it.live; it.advance(a, run_hi))
-        if (it.off == 0 && lane == 0) a.owner[it.index].rows = 0;
+        if (it.off == 0 && lane == 0 && it.index < runs) a.owner[it.index].rows = 0;
     if (dead) {  // copies in flight land before shared memory is given up, each wait bounded
         for (uint32_t i = taken; i != sent; ++i)
             (void)warp_wait_bounded(&ctl->full[warp][i % kStages], (i / kStages) & 1);

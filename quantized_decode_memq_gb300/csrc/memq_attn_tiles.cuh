@@ -98,7 +98,7 @@ __device__ __forceinline__ void next_tile_item(const AttnArgs &a, int rows_per, 
             if (++it.seq >= a.n_seq) {  // not with lengths that stand still: an item without rows and keys
                 it.seq = a.n_seq;
                 it.rows = 0;
-                it.s = AttnSeq{0, 0, 0};
+                it.s = AttnSeq{0, 1, 0};  // (a token that sees none: with t = 0 it came out as one that sees a key)
                 break;
             }
             it.s = attn_seq(a, __ldcg(a.cu_q + it.seq), __ldcg(a.cu_q + it.seq + 1), __ldcg(a.kv_len + it.seq));
@@ -346,6 +346,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tiles_kernel(const AttnA
         mbar_init(&ctl->q_ready, kBlocks * 4);
         mbar_init(&ctl->drain, 1);
         mbar_init_fence();
+        ctl->first = TileItem{};  // no item, should the lengths change before a thread finds the first
+        ctl->first_off = 0;
+        ctl->first_pos = 1ll << 62;
     }
     if (warp == kIssueWarp) tmem_alloc(&ctl->tmem, 512);
     griddep_wait();
