@@ -13,8 +13,8 @@
 // of warp 12 issues the products, and waits for itself (as a warp with votes: 1090).  An f32 query has two terms, two
 // products, and its 128 rows the shared memory of 256.
 //
-// What bounds it, of 2048 tokens over 16384 rows with 64 query and 8 kv heads of 128 (841 to 851 us, 1.21 to 1.23 PFLOP/s, 64 to 65% of the
-// measured bf16 peak): a half's weights take a warp some 1000 cycles besides 500 of waits and hand-over (two warps a
+// What bounds it, of 2048 tokens over 16384 rows with 64 query and 8 kv heads of 128 (841 to 851 us, 1.21 to 1.23 PFLOP/s,
+// 64 to 65% of the measured bf16 peak): a half's weights take a warp some 1000 cycles besides 500 of waits and hand-over (two warps a
 // scheduler: 64 exp2 each are 512), the tensor cores 640 a block and half (QK^T as m128n64 is bound by shared memory, 48
 // cycles an instruction).  What bounds the rest has not been found: without exp2, widening, loads and 7 of 8 products it
 // still takes 80% of the time.  f32 calls, two products of scores and two of outputs, 2048 tokens over 8192 rows: 886 us
